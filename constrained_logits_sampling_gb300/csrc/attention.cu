@@ -1,0 +1,110 @@
+// clsample_chunk_attention: attention of each sequence's newest tokens over its paged cache
+// (formulas in include/clsample.h).  Host side: argument checks, the handle's scratch and
+// the choice of kernels.
+#include <new>
+
+#include "attn_stream.cuh"
+
+struct clsample_attention {
+  int dev, sms;
+  float* partial;
+  int* arrived;
+};
+
+namespace clsample {
+namespace {
+
+constexpr int kStreamCtas = 2;  // per SM
+// two slots of (32 rows of 128 sums, a maximum and a sum each) per CTA
+constexpr size_t kStreamScratch = (size_t)kStreamCtas * 2 * 32 * 130 * sizeof(float);
+
+template <class T, int D, int MT>
+cudaError_t launch_stream(const AttnParams& P, int sms, cudaStream_t st) {
+  auto* fn = attn_stream_kernel<T, D, MT>;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamRing<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  fn<<<sms * kStreamCtas, kStreamThreads, StreamRing<D>::kBytes, st>>>(P);
+  return cudaGetLastError();
+}
+
+template <class T, int D>
+cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
+  P.min_rows = 0;
+  P.max_rows = 0x7fffffff;
+  return P.a.max_new * (int64_t)P.g <= 16 ? launch_stream<T, D, 1>(P, h->sms, st)
+                                          : launch_stream<T, D, 2>(P, h->sms, st);
+}
+
+}  // namespace
+}  // namespace clsample
+
+extern "C" {
+
+int clsample_attention_create(clsample_attention_t** out) {
+  using namespace clsample;
+  if (!out) return CLSAMPLE_ERR_NULL;
+  *out = nullptr;
+  int dev = 0, sms = 0;
+  const int rc = check_device(&dev, &sms);
+  if (rc != CLSAMPLE_SUCCESS) return rc;
+  auto* h = new (std::nothrow) clsample_attention{dev, sms, nullptr, nullptr};
+  if (!h) return CLSAMPLE_ERR_CUDA;
+  if (cudaMalloc(&h->partial, (size_t)sms * kStreamScratch) != cudaSuccess ||
+      cudaMalloc(&h->arrived, (size_t)sms * kStreamCtas * sizeof(int)) != cudaSuccess ||
+      cudaMemset(h->arrived, 0, (size_t)sms * kStreamCtas * sizeof(int)) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {
+    clsample_attention_destroy(h);
+    cudaGetLastError();
+    return CLSAMPLE_ERR_CUDA;
+  }
+  *out = h;
+  return CLSAMPLE_SUCCESS;
+}
+
+void clsample_attention_destroy(clsample_attention_t* h) {
+  if (!h) return;
+  if (h->partial) cudaFree(h->partial);
+  if (h->arrived) cudaFree(h->arrived);
+  delete h;
+}
+
+int clsample_chunk_attention(clsample_attention_t* h, const clsample_attention_args_t* a, clsample_stream_t stream) {
+  using namespace clsample;
+  if (!h || !a) return CLSAMPLE_ERR_NULL;
+  if (a->B < 0 || a->B > (1 << 24) - 1 || a->T < 0 || a->T > kMaxLen) return CLSAMPLE_ERR_BATCH;
+  if (a->dtype != CLSAMPLE_T_BF16 && a->dtype != CLSAMPLE_T_F16) return CLSAMPLE_ERR_DTYPE;
+  if (a->Hkv < 1 || a->Hq < a->Hkv || a->Hq > 65536 || a->Hq % a->Hkv != 0 || (a->D != 64 && a->D != 128) ||
+      a->num_pages < 0 || a->page_size < 1 || a->max_pages < 0 || a->max_new < 0 || a->window < 0 ||
+      !(a->scale > 0.f && a->scale <= 3.0e38f) || (int64_t)a->T * (a->Hq / a->Hkv) > 0x7fffffff - 1024)
+    return CLSAMPLE_ERR_SHAPE;
+  if (a->table_stride < a->max_pages) return CLSAMPLE_ERR_STRIDE;
+  if (a->B == 0) return CLSAMPLE_SUCCESS;
+  if (!a->cu_new || !a->kv_lens || (!a->page_table && a->max_pages > 0)) return CLSAMPLE_ERR_NULL;
+  if (a->T > 0 && (!a->q || !a->out)) return CLSAMPLE_ERR_NULL;
+  if (a->num_pages > 0 && a->T > 0 && (!a->k_cache || !a->v_cache)) return CLSAMPLE_ERR_NULL;
+  const int64_t strides = a->q_stride_t | a->q_stride_h | a->o_stride_t | a->o_stride_h | a->page_stride |
+                          a->slot_stride | a->head_stride;
+  if ((strides & 7) || !aligned16(a->q) || !aligned16(a->out) || !aligned16(a->k_cache) || !aligned16(a->v_cache))
+    return CLSAMPLE_ERR_ALIGN;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CLSAMPLE_ERR_CUDA;
+  if (dev != h->dev) return CLSAMPLE_ERR_DEVICE;
+  AttnParams P{};
+  P.a = *a;
+  if (P.a.window > kMaxLen) P.a.window = kMaxLen;  // longer than any sequence
+  P.g = a->Hq / a->Hkv;
+  P.page_shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz((unsigned)a->page_size) : -1;
+  P.capacity = capacity_of(a->max_pages, a->page_size);
+  P.partial = h->partial;
+  P.arrived = h->arrived;
+  P.scale_log2 = a->scale * 1.44269504088896341f;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (a->dtype == CLSAMPLE_T_BF16)
+    e = a->D == 128 ? launch<__nv_bfloat16, 128>(h, P, st) : launch<__nv_bfloat16, 64>(h, P, st);
+  else
+    e = a->D == 128 ? launch<__half, 128>(h, P, st) : launch<__half, 64>(h, P, st);
+  return e == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
+}
+
+}  // extern "C"

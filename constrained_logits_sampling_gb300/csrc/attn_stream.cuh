@@ -1,0 +1,383 @@
+// Attention for few query rows per key head: bound by reading keys and values once.
+//
+// A unit is 16 MT packed rows (attn_units.cuh).  The four warps of a CTA share the rows and
+// split the keys: of each tile of 64 keys a warp takes 16, loads them itself (cp.async, its
+// own ring of stages) and keeps its own running maximum, sum and output in registers, so no
+// barrier stands between a load and its use and every byte passes shared memory once.  The
+// products are mma.m16n8k16: with so few rows the tensor cores are nearly idle either way,
+// and the row tile can be 16 where tcgen05 has 64 at least.  The four warps' results meet in
+// shared memory at the end of a unit's span.
+#pragma once
+
+#include "attn_units.cuh"
+
+namespace clsample {
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr int kStreamThreads = 128;
+constexpr int kStreamKeys = 64;
+constexpr float kLn2 = 0.693147180559945309f;
+
+// Ring stages of a warp: two CTAs fit an SM, with about 190 KB of loads in flight.
+template <int D>
+struct StreamRing {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kBytes = 4 * kStages * 16 * D * 2 * 2;  // four warps, 16 keys and values a stage
+};
+
+// A scratch slot: R x D sums, then R maxima (log2 units) and R weights' sums.
+template <int R, int D>
+__device__ __forceinline__ float* scratch_slot(const AttnParams& P, int cta, int which) {
+  return P.partial + (int64_t)(cta * 2 + which) * (R * (D + 2));
+}
+
+// Writes four output elements of a packed row.
+template <class T>
+__device__ __forceinline__ void store_out4(const AttnParams& P, const Unit& u, int r, int d, float4 o) {
+  const int row = u.row0 + r;
+  T* dst = (T*)P.a.out + (int64_t)(u.q0 + row / P.g) * P.a.o_stride_t +
+           (int64_t)(u.h * P.g + row % P.g) * P.a.o_stride_h + d;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(Pair<T>::narrow(o.x, o.y), Pair<T>::narrow(o.z, o.w));
+}
+__device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, int r, float m, float l) {
+  const int row = u.row0 + r;
+  if (P.a.lse)
+    P.a.lse[(int64_t)(u.q0 + row / P.g) * P.a.Hq + u.h * P.g + row % P.g] =
+        l > 0.f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xff800000);
+}
+
+// Joins the partial sums of a unit cut by span boundaries: called by all threads of each
+// CTA that wrote a part; the last to arrive joins them all, in key order.
+template <class T, int R, int D, int NT>
+__device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin) {
+  __shared__ int last;
+  const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
+    if (last) P.arrived[c0] = 0;  // for the next call
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int i = threadIdx.x; i < u.rows * (D / 4); i += NT) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    float m = __int_as_float(0xff800000), l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+      const float* s = scratch_slot<R, D>(P, c, c == c0 ? 1 : 0);
+      const float mc = __ldcg(s + R * D + r), lc = __ldcg(s + R * D + R + r);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * D + d));
+      const float mn = fmaxf(m, mc);
+      const float f = m == mn ? 1.f : exp2_fast(m - mn), fc = mc == mn ? 1.f : exp2_fast(mc - mn);
+      o = make_float4(o.x * f + v.x * fc, o.y * f + v.y * fc, o.z * f + v.z * fc, o.w * f + v.w * fc);
+      l = l * f + lc * fc;
+      m = mn;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store_out4<T>(P, u, r, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (d == 0) store_lse(P, u, r, m, l);
+  }
+}
+
+template <class T, int D, int MT>
+__global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __grid_constant__ AttnParams P) {
+  constexpr int R = 16 * MT, S = StreamRing<D>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
+  constexpr int kTileBytes = 16 * D * 2, kStageBytes = 2 * kTileBytes;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ unsigned key_ok[4][S];
+  __shared__ float wm[4][R], wl[4][R];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const clsample_attention_args_t& a = P.a;
+  unsigned char* const ring = smem + warp * S * kStageBytes;
+  const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const float neg_inf = __int_as_float(0xff800000);
+
+  if (a.row_status) attention_status<kStreamThreads>(P);
+  Span span;
+  Unit u;
+  int64_t unit_begin;
+  if (!find_span<R, kStreamKeys, kStreamThreads>(P, &span, &u, &unit_begin)) return;
+
+  int64_t t = span.t0;
+  while (true) {
+    const int j0 = (int)(t - unit_begin);
+    const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+    const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
+    const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
+    const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
+    const int key0 = (u.tile0 + j0) * kStreamKeys + warp * 16;  // the warp's first key
+
+    // the page of this lane's key (lanes 0..15) in the span's tile i; -1: not to be read
+    auto page_of = [&](int i) {
+      const int key = key0 + i * kStreamKeys + (lane & 15);
+      if (i >= cnt || key < u.key_lo || key >= u.key_hi) return -1;
+      const int id = __ldg(table + (P.page_shift >= 0 ? key >> P.page_shift : key / a.page_size));
+      return id < a.num_pages ? id : -1;
+    };
+    auto issue = [&](int i, int page) {
+      const int stage = i % S;
+      const int key = key0 + i * kStreamKeys + (lane & 15);
+      const int slot = P.page_shift >= 0 ? key & ((1 << P.page_shift) - 1) : key % a.page_size;
+      const bool ok = page >= 0;
+      const int64_t off = ok ? (int64_t)page * a.page_stride + (int64_t)slot * a.slot_stride : 0;
+      const unsigned mask = __ballot_sync(~0u, ok) & 0xffffu;
+      if (lane == 0) key_ok[warp][stage] = mask;
+      const uint32_t base = ring_addr + stage * kStageBytes;
+      if (i < cnt) {
+#pragma unroll
+        for (int x = 0; x < KC / 2; ++x) {
+          const int row = (x * 32 + lane) / KC, ch = (x * 32 + lane) % KC;
+          const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
+          const bool live = (mask >> row) & 1;
+          const uint32_t dst = base + row * (D * 2) + ((ch ^ (row & 7)) << 4);
+          cp_async16(dst, kc + o, live);
+          cp_async16(dst + kTileBytes, vc + o, live);
+        }
+      }
+      cp_async_commit();
+    };
+
+    // the first stages are on their way before the queries are read
+    int page = page_of(0);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      const int next = page_of(i + 1);
+      issue(i, page);
+      page = next;
+    }
+
+    // queries as A operands, row limits
+    uint32_t q[MT][D / 16][4];
+    int pos[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = mt * 16 + hf * 8 + (lane >> 2);
+        const bool live = r < u.rows;
+        const int row = u.row0 + r;
+        const T* src = (const T*)a.q + (int64_t)(u.q0 + (live ? row / P.g : 0)) * a.q_stride_t +
+                       (int64_t)(u.h * P.g + (live ? row % P.g : 0)) * a.q_stride_h + (lane & 3) * 2;
+        pos[mt][hf] = live ? u.len - u.n + row / P.g : -1;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          q[mt][ks][hf] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16)) : 0u;
+          q[mt][ks][hf + 2] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16 + 8)) : 0u;
+        }
+      }
+    const int pos_first = u.len - u.n + u.row0 / P.g;
+    const int pos_last = u.len - u.n + (u.row0 + u.rows - 1) / P.g;
+
+    float o[MT][D / 8][4];
+    float m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][d][e] = 0.f;
+      m[mt][0] = m[mt][1] = neg_inf;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+
+    for (int i = 0; i < cnt; ++i) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      const int next = page_of(i + S);
+      issue(i + S - 1, page);
+      page = next;
+      const int stage = i % S;
+      const unsigned live = key_ok[warp][stage];
+      const uint32_t kb = ring_addr + stage * kStageBytes, vb = kb + kTileBytes;
+      const int key = key0 + i * kStreamKeys;
+
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][0][e] = s[mt][1][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int row = (lane & 7) + ((lane >> 4) << 3), ch = ks * 2 + ((lane >> 3) & 1);
+        uint32_t b[4];
+        ldmatrix4(b, kb + row * (D * 2) + ((ch ^ (row & 7)) << 4));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<T>(s[mt][0], q[mt][ks], b[0], b[1]);
+          mma16816<T>(s[mt][1], q[mt][ks], b[2], b[3]);
+        }
+      }
+      // every key of the tile is seen by every row (rows past the unit's are never stored)
+      const bool whole = live == 0xffffu && key + 15 <= pos_first &&
+                         (a.window <= 0 || key > pos_last - a.window);
+      bool moved = false;
+      float keep[MT][2];
+      uint32_t p[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float x[4] = {s[mt][0][hf * 2] * P.scale_log2, s[mt][0][hf * 2 + 1] * P.scale_log2,
+                        s[mt][1][hf * 2] * P.scale_log2, s[mt][1][hf * 2 + 1] * P.scale_log2};
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int c = (e >> 1) * 8 + (lane & 3) * 2 + (e & 1);
+              const int kp = key + c;
+              const bool seen = ((live >> c) & 1) && kp <= pos[mt][hf] &&
+                                (a.window <= 0 || kp > pos[mt][hf] - a.window);
+              if (!seen) x[e] = neg_inf;
+            }
+          }
+          float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+          const float mn = fmaxf(m[mt][hf], top);
+          const float base = mn == neg_inf ? 0.f : mn;  // a row that has seen no key yet
+          keep[mt][hf] = exp2_fast(m[mt][hf] - base);
+          moved |= mn != m[mt][hf];
+          m[mt][hf] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = exp2_fast(x[e] - base);
+            sum += x[e];
+          }
+          l[mt][hf] = l[mt][hf] * keep[mt][hf] + sum;
+          p[mt][hf] = Pair<T>::narrow(x[0], x[1]);
+          p[mt][hf + 2] = Pair<T>::narrow(x[2], x[3]);
+        }
+      }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            o[mt][d][0] *= keep[mt][0];
+            o[mt][d][1] *= keep[mt][0];
+            o[mt][d][2] *= keep[mt][1];
+            o[mt][d][3] *= keep[mt][1];
+          }
+      }
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = d * 2 + (lane >> 4);
+        uint32_t b[4];
+        ldmatrix4_trans(b, vb + row * (D * 2) + ((ch ^ (row & 7)) << 4));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<T>(o[mt][2 * d], p[mt], b[0], b[1]);
+          mma16816<T>(o[mt][2 * d + 1], p[mt], b[2], b[3]);
+        }
+      }
+    }
+
+    // the warps' results meet: each warp's sums go to its own ring, which is drained
+    cp_async_wait<0>();
+    __syncwarp();
+    float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = mt * 16 + hf * 8 + (lane >> 2);
+        float sum = l[mt][hf];
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
+        if ((lane & 3) == 0) {
+          wm[warp][r] = m[mt][hf];
+          wl[warp][r] = sum;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+          *reinterpret_cast<float2*>(mine + r * D + d * 8 + (lane & 3) * 2) =
+              make_float2(o[mt][d][hf * 2], o[mt][d][hf * 2 + 1]);
+      }
+    __syncthreads();
+    const bool done = cnt == u.tiles;
+    float* slot = scratch_slot<R, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
+    for (int i = tid; i < u.rows * (D / 4); i += kStreamThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      const float top = fmaxf(fmaxf(wm[0][r], wm[1][r]), fmaxf(wm[2][r], wm[3][r]));
+      const float base = top == neg_inf ? 0.f : top;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float lsum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = exp2_fast(wm[w][r] - base);
+        const float4 v =
+            *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * S * kStageBytes) + r * D + d);
+        sum = make_float4(sum.x + v.x * f, sum.y + v.y * f, sum.z + v.z * f, sum.w + v.w * f);
+        lsum += wl[w][r] * f;
+      }
+      if (done) {
+        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+        store_out4<T>(P, u, r, d, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+        if (d == 0) store_lse(P, u, r, top, lsum);
+      } else {
+        __stcg(reinterpret_cast<float4*>(slot + r * D + d), sum);
+        if (d == 0) {
+          __stcg(slot + R * D + r, top);
+          __stcg(slot + R * D + R + r, lsum);
+        }
+      }
+    }
+    if (!done) join_parts<T, R, D, kStreamThreads>(P, u, span, unit_begin);
+    t += cnt;
+    if (t >= span.t1) break;
+    __syncthreads();  // the rings and row sums have been read
+    unit_begin = t;
+    next_unit<R, kStreamKeys>(P, &u);
+  }
+}
+
+}  // namespace clsample

@@ -1,0 +1,199 @@
+// How an attention call is cut into work, shared by its kernels.
+//
+// A unit is one tile of query rows of one sequence and one key head: the sequence's n
+// tokens times the g query heads of the key head are n g packed rows (row r is token r / g,
+// head r % g), cut into tiles of R rows.  A unit walks the keys that any of its rows sees in
+// tiles of K keys.  All units' key tiles, laid end to end, are cut into equal spans, one per
+// CTA, whatever the sequences' lengths: a unit that lies in one span is finished there, one
+// that a span boundary cuts leaves partial sums in the handle's scratch, and the CTA that
+// arrives last joins them in key order.  Nothing waits for another CTA.
+#pragma once
+
+#include "paged.cuh"
+
+namespace clsample {
+
+struct AttnParams {
+  clsample_attention_args_t a;
+  int g;            // query heads per key head
+  int page_shift;   // log2(page_size), or -1
+  int capacity;     // positions that the page table holds
+  int min_rows;     // this launch takes the sequences with min_rows <= n g < max_rows
+  int max_rows;
+  float* partial;   // scratch: two slots per CTA
+  int* arrived;     // one counter per CTA, zero between calls
+  float scale_log2; // scale * log2(e)
+};
+
+struct Unit {
+  int b, h, qt;       // sequence, key head, row tile
+  int q0, n, len;     // the sequence's first row, its rows and length
+  int row0, rows;     // packed rows of the tile
+  int key_lo, key_hi; // keys that any row sees
+  int tile0, tiles;   // key tiles, at least one
+};
+
+template <int R, int K>
+struct UnitMap {
+  static __device__ __forceinline__ Seq seq_of(const AttnParams& P, int b) {
+    Seq s = load_seq(P.a.cu_new, P.a.kv_lens, b, P.a.T, P.capacity, P.a.max_new);
+    const int64_t rows = (int64_t)s.n * P.g;
+    if (rows < P.min_rows || rows >= P.max_rows) s.n = 0;  // another launch's
+    return s;
+  }
+  static __device__ __forceinline__ int row_tiles(const AttnParams& P, const Seq& s) {
+    return (int)(((int64_t)s.n * P.g + R - 1) / R);
+  }
+  // key range and tiles of row tile qt
+  static __device__ __forceinline__ void fill(const AttnParams& P, const Seq& s, int qt, Unit* u) {
+    u->q0 = s.q0;
+    u->n = s.n;
+    u->len = s.len;
+    u->qt = qt;
+    u->row0 = qt * R;
+    u->rows = min(R, s.n * P.g - u->row0);
+    const int first = s.len - s.n + u->row0 / P.g;  // positions of the first and last row
+    const int last = s.len - s.n + (u->row0 + u->rows - 1) / P.g;
+    u->key_hi = max(0, min(last + 1, s.len));
+    u->key_lo = P.a.window > 0 ? min(max(0, first - P.a.window + 1), u->key_hi) : 0;
+    u->tile0 = u->key_lo / K;
+    u->tiles = max(1, (u->key_hi + K - 1) / K - u->tile0);
+  }
+  // key tiles of one key head of a sequence
+  static __device__ __forceinline__ int64_t head_tiles(const AttnParams& P, const Seq& s) {
+    const int m = row_tiles(P, s);
+    int64_t t = 0;
+    Unit u;
+    for (int qt = 0; qt < m; ++qt) {
+      fill(P, s, qt, &u);
+      t += u.tiles;
+    }
+    return t;
+  }
+};
+
+// Sum of v over the block, and each thread's exclusive prefix; `buf` holds NT / 32 + 1 values.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* buf, int64_t* exclusive) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t run = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(~0u, run, o);
+    if (lane >= o) run += up;
+  }
+  __syncthreads();
+  if (lane == 31) buf[warp] = run;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) {
+    if (i < warp) base += buf[i];
+    total += buf[i];
+  }
+  *exclusive = base + run - v;
+  return total;
+}
+
+// The whole call's key tiles, and where this CTA's span begins: u is the unit that holds
+// tile t0 = total * cta / ctas, *offset the tile's place in it.  Returns false without work.
+struct Span {
+  int64_t total, t0, t1;
+  int ctas;  // CTAs with work: those with the lower indices
+};
+__device__ __forceinline__ int64_t span_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
+
+template <int R, int K, int NT>
+__device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit* u, int64_t* unit_begin) {
+  using M = UnitMap<R, K>;
+  __shared__ int64_t buf[NT / 32 + 1];
+  __shared__ int64_t found_rest;
+  __shared__ int found_b;
+  const int tid = threadIdx.x, B = P.a.B;
+  int64_t total = 0, ex = 0, mine = 0;
+  for (int base = 0; base < B; base += NT) {
+    mine = base + tid < B ? M::head_tiles(P, M::seq_of(P, base + tid)) * P.a.Hkv : 0;
+    total += block_scan<NT>(mine, buf, &ex);
+  }
+  span->total = total;
+  span->ctas = (int)min((int64_t)gridDim.x, total);
+  if ((int)blockIdx.x >= span->ctas) return false;
+  span->t0 = span_begin(total, span->ctas, blockIdx.x);
+  span->t1 = span_begin(total, span->ctas, blockIdx.x + 1);
+  int64_t seen = 0;
+  for (int base = 0; base < B; base += NT) {
+    if (B > NT) {
+      mine = base + tid < B ? M::head_tiles(P, M::seq_of(P, base + tid)) * P.a.Hkv : 0;
+    }
+    const int64_t sum = block_scan<NT>(mine, buf, &ex);
+    if (seen + ex <= span->t0 && span->t0 < seen + ex + mine) {
+      found_b = base + tid;
+      found_rest = span->t0 - (seen + ex);
+    }
+    seen += sum;
+    if (seen > span->t0) break;  // uniform
+  }
+  __syncthreads();
+  const int b = found_b;
+  const Seq s = M::seq_of(P, b);
+  const int64_t per_head = M::head_tiles(P, s);
+  int64_t rest = found_rest;
+  u->b = b;
+  u->h = (int)(rest / per_head);
+  rest -= u->h * per_head;
+  for (int qt = 0;; ++qt) {
+    M::fill(P, s, qt, u);
+    if (rest < u->tiles) break;
+    rest -= u->tiles;
+  }
+  *unit_begin = span->t0 - rest;
+  return true;
+}
+
+// The unit after u (the caller has checked that the span goes on).
+template <int R, int K>
+__device__ __forceinline__ void next_unit(const AttnParams& P, Unit* u) {
+  using M = UnitMap<R, K>;
+  Seq s{u->q0, u->n, u->len, true};
+  if (u->row0 + R < u->n * P.g) {
+    M::fill(P, s, u->qt + 1, u);
+    return;
+  }
+  if (++u->h >= P.a.Hkv) {
+    u->h = 0;
+    do {
+      s = M::seq_of(P, ++u->b);
+    } while (s.n == 0 && u->b + 1 < P.a.B);
+  }
+  M::fill(P, s, 0, u);
+}
+
+// The CTA whose span holds tile t.
+__device__ __forceinline__ int cta_of_tile(const Span& sp, int64_t t) {
+  int c = (int)(t * sp.ctas / sp.total);
+  while (c + 1 < sp.ctas && span_begin(sp.total, sp.ctas, c + 1) <= t) ++c;
+  while (c > 0 && span_begin(sp.total, sp.ctas, c) > t) --c;
+  return c;
+}
+
+// Statuses: one CTA per sequence at a time looks at its lengths and at every page id that
+// the call touches.
+template <int NT>
+__device__ __forceinline__ void attention_status(const AttnParams& P) {
+  const clsample_attention_args_t& a = P.a;
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Seq s = load_seq(a.cu_new, a.kv_lens, b, a.T, P.capacity, a.max_new);
+    int bad = !s.ok;
+    if (s.ok && s.n > 0 && s.len > 0) {
+      const int lo = a.window > 0 ? max(0, s.len - s.n - a.window + 1) : 0;
+      for (int p = lo / a.page_size + threadIdx.x; p <= (s.len - 1) / a.page_size; p += NT) {
+        const int id = __ldg(a.page_table + (int64_t)b * a.table_stride + p);
+        bad |= id < 0 || id >= a.num_pages;
+      }
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) a.row_status[b] = bad ? CLSAMPLE_ROW_INVALID : CLSAMPLE_ROW_OK;
+  }
+}
+
+}  // namespace clsample

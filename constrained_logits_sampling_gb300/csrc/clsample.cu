@@ -3129,6 +3129,8 @@ const char* clsample_strerror(int code) {
     case CLSAMPLE_ERR_CUDA: return "CUDA runtime error";
     case CLSAMPLE_ERR_DEVICE: return "wrong or unsupported CUDA device";
     case CLSAMPLE_ERR_MODE: return "unknown mode bit";
+    case CLSAMPLE_ERR_SHAPE: return "count, head layout, head size or page size out of range";
+    case CLSAMPLE_ERR_ALIGN: return "address or stride not aligned";
     default: return "unknown error";
   }
 }

@@ -47,7 +47,9 @@ class Args(ctypes.Structure):
 
 EXPORTS = ("clsample_create", "clsample_destroy", "clsample_apply", "clsample_prepare", "clsample_sample",
            "clsample_apply_static", "clsample_strerror", "clsample_geometry", "clsample_occupancy",
-           "clsample_debug_weights", "clsample_debug_uniforms", "clsample_allowed_to_bitmask")
+           "clsample_debug_weights", "clsample_debug_uniforms", "clsample_allowed_to_bitmask",
+           "clsample_kv_append", "clsample_attention_create", "clsample_attention_destroy",
+           "clsample_chunk_attention", "clsample_verify")
 
 
 def load_library(path: str = LIB_PATH):
@@ -83,6 +85,15 @@ def load_library(path: str = LIB_PATH):
                                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
                                                       ctypes.c_void_p]
             L.clsample_allowed_to_bitmask.restype = ctypes.c_int
+            for name in ("clsample_kv_append", "clsample_verify"):
+                getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+                getattr(L, name).restype = ctypes.c_int
+            L.clsample_attention_create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
+            L.clsample_attention_create.restype = ctypes.c_int
+            L.clsample_attention_destroy.argtypes = [ctypes.c_void_p]
+            L.clsample_attention_destroy.restype = None
+            L.clsample_chunk_attention.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+            L.clsample_chunk_attention.restype = ctypes.c_int
             _lib = L
         return _lib
 

@@ -74,7 +74,9 @@ enum {
   CLSAMPLE_ERR_DTYPE = -5,      /* logits_dtype is not a CLSAMPLE_LOGITS_* value */
   CLSAMPLE_ERR_CUDA = -6,       /* a CUDA runtime call failed (launch, attribute, device) */
   CLSAMPLE_ERR_DEVICE = -7,     /* the current device is not the handle's or not sm_103 */
-  CLSAMPLE_ERR_MODE = -8        /* mode has a bit that is not a CLSAMPLE_MODE_* flag */
+  CLSAMPLE_ERR_MODE = -8,       /* mode has a bit that is not a CLSAMPLE_MODE_* flag */
+  CLSAMPLE_ERR_SHAPE = -9,      /* a count, head layout, head size or page size out of range */
+  CLSAMPLE_ERR_ALIGN = -10      /* an address or stride that a kernel needs aligned is not */
 };
 
 /* Bits of clsample_args_t.mode (0: sequential truncation, one draw per row). */
@@ -286,6 +288,180 @@ int clsample_allowed_to_bitmask(const int32_t* offs, const int32_t* ids, int32_t
 int clsample_debug_weights(const float* y, uint64_t* weights, int32_t n, clsample_stream_t stream);
 int clsample_debug_uniforms(const uint64_t* seeds, const int64_t* positions, const int64_t* tokens,
                             float* u, int32_t n, clsample_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The other operators of a speculative-decoding step.  A step takes the n_b newest
+ * tokens of each of B sequences (one token, the last accepted token and the drafted
+ * ones, or a chunk of a prompt): clsample_kv_append writes their keys and values to a
+ * paged cache, clsample_chunk_attention attends to it, the model's LM head gives the
+ * verify rows, and clsample_verify accepts drafted tokens against the target's
+ * probabilities.  No public page is followed here; the formulas stand with each call.
+ *
+ * The batch.  T token rows; sequence b owns rows cu_new[b] .. cu_new[b + 1] (int32[B + 1],
+ * non-decreasing, within [0, T]; n_b may be 0; rows that no sequence owns are not
+ * touched).  kv_lens[b] (int32) is the sequence's length WITH the new tokens, so row
+ * cu_new[b] + i stands at position kv_lens[b] - n_b + i.
+ *
+ * The cache.  Two arrays of `dtype`, for keys and values, with the same strides: element
+ * d of head h in slot s of page p is at p * page_stride + s * slot_stride +
+ * h * head_stride + d (strides in elements, 64-bit).  Position x of sequence b is in slot
+ * x % page_size of page page_table[b * table_stride + x / page_size] (int32).
+ *
+ * Row statuses here are per sequence: INVALID marks offsets out of order or range, a
+ * negative kv_lens[b], one past max_pages * page_size, n_b > max_new, or a page id outside
+ * [0, num_pages) among the pages that the call has to touch.  Nothing is read or written
+ * outside the arrays; the other sequences are not affected. */
+
+/* Element types of queries, keys, values, their cache and outputs. */
+enum { CLSAMPLE_T_BF16 = 0, CLSAMPLE_T_F16 = 1 };
+
+/* Arguments of clsample_kv_append: for each new token, in this order,
+ *   1. q and k of each head: x <- x * rsqrt(mean(x^2) + eps) * weight, if weights are given;
+ *   2. q and k: the first rot_dim elements are rotated by the token's position.  Pair j is
+ *      (x[j], x[j + rot_dim/2]), or (x[2j], x[2j + 1]) with `interleaved`; with c =
+ *      cos_sin[pos][j], s = cos_sin[pos][rot_dim/2 + j]: (a, b) <- (a c - b s, b c + a s);
+ *   3. q goes to q_out, k and v to the token's slot of the cache.
+ * All in float32, rounded once when stored; v is copied bit for bit.
+ *
+ * q, k, v           [T, heads, D] of `dtype` with token and head strides (elements).
+ * q_out             like q; may be q itself (same strides).  NULL with Hq == 0.
+ * cos_sin           f32[max_pos, >= rot_dim], row stride cs_stride; NULL with rot_dim 0.
+ * q_weight/k_weight D elements of `dtype`, or NULL: no norm.
+ * row_status        i32[B] output or NULL.
+ *
+ * A token whose position is negative or not below max_pos (with rotation), or whose page
+ * is not valid, is not written to the cache and its q_out row is zero; its sequence is
+ * INVALID.  Two tokens of a call must not share a slot.
+ * Limits: 1 <= D <= 256, rot_dim even and <= D, any strides.  Fast path: D, rot_dim (and
+ * rot_dim/2 in the half-split form) multiples of 8, arrays and strides multiples of 16 bytes. */
+typedef struct {
+  int32_t B, T, Hq, Hkv, D;
+  int32_t dtype;
+  int32_t num_pages, page_size, max_pages;
+  int32_t rot_dim, max_pos, interleaved;
+  float eps;
+  int32_t reserved0;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, qo_stride_t, qo_stride_h;
+  int64_t page_stride, slot_stride, head_stride;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* cu_new;
+  const int32_t* kv_lens;
+  const float* cos_sin;
+  int64_t cs_stride;
+  const void* q_weight;
+  const void* k_weight;
+  int32_t* row_status;
+} clsample_kv_append_args_t;
+
+/* Enqueues one append on `stream` (one launch; none when T == 0 or B == 0, except that
+ * the statuses of B sequences without tokens are written).  No handle, no scratch. */
+int clsample_kv_append(const clsample_kv_append_args_t* args, clsample_stream_t stream);
+
+/* Arguments of clsample_chunk_attention.  Query head h reads key head h / (Hq / Hkv).  The
+ * row at position x sees the keys at positions <= x, of those only the last `window` when
+ * window > 0:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j).
+ * A row that sees no key (kv_lens[b] < n_b) gets out 0 and lse -inf.  Slots that no row of
+ * the sequence sees are never read: they may hold anything, and their page ids too.
+ *
+ * q, out            [T, Hq, D] of `dtype`, token and head strides (elements).
+ * lse               f32[T, Hq] output or NULL.
+ * max_new           upper bound of n_b, known to the caller; a sequence above it is
+ *                   INVALID and its out rows are 0.
+ * scale             finite, > 0 (1 / sqrt(D) as a rule).
+ * row_status        i32[B] output or NULL.  Keys on a page with an invalid id are left out.
+ *
+ * Products are of `dtype` with float32 sums; the softmax is float32; its weights are
+ * rounded to `dtype` for the product with the values, as the matrix instructions need.
+ * The result of a call does not depend on timing: partial sums over a split key axis are
+ * joined in key order.
+ * Limits: D 64 or 128; Hq a multiple of Hkv; q, out and cache addresses and strides
+ * multiples of 16 bytes (ERR_ALIGN). */
+typedef struct {
+  int32_t B, T, Hq, Hkv, D;
+  int32_t dtype;
+  int32_t num_pages, page_size, max_pages;
+  int32_t max_new, window;
+  float scale;
+  const void* q;
+  void* out;
+  const void* k_cache;
+  const void* v_cache;
+  int64_t q_stride_t, q_stride_h, o_stride_t, o_stride_h;
+  int64_t page_stride, slot_stride, head_stride;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* cu_new;
+  const int32_t* kv_lens;
+  float* lse;
+  int32_t* row_status;
+} clsample_attention_args_t;
+
+/* A handle holds the device scratch in which partial sums of a split key axis meet: its
+ * size depends on the device alone, not on any call.  Bound to the device that was current;
+ * calls on one handle must be ordered, as for clsample_t. */
+typedef struct clsample_attention clsample_attention_t;
+int clsample_attention_create(clsample_attention_t** out);
+void clsample_attention_destroy(clsample_attention_t* handle);
+
+/* Enqueues one call on `stream`; nothing when B == 0. */
+int clsample_chunk_attention(clsample_attention_t* handle, const clsample_attention_args_t* args,
+                             clsample_stream_t stream);
+
+/* Arguments of clsample_verify.  Request b drafted n_b = cu_draft[b + 1] - cu_draft[b] >= 0
+ * tokens (cu_draft int32[B + 1], within [0, N]).  Its n_b + 1 rows of target probabilities
+ * start at row cu_draft[b] + b of `target` (N + B rows); its draft probabilities are rows
+ * cu_draft[b] .. of `draft` (N rows; NULL when the draft is certain of its tokens, q = 1).
+ *   1. Drafted tokens x_i are accepted in order while u_i q_i(x_i) < p_i(x_i), u_i =
+ *      u_accept[cu_draft[b] + i] (the two sides are compared exactly).
+ *   2. One more token is drawn with u = u_sample[b]: at the first refusal from the weights
+ *      max(P_i(t) - Q_i(t), 0), P = floor(p 2^40) and Q = floor(q 2^40) (Q = 2^40 at x_i
+ *      for a certain draft, 0 elsewhere); if none was refused, or if all those weights are
+ *      0, from P.  With W their sum, the token is the lowest t whose inclusive running
+ *      sum is above floor(floor(u 2^31) W / 2^31).  All in integers: the result does not
+ *      depend on how the row is split.
+ * The tokens kept are distributed as the target's own (the standard argument: min(p, q) +
+ * max(p - q, 0) = p).  A greedy target is a row with 1 at its token.
+ *
+ * target, draft     [rows, V] probabilities of `dtype` (CLSAMPLE_LOGITS_F32 or _BF16), row
+ *                   strides >= V (elements).  They need not sum to 1.
+ * draft_tokens      i32[N].   u_accept f32[N], u_sample f32[B], in [0, 1).
+ * tokens            i32[B, token_stride] output, token_stride > max_draft: accepted tokens,
+ *                   the drawn token, then -1 up to place max_draft.
+ * accepted          i32[B] output or NULL: how many drafted tokens were accepted.
+ * row_status        i32[B] output or NULL.  INVALID (tokens all -1, accepted 0): offsets out
+ *                   of order or range, n_b > max_draft, a token outside [0, V), a random
+ *                   number outside [0, 1), a probability outside [0, 1] or NaN where the
+ *                   call reads one (at the drafted tokens, and in the rows it draws from),
+ *                   or a row to draw from without mass.
+ * Limits: 0 < V <= 262144. */
+typedef struct {
+  int32_t B, N, V;
+  int32_t dtype;
+  int32_t max_draft, reserved0;
+  const void* target;
+  int64_t target_stride;
+  const void* draft;
+  int64_t draft_stride;
+  const int32_t* draft_tokens;
+  const int32_t* cu_draft;
+  const float* u_accept;
+  const float* u_sample;
+  int32_t* tokens;
+  int64_t token_stride;
+  int32_t* accepted;
+  int32_t* row_status;
+} clsample_verify_args_t;
+
+/* Enqueues one verification on `stream` (one launch); nothing when B == 0. */
+int clsample_verify(const clsample_verify_args_t* args, clsample_stream_t stream);
 
 #ifdef __cplusplus
 }

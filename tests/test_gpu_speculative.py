@@ -1,0 +1,478 @@
+"""The speculative-step operators on the GPU against 64-bit references (spec_reference)."""
+import math
+
+import numpy as np
+import pytest
+
+import spec_reference as R
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def S():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from constrained_logits_sampling_gb300 import build, speculative
+    build.build()
+    return speculative
+
+
+def gpu(t):
+    """On the device with the strides it has here."""
+    if t is None:
+        return None
+    if t.dim() == 4 and not t.is_contiguous():
+        return t.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+    return t.cuda()
+
+
+def fused(pr):
+    """q, k, v on the device as slices of one projection."""
+    x = torch.cat([pr.q.flatten(1), pr.k.flatten(1), pr.v.flatten(1)], 1).cuda()
+    a, b = pr.Hq * pr.D, (pr.Hq + pr.Hkv) * pr.D
+    return (x[:, :a].view(pr.T, pr.Hq, pr.D), x[:, a:b].view(pr.T, pr.Hkv, pr.D), x[:, b:].view(pr.T, pr.Hkv, pr.D))
+
+
+# ----------------------------------------------------------------------------- attention
+
+ATTEND = [
+    # new, lens, Hq, Hkv, D, page, dtype, window, layout
+    ([1], [1], 4, 4, 64, 16, BF, 0, "nhd"),
+    ([1], [777], 32, 8, 128, 16, BF, 0, "nhd"),
+    ([1], [5000], 4, 1, 128, 64, FP, 0, "nhd"),
+    ([4, 4, 4], [4, 65, 300], 8, 2, 128, 16, BF, 0, "hnd"),
+    ([0, 2, 0, 1, 0], [5, 64, 0, 65, 9], 3, 1, 64, 16, FP, 0, "nhd"),
+    ([3, 5], [1, 0], 4, 2, 128, 16, BF, 0, "nhd"),  # rows without keys
+    ([7, 1], [129, 128], 10, 2, 64, 5, BF, 0, "nhd"),  # pages that end inside a tile, odd group
+    ([2, 3], [70, 33], 6, 6, 128, 1, FP, 0, "hnd"),
+    ([9], [400], 4, 4, 64, 24, BF, 7, "nhd"),
+    ([1, 6], [300, 300], 8, 1, 128, 128, FP, 1, "nhd"),
+    ([5, 40], [200, 260], 4, 2, 64, 32, BF, 100, "hnd"),
+    ([33], [33], 4, 1, 128, 16, BF, 0, "nhd"),
+    ([70, 1, 130], [70, 500, 333], 8, 2, 128, 64, BF, 0, "nhd"),
+    ([150], [700], 4, 4, 64, 16, FP, 50, "nhd"),
+    ([65, 0, 129], [40, 3, 200], 5, 1, 64, 8, BF, 0, "nhd"),  # chunk longer than its keys
+    ([257], [300], 2, 1, 128, 48, FP, 0, "hnd"),
+    ([1] * 300, [(7 * i) % 90 for i in range(300)], 2, 1, 64, 16, BF, 0, "nhd"),
+]
+
+
+def check_attention(S, pr, window=0, handle=None, **kw):
+    att = handle or S.ChunkAttention()
+    out = torch.full((pr.T, pr.Hq, pr.D), 7.0, dtype=pr.dtype, device="cuda")
+    q = fused(pr)[0]
+    args = (q, gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens))
+    got = att(*args, window=window, max_new=max(pr.new), lse=True, out=out, **kw)
+    torch.cuda.synchronize()
+    ref, lse, tol, lse_tol = R.attention(pr, window, kw.get("scale"))
+    err = (got["out"].cpu().double() - ref).abs()
+    assert torch.isfinite(got["out"].float()).all()
+    assert (err <= tol).all(), float((err / tol.clamp(min=1e-30)).max())
+    gl = got["lse"].cpu().double()
+    assert torch.equal(gl == -math.inf, lse == -math.inf)
+    seen = lse > -math.inf
+    assert ((gl - lse)[seen].abs() <= lse_tol[seen]).all()
+    assert got["status"].cpu().tolist() == [0] * pr.B
+    return got
+
+
+@pytest.mark.parametrize("case", ATTEND, ids=lambda c: f"{c[0][:3]}-{c[1][:3]}-{c[2]}x{c[3]}x{c[4]}-p{c[5]}-w{c[7]}")
+def test_attention(S, case):
+    new, lens, Hq, Hkv, D, page, dtype, window, layout = case
+    check_attention(S, R.Problem(new, lens, Hq, Hkv, D, page, dtype, seed=len(lens) + D, layout=layout), window)
+
+
+def test_attention_scale_and_large_scores(S):
+    """Scores far above the exponent range: the running maximum has to hold them."""
+    pr = R.Problem([3, 40], [90, 200], 4, 2, 64, 16, FP, seed=5)
+    check_attention(S, pr, scale=3.0)
+
+
+def test_attention_same_handle_same_bits(S):
+    """One handle over calls of different splits leaves its counters ready, and a call's bits
+    do not depend on timing."""
+    att = S.ChunkAttention()
+    pr = R.Problem([1, 2], [3000, 900], 8, 2, 128, 16, BF, seed=3)
+    small = R.Problem([1], [30], 8, 2, 128, 16, BF, seed=4)
+    chunk = R.Problem([90], [1500], 8, 2, 128, 16, BF, seed=6)
+    first = check_attention(S, pr, handle=att)
+    for _ in range(3):
+        check_attention(S, small, handle=att)
+        check_attention(S, chunk, handle=att)
+        again = check_attention(S, pr, handle=att)
+        assert torch.equal(first["out"], again["out"]) and torch.equal(first["lse"], again["lse"])
+
+
+def test_attention_other_stream(S):
+    pr = R.Problem([4, 1], [700, 900], 8, 2, 64, 16, BF, seed=8)
+    att = S.ChunkAttention()
+    side = torch.cuda.Stream()
+    args = [fused(pr)[0], gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens)]
+    torch.cuda.synchronize()
+    got = att(*args, stream=side)
+    side.synchronize()
+    ref, _, tol, _ = R.attention(pr)
+    assert ((got["out"].cpu().double() - ref).abs() <= tol).all()
+
+
+def test_attention_in_a_graph(S):
+    pr = R.Problem([2, 40], [700, 900], 8, 2, 128, 16, BF, seed=9)
+    att = S.ChunkAttention()
+    q = fused(pr)[0].contiguous()
+    out = torch.empty_like(q)
+    a = att.make_args(q, gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens), out=out)
+    att.apply(a)
+    torch.cuda.synchronize()
+    want = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        att.apply(a)
+    out.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("n", [2, 50])
+def test_attention_bad_sequences(S, n):
+    """A sequence that cannot be is INVALID and the others are what they were."""
+    def problem():
+        return R.Problem([n] * 5, [80, 200, 150, 90, 64], 4, 2, 64, 16, BF, seed=11)
+
+    pr = problem()
+    ref, lse, tol, _ = R.attention(pr)
+    pr.table[1, 3] = pr.pages  # a page past the cache
+    pr.table[4, 0] = -1
+    pr.kv_lens[2] = pr.table.shape[1] * 16 + 1  # longer than its table
+    q = fused(pr)[0]
+    got = S.ChunkAttention()(q, gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens), lse=True)
+    assert got["status"].cpu().tolist() == [0, 2, 2, 0, 2]
+    out = got["out"].cpu().double()
+    for b in (0, 3):
+        assert ((out - ref).abs() <= tol)[b * n:b * n + n].all()
+    assert (out[2 * n:3 * n] == 0).all() and (got["lse"][2 * n:3 * n] == -math.inf).all()
+    assert torch.isfinite(out).all()  # keys on the bad pages are left out
+
+    pr = problem()
+    pr.kv_lens[0] = -1
+    got = S.ChunkAttention()(fused(pr)[0], gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu),
+                             gpu(pr.kv_lens))
+    assert got["status"].cpu().tolist() == [2, 0, 0, 0, 0]
+    pr = problem()
+    pr.cu = torch.tensor([0, n, 3 * n, 2 * n, 4 * n, 9 * n], dtype=torch.int32)  # back, and past the end
+    out = torch.full(pr.q.shape, 5.0, dtype=BF, device="cuda")
+    got = S.ChunkAttention()(fused(pr)[0], gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu),
+                             gpu(pr.kv_lens), out=out)
+    assert got["status"].cpu().tolist() == [0, 0, 2, 0, 2]
+    assert (out[4 * n:] == 5.0).all()  # no sequence owns these rows
+    pr = problem()
+    got = S.ChunkAttention()(fused(pr)[0], gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu),
+                             gpu(pr.kv_lens), max_new=n - 1)
+    assert got["status"].cpu().tolist() == [2] * 5 and (got["out"] == 0).all()
+
+
+def test_attention_far_offsets(S):
+    """A cache whose last pages lie past 2^31 elements."""
+    pages, page, Hkv, D = 1050, 128, 128, 128  # 2.2e9 elements, 4.4 GB each
+    k = torch.zeros(pages, page, Hkv, D, dtype=BF, device="cuda")
+    v = torch.zeros(pages, page, Hkv, D, dtype=BF, device="cuda")
+    pr = R.Problem([2], [200], Hkv, Hkv, D, page, BF, seed=12)
+    for i, far in enumerate((pages - 1, pages - 2)):
+        k[far], v[far] = pr.k_cache[int(pr.table[0, i])].cuda(), pr.v_cache[int(pr.table[0, i])].cuda()
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device="cuda")
+    got = S.ChunkAttention()(fused(pr)[0], k, v, table, gpu(pr.cu), gpu(pr.kv_lens))
+    ref, _, tol, _ = R.attention(pr)
+    assert ((got["out"].cpu().double() - ref).abs() <= tol).all()
+
+
+def test_attention_refusals(S):
+    pr = R.Problem([2], [40], 4, 2, 64, 16, BF, seed=13)
+    att = S.ChunkAttention()
+    q = fused(pr)[0]
+    base = [q, gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens)]
+
+    def call(i=None, t=None, **kw):
+        a = list(base)
+        if i is not None:
+            a[i] = t
+        return att(*a, **kw)
+
+    call()
+    with pytest.raises(ValueError):
+        call(0, q.float())
+    with pytest.raises(ValueError):
+        call(0, q[:, :, :32])
+    with pytest.raises(ValueError):
+        call(1, base[1].to(FP))
+    with pytest.raises(ValueError):
+        call(2, base[2][:-1])
+    with pytest.raises(ValueError):
+        call(3, base[3].long())
+    with pytest.raises(ValueError):
+        call(4, base[4][:-1])
+    with pytest.raises(ValueError):
+        call(4, base[4].cpu())
+    with pytest.raises(ValueError):
+        call(out=torch.empty(3, 4, 64, dtype=BF, device="cuda"))
+    for kw, code in ((dict(window=-1), -9), (dict(scale=0.0), -9), (dict(scale=float("nan")), -9),
+                     (dict(max_new=-1), -9)):
+        with pytest.raises(Exception) as e:
+            call(**kw)
+        assert e.value.code == code
+    with pytest.raises(Exception) as e:  # 3 query heads on 2 key heads
+        call(0, q[:, :3])
+    assert e.value.code == -9
+    with pytest.raises(Exception) as e:
+        wide = torch.zeros(2, 4 * 64 + 1, dtype=BF, device="cuda")
+        call(0, wide[:, 1:].view(2, 4, 64))
+    assert e.value.code == -10
+
+
+# ----------------------------------------------------------------------------- append
+
+APPEND = [
+    # new, lens, Hq, Hkv, D, page, dtype, rot, interleaved, norm, layout
+    ([1], [778], 32, 8, 128, 16, BF, 128, False, True, "nhd"),
+    ([1], [1], 1, 1, 64, 16, FP, 64, True, False, "nhd"),
+    ([4, 4, 4], [4, 70, 300], 8, 2, 128, 64, BF, 128, False, True, "hnd"),
+    ([0, 3, 0, 0, 21, 1, 0], [9, 3, 0, 44, 50, 17, 2], 14, 2, 64, 16, FP, 32, True, True, "nhd"),
+    ([5, 2], [30, 9], 4, 4, 256, 5, BF, 256, False, True, "nhd"),
+    ([5, 2], [30, 9], 4, 1, 96, 16, FP, 48, False, False, "hnd"),
+    ([5, 2], [30, 9], 4, 2, 80, 16, BF, 40, False, True, "nhd"),  # half of 40 is no whole piece
+    ([6], [6], 3, 3, 80, 16, BF, 80, False, True, "nhd"),
+    ([4], [9], 2, 1, 33, 3, FP, 10, True, True, "nhd"),  # odd head size
+    ([4], [9], 2, 1, 1, 3, FP, 0, False, True, "nhd"),
+    ([8], [40], 40, 40, 64, 16, BF, 0, False, False, "nhd"),
+    ([1] * 70, [i + 1 for i in range(70)], 2, 1, 64, 16, BF, 64, False, True, "nhd"),
+    ([3] * 1100, [3 + i % 40 for i in range(1100)], 1, 1, 64, 16, BF, 64, False, False, "nhd"),
+]
+
+
+def tables(pr, rot, seed=1):
+    g = torch.Generator().manual_seed(seed)
+    n = max(pr.lens + [1])
+    a = torch.rand(n, max(rot // 2, 1), generator=g) * 6.2
+    w = [(1 + 0.3 * torch.randn(pr.D, generator=g)).to(pr.dtype) for _ in range(2)]
+    return (torch.cat([a.cos(), a.sin()], 1) if rot else None), w
+
+
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"{c[0][:3]}-{c[2]}x{c[3]}x{c[4]}-p{c[5]}-r{c[7]}{'i' if c[8] else ''}")
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append(S, case, in_place):
+    new, lens, Hq, Hkv, D, page, dtype, rot, inter, norm, layout = case
+    pr = R.Problem(new, lens, Hq, Hkv, D, page, dtype, seed=D + rot, layout=layout)
+    cs, (qw, kw) = tables(pr, rot)
+    if not norm:
+        qw = kw = None
+    q, k, v = fused(pr)
+    kc, vc = gpu(pr.k_cache), gpu(pr.v_cache)
+    op = S.KVAppend()
+    opts = dict(cos_sin=gpu(cs), interleaved=inter, q_weight=gpu(qw), k_weight=gpu(kw))
+    got = op(q, k, v, kc, vc, gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens), q_out=q if in_place else None, **opts)
+    torch.cuda.synchronize()
+    rq, qt, rk, kt, where = R.append(pr, cs, rot, inter, qw, kw)
+    assert got["status"].cpu().tolist() == [0] * pr.B
+    assert ((got["q"].cpu().double() - rq).abs() <= qt).all()
+    kc, vc = kc.cpu(), vc.cpu()
+    want_k, want_v = pr.k_cache.double(), pr.v_cache.clone()
+    tol = torch.zeros_like(want_k)
+    for t, (p, s) in enumerate(where):
+        want_k[p, s], tol[p, s], want_v[p, s] = rk[t], kt[t], pr.v[t]
+    bits = torch.int16
+    assert torch.equal(vc.contiguous().view(bits), want_v.contiguous().view(bits))
+    same = torch.isnan(want_k) & torch.isnan(kc.double())
+    assert (same | ((kc.double() - want_k).abs() <= tol)).all()
+
+
+def test_append_bad_tokens(S):
+    """Tokens without a place are not written, their q_out is zero, their sequence INVALID."""
+    pr = R.Problem([4] * 6, [20, 3, 40, 30, 25, 10], 4, 2, 64, 16, BF, seed=2)
+    cs, _ = tables(pr, 64)
+    cs = cs[:28]  # sequences 2 and 3 run past the table of angles
+    ref = R.append(pr, torch.cat([cs, torch.zeros(20, 64)]), 64)
+    pr.table[4, 1] = pr.pages
+    pr.kv_lens[5] = -3
+    q, k, v = fused(pr)
+    kc, vc = gpu(pr.k_cache), gpu(pr.v_cache)
+    before = kc.clone(), vc.clone()
+    got = S.KVAppend()(q, k, v, kc, vc, gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens), cos_sin=gpu(cs))
+    assert got["status"].cpu().tolist() == [0, 2, 2, 2, 2, 2]
+    out = got["q"].cpu().double()
+    placed = [True] * 4 + [False, True, True, True] + [False] * 4 + [True, True, False, False] + [False] * 8
+    for t, ok in enumerate(placed):
+        if ok:
+            assert ((out[t] - ref[0][t]).abs() <= ref[1][t]).all(), t
+            p, s = ref[4][t]
+            assert torch.equal(vc[p, s].cpu(), pr.v[t])
+            before[0][p, s], before[1][p, s] = kc[p, s], vc[p, s]
+        else:
+            assert (out[t] == 0).all(), t
+    for x, y in zip((kc, vc), before):  # nothing else was touched
+        assert torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
+
+
+def test_append_statuses_without_tokens(S):
+    pr = R.Problem([0, 0, 0], [5, 0, 9], 2, 1, 64, 16, BF)
+    q, k, v = fused(pr)
+    got = S.KVAppend()(q, k, v, gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens))
+    assert got["status"].cpu().tolist() == [0, 0, 0]
+
+
+# ----------------------------------------------------------------------------- verify
+
+def softmax_rows(rng, n, V, sharp):
+    z = rng.standard_normal((n, V)) * sharp
+    e = np.exp(z - z.max(1, keepdims=True))
+    return (e / e.sum(1, keepdims=True)).astype(np.float32)
+
+
+def run_verify(S, target, draft, x, cu, u, ul, most, dtype=torch.float32, pad=0):
+    def rows(a):
+        if a is None:
+            return None
+        t = torch.zeros(a.shape[0], a.shape[1] + pad, dtype=dtype, device="cuda")
+        t[:, :a.shape[1]] = torch.from_numpy(a).cuda()
+        return t[:, :a.shape[1]]
+
+    def up(a, dt):
+        return torch.from_numpy(np.asarray(a, dt)).cuda()
+
+    got = S.DraftVerifier()(rows(target), up(x, np.int32), up(cu, np.int32), up(u, np.float32), up(ul, np.float32),
+                            max_draft=most, draft_probs=rows(draft))
+    torch.cuda.synchronize()
+    return {k: v.cpu().numpy() for k, v in got.items()}
+
+
+def rounded(a, dtype):
+    return a if a is None or dtype == torch.float32 else torch.from_numpy(a).to(dtype).float().numpy()
+
+
+@pytest.mark.parametrize("V,dtype,has_draft,pad", [
+    (1, torch.float32, True, 0), (2, torch.float32, False, 0), (37, BF, True, 0), (1000, torch.float32, True, 3),
+    (1001, torch.float32, True, 0), (1003, BF, False, 0), (1003, BF, True, 2), (4096, BF, True, 0),
+    (9001, torch.float32, False, 0)])
+def test_verify(S, V, dtype, has_draft, pad):
+    rng = np.random.default_rng(V)
+    new = [0, 3, 1, 7, 0, 2, 5, 4, 4, 4]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    N, B = int(cu[-1]), len(new)
+    target = rounded(softmax_rows(rng, N + B, V, 2.0), dtype)
+    draft = rounded(softmax_rows(rng, N, V, 2.0), dtype) if has_draft else None
+    x = rng.integers(0, V, N)
+    for b in range(B):  # likely tokens for some requests, so that runs of acceptances occur
+        for i in range(new[b]):
+            if b % 2:
+                x[cu[b] + i] = int(target[cu[b] + b + i].argmax())
+    u, ul = rng.random(N, dtype=np.float32), rng.random(B, dtype=np.float32)
+    u[cu[6]:cu[7]] = 0.0
+    ul[0], ul[1] = 0.0, np.float32(1) - np.float32(2.0 ** -24)
+    tokens, accepted = R.verify(target, draft, x, cu, u, ul, 7)
+    got = run_verify(S, target, draft, x, cu, u, ul, 7, dtype, pad)
+    assert got["status"].tolist() == [0] * B
+    assert np.array_equal(got["accepted"], accepted)
+    assert np.array_equal(got["tokens"], tokens)
+
+
+def test_verify_full_vocabulary_split(S):
+    """Thresholds that fall in every slice and warp of a large row."""
+    V, B = 151936, 64
+    rng = np.random.default_rng(3)
+    p = softmax_rows(rng, 1, V, 1.0)
+    target = np.repeat(p, B, 0)
+    ul = ((np.arange(B) + 0.5) / B).astype(np.float32)
+    got = run_verify(S, target, None, [], [0] * (B + 1), [], ul, 0)
+    w = np.floor(p[0].astype(np.float64) * 2.0 ** 40).astype(np.int64)
+    c = np.cumsum(w)
+    want = [int(np.searchsorted(c, int(math.floor(float(a) * 2.0 ** 31)) * int(c[-1]) >> 31, side="right")) for a in ul]
+    assert got["tokens"][:, 0].tolist() == want
+
+
+def test_verify_edges(S):
+    V = 8
+    eye = np.eye(V, dtype=np.float32)
+    # greedy rows: accept on the same token, else draw it; all weights above the draft zero -> p
+    got = run_verify(S, eye[[3, 5, 2, 2]], eye[[3, 2]], [3, 1], [0, 1, 2], [0.9, 0.9], [0.5, 0.5], 2)
+    assert got["tokens"].tolist() == [[3, 5, -1], [2, -1, -1]] and got["accepted"].tolist() == [1, 0]
+    # a refused token (u q = p, not below) whose row equals the draft's: drawn from p
+    half = np.full((1, V), 0.125, np.float32)
+    got = run_verify(S, np.repeat(half * 0.5, 2, 0), half, [4], [0, 1], [0.5], [0.0], 1)
+    assert got["tokens"].tolist() == [[0, -1]] and got["status"].tolist() == [0]
+    # zero probability is refused with any number, also 0
+    got = run_verify(S, eye[[3, 3]], None, [1], [0, 1], [0.0], [0.99], 1)
+    assert got["tokens"].tolist() == [[3, -1]]
+
+
+def test_verify_bad_requests(S):
+    V, B = 50, 12
+    rng = np.random.default_rng(9)
+
+    def make():
+        return (softmax_rows(rng, 2 * B + B, V, 1.0), softmax_rows(rng, 2 * B, V, 1.0), rng.integers(0, V, 2 * B),
+                np.arange(0, 2 * B + 1, 2), np.full(2 * B, 0.999, np.float32), rng.random(B, dtype=np.float32))
+
+    target, draft, x, cu, u, ul = make()
+    good = run_verify(S, target, draft, x, cu, u, ul, 2)
+    assert good["status"].tolist() == [0] * B
+    t2, x2, u2, ul2 = target.copy(), x.copy(), u.copy(), ul.copy()
+    x2[0] = V
+    x2[2 * 1 + 1] = -1
+    u2[2 * 2] = 1.0
+    u2[2 * 3] = np.nan
+    ul2[4] = -0.1
+    ul2[5] = np.inf
+    a6 = good["accepted"][6]
+    t2[3 * 6 + a6, 7] = np.nan
+    a7 = good["accepted"][7]
+    t2[3 * 7 + a7, 49] = -0.25
+    t2[3 * 8:3 * 9] = 0.0  # no mass
+    a9 = good["accepted"][9]
+    t2[3 * 9 + a9, 0] = 1.5
+    got = run_verify(S, t2, draft, x2, cu, u2, ul2, 2)
+    assert got["status"].tolist() == [2] * 10 + [0, 0]
+    assert (got["tokens"][:10] == -1).all() and (got["accepted"][:10] == 0).all()
+    assert np.array_equal(got["tokens"][10:], good["tokens"][10:])
+    # offsets out of order, past the end, more drafted than allowed
+    cu2 = cu.copy()
+    cu2[3] = 3
+    cu2[-1] = 2 * B + 5
+    got = run_verify(S, target, draft, x, cu2, u, ul, 2)
+    assert got["status"][2] == 2 and got["status"][3] == 2 and got["status"][-1] == 2
+    assert got["status"][:2].tolist() == [0, 0]
+    assert run_verify(S, target, draft, x, cu, u, ul, 1)["status"].tolist() == [2] * B
+
+
+def test_verify_keeps_the_target_distribution(S):
+    """First token of a verification, over many requests with one drafted token each drawn
+    from q, is distributed as p: chi-square with 7 degrees of freedom below its 1e-6 point."""
+    V, B = 8, 40000
+    rng = np.random.default_rng(21)
+    p, q = softmax_rows(rng, 1, V, 1.0), softmax_rows(rng, 1, V, 1.0)
+    x = rng.choice(V, size=B, p=(q[0].astype(np.float64) / q[0].astype(np.float64).sum()))
+    got = run_verify(S, np.repeat(p, 2 * B, 0), np.repeat(q, B, 0), x, np.arange(B + 1),
+                     rng.random(B, dtype=np.float32), rng.random(B, dtype=np.float32), 1)
+    seen = np.bincount(got["tokens"][:, 0], minlength=V)
+    want = p[0].astype(np.float64) / p[0].astype(np.float64).sum() * B
+    assert ((seen - want) ** 2 / want).sum() < 43.0
+
+
+def test_verify_refusals(S):
+    V = 10
+    t = torch.full((3, V), 0.1, device="cuda")
+    x = torch.zeros(2, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    u, ul = torch.zeros(2, device="cuda"), torch.zeros(1, device="cuda")
+    op = S.DraftVerifier()
+    op(t, x, cu, u, ul, max_draft=2)
+    for bad in ((t.double(), x, cu, u, ul), (t[:2], x, cu, u, ul), (t, x.long(), cu, u, ul), (t, x, cu[:1], u, ul),
+                (t, x, cu, u[:1], ul), (t.cpu(), x, cu, u, ul)):
+        with pytest.raises(ValueError):
+            op(*bad, max_draft=2)
+    with pytest.raises(ValueError):
+        op(t, x, cu, u, ul, max_draft=2, draft_probs=t)
+    with pytest.raises(Exception) as e:
+        op(t, x, cu, u, ul, max_draft=-1)
+    assert isinstance(e.value, (ValueError, RuntimeError))
