@@ -3,6 +3,7 @@
 // the choice of kernels.
 #include <new>
 
+#include "attn_chunk.cuh"
 #include "attn_stream.cuh"
 
 struct clsample_attention {
@@ -15,8 +16,12 @@ namespace clsample {
 namespace {
 
 constexpr int kStreamCtas = 2;  // per SM
-// two slots of (32 rows of 128 sums, a maximum and a sum each) per CTA
-constexpr size_t kStreamScratch = (size_t)kStreamCtas * 2 * 32 * 130 * sizeof(float);
+// Scratch per SM: two slots per CTA of rows of 128 sums, a maximum and a sum.
+constexpr size_t kScratch = 2 * (size_t)kChunkRows * 130 * sizeof(float);
+static_assert(kScratch >= (size_t)kStreamCtas * 2 * 32 * 130 * sizeof(float), "the stream kernel's slots fit too");
+// Up to this many packed rows (a multiple of the stream kernel's tile) a sequence's keys are
+// read once by the stream kernel; above it, once per 256 rows by the chunk kernel.
+constexpr int kStreamRows = 32;
 
 template <class T, int D, int MT>
 cudaError_t launch_stream(const AttnParams& P, int sms, cudaStream_t st) {
@@ -29,10 +34,23 @@ cudaError_t launch_stream(const AttnParams& P, int sms, cudaStream_t st) {
 
 template <class T, int D>
 cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
+  // no valid sequence has more rows than this; one that breaks the bound has no keys
+  const int64_t rows = P.a.max_new * (int64_t)P.g;
   P.min_rows = 0;
   P.max_rows = 0x7fffffff;
-  return P.a.max_new * (int64_t)P.g <= 16 ? launch_stream<T, D, 1>(P, h->sms, st)
-                                          : launch_stream<T, D, 2>(P, h->sms, st);
+  if (rows > kStreamRows) {
+    P.min_rows = kStreamRows + 1;
+    auto* fn = attn_chunk_kernel<T, D>;
+    const int bytes = ChunkShape<D>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    fn<<<h->sms, kChunkThreads, bytes, st>>>(P);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    P.a.row_status = nullptr;  // written
+    P.min_rows = 0;
+    P.max_rows = kStreamRows + 1;
+  }
+  return rows <= 16 ? launch_stream<T, D, 1>(P, h->sms, st) : launch_stream<T, D, 2>(P, h->sms, st);
 }
 
 }  // namespace
@@ -49,7 +67,7 @@ int clsample_attention_create(clsample_attention_t** out) {
   if (rc != CLSAMPLE_SUCCESS) return rc;
   auto* h = new (std::nothrow) clsample_attention{dev, sms, nullptr, nullptr};
   if (!h) return CLSAMPLE_ERR_CUDA;
-  if (cudaMalloc(&h->partial, (size_t)sms * kStreamScratch) != cudaSuccess ||
+  if (cudaMalloc(&h->partial, (size_t)sms * kScratch) != cudaSuccess ||
       cudaMalloc(&h->arrived, (size_t)sms * kStreamCtas * sizeof(int)) != cudaSuccess ||
       cudaMemset(h->arrived, 0, (size_t)sms * kStreamCtas * sizeof(int)) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {

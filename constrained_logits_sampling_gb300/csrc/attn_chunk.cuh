@@ -1,0 +1,386 @@
+// Attention for many query rows per key head: bound by the products, on tcgen05.
+//
+// A unit is 256 packed rows (attn_units.cuh), as two tiles of 128 rows.  One CTA per SM:
+//   warps 0-3, 4-7   softmax of row tile 0 and 1, one row a thread;
+//   warps 8-11       loads: queries, keys and values from their pages, by cp.async into the
+//                    128-byte swizzled layout that the matrix instructions read.  Page
+//                    boundaries may fall anywhere in a tile and slots past the length are
+//                    filled with zeros, which a box copy could do neither of;
+//   warp 12          one thread issues the products.
+// S = Q K^T goes to tensor memory (128 columns a tile), the softmax warps read it, write the
+// weights P over it in the input type, and O += P V takes P from there: scores never touch
+// shared memory.  The two tiles alternate: while one is in its softmax, the tensor cores
+// have the other's PV and next QK^T (2 x 128 x 128 x D each).  O stays in tensor memory;
+// it is rescaled only when a row's maximum has grown by more than 2^8 since the last
+// time (P and its sum are then up to 2^8, which both types hold), so hardly ever.
+#pragma once
+
+#include <type_traits>
+
+#include "attn_stream.cuh"
+#include "tcgen05.cuh"
+
+namespace clsample {
+
+constexpr int kChunkThreads = 13 * 32;
+constexpr int kChunkRows = 256;
+constexpr int kChunkKeys = 128;
+constexpr float kRescaleAt = 8.f;  // log2
+
+template <int D>
+struct ChunkShape {
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kTile = 128 * D * 2;  // 128 rows, in bytes
+  static constexpr int kBytes = (2 + 2 * kStages) * kTile + 1024;  // 1024: alignment of the swizzle
+};
+
+template <int NS>
+struct ChunkShared {
+  unsigned long long k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+  unsigned long long q_full, q_empty, end, s_full[2], p_full[2], o_full[2];
+  uint32_t tmem;
+  volatile int dead;         // a bounded wait ran out: every other wait ends too
+  uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
+};
+
+// Bounded wait for a phase: about two seconds, then the CTA gives up.
+__device__ __forceinline__ bool chunk_wait(unsigned long long* bar, uint32_t parity, volatile int* dead) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long start = clock64();
+  for (uint32_t i = 1; i < kSpinLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0 && (*dead || clock64() - start > 4000000000ll)) break;
+  }
+  *dead = 1;
+  return false;
+}
+
+struct SoftmaxSync {  // the 256 softmax threads
+  static __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+};
+
+template <class T, int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __grid_constant__ AttnParams P) {
+  using Shape = ChunkShape<D>;
+  constexpr int NS = Shape::kStages, kTile = Shape::kTile, KC = D / 8;
+  constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 elements
+  extern __shared__ unsigned char raw[];
+  __shared__ ChunkShared<NS> sh;
+  unsigned char* const smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t q_smem = smem_addr(smem), k_smem = q_smem + 2 * kTile, v_smem = k_smem + NS * kTile;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const clsample_attention_args_t& a = P.a;
+  const float neg_inf = __int_as_float(0xff800000);
+
+  if (a.row_status) attention_status<kChunkThreads>(P);
+  Span span;
+  Unit u;
+  int64_t unit_begin;
+  if (!find_span<kChunkRows, kChunkKeys, kChunkThreads>(P, &span, &u, &unit_begin)) return;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sh.k_full[i], 128 + 4);  // every load thread's copies, and four words of key_ok
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 128);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 128);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.end, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sh.s_full[w], 1);
+      mbar_init(&sh.p_full[w], 4);
+      mbar_init(&sh.o_full[w], 1);
+    }
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) tmem_alloc512(&sh.tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  int64_t t = span.t0;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------------ softmax
+    const int w = warp >> 2;
+    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
+    const uint32_t s_tmem = tmem + lane_base + w * 128, o_tmem = tmem + lane_base + 256 + w * 128;
+    uint32_t s_phase = 0, o_phase = 0, tile = 0;
+    while (true) {
+      const int j0 = (int)(t - unit_begin);
+      const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+      const int nact = u.rows > 128 ? 2 : 1;
+      const bool done = cnt == u.tiles;
+      if (w < nact) {
+        const int r = w * 128 + (warp & 3) * 32 + lane;
+        const bool live = r < u.rows;
+        const int first_pos = u.len - u.n;
+        const int pos = live ? first_pos + (u.row0 + r) / P.g : -1;
+        const int pos_first = first_pos + (u.row0 + w * 128) / P.g;
+        const int pos_last = first_pos + (u.row0 + min(u.rows, w * 128 + 128) - 1) / P.g;
+        float m = neg_inf, l = 0.f;  // reference maximum (log2 units) and weights' sum
+        for (int j = 0; j < cnt; ++j) {
+          const int kb = (u.tile0 + j0 + j) * kChunkKeys;
+          chunk_wait(&sh.s_full[w], s_phase, &sh.dead);
+          s_phase ^= 1;
+          tc_fence_after();
+          const uint32_t* ok = sh.key_ok[(tile + j) % (2 * NS)];
+          const uint32_t ok0 = ok[0], ok1 = ok[1], ok2 = ok[2], ok3 = ok[3];
+          const bool whole = (ok0 & ok1 & ok2 & ok3) == ~0u && kb + 127 <= pos_first &&
+                             (a.window <= 0 || kb > pos_last - a.window);
+          const int hi = pos - kb;  // columns lo .. hi are seen
+          const int lo = a.window > 0 ? hi - a.window + 1 : 0;
+          auto masked = [&](uint32_t (&x)[32], int c) {
+            const uint32_t bits = c == 0 ? ok0 : c == 1 ? ok1 : c == 2 ? ok2 : ok3;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e > hi || c * 32 + e < lo || !((bits >> e) & 1)) x[e] = 0xff800000u;
+          };
+          float top = neg_inf;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(x, s_tmem + c * 32);
+            tmem_wait_ld();
+            if (!whole) masked(x, c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+          }
+          top *= P.scale_log2;
+          const bool grow = top > m + kRescaleAt || (m == neg_inf && top > neg_inf);
+          if (__any_sync(~0u, grow)) {
+            const float keep = grow ? exp2_fast(m - top) : 1.f;
+            if (grow) m = top;
+            l *= keep;
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(x, o_tmem + c * 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
+                tmem_st32(o_tmem + c * 32, x);
+              }
+            }
+          }
+          const float base = m == neg_inf ? 0.f : m;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], p[16];
+            tmem_ld32(x, s_tmem + c * 32);
+            tmem_wait_ld();
+            if (!whole) masked(x, c);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = exp2_fast(fmaf(__uint_as_float(x[2 * e]), P.scale_log2, -base));
+              const float p1 = exp2_fast(fmaf(__uint_as_float(x[2 * e + 1]), P.scale_log2, -base));
+              sum0 += p0;
+              sum1 += p1;
+              p[e] = Pair<T>::narrow(p0, p1);
+            }
+            tmem_st16(s_tmem + c * 16, p);  // over columns that have been read
+          }
+          l += sum0 + sum1;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[w]);
+        }
+        chunk_wait(&sh.o_full[w], o_phase, &sh.dead);
+        o_phase ^= 1;
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(x, o_tmem + c * 32);
+          tmem_wait_ld();
+          if (live) {
+            if (done) {
+              T* dst = (T*)a.out + (int64_t)(u.q0 + (u.row0 + r) / P.g) * a.o_stride_t +
+                       (int64_t)(u.h * P.g + (u.row0 + r) % P.g) * a.o_stride_h + c * 32;
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  y[i] = l == 0.f ? 0u
+                                  : Pair<T>::narrow(__uint_as_float(x[e + 2 * i]) * inv,
+                                                    __uint_as_float(x[e + 2 * i + 1]) * inv);
+                *reinterpret_cast<uint4*>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                __stcg(reinterpret_cast<uint4*>(slot + r * D + c * 32 + e), make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
+            }
+          }
+        }
+        tc_fence_before();  // O has been read: the next unit's products may overwrite it
+        if (live) {
+          if (done) {
+            store_lse(P, u, r, m, l);
+          } else {
+            __stcg(slot + kChunkRows * D + r, m);
+            __stcg(slot + kChunkRows * D + kChunkRows + r, l);
+          }
+        }
+      }
+      if (!done) join_parts<T, kChunkRows, D, 256, SoftmaxSync>(P, u, span, unit_begin);
+      if (sh.dead && tid == 0 && a.row_status) atomicMax(a.row_status + u.b, CLSAMPLE_ROW_OVERFLOW);
+      tile += cnt;
+      t += cnt;
+      if (t >= span.t1) break;
+      unit_begin = t;
+      next_unit<kChunkRows, kChunkKeys>(P, &u);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------------ loads
+    const int lw = warp - 8;
+    uint32_t it = 0, seg = 0;
+    while (true) {
+      const int j0 = (int)(t - unit_begin);
+      const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+      chunk_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
+      for (int x = 0; x < 2 * 32 * KC / 32; ++x) {
+        const int i = x * 32 + lane;
+        const int r = (i / (32 * KC)) * 128 + lw * 32 + i / KC % 32, ch = i % KC;
+        const bool live = r < u.rows;
+        const int row = u.row0 + (live ? r : 0);
+        const T* src = (const T*)a.q + (int64_t)(u.q0 + row / P.g) * a.q_stride_t +
+                       (int64_t)(u.h * P.g + row % P.g) * a.q_stride_h + ch * 8;
+        const int rr = r & 127;
+        cp_async16(q_smem + (r >> 7) * kTile + (ch >> 3) * kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), src, live);
+      }
+      cp_async_arrive(smem_addr(&sh.q_full));
+      const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
+      const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
+      const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
+      auto page_of = [&](int j) {
+        const int key = (u.tile0 + j0 + j) * kChunkKeys + lw * 32 + lane;
+        if (j >= cnt || key < u.key_lo || key >= u.key_hi) return -1;
+        const int id = __ldg(table + (P.page_shift >= 0 ? key >> P.page_shift : key / a.page_size));
+        return id < a.num_pages ? id : -1;
+      };
+      int page = page_of(0);
+      for (int j = 0; j < cnt; ++j, ++it) {
+        const int next = page_of(j + 1);
+        const int key = (u.tile0 + j0 + j) * kChunkKeys + lw * 32 + lane;
+        const int slot = P.page_shift >= 0 ? key & ((1 << P.page_shift) - 1) : key % a.page_size;
+        const bool ok = page >= 0;
+        const int64_t off = ok ? (int64_t)page * a.page_stride + (int64_t)slot * a.slot_stride : 0;
+        const unsigned mask = __ballot_sync(~0u, ok);
+        // keys outside the unit's range are hidden by the rows' limits: only a bad page counts
+        const unsigned shown = __ballot_sync(~0u, ok || key < u.key_lo || key >= u.key_hi);
+        const int st = it % NS;
+        const uint32_t parity = ((it / NS) & 1) ^ 1;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          chunk_wait(kv ? &sh.v_empty[st] : &sh.k_empty[st], parity, &sh.dead);
+          __syncwarp();
+          if (kv == 0 && lane == 0) {
+            sh.key_ok[it % (2 * NS)][lw] = shown;
+            mbar_arrive(&sh.k_full[st]);
+          }
+          const T* src = kv ? vc : kc;
+          const uint32_t dst = (kv ? v_smem : k_smem) + st * kTile;
+#pragma unroll
+          for (int x = 0; x < KC; ++x) {
+            const int i = x * 32 + lane, row = i / KC, ch = i % KC, r = lw * 32 + row;
+            const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
+            cp_async16(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + o, (mask >> row) & 1);
+          }
+          cp_async_arrive(smem_addr(kv ? &sh.v_full[st] : &sh.k_full[st]));
+        }
+        page = next;
+      }
+      ++seg;
+      t += cnt;
+      if (t >= span.t1) break;
+      unit_begin = t;
+      next_unit<kChunkRows, kChunkKeys>(P, &u);
+    }
+    cp_async_wait_all();
+  } else if (lane == 0) {
+    // ------------------------------------------------------------------ products
+    constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kQk = f16_idesc(kBf16, 128, 128, false), kPv = f16_idesc(kBf16, 128, D, true);
+    uint32_t it = 0, seg = 0, p_phase[2] = {0, 0};
+    auto qk = [&](int w, uint32_t tile) {
+      if (sh.dead) return;
+      const uint32_t q0 = q_smem + w * kTile, k0 = k_smem + (tile % NS) * kTile;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t step = (ks >> 2) * kHalf + (ks & 3) * 32;
+        mma_ss(tmem + w * 128, smem_desc(q0 + step, 16, 1024), smem_desc(k0 + step, 16, 1024), kQk, ks > 0);
+      }
+    };
+    auto pv = [&](int w, uint32_t tile, bool add) {
+      if (sh.dead) return;
+      const uint32_t v0 = v_smem + (tile % NS) * kTile;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        mma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8, smem_desc(v0 + ks * 2048, kHalf, 1024), kPv,
+               add || ks > 0);
+    };
+    while (true) {
+      const int j0 = (int)(t - unit_begin);
+      const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+      const int nact = u.rows > 128 ? 2 : 1;
+      chunk_wait(&sh.q_full, seg & 1, &sh.dead);
+      chunk_wait(&sh.k_full[it % NS], (it / NS) & 1, &sh.dead);
+      fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
+      for (int w = 0; w < nact; ++w) {
+        qk(w, it);
+        mma_commit(&sh.s_full[w]);
+      }
+      mma_commit(&sh.k_empty[it % NS]);
+      if (cnt == 1) mma_commit(&sh.q_empty);
+      for (int j = 0; j < cnt; ++j, ++it) {
+        chunk_wait(&sh.v_full[it % NS], (it / NS) & 1, &sh.dead);
+        fence_async_proxy();
+        for (int w = 0; w < nact; ++w) {
+          chunk_wait(&sh.p_full[w], p_phase[w], &sh.dead);
+          p_phase[w] ^= 1;
+          tc_fence_after();
+          pv(w, it, j > 0);
+          if (j + 1 < cnt) {
+            if (w == 0) {
+              chunk_wait(&sh.k_full[(it + 1) % NS], ((it + 1) / NS) & 1, &sh.dead);
+              fence_async_proxy();
+            }
+            qk(w, it + 1);
+            mma_commit(&sh.s_full[w]);
+          } else {
+            mma_commit(&sh.o_full[w]);
+          }
+        }
+        mma_commit(&sh.v_empty[it % NS]);
+        if (j + 1 < cnt) mma_commit(&sh.k_empty[(it + 1) % NS]);
+        if (j + 2 == cnt) mma_commit(&sh.q_empty);
+      }
+      ++seg;
+      t += cnt;
+      if (t >= span.t1) break;
+      unit_begin = t;
+      next_unit<kChunkRows, kChunkKeys>(P, &u);
+    }
+    // products still running when a wait gave up end before their memory is freed
+    if (sh.dead) {
+      mma_commit(&sh.end);
+      for (int i = 0; i < 1 << 16 && !mbar_try_wait(&sh.end, 0); ++i) __nanosleep(100);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_free512(tmem);
+}
+
+}  // namespace clsample

@@ -16,7 +16,12 @@ namespace clsample {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
+// An arrival on `bar` once all of this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -93,19 +98,23 @@ __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, in
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xff800000);
 }
 
-// Joins the partial sums of a unit cut by span boundaries: called by all threads of each
-// CTA that wrote a part; the last to arrive joins them all, in key order.
-template <class T, int R, int D, int NT>
+// Joins the partial sums of a unit cut by span boundaries: called by the NT threads that
+// wrote a CTA's part (threads 0 .. NT - 1, which Sync joins); the CTA that arrives last joins
+// them all, in key order.
+struct BlockSync {
+  static __device__ __forceinline__ void sync() { __syncthreads(); }
+};
+template <class T, int R, int D, int NT, class Sync>
 __device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin) {
   __shared__ int last;
   const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
   __threadfence();
-  __syncthreads();
+  Sync::sync();
   if (threadIdx.x == 0) {
     last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
     if (last) P.arrived[c0] = 0;  // for the next call
   }
-  __syncthreads();
+  Sync::sync();
   if (!last) return;
   __threadfence();
   for (int i = threadIdx.x; i < u.rows * (D / 4); i += NT) {
@@ -371,7 +380,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
         }
       }
     }
-    if (!done) join_parts<T, R, D, kStreamThreads>(P, u, span, unit_begin);
+    if (!done) join_parts<T, R, D, kStreamThreads, BlockSync>(P, u, span, unit_begin);
     t += cnt;
     if (t >= span.t1) break;
     __syncthreads();  // the rings and row sums have been read
