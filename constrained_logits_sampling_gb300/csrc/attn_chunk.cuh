@@ -6,7 +6,7 @@
 //                    128-byte swizzled layout that the matrix instructions read.  Page
 //                    boundaries may fall anywhere in a tile and slots past the length are
 //                    filled with zeros, which a box copy could do neither of;
-//   warp 12          one thread issues the products.
+//   warp 12          one thread issues the products (13-15 make its warpgroup whole).
 // S = Q K^T goes to tensor memory (128 columns a tile), the softmax warps read it, write the
 // weights P over it in the input type, and O += P V takes P from there: scores never touch
 // shared memory.  The two tiles alternate: while one is in its softmax, the tensor cores
@@ -22,10 +22,42 @@
 
 namespace clsample {
 
-constexpr int kChunkThreads = 13 * 32;
+constexpr int kChunkThreads = 512;
 constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 128;
 constexpr float kRescaleAt = 8.f;  // log2
+
+// Registers a thread by warpgroup: 2 x softmax, loads, products.  They add up to what the
+// block is launched with (4 x 128).
+constexpr int kSoftmaxRegs = 176, kLoadRegs = 80, kMmaRegs = 80;
+static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs == 4 * (65536 / kChunkThreads), "the launch's registers");
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split_pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 template <int D>
 struct ChunkShape {
@@ -37,7 +69,7 @@ struct ChunkShape {
 template <int NS>
 struct ChunkShared {
   unsigned long long k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  unsigned long long q_full, q_empty, end, s_full[2], p_full[2], o_full[2];
+  unsigned long long q_full, q_empty, end, s_full[2], p_half[2], p_full[2], o_full[2];
   uint32_t tmem;
   volatile int dead;         // a bounded wait ran out: every other wait ends too
   uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
@@ -90,6 +122,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
     mbar_init(&sh.end, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&sh.s_full[w], 1);
+      mbar_init(&sh.p_half[w], 4);
       mbar_init(&sh.p_full[w], 4);
       mbar_init(&sh.o_full[w], 1);
     }
@@ -105,6 +138,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
 
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax
+    regs_up<kSoftmaxRegs>();
     const int w = warp >> 2;
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
     const uint32_t s_tmem = tmem + lane_base + w * 128, o_tmem = tmem + lane_base + 256 + w * 128;
@@ -133,23 +167,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
                              (a.window <= 0 || kb > pos_last - a.window);
           const int hi = pos - kb;  // columns lo .. hi are seen
           const int lo = a.window > 0 ? hi - a.window + 1 : 0;
-          auto masked = [&](uint32_t (&x)[32], int c) {
-            const uint32_t bits = c == 0 ? ok0 : c == 1 ? ok1 : c == 2 ? ok2 : ok3;
+          uint32_t x[128];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c * 32 + e > hi || c * 32 + e < lo || !((bits >> e) & 1)) x[e] = 0xff800000u;
-          };
-          float top = neg_inf;
+          for (int c = 0; c < 4; ++c) tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + c * 32), s_tmem + c * 32);
+          tmem_wait_ld();
+          if (!whole) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld32(x, s_tmem + c * 32);
-            tmem_wait_ld();
-            if (!whole) masked(x, c);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+            for (int c = 0; c < 128; ++c) {
+              const uint32_t bits = c < 32 ? ok0 : c < 64 ? ok1 : c < 96 ? ok2 : ok3;
+              if (c > hi || c < lo || !((bits >> (c & 31)) & 1)) x[c] = 0xff800000u;
+            }
           }
-          top *= P.scale_log2;
+          float tops[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tops[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+#pragma unroll
+          for (int c = 8; c < 128; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tops[i] = fmaxf(fmaxf(tops[i], __uint_as_float(x[c + i])), __uint_as_float(x[c + 4 + i]));
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * P.scale_log2;
           const bool grow = top > m + kRescaleAt || (m == neg_inf && top > neg_inf);
           if (__any_sync(~0u, grow)) {
             const float keep = grow ? exp2_fast(m - top) : 1.f;
@@ -157,39 +194,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
             l *= keep;
             if (j > 0) {
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                tmem_ld32(x, o_tmem + c * 32);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t y[16];
+                tmem_ld16(y, o_tmem + c * 16);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
-                tmem_st32(o_tmem + c * 32, x);
+                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
+                tmem_st16(o_tmem + c * 16, y);
               }
             }
           }
-          const float base = m == neg_inf ? 0.f : m;
-          float sum0 = 0.f, sum1 = 0.f;
+          const float base = m == neg_inf ? 0.f : -m;
+          const uint64_t scale2 = pair_of(P.scale_log2, P.scale_log2), base2 = pair_of(base, base);
+          uint64_t sums[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t x[32], p[16];
-            tmem_ld32(x, s_tmem + c * 32);
-            tmem_wait_ld();
-            if (!whole) masked(x, c);
+            uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = exp2_fast(fmaf(__uint_as_float(x[2 * e]), P.scale_log2, -base));
-              const float p1 = exp2_fast(fmaf(__uint_as_float(x[2 * e + 1]), P.scale_log2, -base));
-              sum0 += p0;
-              sum1 += p1;
+              const int i = c * 32 + 2 * e;
+              const float2 y = split_pair(fma2(pair_of(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, base2));
+              const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
+              sums[e & 1] = add2(sums[e & 1], pair_of(p0, p1));
               p[e] = Pair<T>::narrow(p0, p1);
             }
-            tmem_st16(s_tmem + c * 16, p);  // over columns that have been read
+            tmem_st16(s_tmem + c * 16, p);
+            if (c & 1) {  // the product starts on the first 64 keys
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(c == 1 ? &sh.p_half[w] : &sh.p_full[w]);
+            }
           }
-          l += sum0 + sum1;
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_full[w]);
+          const float2 s0 = split_pair(add2(sums[0], sums[1]));
+          l += s0.x + s0.y;
         }
         chunk_wait(&sh.o_full[w], o_phase, &sh.dead);
         o_phase ^= 1;
@@ -242,6 +280,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ loads
+    regs_down<kLoadRegs>();
     const int lw = warp - 8;
     uint32_t it = 0, seg = 0;
     while (true) {
@@ -307,8 +346,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
       next_unit<kChunkRows, kChunkKeys>(P, &u);
     }
     cp_async_wait_all();
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------------ products
+    regs_down<kMmaRegs>();
+    if (warp == 12 && lane == 0) {
     constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t kQk = f16_idesc(kBf16, 128, 128, false), kPv = f16_idesc(kBf16, 128, D, true);
     uint32_t it = 0, seg = 0, p_phase[2] = {0, 0};
@@ -321,11 +362,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         mma_ss(tmem + w * 128, smem_desc(q0 + step, 16, 1024), smem_desc(k0 + step, 16, 1024), kQk, ks > 0);
       }
     };
-    auto pv = [&](int w, uint32_t tile, bool add) {
+    auto pv = [&](int w, uint32_t tile, bool add, int half) {
       if (sh.dead) return;
       const uint32_t v0 = v_smem + (tile % NS) * kTile;
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
+      for (int ks = half * 4; ks < half * 4 + 4; ++ks)
         mma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8, smem_desc(v0 + ks * 2048, kHalf, 1024), kPv,
                add || ks > 0);
     };
@@ -346,10 +387,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         chunk_wait(&sh.v_full[it % NS], (it / NS) & 1, &sh.dead);
         fence_async_proxy();
         for (int w = 0; w < nact; ++w) {
+          chunk_wait(&sh.p_half[w], p_phase[w], &sh.dead);
+          tc_fence_after();
+          pv(w, it, j > 0, 0);
           chunk_wait(&sh.p_full[w], p_phase[w], &sh.dead);
           p_phase[w] ^= 1;
           tc_fence_after();
-          pv(w, it, j > 0);
+          pv(w, it, true, 1);
           if (j + 1 < cnt) {
             if (w == 0) {
               chunk_wait(&sh.k_full[(it + 1) % NS], ((it + 1) / NS) & 1, &sh.dead);
@@ -375,6 +419,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
     if (sh.dead) {
       mma_commit(&sh.end);
       for (int i = 0; i < 1 << 16 && !mbar_try_wait(&sh.end, 0); ++i) __nanosleep(100);
+    }
     }
   }
   tc_fence_before();
