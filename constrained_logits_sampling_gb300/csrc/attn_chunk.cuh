@@ -87,6 +87,12 @@ __device__ __forceinline__ bool chunk_wait(unsigned long long* bar, uint32_t par
   return false;
 }
 
+// Bits lo .. hi of a word, of which only 0 .. 31 exist.
+__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
+  const uint32_t upto = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1;
+  return lo <= 0 ? upto : lo > 31 ? 0u : upto & (~0u << lo);
+}
+
 struct SoftmaxSync {  // the 256 softmax threads
   static __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 };
@@ -165,18 +171,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
           const uint32_t ok0 = ok[0], ok1 = ok[1], ok2 = ok[2], ok3 = ok[3];
           const bool whole = (ok0 & ok1 & ok2 & ok3) == ~0u && kb + 127 <= pos_first &&
                              (a.window <= 0 || kb > pos_last - a.window);
-          const int hi = pos - kb;  // columns lo .. hi are seen
-          const int lo = a.window > 0 ? hi - a.window + 1 : 0;
           uint32_t x[128];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + c * 32), s_tmem + c * 32);
           tmem_wait_ld();
           if (!whole) {
+            const int hi = pos - kb;  // columns lo .. hi are seen
+            const int lo = a.window > 0 ? hi - a.window + 1 : 0;
+            const uint32_t shown[4] = {ok0 & column_bits(lo, hi), ok1 & column_bits(lo - 32, hi - 32),
+                                       ok2 & column_bits(lo - 64, hi - 64), ok3 & column_bits(lo - 96, hi - 96)};
 #pragma unroll
-            for (int c = 0; c < 128; ++c) {
-              const uint32_t bits = c < 32 ? ok0 : c < 64 ? ok1 : c < 96 ? ok2 : ok3;
-              if (c > hi || c < lo || !((bits >> (c & 31)) & 1)) x[c] = 0xff800000u;
-            }
+            for (int c = 0; c < 128; ++c)
+              if (!(shown[c >> 5] & (1u << (c & 31)))) x[c] = 0xff800000u;
           }
           float tops[4];
 #pragma unroll
@@ -287,15 +293,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
       const int j0 = (int)(t - unit_begin);
       const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
       chunk_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
-      for (int x = 0; x < 2 * 32 * KC / 32; ++x) {
-        const int i = x * 32 + lane;
-        const int r = (i / (32 * KC)) * 128 + lw * 32 + i / KC % 32, ch = i % KC;
-        const bool live = r < u.rows;
-        const int row = u.row0 + (live ? r : 0);
-        const T* src = (const T*)a.q + (int64_t)(u.q0 + row / P.g) * a.q_stride_t +
-                       (int64_t)(u.h * P.g + row % P.g) * a.q_stride_h + ch * 8;
-        const int rr = r & 127;
-        cp_async16(q_smem + (r >> 7) * kTile + (ch >> 3) * kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), src, live);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int mine = u.row0 + w * 128 + lw * 32 + lane;  // this lane's row, which it hands to the others
+        const bool live = mine < u.row0 + u.rows;
+        const int64_t off = live ? (int64_t)(u.q0 + mine / P.g) * a.q_stride_t +
+                                       (int64_t)(u.h * P.g + mine % P.g) * a.q_stride_h
+                                 : 0;
+        const unsigned mask = __ballot_sync(~0u, live);
+#pragma unroll
+        for (int x = 0; x < KC; ++x) {
+          const int i = x * 32 + lane, row = i / KC, ch = i % KC, r = lw * 32 + row;
+          const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
+          cp_async16(q_smem + w * kTile + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                     (const T*)a.q + o, (mask >> row) & 1);
+        }
       }
       cp_async_arrive(smem_addr(&sh.q_full));
       const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
@@ -349,26 +361,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
   } else {
     // ------------------------------------------------------------------ products
     regs_down<kMmaRegs>();
-    if (warp == 12 && lane == 0) {
-    constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+    if (warp == 12) {
+    // the warp runs this converged, so that operands are uniform; one lane issues
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t kQk = f16_idesc(kBf16, 128, 128, false), kPv = f16_idesc(kBf16, 128, D, true);
-    uint32_t it = 0, seg = 0, p_phase[2] = {0, 0};
+    const uint32_t q_desc = smem_desc_lo(q_smem, 16), k_desc = smem_desc_lo(k_smem, 16),
+                   v_desc = smem_desc_lo(v_smem, kHalf);
+    uint32_t it = 0, seg = 0, p_phase = 0;  // bit w: phase of row tile w
     auto qk = [&](int w, uint32_t tile) {
-      if (sh.dead) return;
-      const uint32_t q0 = q_smem + w * kTile, k0 = k_smem + (tile % NS) * kTile;
+      const uint32_t q0 = q_desc + w * (kTile >> 4), k0 = k_desc + (tile % NS) * (kTile >> 4);
+      if (!sh.dead && elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t step = (ks >> 2) * kHalf + (ks & 3) * 32;
-        mma_ss(tmem + w * 128, smem_desc(q0 + step, 16, 1024), smem_desc(k0 + step, 16, 1024), kQk, ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t step = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+          mma_ss(tmem + w * 128, q0 + step, k0 + step, kQk, ks > 0);
+        }
       }
+      __syncwarp();
     };
     auto pv = [&](int w, uint32_t tile, bool add, int half) {
-      if (sh.dead) return;
-      const uint32_t v0 = v_smem + (tile % NS) * kTile;
+      const uint32_t v0 = v_desc + (tile % NS) * (kTile >> 4) + half * (4 * 2048 >> 4);
+      const uint32_t p0 = tmem + w * 128 + half * 32;
+      if (!sh.dead && elect_one()) {
 #pragma unroll
-      for (int ks = half * 4; ks < half * 4 + 4; ++ks)
-        mma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8, smem_desc(v0 + ks * 2048, kHalf, 1024), kPv,
-               add || ks > 0);
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ts(tmem + 256 + w * 128, p0 + ks * 8, v0 + ks * (2048 >> 4), kPv, add || ks > 0);
+      }
+      __syncwarp();
+    };
+    // elect.sync picks the same lane each time, so completions cover the products before them
+    auto commit = [&](unsigned long long* bar) {
+      if (elect_one()) mma_commit(bar);
+      __syncwarp();
     };
     while (true) {
       const int j0 = (int)(t - unit_begin);
@@ -379,19 +403,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
       fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
       for (int w = 0; w < nact; ++w) {
         qk(w, it);
-        mma_commit(&sh.s_full[w]);
+        commit(&sh.s_full[w]);
       }
-      mma_commit(&sh.k_empty[it % NS]);
-      if (cnt == 1) mma_commit(&sh.q_empty);
+      commit(&sh.k_empty[it % NS]);
+      if (cnt == 1) commit(&sh.q_empty);
       for (int j = 0; j < cnt; ++j, ++it) {
         chunk_wait(&sh.v_full[it % NS], (it / NS) & 1, &sh.dead);
         fence_async_proxy();
         for (int w = 0; w < nact; ++w) {
-          chunk_wait(&sh.p_half[w], p_phase[w], &sh.dead);
+          chunk_wait(&sh.p_half[w], (p_phase >> w) & 1, &sh.dead);
           tc_fence_after();
           pv(w, it, j > 0, 0);
-          chunk_wait(&sh.p_full[w], p_phase[w], &sh.dead);
-          p_phase[w] ^= 1;
+          chunk_wait(&sh.p_full[w], (p_phase >> w) & 1, &sh.dead);
+          p_phase ^= 1u << w;
           tc_fence_after();
           pv(w, it, true, 1);
           if (j + 1 < cnt) {
@@ -400,14 +424,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
               fence_async_proxy();
             }
             qk(w, it + 1);
-            mma_commit(&sh.s_full[w]);
+            commit(&sh.s_full[w]);
           } else {
-            mma_commit(&sh.o_full[w]);
+            commit(&sh.o_full[w]);
           }
         }
-        mma_commit(&sh.v_empty[it % NS]);
-        if (j + 1 < cnt) mma_commit(&sh.k_empty[(it + 1) % NS]);
-        if (j + 2 == cnt) mma_commit(&sh.q_empty);
+        commit(&sh.v_empty[it % NS]);
+        if (j + 1 < cnt) commit(&sh.k_empty[(it + 1) % NS]);
+        if (j + 2 == cnt) commit(&sh.q_empty);
       }
       ++seg;
       t += cnt;
@@ -417,7 +441,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
     }
     // products still running when a wait gave up end before their memory is freed
     if (sh.dead) {
-      mma_commit(&sh.end);
+      commit(&sh.end);
       for (int i = 0; i < 1 << 16 && !mbar_try_wait(&sh.end, 0); ++i) __nanosleep(100);
     }
     }

@@ -53,13 +53,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       : "memory");
 }
 
-// Shared-memory operand descriptor, 128-byte swizzle: address and strides in 16-byte units,
-// the fixed bit 46, swizzle mode 2.  Rows are 128 bytes; eight rows (1024 bytes, the
-// swizzle's period) repeat at sbo; for an operand whose rows run along its K axis, the next
-// 128 bytes of a row are at lbo.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)((lbo >> 4) & 0x3fff) << 16 |
-         (uint64_t)((sbo >> 4) & 0x3fff) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory operand descriptor, 128-byte swizzle, in two words.  Low: address and lbo in
+// 16-byte units, so that a step through a tile is an addition; high: sbo, the fixed bit 46
+// and swizzle mode 2.  Rows are 128 bytes; eight rows (1024 bytes, the swizzle's period)
+// repeat at sbo; for an operand whose rows run along its K axis, the next 128 bytes of a row
+// are at lbo (unused otherwise).
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3fff) | ((lbo >> 4) & 0x3fff) << 16;
+}
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+
+// True in one lane of a warp that runs converged.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
 }
 
 // Instruction descriptor of kind::f16 with float32 sums: M x N, both operands bf16 or both
@@ -69,19 +77,21 @@ __host__ __device__ constexpr uint32_t f16_idesc(bool bf16, int M, int N, bool b
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D (tensor memory) = A B (+ D), one K step of 16; issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// D (tensor memory) = A B (+ D), one K step of 16; issued by one thread.  a and b: low words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kDescHi)
       : "memory");
 }
 
