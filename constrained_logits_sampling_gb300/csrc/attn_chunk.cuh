@@ -6,13 +6,15 @@
 //                    128-byte swizzled layout that the matrix instructions read.  Page
 //                    boundaries may fall anywhere in a tile and slots past the length are
 //                    filled with zeros, which a box copy could do neither of;
-//   warp 12          one thread issues the products (13-15 make its warpgroup whole).
+//   warp 12          issues the products (13-15 make its warpgroup whole).
 // S = Q K^T goes to tensor memory (128 columns a tile), the softmax warps read it, write the
 // weights P over it in the input type, and O += P V takes P from there: scores never touch
 // shared memory.  The two tiles alternate: while one is in its softmax, the tensor cores
 // have the other's PV and next QK^T (2 x 128 x 128 x D each).  O stays in tensor memory;
 // it is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // time (P and its sum are then up to 2^8, which both types hold), so hardly ever.
+// A unit of at most 128 rows has one row tile: both halves of the CTA then take the same
+// queries and every other key tile, and their sums are joined like those of two spans.
 #pragma once
 
 #include <type_traits>
@@ -51,6 +53,11 @@ __device__ __forceinline__ float2 split_pair(uint64_t v) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -152,17 +159,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
     while (true) {
       const int j0 = (int)(t - unit_begin);
       const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
-      const int nact = u.rows > 128 ? 2 : 1;
-      const bool done = cnt == u.tiles;
-      if (w < nact) {
-        const int r = w * 128 + (warp & 3) * 32 + lane;
+      const bool split = u.rows <= 128;  // this half has the key tiles w, w + 2, ..
+      const bool done = cnt == u.tiles && !split;
+      const int step = split ? 2 : 1;
+      const int place = w * 128 + (warp & 3) * 32 + lane;  // of this row's sums in the scratch
+      const int r = split ? place & 127 : place;
+      if (!split || cnt > w) {
         const bool live = r < u.rows;
         const int first_pos = u.len - u.n;
         const int pos = live ? first_pos + (u.row0 + r) / P.g : -1;
-        const int pos_first = first_pos + (u.row0 + w * 128) / P.g;
-        const int pos_last = first_pos + (u.row0 + min(u.rows, w * 128 + 128) - 1) / P.g;
+        const int half0 = split ? 0 : w * 128;
+        const int pos_first = first_pos + (u.row0 + half0) / P.g;
+        const int pos_last = first_pos + (u.row0 + min(u.rows, half0 + 128) - 1) / P.g;
         float m = neg_inf, l = 0.f;  // reference maximum (log2 units) and weights' sum
-        for (int j = 0; j < cnt; ++j) {
+        const int jw = split ? w : 0;
+        for (int j = jw; j < cnt; j += step) {
           const int kb = (u.tile0 + j0 + j) * kChunkKeys;
           chunk_wait(&sh.s_full[w], s_phase, &sh.dead);
           s_phase ^= 1;
@@ -191,14 +202,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
           for (int c = 8; c < 128; c += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              tops[i] = fmaxf(fmaxf(tops[i], __uint_as_float(x[c + i])), __uint_as_float(x[c + 4 + i]));
+              tops[i] = max3(tops[i], __uint_as_float(x[c + i]), __uint_as_float(x[c + 4 + i]));
           const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * P.scale_log2;
           const bool grow = top > m + kRescaleAt || (m == neg_inf && top > neg_inf);
           if (__any_sync(~0u, grow)) {
             const float keep = grow ? exp2_fast(m - top) : 1.f;
             if (grow) m = top;
             l *= keep;
-            if (j > 0) {
+            if (j > jw) {
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t y[16];
@@ -262,7 +273,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
             } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                __stcg(reinterpret_cast<uint4*>(slot + r * D + c * 32 + e), make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
+                __stcg(reinterpret_cast<uint4*>(slot + place * D + c * 32 + e), make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
             }
           }
         }
@@ -271,12 +282,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
           if (done) {
             store_lse(P, u, r, m, l);
           } else {
-            __stcg(slot + kChunkRows * D + r, m);
-            __stcg(slot + kChunkRows * D + kChunkRows + r, l);
+            __stcg(slot + kChunkRows * D + place, m);
+            __stcg(slot + kChunkRows * D + kChunkRows + place, l);
           }
         }
+      } else if (r < u.rows) {  // no key tile for this half
+        float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
+        for (int d = 0; d < D; d += 4) __stcg(reinterpret_cast<float4*>(slot + place * D + d), make_float4(0.f, 0.f, 0.f, 0.f));
+        __stcg(slot + kChunkRows * D + place, neg_inf);
+        __stcg(slot + kChunkRows * D + kChunkRows + place, 0.f);
       }
-      if (!done) join_parts<T, kChunkRows, D, 256, SoftmaxSync>(P, u, span, unit_begin);
+      if (!done) join_parts<T, kChunkRows, D, 256, SoftmaxSync>(P, u, span, unit_begin, split ? 128 : 0);
       if (sh.dead && tid == 0 && a.row_status) atomicMax(a.row_status + u.b, CLSAMPLE_ROW_OVERFLOW);
       tile += cnt;
       t += cnt;
@@ -362,88 +378,122 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
     // ------------------------------------------------------------------ products
     regs_down<kMmaRegs>();
     if (warp == 12) {
-    // the warp runs this converged, so that operands are uniform; one lane issues
-    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr uint32_t kQk = f16_idesc(kBf16, 128, 128, false), kPv = f16_idesc(kBf16, 128, D, true);
-    const uint32_t q_desc = smem_desc_lo(q_smem, 16), k_desc = smem_desc_lo(k_smem, 16),
-                   v_desc = smem_desc_lo(v_smem, kHalf);
-    uint32_t it = 0, seg = 0, p_phase = 0;  // bit w: phase of row tile w
-    auto qk = [&](int w, uint32_t tile) {
-      const uint32_t q0 = q_desc + w * (kTile >> 4), k0 = k_desc + (tile % NS) * (kTile >> 4);
-      if (!sh.dead && elect_one()) {
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t step = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-          mma_ss(tmem + w * 128, q0 + step, k0 + step, kQk, ks > 0);
-        }
-      }
-      __syncwarp();
-    };
-    auto pv = [&](int w, uint32_t tile, bool add, int half) {
-      const uint32_t v0 = v_desc + (tile % NS) * (kTile >> 4) + half * (4 * 2048 >> 4);
-      const uint32_t p0 = tmem + w * 128 + half * 32;
-      if (!sh.dead && elect_one()) {
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_ts(tmem + 256 + w * 128, p0 + ks * 8, v0 + ks * (2048 >> 4), kPv, add || ks > 0);
-      }
-      __syncwarp();
-    };
-    // elect.sync picks the same lane each time, so completions cover the products before them
-    auto commit = [&](unsigned long long* bar) {
-      if (elect_one()) mma_commit(bar);
-      __syncwarp();
-    };
-    while (true) {
-      const int j0 = (int)(t - unit_begin);
-      const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
-      const int nact = u.rows > 128 ? 2 : 1;
-      chunk_wait(&sh.q_full, seg & 1, &sh.dead);
-      chunk_wait(&sh.k_full[it % NS], (it / NS) & 1, &sh.dead);
-      fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
-      for (int w = 0; w < nact; ++w) {
-        qk(w, it);
-        commit(&sh.s_full[w]);
-      }
-      commit(&sh.k_empty[it % NS]);
-      if (cnt == 1) commit(&sh.q_empty);
-      for (int j = 0; j < cnt; ++j, ++it) {
-        chunk_wait(&sh.v_full[it % NS], (it / NS) & 1, &sh.dead);
+      // Everything here is uniform, and made known as such (uni): the operands of a product
+      // have to be in uniform registers for the issue to keep up with the tensor cores.
+      auto uni = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };
+      constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+      constexpr uint32_t kQk = f16_idesc(kBf16, 128, 128, false), kPv = f16_idesc(kBf16, 128, D, true);
+      const uint32_t base = uni(tmem), q_desc = uni(smem_desc_lo(q_smem, 16)), k_desc = uni(smem_desc_lo(k_smem, 16)),
+                     v_desc = uni(smem_desc_lo(v_smem, kHalf));
+      uint32_t it = 0, seg = 0, p_phase = 0;  // bit w of p_phase: half w
+      bool alive = true;
+      auto wait = [&](unsigned long long* bar, uint32_t parity) {
+        alive = __all_sync(~0u, chunk_wait(bar, parity, &sh.dead)) && alive;
+      };
+      auto keys_ready = [&](uint32_t tile) {
+        wait(&sh.k_full[tile % NS], (tile / NS) & 1);
+        fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
+      };
+      auto values_ready = [&](uint32_t tile) {
+        wait(&sh.v_full[tile % NS], (tile / NS) & 1);
         fence_async_proxy();
-        for (int w = 0; w < nact; ++w) {
-          chunk_wait(&sh.p_half[w], (p_phase >> w) & 1, &sh.dead);
-          tc_fence_after();
-          pv(w, it, j > 0, 0);
-          chunk_wait(&sh.p_full[w], (p_phase >> w) & 1, &sh.dead);
-          p_phase ^= 1u << w;
-          tc_fence_after();
-          pv(w, it, true, 1);
-          if (j + 1 < cnt) {
-            if (w == 0) {
-              chunk_wait(&sh.k_full[(it + 1) % NS], ((it + 1) / NS) & 1, &sh.dead);
-              fence_async_proxy();
-            }
-            qk(w, it + 1);
-            commit(&sh.s_full[w]);
-          } else {
-            commit(&sh.o_full[w]);
+      };
+      // S of half w = (row tile rt of Q) K^T
+      auto qk = [&](uint32_t w, uint32_t rt, uint32_t tile) {
+        const uint32_t q0 = q_desc + rt * (kTile >> 4), k0 = k_desc + (tile % NS) * (kTile >> 4);
+        if (alive) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+            mma_ss(base + w * 128, q0 + off, k0 + off, kQk, ks > 0);
           }
         }
-        commit(&sh.v_empty[it % NS]);
-        if (j + 1 < cnt) commit(&sh.k_empty[(it + 1) % NS]);
-        if (j + 2 == cnt) commit(&sh.q_empty);
+        mma_commit(&sh.s_full[w]);
+      };
+      // O of half w (+)= P V, in two parts as P comes
+      auto pv = [&](uint32_t w, uint32_t tile, bool add) {
+        const uint32_t v0 = v_desc + (tile % NS) * (kTile >> 4), o = base + 256 + w * 128, p0 = base + w * 128;
+        wait(&sh.p_half[w], (p_phase >> w) & 1);
+        tc_fence_after();
+        if (alive) {
+          mma_ts(o, p0, v0, kPv, add);
+#pragma unroll
+          for (int ks = 1; ks < 4; ++ks) mma_ts(o, p0 + ks * 8, v0 + ks * (2048 >> 4), kPv, true);
+        }
+        wait(&sh.p_full[w], (p_phase >> w) & 1);
+        tc_fence_after();
+        if (alive) {
+#pragma unroll
+          for (int ks = 4; ks < 8; ++ks) mma_ts(o, p0 + ks * 8, v0 + ks * (2048 >> 4), kPv, true);
+        }
+        p_phase ^= 1u << w;
+      };
+      while (true) {
+        const int j0 = (int)(t - unit_begin);
+        const int cnt = (int)uni((uint32_t)min((int64_t)(u.tiles - j0), span.t1 - t));
+        const bool split = uni(u.rows <= 128);
+        wait(&sh.q_full, seg & 1);
+        keys_ready(it);
+        if (!split) {
+          qk(0, 0, it);
+          qk(1, 1, it);
+          mma_commit(&sh.k_empty[it % NS]);
+          if (cnt == 1) mma_commit(&sh.q_empty);
+          for (int j = 0; j < cnt; ++j, ++it) {
+            const bool more = j + 1 < cnt;
+            values_ready(it);
+            pv(0, it, j > 0);
+            if (more) {
+              keys_ready(it + 1);
+              qk(0, 0, it + 1);
+            } else {
+              mma_commit(&sh.o_full[0]);
+            }
+            pv(1, it, j > 0);
+            mma_commit(&sh.v_empty[it % NS]);
+            if (more) {
+              qk(1, 1, it + 1);
+              mma_commit(&sh.k_empty[(it + 1) % NS]);
+              if (j + 2 == cnt) mma_commit(&sh.q_empty);
+            } else {
+              mma_commit(&sh.o_full[1]);
+            }
+          }
+        } else {
+          qk(0, 0, it);
+          mma_commit(&sh.k_empty[it % NS]);
+          if (cnt > 1) {
+            keys_ready(it + 1);
+            qk(1, 0, it + 1);
+            mma_commit(&sh.k_empty[(it + 1) % NS]);
+          }
+          if (cnt <= 2) mma_commit(&sh.q_empty);
+          for (int j = 0; j < cnt; ++j, ++it) {
+            const uint32_t w = j & 1;
+            values_ready(it);
+            pv(w, it, j > 1);
+            mma_commit(&sh.v_empty[it % NS]);
+            if (j + 2 < cnt) {
+              keys_ready(it + 2);
+              qk(w, 0, it + 2);
+              mma_commit(&sh.k_empty[(it + 2) % NS]);
+              if (j + 3 == cnt) mma_commit(&sh.q_empty);
+            } else {
+              mma_commit(&sh.o_full[w]);
+            }
+          }
+        }
+        ++seg;
+        t += cnt;
+        if (uni(t >= span.t1)) break;
+        unit_begin = t;
+        next_unit<kChunkRows, kChunkKeys>(P, &u);
       }
-      ++seg;
-      t += cnt;
-      if (t >= span.t1) break;
-      unit_begin = t;
-      next_unit<kChunkRows, kChunkKeys>(P, &u);
-    }
-    // products still running when a wait gave up end before their memory is freed
-    if (sh.dead) {
-      commit(&sh.end);
-      for (int i = 0; i < 1 << 16 && !mbar_try_wait(&sh.end, 0); ++i) __nanosleep(100);
-    }
+      // products still running when a wait gave up end before their memory is freed
+      if (!alive) {
+        mma_commit(&sh.end);
+        for (int i = 0; i < 1 << 16 && !mbar_try_wait(&sh.end, 0); ++i) __nanosleep(100);
+      }
     }
   }
   tc_fence_before();

@@ -100,41 +100,76 @@ __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, in
 
 // Joins the partial sums of a unit cut by span boundaries: called by the NT threads that
 // wrote a CTA's part (threads 0 .. NT - 1, which Sync joins); the CTA that arrives last joins
-// them all, in key order.
+// them all, in key order.  With `second`, a CTA's part is two: the row's other sums are
+// `second` rows further in its slot.
 struct BlockSync {
   static __device__ __forceinline__ void sync() { __syncthreads(); }
 };
 template <class T, int R, int D, int NT, class Sync>
-__device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin) {
+__device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin,
+                                           int second = 0) {
   __shared__ int last;
   const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
-  __threadfence();
-  Sync::sync();
-  if (threadIdx.x == 0) {
-    last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
-    if (last) P.arrived[c0] = 0;  // for the next call
-  }
-  Sync::sync();
-  if (!last) return;
-  __threadfence();
-  for (int i = threadIdx.x; i < u.rows * (D / 4); i += NT) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
-    float m = __int_as_float(0xff800000), l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      const float* s = scratch_slot<R, D>(P, c, c == c0 ? 1 : 0);
-      const float mc = __ldcg(s + R * D + r), lc = __ldcg(s + R * D + R + r);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * D + d));
-      const float mn = fmaxf(m, mc);
-      const float f = m == mn ? 1.f : exp2_fast(m - mn), fc = mc == mn ? 1.f : exp2_fast(mc - mn);
-      o = make_float4(o.x * f + v.x * fc, o.y * f + v.y * fc, o.z * f + v.z * fc, o.w * f + v.w * fc);
-      l = l * f + lc * fc;
-      m = mn;
+  if (c0 < c1 || second == 0) {
+    __threadfence();
+    Sync::sync();
+    if (threadIdx.x == 0) {
+      last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
+      if (last) P.arrived[c0] = 0;  // for the next call
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store_out4<T>(P, u, r, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (d == 0) store_lse(P, u, r, m, l);
+    Sync::sync();
+    if (!last) return;
+    __threadfence();
+  } else {
+    Sync::sync();  // only this CTA's own two halves
   }
+  // D / 4 threads a row; several rows in flight
+  constexpr int kPer = D / 4, kRows = 8, kStep = NT / kPer;
+  const int d = threadIdx.x % kPer * 4;
+  const int halves = second ? 2 : 1;
+  for (int r0 = threadIdx.x / kPer; r0 < u.rows; r0 += kRows * kStep) {
+    float m[kRows], l[kRows];
+    float4 o[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      m[k] = __int_as_float(0xff800000);
+      l[k] = 0.f;
+      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int part = 0; part < (c1 - c0 + 1) * halves; ++part) {
+      const int c = c0 + part / halves;
+      const float* s = scratch_slot<R, D>(P, c, c == c0 ? 1 : 0);
+      const int row = r0 + (part % halves) * second;
+      float mc[kRows], lc[kRows];
+      float4 v[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const bool live = r0 + k * kStep < u.rows;
+        const int rk = live ? row + k * kStep : row;
+        mc[k] = __ldcg(s + R * D + rk);
+        lc[k] = __ldcg(s + R * D + R + rk);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(s + rk * D + d));
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const float mn = fmaxf(m[k], mc[k]);
+        const float f = m[k] == mn ? 1.f : exp2_fast(m[k] - mn), fc = mc[k] == mn ? 1.f : exp2_fast(mc[k] - mn);
+        o[k] = make_float4(o[k].x * f + v[k].x * fc, o[k].y * f + v[k].y * fc, o[k].z * f + v[k].z * fc,
+                           o[k].w * f + v[k].w * fc);
+        l[k] = l[k] * f + lc[k] * fc;
+        m[k] = mn;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int r = r0 + k * kStep;
+      if (r >= u.rows) break;
+      const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
+      store_out4<T>(P, u, r, d, make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
+      if (d == 0) store_lse(P, u, r, m[k], l[k]);
+    }
+  }
+  if (second) Sync::sync();  // the CTA may write the same slot for its next unit
 }
 
 template <class T, int D, int MT>

@@ -63,13 +63,6 @@ __device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr, uint32_t lbo) {
 }
 constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
 
-// True in one lane of a warp that runs converged.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t is;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
-  return is != 0;
-}
-
 // Instruction descriptor of kind::f16 with float32 sums: M x N, both operands bf16 or both
 // f16; b_mn: B's rows run along K (its N axis is the contiguous one).
 __host__ __device__ constexpr uint32_t f16_idesc(bool bf16, int M, int N, bool b_mn) {
@@ -77,28 +70,33 @@ __host__ __device__ constexpr uint32_t f16_idesc(bool bf16, int M, int N, bool b
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D (tensor memory) = A B (+ D), one K step of 16; issued by one thread.  a and b: low words.
+// D (tensor memory) = A B (+ D), one K step of 16; a and b are low descriptor words.  Called
+// by a whole converged warp with uniform operands, of which one lane, the same each time,
+// issues: so the operands stay in uniform registers, without which a warp cannot issue a
+// 128 x 128 x 16 product every 64 cycles.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, one;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\telect.sync _|one, 0xffffffff;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, one;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\telect.sync _|one, 0xffffffff;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
       "r"(a_tmem), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kDescHi)
       : "memory");
 }
 
-// Arrives on `bar` when all products issued so far by this thread are complete.
+// Arrives on `bar` when all products issued so far by this warp are complete.
 __device__ __forceinline__ void mma_commit(unsigned long long* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+      "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
