@@ -6,7 +6,9 @@
 //                    128-byte swizzled layout that the matrix instructions read.  Page
 //                    boundaries may fall anywhere in a tile and slots past the length are
 //                    filled with zeros, which a box copy could do neither of;
-//   warp 12          issues the products (13-15 make its warpgroup whole).
+//   warp 12          issues the products;
+//   warp 13          hands what the load warps wrote over to the tensor cores' proxy
+//                    (14 and 15 make the warpgroup whole).
 // S = Q K^T goes to tensor memory (128 columns a tile), the softmax warps read it, write the
 // weights P over it in the input type, and O += P V takes P from there: scores never touch
 // shared memory.  The two tiles alternate: while one is in its softmax, the tensor cores
@@ -68,17 +70,20 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 template <int D>
 struct ChunkShape {
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kTile = 128 * D * 2;  // 128 rows, in bytes
-  static constexpr int kBytes = (2 + 2 * kStages) * kTile + 1024;  // 1024: alignment of the swizzle
+  static constexpr int kKeySlots = D == 128 ? 2 : 4;  // ring of key tiles
+  static constexpr int kValueSlots = kKeySlots + 1;   // values are needed a step later
+  static constexpr int kTile = 128 * D * 2;           // 128 rows, in bytes
+  static constexpr int kBytes = (2 + kKeySlots + kValueSlots) * kTile + 1024;  // 1024: alignment of the swizzle
 };
 
-template <int NS>
+template <int NS, int NV>
 struct ChunkShared {
-  unsigned long long k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+  // filled by the load warps; handed over; S of a tile complete, so that its keys' slot and
+  // the slot of the values before them are free
+  unsigned long long k_landed[NS], v_landed[NV], k_full[NS], v_full[NV], tile_done[NS];
   unsigned long long q_full, q_empty, end, s_full[2], p_half[2], p_full[2], o_full[2];
   uint32_t tmem;
-  volatile int dead;         // a bounded wait ran out: every other wait ends too
+  volatile int dead;           // a bounded wait ran out: every other wait ends too
   uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
 };
 
@@ -104,13 +109,85 @@ struct SoftmaxSync {  // the 256 softmax threads
   static __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 };
 
+// Joins the parts of a unit, as join_parts does, by the 256 softmax threads.  A slot holds
+// four sums of each row side by side, then the next four of each row, so that threads with a
+// row each read and write whole lines.  With `split` a CTA's part is two, 128 rows apart, and
+// two threads share a row.
+template <class T, int D>
+__device__ __forceinline__ void join_rows(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin,
+                                          bool split) {
+  __shared__ int last;
+  const int tid = threadIdx.x;
+  const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
+  if (c0 < c1) {
+    __threadfence();
+    SoftmaxSync::sync();
+    if (tid == 0) {
+      last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
+      if (last) P.arrived[c0] = 0;  // for the next call
+    }
+    SoftmaxSync::sync();
+    if (!last) return;
+    __threadfence();
+  } else {
+    SoftmaxSync::sync();  // only this CTA's own two halves
+  }
+  const int halves = split ? 2 : 1, parts = (c1 - c0 + 1) * halves;
+  const int r = split ? tid & 127 : tid;
+  const int d0 = split ? (tid >> 7) * (D / 2) : 0, d1 = split ? d0 + D / 2 : D;
+  auto slot_of = [&](int part) {
+    const int c = c0 + part / halves;
+    return scratch_slot<kChunkRows, D>(P, c, c == c0 ? 1 : 0);
+  };
+  if (r < u.rows) {
+    float m = __int_as_float(0xff800000), l = 0.f;
+    for (int part = 0; part < parts; ++part) {
+      const float* s = slot_of(part) + kChunkRows * D + r + (part % halves) * 128;
+      const float mc = __ldcg(s), lc = __ldcg(s + kChunkRows);
+      const float mn = fmaxf(m, mc);
+      l = l * (m == mn ? 1.f : exp2_fast(m - mn)) + lc * (mc == mn ? 1.f : exp2_fast(mc - mn));
+      m = mn;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int row = u.row0 + r;
+    T* dst = (T*)P.a.out + (int64_t)(u.q0 + row / P.g) * P.a.o_stride_t +
+             (int64_t)(u.h * P.g + row % P.g) * P.a.o_stride_h;
+    if (d0 == 0) store_lse(P, u, r, m, l);
+    for (int d = d0; d < d1; d += 32) {
+      float4 o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int part = 0; part < parts; ++part) {
+        const float* s = slot_of(part);
+        const int at = r + (part % halves) * 128;
+        const float mc = __ldcg(s + kChunkRows * D + at);
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = __ldcg(reinterpret_cast<const float4*>(s + (d + 4 * i) * kChunkRows + at * 4));
+        const float f = (mc == m ? 1.f : exp2_fast(mc - m)) * inv;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          o[i] = make_float4(fmaf(v[i].x, f, o[i].x), fmaf(v[i].y, f, o[i].y), fmaf(v[i].z, f, o[i].z),
+                             fmaf(v[i].w, f, o[i].w));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i += 2)
+        *reinterpret_cast<uint4*>(dst + d + 4 * i) =
+            make_uint4(Pair<T>::narrow(o[i].x, o[i].y), Pair<T>::narrow(o[i].z, o[i].w),
+                       Pair<T>::narrow(o[i + 1].x, o[i + 1].y), Pair<T>::narrow(o[i + 1].z, o[i + 1].w));
+    }
+  }
+  if (split) SoftmaxSync::sync();  // the CTA may write the same slot for its next unit
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __grid_constant__ AttnParams P) {
   using Shape = ChunkShape<D>;
-  constexpr int NS = Shape::kStages, kTile = Shape::kTile, KC = D / 8;
+  constexpr int NS = Shape::kKeySlots, NV = Shape::kValueSlots, kTile = Shape::kTile, KC = D / 8;
   constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 elements
   extern __shared__ unsigned char raw[];
-  __shared__ ChunkShared<NS> sh;
+  __shared__ ChunkShared<NS, NV> sh;
   unsigned char* const smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_smem = smem_addr(smem), k_smem = q_smem + 2 * kTile, v_smem = k_smem + NS * kTile;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -125,10 +202,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.k_full[i], 128 + 4);  // every load thread's copies, and four words of key_ok
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], 128);
-      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.k_landed[i], 128 + 4);  // every load thread's copies, and four words of key_ok
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.tile_done[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&sh.v_landed[i], 128);
+      mbar_init(&sh.v_full[i], 1);
     }
     mbar_init(&sh.q_full, 128);
     mbar_init(&sh.q_empty, 1);
@@ -273,7 +353,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
             } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                __stcg(reinterpret_cast<uint4*>(slot + place * D + c * 32 + e), make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
+                __stcg(reinterpret_cast<uint4*>(slot + ((c * 32 + e) * kChunkRows + place * 4)),
+                       make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
             }
           }
         }
@@ -288,11 +369,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         }
       } else if (r < u.rows) {  // no key tile for this half
         float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
-        for (int d = 0; d < D; d += 4) __stcg(reinterpret_cast<float4*>(slot + place * D + d), make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int d = 0; d < D; d += 4)
+          __stcg(reinterpret_cast<float4*>(slot + (d * kChunkRows + place * 4)), make_float4(0.f, 0.f, 0.f, 0.f));
         __stcg(slot + kChunkRows * D + place, neg_inf);
         __stcg(slot + kChunkRows * D + kChunkRows + place, 0.f);
       }
-      if (!done) join_parts<T, kChunkRows, D, 256, SoftmaxSync>(P, u, span, unit_begin, split ? 128 : 0);
+      if (!done) join_rows<T, D>(P, u, span, unit_begin, split);
       if (sh.dead && tid == 0 && a.row_status) atomicMax(a.row_status + u.b, CLSAMPLE_ROW_OVERFLOW);
       tile += cnt;
       t += cnt;
@@ -309,7 +391,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
       const int j0 = (int)(t - unit_begin);
       const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
       chunk_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
-#pragma unroll
+#pragma unroll 1
       for (int w = 0; w < 2; ++w) {
         const int mine = u.row0 + w * 128 + lw * 32 + lane;  // this lane's row, which it hands to the others
         const bool live = mine < u.row0 + u.rows;
@@ -345,25 +427,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         const unsigned mask = __ballot_sync(~0u, ok);
         // keys outside the unit's range are hidden by the rows' limits: only a bad page counts
         const unsigned shown = __ballot_sync(~0u, ok || key < u.key_lo || key >= u.key_hi);
-        const int st = it % NS;
-        const uint32_t parity = ((it / NS) & 1) ^ 1;
-#pragma unroll
+        // the slot of the keys is free when S of the tile that had it is complete, and the slot
+        // of the values when O is, which a later tile's completion covers: the next one's if
+        // both halves take each tile, the one after it otherwise (and across units, where
+        // either may have been the case)
+        const int64_t k_gate = (int64_t)it - NS, v_gate = (int64_t)it - NV + (u.rows <= 128 || j < NV ? 2 : 1);
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          chunk_wait(kv ? &sh.v_empty[st] : &sh.k_empty[st], parity, &sh.dead);
+          const int64_t gate = kv ? v_gate : k_gate;
+          // (the keys' gate has been passed: by now its barrier may be a phase further)
+          if (gate >= 0 && (kv == 0 || v_gate > k_gate)) chunk_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
           __syncwarp();
+          unsigned long long* landed = kv ? &sh.v_landed[it % NV] : &sh.k_landed[it % NS];
           if (kv == 0 && lane == 0) {
             sh.key_ok[it % (2 * NS)][lw] = shown;
-            mbar_arrive(&sh.k_full[st]);
+            mbar_arrive(landed);
           }
           const T* src = kv ? vc : kc;
-          const uint32_t dst = (kv ? v_smem : k_smem) + st * kTile;
+          const uint32_t dst = kv ? v_smem + it % NV * kTile : k_smem + it % NS * kTile;
 #pragma unroll
           for (int x = 0; x < KC; ++x) {
             const int i = x * 32 + lane, row = i / KC, ch = i % KC, r = lw * 32 + row;
             const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
             cp_async16(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + o, (mask >> row) & 1);
           }
-          cp_async_arrive(smem_addr(kv ? &sh.v_full[st] : &sh.k_full[st]));
+          cp_async_arrive(smem_addr(landed));
         }
         page = next;
       }
@@ -390,14 +478,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
       auto wait = [&](unsigned long long* bar, uint32_t parity) {
         alive = __all_sync(~0u, chunk_wait(bar, parity, &sh.dead)) && alive;
       };
-      auto keys_ready = [&](uint32_t tile) {
-        wait(&sh.k_full[tile % NS], (tile / NS) & 1);
-        fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
-      };
-      auto values_ready = [&](uint32_t tile) {
-        wait(&sh.v_full[tile % NS], (tile / NS) & 1);
-        fence_async_proxy();
-      };
+      auto keys_ready = [&](uint32_t tile) { wait(&sh.k_full[tile % NS], (tile / NS) & 1); };
+      auto values_ready = [&](uint32_t tile) { wait(&sh.v_full[tile % NV], (tile / NV) & 1); };
       // S of half w = (row tile rt of Q) K^T
       auto qk = [&](uint32_t w, uint32_t rt, uint32_t tile) {
         const uint32_t q0 = q_desc + rt * (kTile >> 4), k0 = k_desc + (tile % NS) * (kTile >> 4);
@@ -412,15 +494,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
       };
       // O of half w (+)= P V, in two parts as P comes
       auto pv = [&](uint32_t w, uint32_t tile, bool add) {
-        const uint32_t v0 = v_desc + (tile % NS) * (kTile >> 4), o = base + 256 + w * 128, p0 = base + w * 128;
-        wait(&sh.p_half[w], (p_phase >> w) & 1);
+        const uint32_t v0 = v_desc + (tile % NV) * (kTile >> 4), o = base + 256 + w * 128, p0 = base + w * 128;
+        const uint32_t parity = (p_phase >> w) & 1;
+        const bool all = __all_sync(~0u, mbar_test_wait(&sh.p_full[w], parity));
+        if (!all) wait(&sh.p_half[w], parity);
         tc_fence_after();
         if (alive) {
           mma_ts(o, p0, v0, kPv, add);
 #pragma unroll
           for (int ks = 1; ks < 4; ++ks) mma_ts(o, p0 + ks * 8, v0 + ks * (2048 >> 4), kPv, true);
         }
-        wait(&sh.p_full[w], (p_phase >> w) & 1);
+        if (!all) wait(&sh.p_full[w], parity);
         tc_fence_after();
         if (alive) {
 #pragma unroll
@@ -433,50 +517,46 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         const int cnt = (int)uni((uint32_t)min((int64_t)(u.tiles - j0), span.t1 - t));
         const bool split = uni(u.rows <= 128);
         wait(&sh.q_full, seg & 1);
+        fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
         keys_ready(it);
         if (!split) {
           qk(0, 0, it);
           qk(1, 1, it);
-          mma_commit(&sh.k_empty[it % NS]);
+          mma_commit(&sh.tile_done[it % NS]);
           if (cnt == 1) mma_commit(&sh.q_empty);
-          for (int j = 0; j < cnt; ++j, ++it) {
-            const bool more = j + 1 < cnt;
+          for (int j = 0; j + 1 < cnt; ++j, ++it) {
             values_ready(it);
+            keys_ready(it + 1);
             pv(0, it, j > 0);
-            if (more) {
-              keys_ready(it + 1);
-              qk(0, 0, it + 1);
-            } else {
-              mma_commit(&sh.o_full[0]);
-            }
+            qk(0, 0, it + 1);
             pv(1, it, j > 0);
-            mma_commit(&sh.v_empty[it % NS]);
-            if (more) {
-              qk(1, 1, it + 1);
-              mma_commit(&sh.k_empty[(it + 1) % NS]);
-              if (j + 2 == cnt) mma_commit(&sh.q_empty);
-            } else {
-              mma_commit(&sh.o_full[1]);
-            }
+            qk(1, 1, it + 1);
+            mma_commit(&sh.tile_done[(it + 1) % NS]);
           }
+          if (cnt > 1) mma_commit(&sh.q_empty);
+          values_ready(it);
+          pv(0, it, cnt > 1);
+          mma_commit(&sh.o_full[0]);
+          pv(1, it, cnt > 1);
+          mma_commit(&sh.o_full[1]);
+          ++it;
         } else {
           qk(0, 0, it);
-          mma_commit(&sh.k_empty[it % NS]);
+          mma_commit(&sh.tile_done[it % NS]);
           if (cnt > 1) {
             keys_ready(it + 1);
             qk(1, 0, it + 1);
-            mma_commit(&sh.k_empty[(it + 1) % NS]);
+            mma_commit(&sh.tile_done[(it + 1) % NS]);
           }
           if (cnt <= 2) mma_commit(&sh.q_empty);
           for (int j = 0; j < cnt; ++j, ++it) {
             const uint32_t w = j & 1;
             values_ready(it);
             pv(w, it, j > 1);
-            mma_commit(&sh.v_empty[it % NS]);
             if (j + 2 < cnt) {
               keys_ready(it + 2);
               qk(w, 0, it + 2);
-              mma_commit(&sh.k_empty[(it + 2) % NS]);
+              mma_commit(&sh.tile_done[(it + 2) % NS]);
               if (j + 3 == cnt) mma_commit(&sh.q_empty);
             } else {
               mma_commit(&sh.o_full[w]);
@@ -493,6 +573,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
       if (!alive) {
         mma_commit(&sh.end);
         for (int i = 0; i < 1 << 16 && !mbar_try_wait(&sh.end, 0); ++i) __nanosleep(100);
+      }
+    } else if (warp == 13 && lane == 0) {
+      // The copies are ordinary writes, the products read by the async proxy: the fence between
+      // them costs a hundred cycles or so, which the issuing warp has not got.
+      const int tiles = (int)(span.t1 - span.t0);
+      for (int i = 0; i < tiles; ++i) {
+        chunk_wait(&sh.k_landed[i % NS], (i / NS) & 1, &sh.dead);
+        fence_async_proxy();
+        mbar_arrive(&sh.k_full[i % NS]);
+        chunk_wait(&sh.v_landed[i % NV], (i / NV) & 1, &sh.dead);
+        fence_async_proxy();
+        mbar_arrive(&sh.v_full[i % NV]);
       }
     }
   }

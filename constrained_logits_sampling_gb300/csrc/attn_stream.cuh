@@ -98,35 +98,24 @@ __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, in
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xff800000);
 }
 
-// Joins the partial sums of a unit cut by span boundaries: called by the NT threads that
-// wrote a CTA's part (threads 0 .. NT - 1, which Sync joins); the CTA that arrives last joins
-// them all, in key order.  With `second`, a CTA's part is two: the row's other sums are
-// `second` rows further in its slot.
-struct BlockSync {
-  static __device__ __forceinline__ void sync() { __syncthreads(); }
-};
-template <class T, int R, int D, int NT, class Sync>
-__device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin,
-                                           int second = 0) {
+// Joins the partial sums of a unit cut by span boundaries: called by all NT threads of each
+// CTA that wrote a part; the CTA that arrives last joins them all, in key order.
+template <class T, int R, int D, int NT>
+__device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin) {
   __shared__ int last;
   const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
-  if (c0 < c1 || second == 0) {
-    __threadfence();
-    Sync::sync();
-    if (threadIdx.x == 0) {
-      last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
-      if (last) P.arrived[c0] = 0;  // for the next call
-    }
-    Sync::sync();
-    if (!last) return;
-    __threadfence();
-  } else {
-    Sync::sync();  // only this CTA's own two halves
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
+    if (last) P.arrived[c0] = 0;  // for the next call
   }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
   // D / 4 threads a row; several rows in flight
   constexpr int kPer = D / 4, kRows = 8, kStep = NT / kPer;
   const int d = threadIdx.x % kPer * 4;
-  const int halves = second ? 2 : 1;
   for (int r0 = threadIdx.x / kPer; r0 < u.rows; r0 += kRows * kStep) {
     float m[kRows], l[kRows];
     float4 o[kRows];
@@ -136,16 +125,14 @@ __device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, c
       l[k] = 0.f;
       o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int part = 0; part < (c1 - c0 + 1) * halves; ++part) {
-      const int c = c0 + part / halves;
+    for (int c = c0; c <= c1; ++c) {
       const float* s = scratch_slot<R, D>(P, c, c == c0 ? 1 : 0);
-      const int row = r0 + (part % halves) * second;
       float mc[kRows], lc[kRows];
       float4 v[kRows];
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         const bool live = r0 + k * kStep < u.rows;
-        const int rk = live ? row + k * kStep : row;
+        const int rk = live ? r0 + k * kStep : r0;
         mc[k] = __ldcg(s + R * D + rk);
         lc[k] = __ldcg(s + R * D + R + rk);
         v[k] = __ldcg(reinterpret_cast<const float4*>(s + rk * D + d));
@@ -169,7 +156,6 @@ __device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, c
       if (d == 0) store_lse(P, u, r, m[k], l[k]);
     }
   }
-  if (second) Sync::sync();  // the CTA may write the same slot for its next unit
 }
 
 template <class T, int D, int MT>
@@ -415,7 +401,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
         }
       }
     }
-    if (!done) join_parts<T, R, D, kStreamThreads, BlockSync>(P, u, span, unit_begin);
+    if (!done) join_parts<T, R, D, kStreamThreads>(P, u, span, unit_begin);
     t += cnt;
     if (t >= span.t1) break;
     __syncthreads();  // the rings and row sums have been read
