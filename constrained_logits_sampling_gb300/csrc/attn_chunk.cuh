@@ -255,7 +255,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         const int jw = split ? w : 0;
         for (int j = jw; j < cnt; j += step) {
           const int kb = (u.tile0 + j0 + j) * kChunkKeys;
-          chunk_wait(&sh.s_full[w], s_phase, &sh.dead);
+          if (lane == 0) {
+            chunk_wait(&sh.s_full[w], s_phase, &sh.dead);
+            // S of the tile's last half is complete
+            if ((warp & 3) == 0 && (split || w == 1)) mbar_arrive(&sh.tile_done[(tile + j) % NS]);
+          }
+          __syncwarp();
           s_phase ^= 1;
           tc_fence_after();
           const uint32_t* ok = sh.key_ok[(tile + j) % (2 * NS)];
@@ -522,16 +527,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         if (!split) {
           qk(0, 0, it);
           qk(1, 1, it);
-          mma_commit(&sh.tile_done[it % NS]);
           if (cnt == 1) mma_commit(&sh.q_empty);
           for (int j = 0; j + 1 < cnt; ++j, ++it) {
-            values_ready(it);
-            keys_ready(it + 1);
+            keys_ready(it + 1);  // handed over after the values of tile it
             pv(0, it, j > 0);
             qk(0, 0, it + 1);
             pv(1, it, j > 0);
             qk(1, 1, it + 1);
-            mma_commit(&sh.tile_done[(it + 1) % NS]);
           }
           if (cnt > 1) mma_commit(&sh.q_empty);
           values_ready(it);
@@ -542,11 +544,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
           ++it;
         } else {
           qk(0, 0, it);
-          mma_commit(&sh.tile_done[it % NS]);
           if (cnt > 1) {
             keys_ready(it + 1);
             qk(1, 0, it + 1);
-            mma_commit(&sh.tile_done[(it + 1) % NS]);
           }
           if (cnt <= 2) mma_commit(&sh.q_empty);
           for (int j = 0; j < cnt; ++j, ++it) {
@@ -556,7 +556,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
             if (j + 2 < cnt) {
               keys_ready(it + 2);
               qk(w, 0, it + 2);
-              mma_commit(&sh.tile_done[(it + 2) % NS]);
               if (j + 3 == cnt) mma_commit(&sh.q_empty);
             } else {
               mma_commit(&sh.o_full[w]);
