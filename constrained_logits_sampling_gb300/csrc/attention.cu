@@ -32,6 +32,47 @@ cudaError_t launch_stream(const AttnParams& P, int sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// The cache as a tensor of (element, slot, head, page), copied in boxes of 64 elements of the
+// slots of a page (of 128 at most).
+bool cache_map(const AttnParams& P, const void* base, CUtensorMap* map) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<Encode>(fn);
+  }();
+  const clsample_attention_args_t& a = P.a;
+  if (!encode || a.num_pages == 0) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+  // the stride of a dimension of one element is never used, but has to be valid
+  auto stride = [](int64_t s, int n) { return n > 1 ? (cuuint64_t)s * 2 : (cuuint64_t)16; };
+  const cuuint64_t strides[3] = {stride(a.slot_stride, a.page_size), stride(a.head_stride, a.Hkv),
+                                 stride(a.page_stride, a.num_pages)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(a.page_size < kChunkKeys ? a.page_size : kChunkKeys), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return encode(map, a.dtype == CLSAMPLE_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int D, bool kTma>
+cudaError_t launch_chunk(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap& v_map, int sms,
+                         cudaStream_t st) {
+  auto* fn = attn_chunk_kernel<T, D, kTma>;
+  const int bytes = ChunkShape<D>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  fn<<<sms, kChunkThreads, bytes, st>>>(P, k_map, v_map);
+  return cudaGetLastError();
+}
+
 template <class T, int D>
 cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
   // no valid sequence has more rows than this; one that breaks the bound has no keys
@@ -40,12 +81,14 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
   P.max_rows = 0x7fffffff;
   if (rows > kStreamRows) {
     P.min_rows = kStreamRows + 1;
-    auto* fn = attn_chunk_kernel<T, D>;
-    const int bytes = ChunkShape<D>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // boxes have to start on the eight rows of the swizzle and fill a tile
+    const int page = P.a.page_size;
+    const bool boxes = page >= 8 && (page % kChunkKeys == 0 || kChunkKeys % page == 0);
+    CUtensorMap k_map{}, v_map{};
+    const cudaError_t e = boxes && cache_map(P, P.a.k_cache, &k_map) && cache_map(P, P.a.v_cache, &v_map)
+                              ? launch_chunk<T, D, true>(P, k_map, v_map, h->sms, st)
+                              : launch_chunk<T, D, false>(P, k_map, v_map, h->sms, st);
     if (e != cudaSuccess) return e;
-    fn<<<h->sms, kChunkThreads, bytes, st>>>(P);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     P.a.row_status = nullptr;  // written
     P.min_rows = 0;
     P.max_rows = kStreamRows + 1;

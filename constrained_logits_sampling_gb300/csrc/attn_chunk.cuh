@@ -2,13 +2,14 @@
 //
 // A unit is 256 packed rows (attn_units.cuh), as two tiles of 128 rows.  One CTA per SM:
 //   warps 0-3, 4-7   softmax of row tile 0 and 1, one row a thread;
-//   warps 8-11       loads: queries, keys and values from their pages, by cp.async into the
-//                    128-byte swizzled layout that the matrix instructions read.  Page
-//                    boundaries may fall anywhere in a tile and slots past the length are
-//                    filled with zeros, which a box copy could do neither of;
-//   warp 12          issues the products;
-//   warp 13          hands what the load warps wrote over to the tensor cores' proxy
-//                    (14 and 15 make the warpgroup whole).
+//   warps 8, 9, 11   loads (below);
+//   warp 10          issues the products.
+// Loads come in two forms.  Where pages are whole boxes of a tile (8, 16, 32, 64 or a
+// multiple of 128 slots) warp 8 copies keys and values by TMA, one box a page and 64
+// elements, an invalid page as zeros; warps 9 and 11 load the queries, and warp 9 clears the
+// value slots that lie outside the unit's keys (they may hold anything, and 0 x NaN is NaN).
+// Other page sizes are copied row by row with cp.async by warps 8 and 9, zeros where there
+// is no key, and warp 11 hands what has landed over to the tensor cores' proxy.
 // S = Q K^T goes to tensor memory (128 columns a tile), the softmax warps read it, write the
 // weights P over it in the input type, and O += P V takes P from there: scores never touch
 // shared memory.  The two tiles alternate: while one is in its softmax, the tensor cores
@@ -19,6 +20,8 @@
 // queries and every other key tile, and their sums are joined like those of two spans.
 #pragma once
 
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "attn_stream.cuh"
@@ -26,15 +29,15 @@
 
 namespace clsample {
 
-constexpr int kChunkThreads = 512;
+constexpr int kChunkThreads = 384;
 constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 128;
 constexpr float kRescaleAt = 8.f;  // log2
 
-// Registers a thread by warpgroup: 2 x softmax, loads, products.  They add up to what the
-// block is launched with (4 x 128).
-constexpr int kSoftmaxRegs = 176, kLoadRegs = 80, kMmaRegs = 80;
-static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs == 4 * (65536 / kChunkThreads), "the launch's registers");
+// Registers a thread: the two softmax warpgroups, and the one of loads and products.  They
+// add up to what the block is launched with (3 x 168).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168 && 168 * kChunkThreads <= 65536, "the launch's registers");
 
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -84,8 +87,18 @@ struct ChunkShared {
   unsigned long long q_full, q_empty, end, s_full[2], p_half[2], p_full[2], o_full[2];
   uint32_t tmem;
   volatile int dead;           // a bounded wait ran out: every other wait ends too
-  uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
+  alignas(16) uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
 };
+
+// One box of a tensor map of rank 4 to shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int x, int slot, int head, int page,
+                                          unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
+      : "memory");
+}
 
 // Bounded wait for a phase: about two seconds, then the CTA gives up.
 __device__ __forceinline__ bool chunk_wait(unsigned long long* bar, uint32_t parity, volatile int* dead) {
@@ -181,8 +194,10 @@ __device__ __forceinline__ void join_rows(const AttnParams& P, const Unit& u, co
   if (split) SoftmaxSync::sync();  // the CTA may write the same slot for its next unit
 }
 
-template <class T, int D>
-__global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __grid_constant__ AttnParams P) {
+template <class T, int D, bool kTma>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    attn_chunk_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap k_map,
+                      const __grid_constant__ CUtensorMap v_map) {
   using Shape = ChunkShape<D>;
   constexpr int NS = Shape::kKeySlots, NV = Shape::kValueSlots, kTile = Shape::kTile, KC = D / 8;
   constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 elements
@@ -202,15 +217,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.k_landed[i], 128 + 4);  // every load thread's copies, and four words of key_ok
+      mbar_init(&sh.k_landed[i], 64 + 2);  // every load thread's copies, and each warp's words of key_ok
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.tile_done[i], 1);
     }
     for (int i = 0; i < NV; ++i) {
-      mbar_init(&sh.v_landed[i], 128);
+      mbar_init(&sh.v_landed[i], kTma ? 1 : 64);
       mbar_init(&sh.v_full[i], 1);
     }
-    mbar_init(&sh.q_full, 128);
+    mbar_init(&sh.q_full, 64);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.end, 1);
     for (int w = 0; w < 2; ++w) {
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
     sh.dead = 0;
     fence_mbar_init();
   }
-  if (warp == 12) tmem_alloc512(&sh.tmem);
+  if (warp == 10) tmem_alloc512(&sh.tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -264,22 +279,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
           s_phase ^= 1;
           tc_fence_after();
           const uint32_t* ok = sh.key_ok[(tile + j) % (2 * NS)];
-          const uint32_t ok0 = ok[0], ok1 = ok[1], ok2 = ok[2], ok3 = ok[3];
-          const bool whole = (ok0 & ok1 & ok2 & ok3) == ~0u && kb + 127 <= pos_first &&
+          const uint4 bits = *reinterpret_cast<const uint4*>(ok);
+          const bool whole = (bits.x & bits.y & bits.z & bits.w) == ~0u && kb + 127 <= pos_first &&
                              (a.window <= 0 || kb > pos_last - a.window);
           uint32_t x[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + c * 32), s_tmem + c * 32);
-          tmem_wait_ld();
+          tmem_ld128(x, s_tmem);
           if (!whole) {
             const int hi = pos - kb;  // columns lo .. hi are seen
             const int lo = a.window > 0 ? hi - a.window + 1 : 0;
-            const uint32_t shown[4] = {ok0 & column_bits(lo, hi), ok1 & column_bits(lo - 32, hi - 32),
-                                       ok2 & column_bits(lo - 64, hi - 64), ok3 & column_bits(lo - 96, hi - 96)};
+            const uint32_t shown[4] = {bits.x & column_bits(lo, hi), bits.y & column_bits(lo - 32, hi - 32),
+                                       bits.z & column_bits(lo - 64, hi - 64), bits.w & column_bits(lo - 96, hi - 96)};
 #pragma unroll
             for (int c = 0; c < 128; ++c)
               if (!(shown[c >> 5] & (1u << (c & 31)))) x[c] = 0xff800000u;
           }
+          // weights of columns c0 .. c0 + 63 against the reference maximum, and their sums
+          const uint64_t scale2 = pair_of(P.scale_log2, P.scale_log2);
+          uint32_t p[32];
+          uint64_t sums[2];
+          auto weights = [&](int c0) {
+            const float base = m == neg_inf ? 0.f : -m;
+            const uint64_t base2 = pair_of(base, base);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int i = c0 + 2 * e;
+              const float2 y = split_pair(fma2(pair_of(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, base2));
+              const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
+              sums[e & 1] = add2(sums[e & 1], pair_of(p0, p1));
+              p[e] = Pair<T>::narrow(p0, p1);
+            }
+          };
+          auto hand_over = [&](int c0, unsigned long long* bar) {
+            tmem_st32(s_tmem + c0 / 2, p);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+          };
+          // the first half is computed before the tile's maximum is known, which hardly ever
+          // calls for another reference, so that the two overlap
+          sums[0] = sums[1] = 0;
+          weights(0);
           float tops[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) tops[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
@@ -295,39 +335,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
             if (grow) m = top;
             l *= keep;
             if (j > jw) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t y[16];
                 tmem_ld16(y, o_tmem + c * 16);
-                tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
                 tmem_st16(o_tmem + c * 16, y);
               }
             }
+            sums[0] = sums[1] = 0;
+            weights(0);
           }
-          const float base = m == neg_inf ? 0.f : -m;
-          const uint64_t scale2 = pair_of(P.scale_log2, P.scale_log2), base2 = pair_of(base, base);
-          uint64_t sums[2] = {0, 0};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int i = c * 32 + 2 * e;
-              const float2 y = split_pair(fma2(pair_of(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, base2));
-              const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
-              sums[e & 1] = add2(sums[e & 1], pair_of(p0, p1));
-              p[e] = Pair<T>::narrow(p0, p1);
-            }
-            tmem_st16(s_tmem + c * 16, p);
-            if (c & 1) {  // the product starts on the first 64 keys
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(c == 1 ? &sh.p_half[w] : &sh.p_full[w]);
-            }
-          }
+          hand_over(0, &sh.p_half[w]);  // the product starts on the first 64 keys
+          weights(64);
+          hand_over(64, &sh.p_full[w]);
           const float2 s0 = split_pair(add2(sums[0], sums[1]));
           l += s0.x + s0.y;
         }
@@ -340,7 +362,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         for (int c = 0; c < D / 32; ++c) {
           uint32_t x[32];
           tmem_ld32(x, o_tmem + c * 32);
-          tmem_wait_ld();
           if (live) {
             if (done) {
               T* dst = (T*)a.out + (int64_t)(u.q0 + (u.row0 + r) / P.g) * a.o_stride_t +
@@ -387,90 +408,217 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
       unit_begin = t;
       next_unit<kChunkRows, kChunkKeys>(P, &u);
     }
-  } else if (warp < 12) {
+  } else if (warp != 10) {
     // ------------------------------------------------------------------ loads
-    regs_down<kLoadRegs>();
-    const int lw = warp - 8;
-    uint32_t it = 0, seg = 0;
-    while (true) {
-      const int j0 = (int)(t - unit_begin);
-      const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
-      chunk_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
-#pragma unroll 1
-      for (int w = 0; w < 2; ++w) {
-        const int mine = u.row0 + w * 128 + lw * 32 + lane;  // this lane's row, which it hands to the others
-        const bool live = mine < u.row0 + u.rows;
-        const int64_t off = live ? (int64_t)(u.q0 + mine / P.g) * a.q_stride_t +
-                                       (int64_t)(u.h * P.g + mine % P.g) * a.q_stride_h
-                                 : 0;
-        const unsigned mask = __ballot_sync(~0u, live);
+    regs_down<kOtherRegs>();
+    const int lw = warp == 8 ? 0 : warp == 9 ? (kTma ? 0 : 1) : 1;  // of the two warps that copy rows
+    const int tiles = (int)(span.t1 - span.t0);
+    // 32 rows to rows r0.. of a tile; lane i has the place of row i, bit i of `live` tells
+    // whether it is read or zero
+    auto copy_rows = [&](const T* src, int64_t off, unsigned live, uint32_t dst, int r0) {
 #pragma unroll
-        for (int x = 0; x < KC; ++x) {
-          const int i = x * 32 + lane, row = i / KC, ch = i % KC, r = lw * 32 + row;
-          const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
-          cp_async16(q_smem + w * kTile + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                     (const T*)a.q + o, (mask >> row) & 1);
-        }
+      for (int x = 0; x < KC; ++x) {
+        const int i = x * 32 + lane, row = i / KC, ch = i % KC, r = r0 + row;
+        const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
+        cp_async16(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + o, (live >> row) & 1);
+      }
+    };
+    auto copy_queries = [&](uint32_t seg) {
+      chunk_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
+      __syncwarp();
+#pragma unroll 1
+      for (int w = 0; w < 4; ++w) {
+        const int first = (w * 2 + lw) * 32;  // of 32 rows, one a lane, whose place it hands to the others
+        const int mine = first + lane, row = u.row0 + mine;
+        const bool live = mine < u.rows;
+        const int64_t off = live ? (int64_t)(u.q0 + row / P.g) * a.q_stride_t +
+                                       (int64_t)(u.h * P.g + row % P.g) * a.q_stride_h
+                                 : 0;
+        copy_rows((const T*)a.q, off, __ballot_sync(~0u, live), q_smem + (first >> 7) * kTile, first & 127);
       }
       cp_async_arrive(smem_addr(&sh.q_full));
-      const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
-      const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
-      const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
-      auto page_of = [&](int j) {
-        const int key = (u.tile0 + j0 + j) * kChunkKeys + lw * 32 + lane;
-        if (j >= cnt || key < u.key_lo || key >= u.key_hi) return -1;
-        const int id = __ldg(table + (P.page_shift >= 0 ? key >> P.page_shift : key / a.page_size));
-        return id < a.num_pages ? id : -1;
-      };
-      int page = page_of(0);
-      for (int j = 0; j < cnt; ++j, ++it) {
-        const int next = page_of(j + 1);
-        const int key = (u.tile0 + j0 + j) * kChunkKeys + lw * 32 + lane;
-        const int slot = P.page_shift >= 0 ? key & ((1 << P.page_shift) - 1) : key % a.page_size;
-        const bool ok = page >= 0;
-        const int64_t off = ok ? (int64_t)page * a.page_stride + (int64_t)slot * a.slot_stride : 0;
-        const unsigned mask = __ballot_sync(~0u, ok);
-        // keys outside the unit's range are hidden by the rows' limits: only a bad page counts
-        const unsigned shown = __ballot_sync(~0u, ok || key < u.key_lo || key >= u.key_hi);
-        // the slot of the keys is free when S of the tile that had it is complete, and the slot
-        // of the values when O is, which a later tile's completion covers: the next one's if
-        // both halves take each tile, the one after it otherwise (and across units, where
-        // either may have been the case)
-        const int64_t k_gate = (int64_t)it - NS, v_gate = (int64_t)it - NV + (u.rows <= 128 || j < NV ? 2 : 1);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const int64_t gate = kv ? v_gate : k_gate;
-          // (the keys' gate has been passed: by now its barrier may be a phase further)
-          if (gate >= 0 && (kv == 0 || v_gate > k_gate)) chunk_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
+    };
+    // The slot of a tile's keys is free when S of the tile that had it is complete, and the
+    // slot of its values when O is, which a later tile's completion covers: the next one's if
+    // both halves take each tile, the one after it otherwise (and across units, where either
+    // may have been the case).  The values' gate is only waited for where it is the later
+    // one: the keys' has been passed, and by now its barrier may be a phase further.
+    auto key_slot = [&](uint32_t it) {
+      const int64_t gate = (int64_t)it - NS;
+      if (gate >= 0) chunk_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
+      __syncwarp();
+    };
+    auto value_slot = [&](uint32_t it, int j) {
+      const int64_t gate = (int64_t)it - NV + (u.rows <= 128 || j < NV ? 2 : 1);
+      if (gate >= 0 && gate > (int64_t)it - NS) chunk_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
+      __syncwarp();
+    };
+    // a tile with values outside the unit's keys
+    auto edge = [&](int tile) { return tile * kChunkKeys < u.key_lo || tile * kChunkKeys + kChunkKeys > u.key_hi; };
+
+    if (kTma && warp == 8) {
+      // lane i has the i-th page (or 128 slots of one) of a tile
+      const int box = min(a.page_size, kChunkKeys), boxes = kChunkKeys / box;
+      uint32_t it = 0;
+      while (true) {
+        const int j0 = (int)(t - unit_begin);
+        const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+        const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
+        auto page_of = [&](int j) {  // num_pages, which is out of bounds: zeros
+          const int key = (u.tile0 + j0 + j) * kChunkKeys + lane * box;
+          if (j >= cnt || lane >= boxes || key + box <= u.key_lo || key >= u.key_hi) return a.num_pages;
+          const int id = __ldg(table + (P.page_shift >= 0 ? key >> P.page_shift : key / a.page_size));
+          return id >= 0 && id < a.num_pages ? id : -1;
+        };
+        int page = page_of(0);
+        for (int j = 0; j < cnt; ++j, ++it) {
+          const int tile = u.tile0 + j0 + j;
+          const int key = tile * kChunkKeys + lane * box;
+          const int slot = a.page_size > kChunkKeys ? key % a.page_size : 0;
+          const unsigned bad = __ballot_sync(~0u, page < 0);
+          const int from = page < 0 ? a.num_pages : page;
+          page = page_of(j + 1);
+          key_slot(it);
+          if (lane < 4) {
+            uint32_t word = ~0u;
+            if (bad)
+              for (int e = 0; e < 32; ++e)
+                if ((bad >> ((lane * 32 + e) / box)) & 1) word &= ~(1u << e);
+            sh.key_ok[it % (2 * NS)][lane] = word;
+          }
           __syncwarp();
-          unsigned long long* landed = kv ? &sh.v_landed[it % NV] : &sh.k_landed[it % NS];
-          if (kv == 0 && lane == 0) {
-            sh.key_ok[it % (2 * NS)][lw] = shown;
-            mbar_arrive(landed);
-          }
-          const T* src = kv ? vc : kc;
-          const uint32_t dst = kv ? v_smem + it % NV * kTile : k_smem + it % NS * kTile;
-#pragma unroll
-          for (int x = 0; x < KC; ++x) {
-            const int i = x * 32 + lane, row = i / KC, ch = i % KC, r = lw * 32 + row;
-            const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
-            cp_async16(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + o, (mask >> row) & 1);
-          }
-          cp_async_arrive(smem_addr(landed));
+          unsigned long long* full = &sh.k_full[it % NS];
+          if (lane == 0) mbar_arrive_expect_tx(full, kTile);
+          __syncwarp();
+          if (lane < boxes && !sh.dead)
+            for (int x = 0; x < D / 64; ++x)
+              tma_load4(k_smem + it % NS * kTile + x * kHalf + lane * box * 128, &k_map, x * 64, slot, u.h, from, full);
+          value_slot(it, j);
+          full = edge(tile) ? &sh.v_landed[it % NV] : &sh.v_full[it % NV];
+          if (lane == 0) mbar_arrive_expect_tx(full, kTile);
+          __syncwarp();
+          if (lane < boxes && !sh.dead)
+            for (int x = 0; x < D / 64; ++x)
+              tma_load4(v_smem + it % NV * kTile + x * kHalf + lane * box * 128, &v_map, x * 64, slot, u.h, from, full);
         }
-        page = next;
+        t += cnt;
+        if (t >= span.t1) break;
+        unit_begin = t;
+        next_unit<kChunkRows, kChunkKeys>(P, &u);
       }
-      ++seg;
-      t += cnt;
-      if (t >= span.t1) break;
-      unit_begin = t;
-      next_unit<kChunkRows, kChunkKeys>(P, &u);
+      // copies still in flight when a wait gave up land before the CTA ends
+      if (sh.dead)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    } else if (kTma) {
+      uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
+      while (true) {
+        const int j0 = (int)(t - unit_begin);
+        const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+        copy_queries(seg);
+        if (warp == 9) {
+          for (int j = 0; j < cnt; ++j) {
+            const int tile = u.tile0 + j0 + j;
+            if (!edge(tile)) continue;
+            const uint32_t st = (it + j) % NV;
+            uint32_t parity = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+              if (i == st) parity = edges[i]++ & 1;
+            chunk_wait(&sh.v_landed[st], parity, &sh.dead);
+            __syncwarp();
+            const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
+            for (int i = lane; i < 128 * KC; i += 32) {  // a row's pieces may lie anywhere in it: all are cleared
+              const int row = i / KC, ch = i % KC;
+              if (row < lo || row >= hi)
+                *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.v_full[st]);
+          }
+        }
+        it += cnt;
+        ++seg;
+        t += cnt;
+        if (t >= span.t1) break;
+        unit_begin = t;
+        next_unit<kChunkRows, kChunkKeys>(P, &u);
+      }
+      cp_async_wait_all();
+    } else if (warp < 10) {
+      uint32_t it = 0, seg = 0;
+      while (true) {
+        const int j0 = (int)(t - unit_begin);
+        const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+        copy_queries(seg);
+        const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
+        const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
+        const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
+        // warp lw has keys 64 lw .. 64 lw + 63 of a tile, two a lane
+        auto page_of = [&](int j, int half) {
+          const int key = (u.tile0 + j0 + j) * kChunkKeys + lw * 64 + half * 32 + lane;
+          if (j >= cnt || key < u.key_lo || key >= u.key_hi) return -1;
+          const int id = __ldg(table + (P.page_shift >= 0 ? key >> P.page_shift : key / a.page_size));
+          return id < a.num_pages ? id : -1;
+        };
+        int page[2] = {page_of(0, 0), page_of(0, 1)};
+        for (int j = 0; j < cnt; ++j, ++it) {
+          int64_t off[2];
+          unsigned live[2], shown[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int key = (u.tile0 + j0 + j) * kChunkKeys + lw * 64 + half * 32 + lane;
+            const int slot = P.page_shift >= 0 ? key & ((1 << P.page_shift) - 1) : key % a.page_size;
+            const bool ok = page[half] >= 0;
+            off[half] = ok ? (int64_t)page[half] * a.page_stride + (int64_t)slot * a.slot_stride : 0;
+            live[half] = __ballot_sync(~0u, ok);
+            // keys outside the unit's range are hidden by the rows' limits: only a bad page counts
+            shown[half] = __ballot_sync(~0u, ok || key < u.key_lo || key >= u.key_hi);
+            page[half] = page_of(j + 1, half);
+          }
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            if (kv)
+              value_slot(it, j);
+            else
+              key_slot(it);
+            unsigned long long* landed = kv ? &sh.v_landed[it % NV] : &sh.k_landed[it % NS];
+            if (kv == 0 && lane == 0) {
+              sh.key_ok[it % (2 * NS)][lw * 2] = shown[0];
+              sh.key_ok[it % (2 * NS)][lw * 2 + 1] = shown[1];
+              mbar_arrive(landed);
+            }
+            const T* src = kv ? vc : kc;
+            const uint32_t dst = kv ? v_smem + it % NV * kTile : k_smem + it % NS * kTile;
+            copy_rows(src, off[0], live[0], dst, lw * 64);
+            copy_rows(src, off[1], live[1], dst, lw * 64 + 32);
+            cp_async_arrive(smem_addr(landed));
+          }
+        }
+        ++seg;
+        t += cnt;
+        if (t >= span.t1) break;
+        unit_begin = t;
+        next_unit<kChunkRows, kChunkKeys>(P, &u);
+      }
+      cp_async_wait_all();
+    } else if (lane == 0) {
+      // The copies are ordinary writes, the products read by the async proxy: the fence between
+      // them costs a hundred cycles or so, which the issuing warp has not got.
+      for (int i = 0; i < tiles; ++i) {
+        chunk_wait(&sh.k_landed[i % NS], (i / NS) & 1, &sh.dead);
+        fence_async_proxy();
+        mbar_arrive(&sh.k_full[i % NS]);
+        chunk_wait(&sh.v_landed[i % NV], (i / NV) & 1, &sh.dead);
+        fence_async_proxy();
+        mbar_arrive(&sh.v_full[i % NV]);
+      }
     }
-    cp_async_wait_all();
   } else {
     // ------------------------------------------------------------------ products
-    regs_down<kMmaRegs>();
-    if (warp == 12) {
+    regs_down<kOtherRegs>();
+    {
       // Everything here is uniform, and made known as such (uni): the operands of a product
       // have to be in uniform registers for the issue to keep up with the tensor cores.
       auto uni = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };
@@ -529,7 +677,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
           qk(1, 1, it);
           if (cnt == 1) mma_commit(&sh.q_empty);
           for (int j = 0; j + 1 < cnt; ++j, ++it) {
-            keys_ready(it + 1);  // handed over after the values of tile it
+            if (kTma) values_ready(it);
+            keys_ready(it + 1);  // without TMA handed over after the values of tile it
             pv(0, it, j > 0);
             qk(0, 0, it + 1);
             pv(1, it, j > 0);
@@ -573,24 +722,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) attn_chunk_kernel(const __gr
         mma_commit(&sh.end);
         for (int i = 0; i < 1 << 16 && !mbar_try_wait(&sh.end, 0); ++i) __nanosleep(100);
       }
-    } else if (warp == 13 && lane == 0) {
-      // The copies are ordinary writes, the products read by the async proxy: the fence between
-      // them costs a hundred cycles or so, which the issuing warp has not got.
-      const int tiles = (int)(span.t1 - span.t0);
-      for (int i = 0; i < tiles; ++i) {
-        chunk_wait(&sh.k_landed[i % NS], (i / NS) & 1, &sh.dead);
-        fence_async_proxy();
-        mbar_arrive(&sh.k_full[i % NS]);
-        chunk_wait(&sh.v_landed[i % NV], (i / NV) & 1, &sh.dead);
-        fence_async_proxy();
-        mbar_arrive(&sh.v_full[i % NV]);
-      }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_free512(tmem);
+  if (warp == 10) tmem_free512(tmem);
 }
 
 }  // namespace clsample
