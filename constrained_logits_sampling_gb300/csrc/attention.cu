@@ -111,8 +111,8 @@ int clsample_attention_create(clsample_attention_t** out) {
   auto* h = new (std::nothrow) clsample_attention{dev, sms, nullptr, nullptr};
   if (!h) return CLSAMPLE_ERR_CUDA;
   if (cudaMalloc(&h->partial, (size_t)sms * kScratch) != cudaSuccess ||
-      cudaMalloc(&h->arrived, (size_t)sms * kStreamCtas * sizeof(int)) != cudaSuccess ||
-      cudaMemset(h->arrived, 0, (size_t)sms * kStreamCtas * sizeof(int)) != cudaSuccess ||
+      cudaMalloc(&h->arrived, (size_t)sms * kStreamCtas * 2 * sizeof(int)) != cudaSuccess ||
+      cudaMemset(h->arrived, 0, (size_t)sms * kStreamCtas * 2 * sizeof(int)) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
     clsample_attention_destroy(h);
     cudaGetLastError();

@@ -17,7 +17,7 @@
 // it is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // time (P and its sum are then up to 2^8, which both types hold), so hardly ever.
 // A unit of at most 128 rows has one row tile: both halves of the CTA then take the same
-// queries and every other key tile, and their sums are joined like those of two spans.
+// queries and every other key tile, and their sums are joined at the end.
 #pragma once
 
 #include <cuda.h>
@@ -36,7 +36,7 @@ constexpr float kRescaleAt = 8.f;  // log2
 
 // Registers a thread: the two softmax warpgroups, and the one of loads and products.  They
 // add up to what the block is launched with (3 x 168).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168 && 168 * kChunkThreads <= 65536, "the launch's registers");
 
 template <int N>
@@ -86,6 +86,10 @@ struct ChunkShared {
   unsigned long long k_landed[NS], v_landed[NV], k_full[NS], v_full[NV], tile_done[NS];
   unsigned long long q_full, q_empty, end, s_full[2], p_half[2], p_full[2], o_full[2];
   uint32_t tmem;
+  // where the softmax warps are: they have no registers to spare for it
+  Unit unit;
+  Span span;
+  int64_t unit_begin, at;
   volatile int dead;           // a bounded wait ran out: every other wait ends too
   alignas(16) uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
 };
@@ -122,76 +126,73 @@ struct SoftmaxSync {  // the 256 softmax threads
   static __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 };
 
-// Joins the parts of a unit, as join_parts does, by the 256 softmax threads.  A slot holds
-// four sums of each row side by side, then the next four of each row, so that threads with a
-// row each read and write whole lines.  With `split` a CTA's part is two, 128 rows apart, and
-// two threads share a row.
+// join() of join_parts, by the 256 softmax threads.  A slot holds four sums of each row side by
+// side, then the next four of each row, so that threads with a row each read and write whole
+// lines.  Up to 128 rows have two threads each.
 template <class T, int D>
-__device__ __forceinline__ void join_rows(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin,
-                                          bool split) {
-  __shared__ int last;
-  const int tid = threadIdx.x;
-  const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
-  if (c0 < c1) {
-    __threadfence();
-    SoftmaxSync::sync();
-    if (tid == 0) {
-      last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
-      if (last) P.arrived[c0] = 0;  // for the next call
-    }
-    SoftmaxSync::sync();
-    if (!last) return;
-    __threadfence();
-  } else {
-    SoftmaxSync::sync();  // only this CTA's own two halves
-  }
-  const int halves = split ? 2 : 1, parts = (c1 - c0 + 1) * halves;
-  const int r = split ? tid & 127 : tid;
-  const int d0 = split ? (tid >> 7) * (D / 2) : 0, d1 = split ? d0 + D / 2 : D;
+__device__ __forceinline__ void join_rows(const AttnParams& P, const Unit& u, int c0, int first, int step, int count,
+                                          bool final) {
+  const bool two = u.rows <= 128;
+  const int r = two ? threadIdx.x & 127 : threadIdx.x;
+  const int d0 = two ? (threadIdx.x >> 7) * (D / 2) : 0, d1 = two ? d0 + D / 2 : D;
   auto slot_of = [&](int part) {
-    const int c = c0 + part / halves;
+    const int c = first + part * step;
     return scratch_slot<kChunkRows, D>(P, c, c == c0 ? 1 : 0);
   };
+  float m = __int_as_float(0xff800000), l = 0.f;
   if (r < u.rows) {
-    float m = __int_as_float(0xff800000), l = 0.f;
-    for (int part = 0; part < parts; ++part) {
-      const float* s = slot_of(part) + kChunkRows * D + r + (part % halves) * 128;
+#pragma unroll 4
+    for (int part = 0; part < count; ++part) {
+      const float* s = slot_of(part) + kChunkRows * D + r;
       const float mc = __ldcg(s), lc = __ldcg(s + kChunkRows);
       const float mn = fmaxf(m, mc);
       l = l * (m == mn ? 1.f : exp2_fast(m - mn)) + lc * (mc == mn ? 1.f : exp2_fast(mc - mn));
       m = mn;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float scale = final ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
     const int row = u.row0 + r;
     T* dst = (T*)P.a.out + (int64_t)(u.q0 + row / P.g) * P.a.o_stride_t +
              (int64_t)(u.h * P.g + row % P.g) * P.a.o_stride_h;
-    if (d0 == 0) store_lse(P, u, r, m, l);
-    for (int d = d0; d < d1; d += 32) {
-      float4 o[8];
+    if (d0 == 0 && final) store_lse(P, u, r, m, l);
+    float* to = slot_of(0);
+    for (int d = d0; d < d1; d += 16) {
+      float4 o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int part = 0; part < parts; ++part) {
+      for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int part = 0; part < count; ++part) {
         const float* s = slot_of(part);
-        const int at = r + (part % halves) * 128;
-        const float mc = __ldcg(s + kChunkRows * D + at);
-        float4 v[8];
+        const float mc = __ldcg(s + kChunkRows * D + r);
+        float4 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = __ldcg(reinterpret_cast<const float4*>(s + (d + 4 * i) * kChunkRows + at * 4));
-        const float f = (mc == m ? 1.f : exp2_fast(mc - m)) * inv;
+        for (int i = 0; i < 4; ++i)
+          v[i] = __ldcg(reinterpret_cast<const float4*>(s + (d + 4 * i) * kChunkRows + r * 4));
+        const float f = (mc == m ? 1.f : exp2_fast(mc - m)) * scale;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
           o[i] = make_float4(fmaf(v[i].x, f, o[i].x), fmaf(v[i].y, f, o[i].y), fmaf(v[i].z, f, o[i].z),
                              fmaf(v[i].w, f, o[i].w));
       }
+      if (final) {
 #pragma unroll
-      for (int i = 0; i < 8; i += 2)
-        *reinterpret_cast<uint4*>(dst + d + 4 * i) =
-            make_uint4(Pair<T>::narrow(o[i].x, o[i].y), Pair<T>::narrow(o[i].z, o[i].w),
-                       Pair<T>::narrow(o[i + 1].x, o[i + 1].y), Pair<T>::narrow(o[i + 1].z, o[i + 1].w));
+        for (int i = 0; i < 4; i += 2)
+          *reinterpret_cast<uint4*>(dst + d + 4 * i) =
+              make_uint4(Pair<T>::narrow(o[i].x, o[i].y), Pair<T>::narrow(o[i].z, o[i].w),
+                         Pair<T>::narrow(o[i + 1].x, o[i + 1].y), Pair<T>::narrow(o[i + 1].z, o[i + 1].w));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __stcg(reinterpret_cast<float4*>(to + (d + 4 * i) * kChunkRows + r * 4), o[i]);
+      }
     }
   }
-  if (split) SoftmaxSync::sync();  // the CTA may write the same slot for its next unit
+  if (!final) {
+    SoftmaxSync::sync();  // maxima and sums have been read by all before they are replaced
+    if (r < u.rows && d0 == 0) {
+      float* s = slot_of(0) + kChunkRows * D + r;
+      __stcg(s, m);
+      __stcg(s + kChunkRows, l);
+    }
+  }
 }
 
 template <class T, int D, bool kTma>
@@ -235,6 +236,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.o_full[w], 1);
     }
     sh.dead = 0;
+    sh.unit = u;
+    sh.span = span;
+    sh.unit_begin = unit_begin;
+    sh.at = span.t0;
     fence_mbar_init();
   }
   if (warp == 10) tmem_alloc512(&sh.tmem);
@@ -252,27 +257,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t s_tmem = tmem + lane_base + w * 128, o_tmem = tmem + lane_base + 256 + w * 128;
     uint32_t s_phase = 0, o_phase = 0, tile = 0;
     while (true) {
-      const int j0 = (int)(t - unit_begin);
-      const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+      const Unit& u = sh.unit;
+      const int j0 = (int)(sh.at - sh.unit_begin);
+      const int cnt = (int)min((int64_t)(u.tiles - j0), sh.span.t1 - sh.at);
       const bool split = u.rows <= 128;  // this half has the key tiles w, w + 2, ..
-      const bool done = cnt == u.tiles && !split;
-      const int step = split ? 2 : 1;
-      const int place = w * 128 + (warp & 3) * 32 + lane;  // of this row's sums in the scratch
-      const int r = split ? place & 127 : place;
-      if (!split || cnt > w) {
-        const bool live = r < u.rows;
-        const int first_pos = u.len - u.n;
+      const int step = split ? 2 : 1, jw = split ? w : 0;
+      const int place = w * 128 + (warp & 3) * 32 + lane;  // of this thread's sums in the scratch
+      const int r = split ? place & 127 : place;            // its row
+      const bool live = r < u.rows;
+      float m = neg_inf, l = 0.f;  // reference maximum (log2 units) and weights' sum
+      if (cnt > jw) {
+        const int first_pos = u.len - u.n, kb0 = (u.tile0 + j0) * kChunkKeys;
         const int pos = live ? first_pos + (u.row0 + r) / P.g : -1;
         const int half0 = split ? 0 : w * 128;
         const int pos_first = first_pos + (u.row0 + half0) / P.g;
         const int pos_last = first_pos + (u.row0 + min(u.rows, half0 + 128) - 1) / P.g;
-        float m = neg_inf, l = 0.f;  // reference maximum (log2 units) and weights' sum
-        const int jw = split ? w : 0;
         for (int j = jw; j < cnt; j += step) {
-          const int kb = (u.tile0 + j0 + j) * kChunkKeys;
+          const int kb = kb0 + j * kChunkKeys;
+          chunk_wait(&sh.s_full[w], s_phase, &sh.dead);
           if (lane == 0) {
-            chunk_wait(&sh.s_full[w], s_phase, &sh.dead);
-            // S of the tile's last half is complete
             if ((warp & 3) == 0 && (split || w == 1)) mbar_arrive(&sh.tile_done[(tile + j) % NS]);
           }
           __syncwarp();
@@ -356,57 +359,104 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         chunk_wait(&sh.o_full[w], o_phase, &sh.dead);
         o_phase ^= 1;
         tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
+      }
+      float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
+      float mine = 1.f, others = 0.f;  // weights of this half's sums and of the other's
+      if (split) {
+        // the second half's sums go through the scratch to the first, whose rows they belong to
+        if (w == 1 && cnt > 1) {
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t x[16];
+            __syncwarp();
+            tmem_ld16(x, o_tmem + c * 16);
+            if (live) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          tmem_ld32(x, o_tmem + c * 32);
-          if (live) {
-            if (done) {
-              T* dst = (T*)a.out + (int64_t)(u.q0 + (u.row0 + r) / P.g) * a.o_stride_t +
-                       (int64_t)(u.h * P.g + (u.row0 + r) % P.g) * a.o_stride_h + c * 32;
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  y[i] = l == 0.f ? 0u
-                                  : Pair<T>::narrow(__uint_as_float(x[e + 2 * i]) * inv,
-                                                    __uint_as_float(x[e + 2 * i + 1]) * inv);
-                *reinterpret_cast<uint4*>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                __stcg(reinterpret_cast<uint4*>(slot + ((c * 32 + e) * kChunkRows + place * 4)),
+              for (int e = 0; e < 16; e += 4)
+                __stcg(reinterpret_cast<uint4*>(slot + ((c * 16 + e) * kChunkRows + place * 4)),
                        make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
             }
           }
-        }
-        tc_fence_before();  // O has been read: the next unit's products may overwrite it
-        if (live) {
-          if (done) {
-            store_lse(P, u, r, m, l);
-          } else {
+          if (live) {
             __stcg(slot + kChunkRows * D + place, m);
             __stcg(slot + kChunkRows * D + kChunkRows + place, l);
           }
         }
-      } else if (r < u.rows) {  // no key tile for this half
-        float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
-        for (int d = 0; d < D; d += 4)
-          __stcg(reinterpret_cast<float4*>(slot + (d * kChunkRows + place * 4)), make_float4(0.f, 0.f, 0.f, 0.f));
-        __stcg(slot + kChunkRows * D + place, neg_inf);
-        __stcg(slot + kChunkRows * D + kChunkRows + place, 0.f);
+        SoftmaxSync::sync();
+        if (w == 0 && live && cnt > 1) {
+          const float mo = __ldcg(slot + kChunkRows * D + place + 128);
+          const float lo = __ldcg(slot + kChunkRows * D + kChunkRows + place + 128);
+          const float mn = fmaxf(m, mo);
+          mine = m == mn ? 1.f : exp2_fast(m - mn);
+          others = mo == mn ? 1.f : exp2_fast(mo - mn);
+          l = l * mine + lo * others;
+          m = mn;
+        }
       }
-      if (!done) join_rows<T, D>(P, u, span, unit_begin, split);
+      const bool done = cnt == u.tiles;
+      if (w == 0 || !split) {
+        const float inv = !done ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const int row = u.row0 + r;
+        T* dst = (T*)a.out + (int64_t)(u.q0 + row / P.g) * a.o_stride_t +
+                 (int64_t)(u.h * P.g + row % P.g) * a.o_stride_h;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t x[16];
+          __syncwarp();
+          tmem_ld16(x, o_tmem + c * 16);
+          if (live) {
+            if (split && cnt > 1) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 v =
+                    __ldcg(reinterpret_cast<const float4*>(slot + ((c * 16 + e) * kChunkRows + (place + 128) * 4)));
+                x[e] = __float_as_uint(__uint_as_float(x[e]) * mine + v.x * others);
+                x[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * mine + v.y * others);
+                x[e + 2] = __float_as_uint(__uint_as_float(x[e + 2]) * mine + v.z * others);
+                x[e + 3] = __float_as_uint(__uint_as_float(x[e + 3]) * mine + v.w * others);
+              }
+            }
+            if (done) {
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                y[e] = l == 0.f ? 0u
+                                : Pair<T>::narrow(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(dst + c * 16 + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                __stcg(reinterpret_cast<uint4*>(slot + ((c * 16 + e) * kChunkRows + place * 4)),
+                       make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
+            }
+          }
+        }
+        if (live && done) store_lse(P, u, r, m, l);
+        if (live && !done) {
+          __stcg(slot + kChunkRows * D + place, m);
+          __stcg(slot + kChunkRows * D + kChunkRows + place, l);
+        }
+      }
+      tc_fence_before();  // O has been read: the next unit's products may overwrite it
+      if (!done) {
+        const int c0 = cta_of_tile(sh.span, sh.unit_begin);
+        const int c1 = cta_of_tile(sh.span, sh.unit_begin + u.tiles - 1);
+        join_parts<SoftmaxSync>(P, c0, c1, [&](int first, int step, int count, bool final) {
+          join_rows<T, D>(P, u, c0, first, step, count, final);
+        });
+      }
       if (sh.dead && tid == 0 && a.row_status) atomicMax(a.row_status + u.b, CLSAMPLE_ROW_OVERFLOW);
       tile += cnt;
-      t += cnt;
-      if (t >= span.t1) break;
-      unit_begin = t;
-      next_unit<kChunkRows, kChunkKeys>(P, &u);
+      // (of two halves, the first has read here what the second may write again)
+      SoftmaxSync::sync();
+      if (tid == 0) {
+        sh.at += cnt;
+        sh.unit_begin = sh.at;
+        if (sh.at < sh.span.t1) next_unit<kChunkRows, kChunkKeys>(P, &sh.unit);
+      }
+      SoftmaxSync::sync();
+      if (sh.at >= sh.span.t1) break;
     }
   } else if (warp != 10) {
     // ------------------------------------------------------------------ loads

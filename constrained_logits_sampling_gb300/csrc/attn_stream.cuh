@@ -98,62 +98,59 @@ __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, in
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xff800000);
 }
 
-// Joins the partial sums of a unit cut by span boundaries: called by all NT threads of each
-// CTA that wrote a part; the CTA that arrives last joins them all, in key order.
+struct BlockSync {
+  static __device__ __forceinline__ void sync() { __syncthreads(); }
+};
+
+// join() of join_parts: one thread has four elements of a row, with eight parts in flight.
 template <class T, int R, int D, int NT>
-__device__ __forceinline__ void join_parts(const AttnParams& P, const Unit& u, const Span& span, int64_t unit_begin) {
-  __shared__ int last;
-  const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    last = atomicAdd(P.arrived + c0, 1) == c1 - c0;
-    if (last) P.arrived[c0] = 0;  // for the next call
+__device__ __forceinline__ void join_slots(const AttnParams& P, const Unit& u, int c0, int first, int step, int count,
+                                           bool final) {
+  static_assert(R <= NT, "a thread for each row");
+  __shared__ float ms[R], ls[R];
+  for (int i = threadIdx.x; i < u.rows * (D / 4); i += NT) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    float m = __int_as_float(0xff800000), l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < count; p0 += 8) {
+      float mc[8], lc[8];
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = first + min(p0 + k, count - 1) * step;
+        const float* s = scratch_slot<R, D>(P, c, c == c0 ? 1 : 0);
+        mc[k] = __ldcg(s + R * D + r);
+        lc[k] = __ldcg(s + R * D + R + r);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(s + r * D + d));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (p0 + k >= count) break;
+        const float mn = fmaxf(m, mc[k]);
+        const float f = m == mn ? 1.f : exp2_fast(m - mn), fc = mc[k] == mn ? 1.f : exp2_fast(mc[k] - mn);
+        o = make_float4(o.x * f + v[k].x * fc, o.y * f + v[k].y * fc, o.z * f + v[k].z * fc, o.w * f + v[k].w * fc);
+        l = l * f + lc[k] * fc;
+        m = mn;
+      }
+    }
+    if (final) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      store_out4<T>(P, u, r, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+      if (d == 0) store_lse(P, u, r, m, l);
+    } else {
+      __stcg(reinterpret_cast<float4*>(scratch_slot<R, D>(P, first, first == c0 ? 1 : 0) + r * D + d), o);
+      if (d == 0) {
+        ms[r] = m;
+        ls[r] = l;
+      }
+    }
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // D / 4 threads a row; several rows in flight
-  constexpr int kPer = D / 4, kRows = 8, kStep = NT / kPer;
-  const int d = threadIdx.x % kPer * 4;
-  for (int r0 = threadIdx.x / kPer; r0 < u.rows; r0 += kRows * kStep) {
-    float m[kRows], l[kRows];
-    float4 o[kRows];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      m[k] = __int_as_float(0xff800000);
-      l[k] = 0.f;
-      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    for (int c = c0; c <= c1; ++c) {
-      const float* s = scratch_slot<R, D>(P, c, c == c0 ? 1 : 0);
-      float mc[kRows], lc[kRows];
-      float4 v[kRows];
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const bool live = r0 + k * kStep < u.rows;
-        const int rk = live ? r0 + k * kStep : r0;
-        mc[k] = __ldcg(s + R * D + rk);
-        lc[k] = __ldcg(s + R * D + R + rk);
-        v[k] = __ldcg(reinterpret_cast<const float4*>(s + rk * D + d));
-      }
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const float mn = fmaxf(m[k], mc[k]);
-        const float f = m[k] == mn ? 1.f : exp2_fast(m[k] - mn), fc = mc[k] == mn ? 1.f : exp2_fast(mc[k] - mn);
-        o[k] = make_float4(o[k].x * f + v[k].x * fc, o[k].y * f + v[k].y * fc, o[k].z * f + v[k].z * fc,
-                           o[k].w * f + v[k].w * fc);
-        l[k] = l[k] * f + lc[k] * fc;
-        m[k] = mn;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int r = r0 + k * kStep;
-      if (r >= u.rows) break;
-      const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
-      store_out4<T>(P, u, r, d, make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
-      if (d == 0) store_lse(P, u, r, m[k], l[k]);
+  if (!final) {
+    __syncthreads();  // maxima and sums have been read by all before they are replaced
+    float* s = scratch_slot<R, D>(P, first, first == c0 ? 1 : 0) + R * D;
+    if (threadIdx.x < u.rows) {
+      __stcg(s + threadIdx.x, ms[threadIdx.x]);
+      __stcg(s + R + threadIdx.x, ls[threadIdx.x]);
     }
   }
 }
@@ -401,7 +398,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
         }
       }
     }
-    if (!done) join_parts<T, R, D, kStreamThreads>(P, u, span, unit_begin);
+    if (!done) {
+      const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
+      join_parts<BlockSync>(P, c0, c1, [&](int first, int step, int count, bool final) {
+        join_slots<T, R, D, kStreamThreads>(P, u, c0, first, step, count, final);
+      });
+    }
     t += cnt;
     if (t >= span.t1) break;
     __syncthreads();  // the rings and row sums have been read

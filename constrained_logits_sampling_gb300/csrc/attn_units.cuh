@@ -6,7 +6,9 @@
 // tiles of K keys.  All units' key tiles, laid end to end, are cut into equal spans, one per
 // CTA, whatever the sequences' lengths: a unit that lies in one span is finished there, one
 // that a span boundary cuts leaves partial sums in the handle's scratch, and the CTA that
-// arrives last joins them in key order.  Nothing waits for another CTA.
+// arrives last joins them in key order.  Nothing waits for another CTA.  A long unit has parts
+// by the hundred, which one CTA would take longer to read than all did to make: there the
+// last CTA of each group of neighbours joins the group's parts, and the last group the rest.
 #pragma once
 
 #include "paged.cuh"
@@ -21,7 +23,7 @@ struct AttnParams {
   int min_rows;     // this launch takes the sequences with min_rows <= n g < max_rows
   int max_rows;
   float* partial;   // scratch: two slots per CTA
-  int* arrived;     // one counter per CTA, zero between calls
+  int* arrived;     // two counters per CTA, zero between calls
   float scale_log2; // scale * log2(e)
 };
 
@@ -174,6 +176,43 @@ __device__ __forceinline__ int cta_of_tile(const Span& sp, int64_t t) {
   while (c + 1 < sp.ctas && span_begin(sp.total, sp.ctas, c + 1) <= t) ++c;
   while (c > 0 && span_begin(sp.total, sp.ctas, c) > t) --c;
   return c;
+}
+
+// Whether this CTA is the last of `count` to come here with its part written; called by the NT
+// threads that wrote it.
+template <class Sync>
+__device__ __forceinline__ bool arrive_last(int* counter, int count) {
+  __shared__ int last;
+  __threadfence();
+  Sync::sync();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(counter, 1) == count - 1;
+    if (last) *counter = 0;  // for the next call
+  }
+  Sync::sync();
+  if (!last) return false;
+  __threadfence();
+  return true;
+}
+
+// Joins the parts of a unit cut by span boundaries, by the CTAs c0 .. c1 that have one.
+// join(first, step, count, final) joins the parts of the CTAs first, first + step, .. into the
+// slot of the first one or, if final, into the outputs.
+template <class Sync, class Join>
+__device__ __forceinline__ void join_parts(const AttnParams& P, int c0, int c1, Join join) {
+  const int n = c1 - c0 + 1;
+  int group = 8;
+  while (group * group < n) group *= 2;
+  const int groups = (n + group - 1) / group;
+  const int first = c0 + ((int)blockIdx.x - c0) / group * group, count = min(group, c1 - first + 1);
+  if (!arrive_last<Sync>(P.arrived + 2 * first, count)) return;
+  if (groups > 1) {
+    if (count > 1) join(first, 1, count, false);
+    if (!arrive_last<Sync>(P.arrived + 2 * c0 + 1, groups)) return;
+    join(c0, group, groups, true);
+  } else {
+    join(c0, 1, count, true);
+  }
 }
 
 // Statuses: one CTA per sequence at a time looks at its lengths and at every page id that
