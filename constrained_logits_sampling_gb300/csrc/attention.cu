@@ -4,31 +4,52 @@
 #include <new>
 
 #include "attn_chunk.cuh"
+#include "attn_join.cuh"
 #include "attn_stream.cuh"
 
 struct clsample_attention {
   int dev, sms;
-  float* partial;
-  int* arrived;
+  unsigned char* scratch;
 };
 
 namespace clsample {
 namespace {
 
 constexpr int kStreamCtas = 2;  // per SM
-// Scratch per SM: two slots per CTA of rows of 128 sums, a maximum and a sum.
-constexpr size_t kScratch = 2 * (size_t)kChunkRows * 130 * sizeof(float);
-static_assert(kScratch >= (size_t)kStreamCtas * 2 * 32 * 130 * sizeof(float), "the stream kernel's slots fit too");
+// The scratch, per SM: both kernels' slots (two per CTA, of rows of 128 sums, a maximum and a
+// sum), their cut units, and one word for all.
+constexpr size_t kChunkSlots = 2 * (size_t)kChunkRows * 130 * sizeof(float);
+constexpr size_t kStreamSlots = kStreamCtas * 2 * (size_t)32 * 130 * sizeof(float);
+constexpr size_t kCuts = (1 + kStreamCtas) * sizeof(CutUnit);
+constexpr size_t kScratch = kChunkSlots + kStreamSlots + kCuts;
 // Up to this many packed rows (a multiple of the stream kernel's tile) a sequence's keys are
 // read once by the stream kernel; above it, once per 256 rows by the chunk kernel.
 constexpr int kStreamRows = 32;
 
+// A launch that may start while the one before it ends.
+template <class Kernel, class... Args>
+cudaError_t launch_after(Kernel fn, int grid, int threads, int smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 template <class T, int D, int MT>
-cudaError_t launch_stream(const AttnParams& P, int sms, cudaStream_t st) {
+cudaError_t launch_stream(const AttnParams& P, int sms, bool first, cudaStream_t st) {
   auto* fn = attn_stream_kernel<T, D, MT>;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamRing<D>::kBytes);
+  const int bytes = StreamRing<D>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  fn<<<sms * kStreamCtas, kStreamThreads, StreamRing<D>::kBytes, st>>>(P);
+  if (!first) return launch_after(fn, sms * kStreamCtas, kStreamThreads, bytes, st, P);
+  fn<<<sms * kStreamCtas, kStreamThreads, bytes, st>>>(P);
   return cudaGetLastError();
 }
 
@@ -77,23 +98,40 @@ template <class T, int D>
 cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
   // no valid sequence has more rows than this; one that breaks the bound has no keys
   const int64_t rows = P.a.max_new * (int64_t)P.g;
-  P.min_rows = 0;
-  P.max_rows = 0x7fffffff;
-  if (rows > kStreamRows) {
-    P.min_rows = kStreamRows + 1;
+  float* const chunk_partial = reinterpret_cast<float*>(h->scratch);
+  float* const stream_partial = reinterpret_cast<float*>(h->scratch + h->sms * kChunkSlots);
+  CutUnit* const chunk_cut = reinterpret_cast<CutUnit*>(h->scratch + h->sms * (kChunkSlots + kStreamSlots));
+  CutUnit* const stream_cut = chunk_cut + h->sms;
+  P.gave_up = reinterpret_cast<int*>(stream_cut + h->sms * kStreamCtas);
+  const bool chunks = rows > kStreamRows;
+  // beside sequences with many rows, a few with few are not worth a launch of their own
+  const bool alone = chunks && (int64_t)P.a.B * P.a.Hkv <= 2 * h->sms;
+  cudaError_t e;
+  if (chunks) {
+    P.min_rows = alone ? 0 : kStreamRows + 1;
+    P.max_rows = 0x7fffffff;
+    P.partial = chunk_partial;
+    P.cut = chunk_cut;
     // boxes have to start on the eight rows of the swizzle and fill a tile
     const int page = P.a.page_size;
     const bool boxes = page >= 8 && (page % kChunkKeys == 0 || kChunkKeys % page == 0);
     CUtensorMap k_map{}, v_map{};
-    const cudaError_t e = boxes && cache_map(P, P.a.k_cache, &k_map) && cache_map(P, P.a.v_cache, &v_map)
-                              ? launch_chunk<T, D, true>(P, k_map, v_map, h->sms, st)
-                              : launch_chunk<T, D, false>(P, k_map, v_map, h->sms, st);
+    e = boxes && cache_map(P, P.a.k_cache, &k_map) && cache_map(P, P.a.v_cache, &v_map)
+            ? launch_chunk<T, D, true>(P, k_map, v_map, h->sms, st)
+            : launch_chunk<T, D, false>(P, k_map, v_map, h->sms, st);
     if (e != cudaSuccess) return e;
-    P.a.row_status = nullptr;  // written
-    P.min_rows = 0;
-    P.max_rows = kStreamRows + 1;
   }
-  return rows <= 16 ? launch_stream<T, D, 1>(P, h->sms, st) : launch_stream<T, D, 2>(P, h->sms, st);
+  P.min_rows = 0;
+  P.max_rows = chunks ? kStreamRows + 1 : 0x7fffffff;
+  P.partial = stream_partial;
+  P.cut = stream_cut;
+  const int tile = rows <= 16 ? 16 : 32;
+  if (!alone) {
+    e = tile == 16 ? launch_stream<T, D, 1>(P, h->sms, !chunks, st) : launch_stream<T, D, 2>(P, h->sms, !chunks, st);
+    if (e != cudaSuccess) return e;
+  }
+  const JoinParams J{P, chunk_partial, chunk_cut, chunks ? h->sms : 0, alone ? 0 : h->sms * kStreamCtas, tile};
+  return launch_after(attn_join_kernel<T, D>, h->sms * 2, kJoinThreads, 0, st, J);
 }
 
 }  // namespace
@@ -108,11 +146,11 @@ int clsample_attention_create(clsample_attention_t** out) {
   int dev = 0, sms = 0;
   const int rc = check_device(&dev, &sms);
   if (rc != CLSAMPLE_SUCCESS) return rc;
-  auto* h = new (std::nothrow) clsample_attention{dev, sms, nullptr, nullptr};
+  if (sms * (1 + kStreamCtas) > kMaxCuts) return CLSAMPLE_ERR_DEVICE;
+  auto* h = new (std::nothrow) clsample_attention{dev, sms, nullptr};
   if (!h) return CLSAMPLE_ERR_CUDA;
-  if (cudaMalloc(&h->partial, (size_t)sms * kScratch) != cudaSuccess ||
-      cudaMalloc(&h->arrived, (size_t)sms * kStreamCtas * 2 * sizeof(int)) != cudaSuccess ||
-      cudaMemset(h->arrived, 0, (size_t)sms * kStreamCtas * 2 * sizeof(int)) != cudaSuccess ||
+  const size_t bytes = sms * kScratch + sizeof(int);
+  if (cudaMalloc(&h->scratch, bytes) != cudaSuccess || cudaMemset(h->scratch, 0, bytes) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
     clsample_attention_destroy(h);
     cudaGetLastError();
@@ -124,8 +162,7 @@ int clsample_attention_create(clsample_attention_t** out) {
 
 void clsample_attention_destroy(clsample_attention_t* h) {
   if (!h) return;
-  if (h->partial) cudaFree(h->partial);
-  if (h->arrived) cudaFree(h->arrived);
+  if (h->scratch) cudaFree(h->scratch);
   delete h;
 }
 
@@ -156,8 +193,6 @@ int clsample_chunk_attention(clsample_attention_t* h, const clsample_attention_a
   P.g = a->Hq / a->Hkv;
   P.page_shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz((unsigned)a->page_size) : -1;
   P.capacity = capacity_of(a->max_pages, a->page_size);
-  P.partial = h->partial;
-  P.arrived = h->arrived;
   P.scale_log2 = a->scale * 1.44269504088896341f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

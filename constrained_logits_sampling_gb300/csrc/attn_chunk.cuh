@@ -126,75 +126,6 @@ struct SoftmaxSync {  // the 256 softmax threads
   static __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 };
 
-// join() of join_parts, by the 256 softmax threads.  A slot holds four sums of each row side by
-// side, then the next four of each row, so that threads with a row each read and write whole
-// lines.  Up to 128 rows have two threads each.
-template <class T, int D>
-__device__ __forceinline__ void join_rows(const AttnParams& P, const Unit& u, int c0, int first, int step, int count,
-                                          bool final) {
-  const bool two = u.rows <= 128;
-  const int r = two ? threadIdx.x & 127 : threadIdx.x;
-  const int d0 = two ? (threadIdx.x >> 7) * (D / 2) : 0, d1 = two ? d0 + D / 2 : D;
-  auto slot_of = [&](int part) {
-    const int c = first + part * step;
-    return scratch_slot<kChunkRows, D>(P, c, c == c0 ? 1 : 0);
-  };
-  float m = __int_as_float(0xff800000), l = 0.f;
-  if (r < u.rows) {
-#pragma unroll 4
-    for (int part = 0; part < count; ++part) {
-      const float* s = slot_of(part) + kChunkRows * D + r;
-      const float mc = __ldcg(s), lc = __ldcg(s + kChunkRows);
-      const float mn = fmaxf(m, mc);
-      l = l * (m == mn ? 1.f : exp2_fast(m - mn)) + lc * (mc == mn ? 1.f : exp2_fast(mc - mn));
-      m = mn;
-    }
-    const float scale = final ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-    const int row = u.row0 + r;
-    T* dst = (T*)P.a.out + (int64_t)(u.q0 + row / P.g) * P.a.o_stride_t +
-             (int64_t)(u.h * P.g + row % P.g) * P.a.o_stride_h;
-    if (d0 == 0 && final) store_lse(P, u, r, m, l);
-    float* to = slot_of(0);
-    for (int d = d0; d < d1; d += 16) {
-      float4 o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int part = 0; part < count; ++part) {
-        const float* s = slot_of(part);
-        const float mc = __ldcg(s + kChunkRows * D + r);
-        float4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = __ldcg(reinterpret_cast<const float4*>(s + (d + 4 * i) * kChunkRows + r * 4));
-        const float f = (mc == m ? 1.f : exp2_fast(mc - m)) * scale;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = make_float4(fmaf(v[i].x, f, o[i].x), fmaf(v[i].y, f, o[i].y), fmaf(v[i].z, f, o[i].z),
-                             fmaf(v[i].w, f, o[i].w));
-      }
-      if (final) {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2)
-          *reinterpret_cast<uint4*>(dst + d + 4 * i) =
-              make_uint4(Pair<T>::narrow(o[i].x, o[i].y), Pair<T>::narrow(o[i].z, o[i].w),
-                         Pair<T>::narrow(o[i + 1].x, o[i + 1].y), Pair<T>::narrow(o[i + 1].z, o[i + 1].w));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) __stcg(reinterpret_cast<float4*>(to + (d + 4 * i) * kChunkRows + r * 4), o[i]);
-      }
-    }
-  }
-  if (!final) {
-    SoftmaxSync::sync();  // maxima and sums have been read by all before they are replaced
-    if (r < u.rows && d0 == 0) {
-      float* s = slot_of(0) + kChunkRows * D + r;
-      __stcg(s, m);
-      __stcg(s + kChunkRows, l);
-    }
-  }
-}
-
 template <class T, int D, bool kTma>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     attn_chunk_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap k_map,
@@ -210,11 +141,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const clsample_attention_args_t& a = P.a;
   const float neg_inf = __int_as_float(0xff800000);
 
-  if (a.row_status) attention_status<kChunkThreads>(P);
+  let_next_grid_start();
   Span span;
   Unit u;
   int64_t unit_begin;
-  if (!find_span<kChunkRows, kChunkKeys, kChunkThreads>(P, &span, &u, &unit_begin)) return;
+  if (!find_span<kChunkRows, kChunkKeys, kChunkThreads>(P, &span, &u, &unit_begin)) {
+    if (tid == 0) P.cut[blockIdx.x].rows = 0;
+    return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -360,6 +294,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         o_phase ^= 1;
         tc_fence_after();
       }
+      // A slot holds four sums of each row side by side, then the next four of each row, so that
+      // threads with a row each write whole lines.
       float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
       float mine = 1.f, others = 0.f;  // weights of this half's sums and of the other's
       if (split) {
@@ -439,21 +375,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       tc_fence_before();  // O has been read: the next unit's products may overwrite it
-      if (!done) {
-        const int c0 = cta_of_tile(sh.span, sh.unit_begin);
-        const int c1 = cta_of_tile(sh.span, sh.unit_begin + u.tiles - 1);
-        join_parts<SoftmaxSync>(P, c0, c1, [&](int first, int step, int count, bool final) {
-          join_rows<T, D>(P, u, c0, first, step, count, final);
-        });
-      }
-      if (sh.dead && tid == 0 && a.row_status) atomicMax(a.row_status + u.b, CLSAMPLE_ROW_OVERFLOW);
       tile += cnt;
       // (of two halves, the first has read here what the second may write again)
       SoftmaxSync::sync();
       if (tid == 0) {
         sh.at += cnt;
-        sh.unit_begin = sh.at;
-        if (sh.at < sh.span.t1) next_unit<kChunkRows, kChunkKeys>(P, &sh.unit);
+        if (sh.at < sh.span.t1) {
+          sh.unit_begin = sh.at;
+          next_unit<kChunkRows, kChunkKeys>(P, &sh.unit);
+        } else {
+          note_cut(P, sh.span, sh.unit, sh.unit_begin);
+          if (sh.dead) *P.gave_up = 1;
+        }
       }
       SoftmaxSync::sync();
       if (sh.at >= sh.span.t1) break;

@@ -91,68 +91,12 @@ __device__ __forceinline__ void store_out4(const AttnParams& P, const Unit& u, i
            (int64_t)(u.h * P.g + row % P.g) * P.a.o_stride_h + d;
   *reinterpret_cast<uint2*>(dst) = make_uint2(Pair<T>::narrow(o.x, o.y), Pair<T>::narrow(o.z, o.w));
 }
+__device__ __forceinline__ float lse_of(float m, float l) {  // m in log2 units
+  return l > 0.f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xff800000);
+}
 __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, int r, float m, float l) {
   const int row = u.row0 + r;
-  if (P.a.lse)
-    P.a.lse[(int64_t)(u.q0 + row / P.g) * P.a.Hq + u.h * P.g + row % P.g] =
-        l > 0.f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xff800000);
-}
-
-struct BlockSync {
-  static __device__ __forceinline__ void sync() { __syncthreads(); }
-};
-
-// join() of join_parts: one thread has four elements of a row, with eight parts in flight.
-template <class T, int R, int D, int NT>
-__device__ __forceinline__ void join_slots(const AttnParams& P, const Unit& u, int c0, int first, int step, int count,
-                                           bool final) {
-  static_assert(R <= NT, "a thread for each row");
-  __shared__ float ms[R], ls[R];
-  for (int i = threadIdx.x; i < u.rows * (D / 4); i += NT) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
-    float m = __int_as_float(0xff800000), l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < count; p0 += 8) {
-      float mc[8], lc[8];
-      float4 v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = first + min(p0 + k, count - 1) * step;
-        const float* s = scratch_slot<R, D>(P, c, c == c0 ? 1 : 0);
-        mc[k] = __ldcg(s + R * D + r);
-        lc[k] = __ldcg(s + R * D + R + r);
-        v[k] = __ldcg(reinterpret_cast<const float4*>(s + r * D + d));
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (p0 + k >= count) break;
-        const float mn = fmaxf(m, mc[k]);
-        const float f = m == mn ? 1.f : exp2_fast(m - mn), fc = mc[k] == mn ? 1.f : exp2_fast(mc[k] - mn);
-        o = make_float4(o.x * f + v[k].x * fc, o.y * f + v[k].y * fc, o.z * f + v[k].z * fc, o.w * f + v[k].w * fc);
-        l = l * f + lc[k] * fc;
-        m = mn;
-      }
-    }
-    if (final) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      store_out4<T>(P, u, r, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-      if (d == 0) store_lse(P, u, r, m, l);
-    } else {
-      __stcg(reinterpret_cast<float4*>(scratch_slot<R, D>(P, first, first == c0 ? 1 : 0) + r * D + d), o);
-      if (d == 0) {
-        ms[r] = m;
-        ls[r] = l;
-      }
-    }
-  }
-  if (!final) {
-    __syncthreads();  // maxima and sums have been read by all before they are replaced
-    float* s = scratch_slot<R, D>(P, first, first == c0 ? 1 : 0) + R * D;
-    if (threadIdx.x < u.rows) {
-      __stcg(s + threadIdx.x, ms[threadIdx.x]);
-      __stcg(s + R + threadIdx.x, ls[threadIdx.x]);
-    }
-  }
+  if (P.a.lse) P.a.lse[(int64_t)(u.q0 + row / P.g) * P.a.Hq + u.h * P.g + row % P.g] = lse_of(m, l);
 }
 
 template <class T, int D, int MT>
@@ -168,16 +112,21 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
   const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   const float neg_inf = __int_as_float(0xff800000);
 
-  if (a.row_status) attention_status<kStreamThreads>(P);
+  let_next_grid_start();
   Span span;
   Unit u;
   int64_t unit_begin;
-  if (!find_span<R, kStreamKeys, kStreamThreads>(P, &span, &u, &unit_begin)) return;
+  if (!find_span<R, kStreamKeys, kStreamThreads>(P, &span, &u, &unit_begin)) {
+    if (tid == 0) P.cut[blockIdx.x].rows = 0;
+    wait_for_earlier_grids();  // this grid's end stands for theirs
+    return;
+  }
 
   int64_t t = span.t0;
   while (true) {
     const int j0 = (int)(t - unit_begin);
     const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+    if (tid == 0 && t + cnt >= span.t1) note_cut(P, span, u, unit_begin);
     const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
     const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
     const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
@@ -398,18 +347,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
         }
       }
     }
-    if (!done) {
-      const int c0 = cta_of_tile(span, unit_begin), c1 = cta_of_tile(span, unit_begin + u.tiles - 1);
-      join_parts<BlockSync>(P, c0, c1, [&](int first, int step, int count, bool final) {
-        join_slots<T, R, D, kStreamThreads>(P, u, c0, first, step, count, final);
-      });
-    }
     t += cnt;
     if (t >= span.t1) break;
     __syncthreads();  // the rings and row sums have been read
     unit_begin = t;
     next_unit<R, kStreamKeys>(P, &u);
   }
+  wait_for_earlier_grids();  // this grid's end stands for theirs
 }
 
 }  // namespace clsample

@@ -5,10 +5,8 @@
 // head r % g), cut into tiles of R rows.  A unit walks the keys that any of its rows sees in
 // tiles of K keys.  All units' key tiles, laid end to end, are cut into equal spans, one per
 // CTA, whatever the sequences' lengths: a unit that lies in one span is finished there, one
-// that a span boundary cuts leaves partial sums in the handle's scratch, and the CTA that
-// arrives last joins them in key order.  Nothing waits for another CTA.  A long unit has parts
-// by the hundred, which one CTA would take longer to read than all did to make: there the
-// last CTA of each group of neighbours joins the group's parts, and the last group the rest.
+// that a span boundary cuts leaves partial sums in the handle's scratch, which a last launch
+// joins in key order (attn_join.cuh).  Nothing waits for another CTA.
 #pragma once
 
 #include "paged.cuh"
@@ -23,8 +21,15 @@ struct AttnParams {
   int min_rows;     // this launch takes the sequences with min_rows <= n g < max_rows
   int max_rows;
   float* partial;   // scratch: two slots per CTA
-  int* arrived;     // two counters per CTA, zero between calls
+  struct CutUnit* cut;  // one per CTA: the unit that starts in its span and ends in another's
+  int* gave_up;     // set when a bounded wait ran out
   float scale_log2; // scale * log2(e)
+};
+
+struct CutUnit {
+  int rows;          // 0: none
+  int row0, q0, h;   // as in Unit
+  int c0, c1;        // the CTAs that have its parts: c0 in its second slot, the others in the first
 };
 
 struct Unit {
@@ -103,7 +108,13 @@ struct Span {
   int64_t total, t0, t1;
   int ctas;  // CTAs with work: those with the lower indices
 };
-__device__ __forceinline__ int64_t span_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // of numbers >= 0; 64-bit division is slow
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int64_t span_begin(int64_t total, int ctas, int c) {
+  const int64_t each = quotient(total, ctas);
+  return each * c + (uint32_t)((int)(total - each * ctas) * c) / (uint32_t)ctas;
+}
 
 template <int R, int K, int NT>
 __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit* u, int64_t* unit_begin) {
@@ -141,7 +152,7 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
   const int64_t per_head = M::head_tiles(P, s);
   int64_t rest = found_rest;
   u->b = b;
-  u->h = (int)(rest / per_head);
+  u->h = (int)quotient(rest, per_head);
   rest -= u->h * per_head;
   for (int qt = 0;; ++qt) {
     M::fill(P, s, qt, u);
@@ -172,67 +183,24 @@ __device__ __forceinline__ void next_unit(const AttnParams& P, Unit* u) {
 
 // The CTA whose span holds tile t.
 __device__ __forceinline__ int cta_of_tile(const Span& sp, int64_t t) {
-  int c = (int)(t * sp.ctas / sp.total);
+  int c = (int)quotient(t * sp.ctas, sp.total);
   while (c + 1 < sp.ctas && span_begin(sp.total, sp.ctas, c + 1) <= t) ++c;
   while (c > 0 && span_begin(sp.total, sp.ctas, c) > t) --c;
   return c;
 }
 
-// Whether this CTA is the last of `count` to come here with its part written; called by the NT
-// threads that wrote it.
-template <class Sync>
-__device__ __forceinline__ bool arrive_last(int* counter, int count) {
-  __shared__ int last;
-  __threadfence();
-  Sync::sync();
-  if (threadIdx.x == 0) {
-    last = atomicAdd(counter, 1) == count - 1;
-    if (last) *counter = 0;  // for the next call
-  }
-  Sync::sync();
-  if (!last) return false;
-  __threadfence();
-  return true;
+// Called by one thread of each CTA, with the unit that its span ends with: whether the rest of
+// it is another's.
+__device__ __forceinline__ void note_cut(const AttnParams& P, const Span& span, const Unit& u, int64_t unit_begin) {
+  CutUnit c{0, 0, 0, 0, 0, 0};
+  if (unit_begin >= span.t0 && unit_begin + u.tiles > span.t1)
+    c = CutUnit{u.rows, u.row0, u.q0, u.h, (int)blockIdx.x, cta_of_tile(span, unit_begin + u.tiles - 1)};
+  P.cut[blockIdx.x] = c;
 }
 
-// Joins the parts of a unit cut by span boundaries, by the CTAs c0 .. c1 that have one.
-// join(first, step, count, final) joins the parts of the CTAs first, first + step, .. into the
-// slot of the first one or, if final, into the outputs.
-template <class Sync, class Join>
-__device__ __forceinline__ void join_parts(const AttnParams& P, int c0, int c1, Join join) {
-  const int n = c1 - c0 + 1;
-  int group = 8;
-  while (group * group < n) group *= 2;
-  const int groups = (n + group - 1) / group;
-  const int first = c0 + ((int)blockIdx.x - c0) / group * group, count = min(group, c1 - first + 1);
-  if (!arrive_last<Sync>(P.arrived + 2 * first, count)) return;
-  if (groups > 1) {
-    if (count > 1) join(first, 1, count, false);
-    if (!arrive_last<Sync>(P.arrived + 2 * c0 + 1, groups)) return;
-    join(c0, group, groups, true);
-  } else {
-    join(c0, 1, count, true);
-  }
-}
-
-// Statuses: one CTA per sequence at a time looks at its lengths and at every page id that
-// the call touches.
-template <int NT>
-__device__ __forceinline__ void attention_status(const AttnParams& P) {
-  const clsample_attention_args_t& a = P.a;
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const Seq s = load_seq(a.cu_new, a.kv_lens, b, a.T, P.capacity, a.max_new);
-    int bad = !s.ok;
-    if (s.ok && s.n > 0 && s.len > 0) {
-      const int lo = a.window > 0 ? max(0, s.len - s.n - a.window + 1) : 0;
-      for (int p = lo / a.page_size + threadIdx.x; p <= (s.len - 1) / a.page_size; p += NT) {
-        const int id = __ldg(a.page_table + (int64_t)b * a.table_stride + p);
-        bad |= id < 0 || id >= a.num_pages;
-      }
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) a.row_status[b] = bad ? CLSAMPLE_ROW_INVALID : CLSAMPLE_ROW_OK;
-  }
-}
+// Launches that follow one another without a gap: the next grid may start as this one's blocks
+// leave, and takes no result before wait_for_earlier_grids().
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_earlier_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace clsample
