@@ -10,45 +10,52 @@ namespace {
 
 constexpr int kThreads = 256;
 
+constexpr int kMaxTokens = kThreads / 32;  // of a block: one a warp
+constexpr int kMaxHeads = 256;             // Hq + 2 Hkv of the fast path
+
 struct AppendParams {
   clsample_kv_append_args_t a;
+  int tokens;  // of a block of the fast path
 };
-
-// The sequence that owns row t, by a 32-way search of the offsets in one warp: the last b
-// with cu[b] <= t, if t < cu[b + 1]; -1 when no sequence owns the row.  Offsets out of
-// order can only give a wrong or no owner; load_seq and the caller's check t against it.
-__device__ __forceinline__ int owner_of(const int32_t* cu, int B, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = B;  // the owner is in [lo, hi)
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + lane * step;
-    const bool le = at < hi && __ldg(cu + at) <= t;
-    const unsigned m = __ballot_sync(~0u, le);
-    if (!(m & 1u)) return -1;
-    const int j = 31 - __clz(m);
-    lo = lo + j * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
 
 struct Token {
   int b, pos, page, slot;
   bool ok;  // in a sequence, at a position with a cos/sin row and a valid page
 };
 
+// The sequence that owns row t (the last b with cu[b] <= t, if t < cu[b + 1]), the row's
+// position, page and slot, by one warp: a 32-way search of the offsets, whose last step reads
+// the lengths along.  b is -1 when no sequence owns the row.  Offsets out of order can only
+// give a wrong owner or none: what is found is checked against them.
 __device__ __forceinline__ Token find_token(const clsample_kv_append_args_t& a, int t) {
+  const int lane = threadIdx.x & 31;
   Token k{-1, 0, 0, 0, false};
-  k.b = owner_of(a.cu_new, a.B, t);
-  if (k.b < 0) return k;
-  const Seq s = load_seq(a.cu_new, a.kv_lens, k.b, a.T, capacity_of(a.max_pages, a.page_size), a.T);
-  if (t < s.q0 || t >= s.q0 + s.n) {
-    k.b = -1;
-    return k;
+  int lo = 0, hi = a.B;  // the owner is in [lo, hi)
+  while (hi - lo > 32) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned m = __ballot_sync(~0u, at < hi && __ldg(a.cu_new + at) <= t);
+    if (!(m & 1u)) return k;
+    lo += (31 - __clz(m)) * step;
+    hi = min(hi, lo + step);
   }
-  if (!s.ok) return k;
-  k.pos = s.len - s.n + (t - s.q0);
+  const int at = lo + lane;
+  int from = 0, to = 0, len = 0;
+  if (at < hi) {
+    from = __ldg(a.cu_new + at);
+    to = __ldg(a.cu_new + at + 1);
+    len = __ldg(a.kv_lens + at);
+  }
+  const unsigned m = __ballot_sync(~0u, at < hi && from <= t);
+  if (!m) return k;
+  const int src = 31 - __clz(m);
+  from = __shfl_sync(~0u, from, src);
+  to = __shfl_sync(~0u, to, src);
+  len = __shfl_sync(~0u, len, src);
+  if (from < 0 || to > a.T || t < from || t >= to) return k;
+  k.b = lo + src;
+  if (len < 0 || len > capacity_of(a.max_pages, a.page_size)) return k;
+  k.pos = len - (to - from) + (t - from);
   if (k.pos < 0 || (a.rot_dim > 0 && k.pos >= a.max_pos)) return k;
   k.page = __ldg(a.page_table + (int64_t)k.b * a.table_stride + k.pos / a.page_size);
   k.slot = k.pos % a.page_size;
@@ -79,7 +86,7 @@ __device__ __forceinline__ void write_status(const clsample_kv_append_args_t& a,
 // Any head size, strides and rotation: one warp per head row, elements one by one through
 // shared memory.
 template <class T>
-__global__ void __launch_bounds__(kThreads) append_any_kernel(AppendParams P) {
+__global__ void __launch_bounds__(kThreads) append_any_kernel(const __grid_constant__ AppendParams P) {
   const clsample_kv_append_args_t& a = P.a;
   __shared__ float rows[kThreads / 32][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.D;
@@ -140,95 +147,137 @@ __global__ void __launch_bounds__(kThreads) append_any_kernel(AppendParams P) {
     for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += gridDim.x * kThreads) write_status(a, b);
 }
 
+// Where a head row comes from and goes to, for the block's first token.
+struct HeadRow {
+  const unsigned char* src;
+  unsigned char* dst;  // of k and v: of the cache's first slot
+  int64_t src_stride;  // bytes from a token to the next
+  int kind;            // 0 q, 1 k, 2 v
+};
+
 // Head rows in 16-byte pieces: lane l of a group of G lanes holds elements 8l .. 8l + 7 of a
 // row, so the norm is a reduction over the group and the half-split rotation one exchange
-// between lanes.  One block per token: all of a token's rows are in flight at once, and
-// while they are, each warp finds the token's sequence, position and page.
+// between lanes.  A block takes a few consecutive tokens.  Its first head rows are on their way
+// while each warp finds one token's sequence, position and page; from then on a token's rows
+// are loaded while the one before it is worked on.  Addresses come from a table in shared
+// memory: with the selection between q, k and v in each row the instructions took longer than
+// the memory.
 template <class T, int G>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendParams P) {
   const clsample_kv_append_args_t& a = P.a;
   constexpr int kGroups = kThreads / G;
-  constexpr int kUnroll = 4;
-  const int t = blockIdx.x;
-  const int group = threadIdx.x / G, l = threadIdx.x % G;
+  constexpr int kUnroll = 3;  // head rows of a group in flight
+  __shared__ Token tokens[kMaxTokens];
+  __shared__ HeadRow table[kMaxHeads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = tid / G, l = tid % G;
   const bool in = l * 8 < a.D;
   const int heads = a.Hq + 2 * a.Hkv;
-  Token k;
-  bool found = false;
-  for (int r0 = 0; r0 < heads && t < a.T; r0 += kGroups * kUnroll) {
-    uint4 raw[kUnroll];
+  const int t0 = blockIdx.x * P.tokens, count = min(P.tokens, a.T - t0);
+  const int half = a.rot_dim / 2;
+
+  for (int r = tid; r < heads; r += kThreads) {
+    const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
+    const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
+    const T* src = (const T*)(kind == 0 ? a.q : kind == 1 ? a.k : a.v);
+    const int64_t st = kind == 0 ? a.q_stride_t : kind == 1 ? a.k_stride_t : a.v_stride_t;
+    const int64_t hd = kind == 0 ? a.q_stride_h : kind == 1 ? a.k_stride_h : a.v_stride_h;
+    T* dst = (T*)(kind == 0 ? a.q_out : kind == 1 ? a.k_cache : a.v_cache);
+    table[r] = HeadRow{(const unsigned char*)(src + t0 * st + h * hd),
+                       (unsigned char*)(kind == 0 ? dst + t0 * a.qo_stride_t + h * a.qo_stride_h : dst + h * a.head_stride),
+                       st * (int64_t)sizeof(T), kind};
+  }
+  __syncthreads();
+
+  uint4 raw[kUnroll];
+  auto fetch = [&](int token, int r0) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int r = r0 + i * kGroups + group;
       raw[i] = make_uint4(0, 0, 0, 0);
       if (r < heads && in) {
-        const T* src = r < a.Hq ? (const T*)a.q + (int64_t)t * a.q_stride_t + (int64_t)r * a.q_stride_h
-                       : r < a.Hq + a.Hkv
-                           ? (const T*)a.k + (int64_t)t * a.k_stride_t + (int64_t)(r - a.Hq) * a.k_stride_h
-                           : (const T*)a.v + (int64_t)t * a.v_stride_t + (int64_t)(r - a.Hq - a.Hkv) * a.v_stride_h;
-        raw[i] = *reinterpret_cast<const uint4*>(src + l * 8);
+        const HeadRow& h = table[r];
+        raw[i] = *reinterpret_cast<const uint4*>(h.src + token * h.src_stride + l * 16);
       }
     }
-    if (!found) {
-      k = find_token(a, t);
-      found = true;
+  };
+  if (count > 0) fetch(0, 0);
+  if (warp < count) {
+    const Token k = find_token(a, t0 + warp);
+    if (lane == 0) tokens[warp] = k;
+  }
+  __syncthreads();
+
+  // the lane that holds the other elements of this one's pairs; where it is the second of them
+  const bool second = !a.interleaved && l * 8 >= half;
+  const int from = !a.interleaved && l * 8 < a.rot_dim ? (second ? lane - half / 8 : lane + half / 8) : lane;
+  const int turn_at = a.interleaved ? l * 4 : second ? l * 8 - half : l * 8;
+  const bool norm = a.q_weight || a.k_weight;
+
+  for (int token = 0, r0 = 0; token < count;) {
+    const Token& k = tokens[token];
+    uint4 now[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) now[i] = raw[i];
+    const int this_r0 = r0, this_token = token;
+    r0 += kGroups * kUnroll;
+    if (r0 >= heads) {
+      r0 = 0;
+      ++token;
     }
-    if (k.b < 0) break;
-    // the lane's cosines and sines: pairs 8l.. of the half-split form, 4l.. interleaved
-    const int half = a.rot_dim / 2;
+    if (token < count) fetch(token, r0);
+    if (k.b < 0) continue;
     const bool turns = k.ok && l * 8 < a.rot_dim;
-    float c[8], s[8];
+    float c[8], s[8];  // cosines; sines, negative for the first elements of pairs
     if (turns) {
-      const float* cs = a.cos_sin + (int64_t)k.pos * a.cs_stride;
-      if (a.interleaved) {
+      const float* cs = a.cos_sin + (int64_t)k.pos * a.cs_stride + turn_at;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c[e] = __ldg(cs + l * 4 + e);
-          s[e] = __ldg(cs + half + l * 4 + e);
-        }
-      } else {
-        const int j = l * 8 < half ? l * 8 : l * 8 - half;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          c[e] = __ldg(cs + j + e);
-          s[e] = __ldg(cs + half + j + e);
+      for (int e = 0; e < 2; ++e) {
+        if (e == 0 || !a.interleaved) {
+          const float4 x = __ldg(reinterpret_cast<const float4*>(cs + 4 * e));
+          const float4 y = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * e));
+          const float sign = second || a.interleaved ? 1.f : -1.f;
+          c[4 * e] = x.x, c[4 * e + 1] = x.y, c[4 * e + 2] = x.z, c[4 * e + 3] = x.w;
+          s[4 * e] = y.x * sign, s[4 * e + 1] = y.y * sign, s[4 * e + 2] = y.z * sign, s[4 * e + 3] = y.w * sign;
         }
       }
     }
+    const int64_t cache_at = ((int64_t)k.page * a.page_stride + (int64_t)k.slot * a.slot_stride) * (int64_t)sizeof(T);
+    const int64_t out_at = this_token * a.qo_stride_t * (int64_t)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      if (r0 + i * kGroups >= heads) break;  // uniform over the block
-      const int r = r0 + i * kGroups + group;
-      const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
-      const int h = is_q ? r : is_k ? r - a.Hq : r - a.Hq - a.Hkv;
-      float x[8];
-      const uint32_t wds[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      const int r = this_r0 + i * kGroups + group;
+      if (r - group >= heads) break;  // uniform over the block
+      const int kind = r < heads ? table[r].kind : 2;
+      uint4 y = now[i];
+      if (__any_sync(~0u, kind < 2)) {  // not a warp of values
+        float x[8];
+        const uint32_t wds[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = Pair<T>::widen(wds[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
-      }
-      const T* w = (const T*)(is_q ? a.q_weight : is_k ? a.k_weight : nullptr);
-      if (a.q_weight || a.k_weight) {
-        float ss = 0.f;
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = Pair<T>::widen(wds[e]);
+          x[2 * e] = f.x;
+          x[2 * e + 1] = f.y;
+        }
+        if (norm) {
+          const T* w = (const T*)(kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr);
+          float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-        if (w && in) {
-          const float inv = rsqrtf(ss / (float)a.D + a.eps);
-          const uint4 wr = __ldg(reinterpret_cast<const uint4*>(w + l * 8));
-          const uint32_t ww[4] = {wr.x, wr.y, wr.z, wr.w};
+          for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+          if (w && in) {
+            const float inv = rsqrtf(ss / (float)a.D + a.eps);
+            const uint4 wr = __ldg(reinterpret_cast<const uint4*>(w + l * 8));
+            const uint32_t ww[4] = {wr.x, wr.y, wr.z, wr.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = Pair<T>::widen(ww[e]);
-            x[2 * e] = x[2 * e] * inv * f.x;
-            x[2 * e + 1] = x[2 * e + 1] * inv * f.y;
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = Pair<T>::widen(ww[e]);
+              x[2 * e] = x[2 * e] * inv * f.x;
+              x[2 * e + 1] = x[2 * e + 1] * inv * f.y;
+            }
           }
         }
-      }
-      if (a.rot_dim > 0) {
         if (a.interleaved) {
           if (turns) {
 #pragma unroll
@@ -238,44 +287,40 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
               x[2 * e + 1] = q * c[e] + p * s[e];
             }
           }
-        } else {
-          const bool second = l * 8 >= half;
-          const int lane = threadIdx.x & 31;
-          const int from = l * 8 < a.rot_dim ? (second ? lane - half / 8 : lane + half / 8) : lane;
+        } else if (half > 0) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float o = __shfl_sync(~0u, x[e], from);
-            if (turns) x[e] = second ? x[e] * c[e] + o * s[e] : x[e] * c[e] - o * s[e];
+            if (turns) x[e] = x[e] * c[e] + o * s[e];
           }
         }
-      }
-      if (r < heads && in) {
-        uint4 y = raw[i];
-        if (is_q || is_k)
+        if (kind < 2)
           y = make_uint4(Pair<T>::narrow(x[0], x[1]), Pair<T>::narrow(x[2], x[3]), Pair<T>::narrow(x[4], x[5]),
                          Pair<T>::narrow(x[6], x[7]));
-        if (is_q) {
-          if (!k.ok) y = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>((T*)a.q_out + (int64_t)t * a.qo_stride_t + (int64_t)h * a.qo_stride_h + l * 8) = y;
-        } else if (k.ok) {
-          T* cache = (T*)(is_k ? a.k_cache : a.v_cache);
-          *reinterpret_cast<uint4*>(cache + (int64_t)k.page * a.page_stride + (int64_t)k.slot * a.slot_stride +
-                                    (int64_t)h * a.head_stride + l * 8) = y;
-        }
+      }
+      if (r < heads && in && (k.ok || kind == 0)) {
+        if (!k.ok) y = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(table[r].dst + (kind == 0 ? out_at : cache_at) + l * 16) = y;
       }
     }
   }
   if (a.row_status)
-    for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += gridDim.x * kThreads) write_status(a, b);
+    for (int b = blockIdx.x * kThreads + tid; b < a.B; b += gridDim.x * kThreads) write_status(a, b);
 }
 
 template <class T>
-void launch_append(const AppendParams& P, bool fast, cudaStream_t st) {
+void launch_append(AppendParams P, bool fast, int sms, cudaStream_t st) {
   // without tokens the blocks only write statuses
-  const unsigned grid = P.a.T > 0 ? (unsigned)P.a.T : (unsigned)((P.a.B + kThreads - 1) / kThreads);
-  if (!fast)
-    append_any_kernel<T><<<grid, kThreads, 0, st>>>(P);
-  else if (P.a.D <= 64)
+  const int status_blocks = (P.a.B + kThreads - 1) / kThreads;
+  if (!fast) {
+    append_any_kernel<T><<<P.a.T > 0 ? P.a.T : status_blocks, kThreads, 0, st>>>(P);
+    return;
+  }
+  // one token a block while the blocks fit the device at once, more beyond
+  P.tokens = P.a.T / (sms * 8);
+  P.tokens = P.tokens < 1 ? 1 : P.tokens > kMaxTokens ? kMaxTokens : P.tokens;
+  const int grid = P.a.T > 0 ? (P.a.T + P.tokens - 1) / P.tokens : status_blocks;
+  if (P.a.D <= 64)
     append_kernel<T, 8><<<grid, kThreads, 0, st>>>(P);
   else if (P.a.D <= 128)
     append_kernel<T, 16><<<grid, kThreads, 0, st>>>(P);
@@ -301,19 +346,21 @@ extern "C" int clsample_kv_append(const clsample_kv_append_args_t* a, clsample_s
   if (a->T > 0 && (!a->k || !a->v || !a->k_cache || !a->v_cache || (a->Hq > 0 && (!a->q || !a->q_out)) ||
                    (a->rot_dim > 0 && !a->cos_sin)))
     return CLSAMPLE_ERR_NULL;
-  const int rc = check_device();
+  int sms = 0;
+  const int rc = check_device(nullptr, &sms);
   if (rc != CLSAMPLE_SUCCESS) return rc;
   const int64_t strides = a->q_stride_t | a->q_stride_h | a->k_stride_t | a->k_stride_h | a->v_stride_t |
                           a->v_stride_h | a->qo_stride_t | a->qo_stride_h | a->page_stride | a->slot_stride |
                           a->head_stride;
-  const bool fast = a->D % 8 == 0 && a->rot_dim % (a->interleaved ? 8 : 16) == 0 && (strides & 7) == 0 &&
+  const bool fast = a->Hq + 2 * a->Hkv <= kMaxHeads && a->D % 8 == 0 && a->rot_dim % (a->interleaved ? 8 : 16) == 0 && (strides & 7) == 0 &&
                     aligned16(a->q) && aligned16(a->k) && aligned16(a->v) && aligned16(a->q_out) &&
-                    aligned16(a->k_cache) && aligned16(a->v_cache) && aligned16(a->q_weight) && aligned16(a->k_weight);
-  const AppendParams P{*a};
+                    aligned16(a->k_cache) && aligned16(a->v_cache) && aligned16(a->q_weight) && aligned16(a->k_weight) &&
+                    aligned16(a->cos_sin) && a->cs_stride % 4 == 0;
+  const AppendParams P{*a, 1};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a->dtype == CLSAMPLE_T_BF16)
-    launch_append<__nv_bfloat16>(P, fast, st);
+    launch_append<__nv_bfloat16>(P, fast, sms, st);
   else
-    launch_append<__half>(P, fast, st);
+    launch_append<__half>(P, fast, sms, st);
   return cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
 }

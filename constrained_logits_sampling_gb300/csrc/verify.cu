@@ -3,10 +3,10 @@
 //
 // One cluster of CTAs per request.  Every CTA takes the accept decisions for itself (a few
 // gathered words), then sums the integer weights of its contiguous slice of the row to draw
-// from; the slices' sums meet in distributed shared memory, and the CTA whose slice holds
-// the threshold reads it once more, warp by warp, for the token.  Weights are integers, so
-// the token does not depend on the split.  Bound by memory: one row of p, and one of q
-// after a refusal, are read once from HBM.
+// from, each warp a contiguous part; the slices' sums meet in distributed shared memory, and
+// the CTA whose slice holds the threshold reads the part that holds it once more, a vector a
+// thread, for the token.  Weights are integers, so the token does not depend on the split.
+// Bound by memory: one row of p, and one of q after a refusal, are read once from HBM.
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
@@ -16,58 +16,215 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 262144;
 
-// 2^40 p as an integer for p in [0, 1]; the scaling is exact, the conversion truncates.
-__device__ __forceinline__ int64_t mass_of(float p) { return __float2ll_rz(p * 1099511627776.f); }
+// floor(2^40 p) for p in [0, 1], as hi 2^23 + lo, hi = floor(2^17 p) and lo = floor(2^23 times
+// the rest).  Adding 2^23 and truncating leaves an integer below 2^23 in a float's low bits;
+// the rest is exact.  Four float32 operations: a conversion to 64 bits would run in the
+// float64 unit, whose rate here bounds a call at four times the memory's time.
+constexpr int kIntBits = 0x4b000000;  // of 2^23
+struct Mass {
+  int hi, lo;  // with kIntBits added to each
+  __device__ __forceinline__ explicit Mass(float p) {
+    const float y = __fmaf_rz(p, 131072.f, 8388608.f);
+    const float rest = fmaf(p, 131072.f, -(y - 8388608.f));
+    hi = __float_as_int(y);
+    lo = __float_as_int(__fmaf_rz(rest, 8388608.f, 8388608.f));
+  }
+};
+__device__ __forceinline__ int64_t mass_of(int hi, int lo) { return ((int64_t)hi << 23) + lo; }
 
 __device__ __forceinline__ bool bad_prob(float p) { return !(p >= 0.f && p <= 1.f); }
+
+// Whether any of the probabilities seen was outside [0, 1] or NaN.
+struct Range {
+  float lo = 0.f, hi = 0.f;
+  __device__ __forceinline__ void see(float p) {
+    lo = fminf(lo, p);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(p));  // keeps a NaN
+  }
+  __device__ __forceinline__ void see(float p, float q) {
+    asm("min.f32 %0, %0, %1, %2;" : "+f"(lo) : "f"(p), "f"(q));
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(p), "f"(q));
+  }
+  __device__ __forceinline__ bool bad() const { return !(lo >= 0.f && hi <= 1.f); }
+};
 
 __device__ __forceinline__ float load_prob(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_prob(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
 
+__device__ __forceinline__ void widen16(const uint32_t (&w)[4], float (&x)[4], const float*) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void widen16(const uint32_t (&w)[4], float (&x)[8], const __nv_bfloat16*) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Pair<__nv_bfloat16>::widen(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+template <class P>
+__device__ __forceinline__ int misaligned(const P* row) {  // elements past a 16-byte boundary
+  return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(P));
+}
+
 // What is drawn from: the target row, less the draft's row (q) or less everything at one
-// token (hole), or neither.
+// token (hole), or neither.  The row is taken in 16-byte vectors that are aligned in p: vector
+// v has the tokens v N - a .. v N - a + N - 1, a = misaligned(p), those of them that exist.  q
+// may be aligned otherwise: its vector is then put together from the two that hold it.
 template <class P>
 struct Weights {
+  static constexpr int N = 16 / sizeof(P);
   const P* p;
   const P* q;
-  int hole;
-  __device__ __forceinline__ int64_t at(int t, bool* bad) const {
-    const float x = load_prob(p + t);
-    *bad |= bad_prob(x);
-    int64_t w = mass_of(x);
-    if (q) {
-      const float y = load_prob(q + t);
-      *bad |= bad_prob(y);
-      w = max(w - mass_of(y), (int64_t)0);
+  int hole, V, a, turn;  // turn: elements by which q's vectors lie later than p's
+  __device__ __forceinline__ void set(const P* p_row, const P* q_row, int hole_at, int vocab) {
+    p = p_row;
+    q = q_row;
+    hole = hole_at;
+    V = vocab;
+    a = misaligned(p);
+    turn = q ? (misaligned(q) - a) & (N - 1) : 0;
+  }
+  __device__ __forceinline__ int vectors() const { return (V + a + N - 1) / N; }
+  // vectors whose loads stay within the rows, in p and in q
+  __device__ __forceinline__ int whole_from() const { return (a + turn + N - 1) / N; }
+  __device__ __forceinline__ int whole_to() const { return max(0, (V + a - (turn ? N - turn : 0)) / N); }
+
+  // 16 bytes of a row from token t0 on, of which the aligned vector before starts `shift` earlier
+  __device__ __forceinline__ uint4 bits(const P* row, int t0, int shift) const {
+    const uint4* at = reinterpret_cast<const uint4*>(row + t0 - shift);
+    const uint4 v = __ldg(at);
+    if (shift == 0) return v;
+    const uint4 u = __ldg(at + 1);
+    uint32_t z[9] = {v.x, v.y, v.z, v.w, u.x, u.y, u.z, u.w, 0};
+    const int bytes = shift * (int)sizeof(P);
+    if (bytes & 8)
+#pragma unroll
+      for (int i = 0; i < 7; ++i) z[i] = z[i + 2];
+    if (bytes & 4)
+#pragma unroll
+      for (int i = 0; i < 7; ++i) z[i] = z[i + 1];
+    const int b = (bytes & 2) * 8;
+    return make_uint4(__funnelshift_r(z[0], z[1], b), __funnelshift_r(z[1], z[2], b), __funnelshift_r(z[2], z[3], b),
+                      __funnelshift_r(z[3], z[4], b));
+  }
+  __device__ __forceinline__ void unpack(uint4 v, float (&x)[N]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    widen16(w, x, p);
+  }
+  // a vector's tokens one by one, those that there are
+  __device__ __forceinline__ void edge(const P* row, int t0, float (&x)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = t0 + i >= 0 && t0 + i < V ? load_prob(row + t0 + i) : 0.f;
+  }
+  __device__ __forceinline__ void values(int v, float (&x)[N], float (&y)[N]) const {
+    const int t0 = v * N - a;
+    if (v >= whole_from() && v < whole_to()) {
+      unpack(bits(p, t0, 0), x);
+      if (q) unpack(bits(q, t0, turn), y);
+    } else {
+      edge(p, t0, x);
+      if (q) edge(q, t0, y);
     }
-    return t == hole ? 0 : w;
+  }
+  // The weights' sum.  Where p > q, P >= Q, and elsewhere P <= Q.
+  __device__ __forceinline__ int64_t sum_of(int v, const float (&x)[N], const float (&y)[N], Range* range) const {
+    int hi = 0, lo = 0;  // of at most eight weights
+    if (q) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        range->see(x[i], y[i]);
+        const Mass mp(x[i]), mq(y[i]);
+        if (x[i] > y[i]) {
+          hi += mp.hi - mq.hi;
+          lo += mp.lo - mq.lo;
+        }
+      }
+    } else {
+      const int t0 = v * N - a;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        range->see(x[i]);
+        const Mass mp(x[i]);
+        if (t0 + i != hole) {
+          hi += mp.hi - kIntBits;
+          lo += mp.lo - kIntBits;
+        }
+      }
+    }
+    return mass_of(hi, lo);
+  }
+  __device__ __forceinline__ void vector(int v, int64_t (&w)[N]) const {
+    float x[N], y[N];
+    values(v, x, y);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const Mass mp(x[i]), mq(q ? y[i] : 0.f);
+      w[i] = (q && x[i] <= y[i]) || v * N - a + i == hole ? 0 : mass_of(mp.hi - mq.hi, mp.lo - mq.lo);
+    }
+  }
+  // Sum over the vectors first, first + 32, .. below `end`, four of them in flight.
+  __device__ __forceinline__ int64_t sum_range(int first, int end, Range* range) const {
+    constexpr int kAhead = 4;
+    const int lane = threadIdx.x & 31, from = whole_from(), to = min(end, whole_to());
+    int64_t sum = 0;
+    for (int v0 = first; v0 < end; v0 += 32 * kAhead) {  // uniform over the warp
+      if (v0 >= from && v0 + 32 * kAhead <= to) {
+        uint4 x4[kAhead], y4[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x4[k] = bits(p, (v0 + 32 * k + lane) * N - a, 0);
+        if (q) {
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) y4[k] = bits(q, (v0 + 32 * k + lane) * N - a, turn);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          float x[N], y[N];
+          unpack(x4[k], x);
+          unpack(y4[k], y);
+          sum += sum_of(v0 + 32 * k + lane, x, y, range);
+        }
+      } else {
+#pragma unroll 1
+        for (int v = v0 + lane; v < min(end, v0 + 32 * kAhead); v += 32) {
+          float x[N], y[N];
+          values(v, x, y);
+          sum += sum_of(v, x, y, range);
+        }
+      }
+    }
+    return sum;
   }
 };
 
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+__device__ __forceinline__ int64_t warp_total(int64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
 
 struct Shared {
-  int64_t slice_sum[kCluster];  // written by the cluster's CTAs
-  int slice_bad[kCluster];
-  int64_t warp_sum[kWarps];
+  int64_t slice_sum[kMaxCluster];  // written by the cluster's CTAs
+  int slice_bad[kMaxCluster];
+  int64_t warp_sum[kWarps], scan[kWarps];
   int first;  // first refused drafted token, or n
   int bad;
 };
 
-template <class P>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(clsample_verify_args_t a) {
+template <class P, int C>
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ clsample_verify_args_t a) {
+  using W = Weights<P>;
+  constexpr int N = W::N;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
-  const int b = blockIdx.x / kCluster;
+  const int b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ Shared sh;
   // a CTA's shared memory may be written from afar only once it has started
@@ -106,29 +263,28 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(clsample_verify_arg
   const bool refused = acc < n;
   cluster.barrier_wait();
 
-  const int share = (a.V + kCluster - 1) / kCluster;
-  const int s0 = min(a.V, rank * share), s1 = min(a.V, s0 + share);
-  // each warp sums a contiguous part of the slice
-  const int part = (s1 - s0 + kWarps - 1) / kWarps;
-  const int w0 = min(s1, s0 + warp * part), w1 = min(s1, w0 + part);
-  Weights<P> w{};
+  W w{};
   int64_t total = 0, before = 0;
+  int begin = 0, end = 0, part = 0;  // the slice's vectors, and how many of them a warp has
   if (!bad) {  // uniform over the cluster: every CTA took the same decisions
-    w.p = target + (int64_t)(lo + b + acc) * a.target_stride;
-    w.q = refused && draft ? draft + (int64_t)(lo + acc) * a.draft_stride : nullptr;
-    w.hole = refused && !draft ? __ldg(a.draft_tokens + lo + acc) : -1;
+    w.set(target + (int64_t)(lo + b + acc) * a.target_stride,
+          refused && draft ? draft + (int64_t)(lo + acc) * a.draft_stride : nullptr,
+          refused && !draft ? __ldg(a.draft_tokens + lo + acc) : -1, a.V);
     for (int pass = 0; pass < 2; ++pass) {
-      int64_t sum = 0;
-      bool odd = false;
-      for (int t = w0 + lane; t < w1; t += 32) sum += w.at(t, &odd);
-      sum = warp_sum(sum);
-      odd = __any_sync(~0u, odd);
+      const int share = (w.vectors() + C - 1) / C;
+      begin = min(w.vectors(), rank * share);
+      end = min(w.vectors(), begin + share);
+      part = (share + kWarps - 1) / kWarps;
+      const int w0 = min(end, begin + warp * part), w1 = min(end, w0 + part);
+      Range range;
+      const int64_t sum = warp_total(w.sum_range(w0, w1, &range));
+      const bool odd = __any_sync(~0u, range.bad());
       if (lane == 0) {
         sh.warp_sum[warp] = sum;
         if (odd) atomicOr(&sh.bad, 1);
       }
       __syncthreads();
-      if (tid < kCluster) {
+      if (tid < C) {
         int64_t mine = 0;
         for (int i = 0; i < kWarps; ++i) mine += sh.warp_sum[i];
         Shared* other = cluster.map_shared_rank(&sh, tid);
@@ -137,15 +293,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(clsample_verify_arg
       }
       cluster.sync();
       total = before = 0;
-      for (int i = 0; i < kCluster; ++i) {
+      for (int i = 0; i < C; ++i) {
         if (i < rank) before += sh.slice_sum[i];
         total += sh.slice_sum[i];
         bad |= sh.slice_bad[i] != 0;
       }
       if (total > 0 || bad || (!w.q && w.hole < 0)) break;
       // nothing of p is above q: draw from p itself
-      w.q = nullptr;
-      w.hole = -1;
+      w.set(w.p, nullptr, -1, a.V);
       cluster.sync();  // the sums have been read by all before they are written again
     }
     bad |= total == 0;
@@ -166,39 +321,59 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(clsample_verify_arg
   const int64_t k = u31 * (total >> 31) + ((u31 * (total & 0x7fffffff)) >> 31);
   int64_t left = k - before;
   if (left < 0 || left >= sh.slice_sum[rank]) return;  // another slice's
-  for (int i = 0; i < warp; ++i) left -= sh.warp_sum[i];
-  if (left < 0 || left >= sh.warp_sum[warp]) return;  // another warp's
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    bool odd = false;
-    const int64_t v = t0 + lane < w1 ? w.at(t0 + lane, &odd) : 0;
-    int64_t run = v;
+  int at = 0;  // the warp whose part holds the threshold
+  while (left >= sh.warp_sum[at]) left -= sh.warp_sum[at++];
+  const int p0 = begin + at * part, p1 = min(end, p0 + part);
+  for (int v0 = p0; v0 < p1; v0 += kThreads) {  // uniform over the CTA
+    const int v = v0 + tid;
+    int64_t x[N];
+    int64_t mine = 0;
+    if (v < p1) {
+      w.vector(v, x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) mine += x[i];
+    }
+    int64_t run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(~0u, run, o);
       if (lane >= o) run += up;
     }
-    const unsigned above = __ballot_sync(~0u, run > left);
-    if (above) {
-      if (lane == __ffs(above) - 1) out[acc] = t0 + lane;
-      return;
+    __syncthreads();
+    if (lane == 31) sh.scan[warp] = run;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) run += sh.scan[i];
+      all += sh.scan[i];
     }
-    left -= __shfl_sync(~0u, run, 31);
+    if (mine > 0 && run > left && run - mine <= left) {
+      int64_t c = run - mine;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (c <= left && left < c + x[i]) out[acc] = v * N - w.a + i;
+        c += x[i];
+      }
+    }
+    if (all > left) return;
+    left -= all;
   }
 }
 
-template <class P>
+template <class P, int C>
 cudaError_t launch_verify(const clsample_verify_args_t& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.B * kCluster);
+  cfg.gridDim = dim3((unsigned)a.B * C);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCluster;
+  at[0].val.clusterDim.x = C;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<P>, a);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<P, C>, a);
 }
 
 }  // namespace
@@ -220,6 +395,7 @@ extern "C" int clsample_verify(const clsample_verify_args_t* a, clsample_stream_
   if (rc != CLSAMPLE_SUCCESS) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      a->dtype == CLSAMPLE_LOGITS_F32 ? launch_verify<float>(*a, st) : launch_verify<__nv_bfloat16>(*a, st);
+      a->dtype == CLSAMPLE_LOGITS_F32 ? launch_verify<float, kMaxCluster>(*a, st)
+                                      : launch_verify<__nv_bfloat16, kMaxCluster>(*a, st);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
 }

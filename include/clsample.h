@@ -333,7 +333,8 @@ enum { CLSAMPLE_T_BF16 = 0, CLSAMPLE_T_F16 = 1 };
  * is not valid, is not written to the cache and its q_out row is zero; its sequence is
  * INVALID.  Two tokens of a call must not share a slot.
  * Limits: 1 <= D <= 256, rot_dim even and <= D, any strides.  Fast path: D, rot_dim (and
- * rot_dim/2 in the half-split form) multiples of 8, arrays and strides multiples of 16 bytes. */
+ * rot_dim/2 in the half-split form) multiples of 8, arrays and strides multiples of 16 bytes,
+ * at most 256 heads in all. */
 typedef struct {
   int32_t B, T, Hq, Hkv, D;
   int32_t dtype;
