@@ -16,9 +16,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kBatch = 128;  // vectors of a warp between two marks
 constexpr int kMaxVocab = 262144;
 
 // floor(2^40 p) for p in [0, 1], as hi 2^23 + lo, hi = floor(2^17 p) and lo = floor(2^23 times
@@ -170,22 +172,23 @@ struct Weights {
       w[i] = (q && x[i] <= y[i]) || v * N - a + i == hole ? 0 : mass_of(mp.hi - mq.hi, mp.lo - mq.lo);
     }
   }
-  // Sum over the vectors first, first + 32, .. below `end`, four of them in flight.
-  __device__ __forceinline__ int64_t sum_range(int first, int end, Range* range) const {
-    constexpr int kAhead = 4;
+  // Sum over a warp's vectors first .. end - 1, kBatch at a time with four loads of each row in
+  // flight; the lane's sum of each batch is left in marks[batch * kThreads].
+  __device__ __forceinline__ int64_t sum_range(int first, int end, Range* range, int64_t* marks) const {
     const int lane = threadIdx.x & 31, from = whole_from(), to = min(end, whole_to());
-    int64_t sum = 0;
-    for (int v0 = first; v0 < end; v0 += 32 * kAhead) {  // uniform over the warp
-      if (v0 >= from && v0 + 32 * kAhead <= to) {
-        uint4 x4[kAhead], y4[kAhead];
+    int64_t total = 0;
+    for (int v0 = first; v0 < end; v0 += kBatch) {  // uniform over the warp
+      int64_t sum = 0;
+      if (v0 >= from && v0 + kBatch <= to) {
+        uint4 x4[4], y4[4];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) x4[k] = bits(p, (v0 + 32 * k + lane) * N - a, 0);
+        for (int k = 0; k < 4; ++k) x4[k] = bits(p, (v0 + 32 * k + lane) * N - a, 0);
         if (q) {
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) y4[k] = bits(q, (v0 + 32 * k + lane) * N - a, turn);
+          for (int k = 0; k < 4; ++k) y4[k] = bits(q, (v0 + 32 * k + lane) * N - a, turn);
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
+        for (int k = 0; k < 4; ++k) {
           float x[N], y[N];
           unpack(x4[k], x);
           unpack(y4[k], y);
@@ -193,14 +196,17 @@ struct Weights {
         }
       } else {
 #pragma unroll 1
-        for (int v = v0 + lane; v < min(end, v0 + 32 * kAhead); v += 32) {
+        for (int v = v0 + lane; v < min(end, v0 + kBatch); v += 32) {
           float x[N], y[N];
           values(v, x, y);
           sum += sum_of(v, x, y, range);
         }
       }
+      *marks = sum;
+      marks += kThreads;
+      total += sum;
     }
-    return sum;
+    return total;
   }
 };
 
@@ -219,7 +225,7 @@ struct Shared {
 };
 
 template <class P, int C>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ clsample_verify_args_t a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const __grid_constant__ clsample_verify_args_t a) {
   using W = Weights<P>;
   constexpr int N = W::N;
   cg::cluster_group cluster = cg::this_cluster();
@@ -227,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
   const int b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ Shared sh;
+  extern __shared__ int64_t marks[];  // each thread's sums of its warp's batches
   // a CTA's shared memory may be written from afar only once it has started
   cluster.barrier_arrive();
 
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
       part = (share + kWarps - 1) / kWarps;
       const int w0 = min(end, begin + warp * part), w1 = min(end, w0 + part);
       Range range;
-      const int64_t sum = warp_total(w.sum_range(w0, w1, &range));
+      const int64_t sum = warp_total(w.sum_range(w0, w1, &range, marks + tid));
       const bool odd = __any_sync(~0u, range.bad());
       if (lane == 0) {
         sh.warp_sum[warp] = sum;
@@ -323,42 +330,56 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
   if (left < 0 || left >= sh.slice_sum[rank]) return;  // another slice's
   int at = 0;  // the warp whose part holds the threshold
   while (left >= sh.warp_sum[at]) left -= sh.warp_sum[at++];
-  const int p0 = begin + at * part, p1 = min(end, p0 + part);
-  for (int v0 = p0; v0 < p1; v0 += kThreads) {  // uniform over the CTA
-    const int v = v0 + tid;
-    int64_t x[N];
-    int64_t mine = 0;
-    if (v < p1) {
-      w.vector(v, x);
+  // the batch of that warp: lane i adds up batch i
+  int p0 = begin + at * part;
+  const int p1 = min(end, p0 + part);
+  const int batches = (p1 - p0 + kBatch - 1) / kBatch;  // at most 32
+  int64_t run = 0;
+  if (lane < batches)
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) run += marks[lane * kThreads + at * 32 + (i + lane) % 32];
+  const int64_t batch_sum = run;
 #pragma unroll
-      for (int i = 0; i < N; ++i) mine += x[i];
-    }
-    int64_t run = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(~0u, run, o);
-      if (lane >= o) run += up;
-    }
-    __syncthreads();
-    if (lane == 31) sh.scan[warp] = run;
-    __syncthreads();
-    int64_t all = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) run += sh.scan[i];
-      all += sh.scan[i];
-    }
-    if (mine > 0 && run > left && run - mine <= left) {
-      int64_t c = run - mine;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (c <= left && left < c + x[i]) out[acc] = v * N - w.a + i;
-        c += x[i];
-      }
-    }
-    if (all > left) return;
-    left -= all;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(~0u, run, o);
+    if (lane >= o) run += up;
   }
+  const int batch = __ffs(__ballot_sync(~0u, run > left)) - 1;
+  left -= __shfl_sync(~0u, run - batch_sum, batch);
+  p0 += batch * kBatch;
+  // the token, a vector a thread
+  const int v = p0 + tid;
+  int64_t x[N], mine = 0;
+  if (tid < kBatch && v < p1) {
+    w.vector(v, x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine += x[i];
+  }
+  run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(~0u, run, o);
+    if (lane >= o) run += up;
+  }
+  if (lane == 31) sh.scan[warp] = run;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) run += sh.scan[i];
+  if (run > left && run - mine <= left) {
+    int64_t c = run - mine;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (c <= left && left < c + x[i]) out[acc] = v * N - w.a + i;
+      c += x[i];
+    }
+  }
+}
+
+// Shared memory for the marks: a row may take one vector more than its tokens fill.
+template <class P, int C>
+int marks_bytes(int V) {
+  constexpr int N = 16 / sizeof(P);
+  const int vectors = (V + 2 * N - 2) / N, share = (vectors + C - 1) / C, part = (share + kWarps - 1) / kWarps;
+  return (part + kBatch - 1) / kBatch * kThreads * (int)sizeof(int64_t);
 }
 
 template <class P, int C>
@@ -366,6 +387,7 @@ cudaError_t launch_verify(const clsample_verify_args_t& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.B * C);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)marks_bytes<P, C>(a.V);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -373,7 +395,19 @@ cudaError_t launch_verify(const clsample_verify_args_t& a, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<P, C>, a);
+  const cudaError_t e = cudaFuncSetAttribute(verify_kernel<P, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             marks_bytes<P, C>(kMaxVocab));
+  return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, verify_kernel<P, C>, a) : e;
+}
+
+// The largest cluster with which all requests are resident at once: one wave, each request
+// over as many SMs as that leaves it.
+template <class P>
+cudaError_t launch_verify(const clsample_verify_args_t& a, int sms, cudaStream_t st) {
+  const int64_t slots = (int64_t)sms * kCtasPerSm;
+  if (a.B * (int64_t)8 <= slots) return launch_verify<P, 8>(a, st);
+  if (a.B * (int64_t)4 <= slots) return launch_verify<P, 4>(a, st);
+  return launch_verify<P, 2>(a, st);
 }
 
 }  // namespace
@@ -391,11 +425,11 @@ extern "C" int clsample_verify(const clsample_verify_args_t* a, clsample_stream_
   if (a->B == 0) return CLSAMPLE_SUCCESS;
   if (!a->target || !a->cu_draft || !a->u_sample || !a->tokens || (a->N > 0 && (!a->draft_tokens || !a->u_accept)))
     return CLSAMPLE_ERR_NULL;
-  const int rc = check_device();
+  int sms = 0;
+  const int rc = check_device(nullptr, &sms);
   if (rc != CLSAMPLE_SUCCESS) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      a->dtype == CLSAMPLE_LOGITS_F32 ? launch_verify<float, kMaxCluster>(*a, st)
-                                      : launch_verify<__nv_bfloat16, kMaxCluster>(*a, st);
+      a->dtype == CLSAMPLE_LOGITS_F32 ? launch_verify<float>(*a, sms, st) : launch_verify<__nv_bfloat16>(*a, sms, st);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
 }
