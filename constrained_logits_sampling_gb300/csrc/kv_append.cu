@@ -9,9 +9,10 @@ namespace clsample {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 4;  // of the fast path
 
-constexpr int kMaxTokens = kThreads / 32;  // of a block: one a warp
-constexpr int kMaxHeads = 256;             // Hq + 2 Hkv of the fast path
+constexpr int kMaxTokens = 16;   // of a block
+constexpr int kMaxHeads = 256;   // Hq + 2 Hkv of the fast path
 
 struct AppendParams {
   clsample_kv_append_args_t a;
@@ -162,8 +163,10 @@ struct HeadRow {
 // are loaded while the one before it is worked on.  Addresses come from a table in shared
 // memory: with the selection between q, k and v in each row the instructions took longer than
 // the memory.
-template <class T, int G>
-__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendParams P) {
+// kPaired, for the usual case of a whole head rotated in halves: lane l has elements 4l .. 4l + 3
+// of both halves instead, so that pairs meet in a lane and nothing is exchanged.
+template <class T, int G, bool kPaired>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __grid_constant__ AppendParams P) {
   const clsample_kv_append_args_t& a = P.a;
   constexpr int kGroups = kThreads / G;
   constexpr int kUnroll = 3;  // head rows of a group in flight
@@ -196,22 +199,28 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
       const int r = r0 + i * kGroups + group;
       raw[i] = make_uint4(0, 0, 0, 0);
       if (r < heads && in) {
-        const HeadRow& h = table[r];
-        raw[i] = *reinterpret_cast<const uint4*>(h.src + token * h.src_stride + l * 16);
+        const unsigned char* src = table[r].src + token * table[r].src_stride;
+        if (kPaired) {
+          const uint2 x = *reinterpret_cast<const uint2*>(src + l * 8);
+          const uint2 y = *reinterpret_cast<const uint2*>(src + a.D + l * 8);  // D / 2 elements further
+          raw[i] = make_uint4(x.x, x.y, y.x, y.y);
+        } else {
+          raw[i] = *reinterpret_cast<const uint4*>(src + l * 16);
+        }
       }
     }
   };
   if (count > 0) fetch(0, 0);
-  if (warp < count) {
-    const Token k = find_token(a, t0 + warp);
-    if (lane == 0) tokens[warp] = k;
+  for (int i = warp; i < count; i += kThreads / 32) {
+    const Token k = find_token(a, t0 + i);
+    if (lane == 0) tokens[i] = k;
   }
   __syncthreads();
 
   // the lane that holds the other elements of this one's pairs; where it is the second of them
   const bool second = !a.interleaved && l * 8 >= half;
   const int from = !a.interleaved && l * 8 < a.rot_dim ? (second ? lane - half / 8 : lane + half / 8) : lane;
-  const int turn_at = a.interleaved ? l * 4 : second ? l * 8 - half : l * 8;
+  const int turn_at = kPaired || a.interleaved ? l * 4 : second ? l * 8 - half : l * 8;
   const bool norm = a.q_weight || a.k_weight;
 
   for (int token = 0, r0 = 0; token < count;) {
@@ -233,10 +242,10 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
       const float* cs = a.cos_sin + (int64_t)k.pos * a.cs_stride + turn_at;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        if (e == 0 || !a.interleaved) {
+        if (e == 0 || (!kPaired && !a.interleaved)) {
           const float4 x = __ldg(reinterpret_cast<const float4*>(cs + 4 * e));
           const float4 y = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * e));
-          const float sign = second || a.interleaved ? 1.f : -1.f;
+          const float sign = kPaired || second || a.interleaved ? 1.f : -1.f;
           c[4 * e] = x.x, c[4 * e + 1] = x.y, c[4 * e + 2] = x.z, c[4 * e + 3] = x.w;
           s[4 * e] = y.x * sign, s[4 * e + 1] = y.y * sign, s[4 * e + 2] = y.z * sign, s[4 * e + 3] = y.w * sign;
         }
@@ -268,8 +277,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
           for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
           if (w && in) {
             const float inv = rsqrtf(ss / (float)a.D + a.eps);
-            const uint4 wr = __ldg(reinterpret_cast<const uint4*>(w + l * 8));
-            const uint32_t ww[4] = {wr.x, wr.y, wr.z, wr.w};
+            const uint2 wa = __ldg(reinterpret_cast<const uint2*>(kPaired ? w + l * 4 : w + l * 8));
+            const uint2 wb = __ldg(reinterpret_cast<const uint2*>(kPaired ? w + half + l * 4 : w + l * 8 + 4));
+            const uint32_t ww[4] = {wa.x, wa.y, wb.x, wb.y};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 f = Pair<T>::widen(ww[e]);
@@ -278,7 +288,16 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
             }
           }
         }
-        if (a.interleaved) {
+        if (kPaired) {
+          if (turns) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p = x[e], q = x[e + 4];
+              x[e] = p * c[e] - q * s[e];
+              x[e + 4] = q * c[e] + p * s[e];
+            }
+          }
+        } else if (a.interleaved) {
           if (turns) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -300,7 +319,13 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
       }
       if (r < heads && in && (k.ok || kind == 0)) {
         if (!k.ok) y = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(table[r].dst + (kind == 0 ? out_at : cache_at) + l * 16) = y;
+        unsigned char* dst = table[r].dst + (kind == 0 ? out_at : cache_at);
+        if (kPaired) {
+          *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(y.x, y.y);
+          *reinterpret_cast<uint2*>(dst + a.D + l * 8) = make_uint2(y.z, y.w);
+        } else {
+          *reinterpret_cast<uint4*>(dst + l * 16) = y;
+        }
       }
     }
   }
@@ -316,16 +341,15 @@ void launch_append(AppendParams P, bool fast, int sms, cudaStream_t st) {
     append_any_kernel<T><<<P.a.T > 0 ? P.a.T : status_blocks, kThreads, 0, st>>>(P);
     return;
   }
-  // one token a block while the blocks fit the device at once, more beyond
-  P.tokens = P.a.T / (sms * 8);
+  // as many tokens a block as it takes for the blocks to fit the device at once
+  P.tokens = (P.a.T + sms * kBlocksPerSm - 1) / (sms * kBlocksPerSm);
   P.tokens = P.tokens < 1 ? 1 : P.tokens > kMaxTokens ? kMaxTokens : P.tokens;
   const int grid = P.a.T > 0 ? (P.a.T + P.tokens - 1) / P.tokens : status_blocks;
-  if (P.a.D <= 64)
-    append_kernel<T, 8><<<grid, kThreads, 0, st>>>(P);
-  else if (P.a.D <= 128)
-    append_kernel<T, 16><<<grid, kThreads, 0, st>>>(P);
-  else
-    append_kernel<T, 32><<<grid, kThreads, 0, st>>>(P);
+  const bool paired = P.a.rot_dim == P.a.D && !P.a.interleaved;
+  auto* fn = P.a.D <= 64    ? (paired ? append_kernel<T, 8, true> : append_kernel<T, 8, false>)
+             : P.a.D <= 128 ? (paired ? append_kernel<T, 16, true> : append_kernel<T, 16, false>)
+                            : (paired ? append_kernel<T, 32, true> : append_kernel<T, 32, false>);
+  fn<<<grid, kThreads, 0, st>>>(P);
 }
 
 }  // namespace
