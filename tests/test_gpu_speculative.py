@@ -476,3 +476,45 @@ def test_verify_refusals(S):
     with pytest.raises(Exception) as e:
         op(t, x, cu, u, ul, max_draft=-1)
     assert isinstance(e.value, (ValueError, RuntimeError))
+
+
+# ----------------------------------------------------------------------------- together
+
+def test_example_step(S):
+    """The example's loop: verified tokens are those of the rule on the probabilities that the
+    step used, and logits of a chunk equal those of its tokens one by one on a second cache
+    within the rounding of the chunk's bf16 activations."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "speculative_step.py")
+    spec = importlib.util.spec_from_file_location("speculative_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    B, V, k = 3, 500, 3
+    shape = dict(vocab=V, Hq=4, Hkv=2, D=64, batch=B, max_len=128)
+    target, draft = ex.Decoder(layers=2, seed=0, **shape), ex.Decoder(layers=1, seed=0, **shape)
+    loop = ex.SpeculativeLoop(target, draft, V, B, k)
+    loop.prefill([[1, 2, 3, 4], [5] * 20, list(range(40, 97))])
+    for _ in range(5):
+        before = loop.lens.clone()
+        out = loop.step()
+        torch.cuda.synchronize()
+        used = {n: t.cpu().numpy() if torch.is_tensor(t) else t for n, t in loop.used.items()}
+        tokens, accepted = R.verify(used["target_probs"], used["draft_probs"], used["draft_tokens"], used["cu_draft"],
+                                    used["u_accept"], used["u_sample"], k)
+        assert np.array_equal(out["tokens"].cpu().numpy(), tokens)
+        assert np.array_equal(out["accepted"].cpu().numpy(), accepted)
+        assert torch.equal(loop.lens.cpu(), before.cpu() + 1 + torch.from_numpy(accepted))
+    # the same weights, one token at a time
+    chunk, single = ex.Decoder(layers=2, seed=3, **shape), ex.Decoder(layers=2, seed=3, **shape)
+    n = 40
+    ids = torch.randint(0, V, (B, n), generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    one = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    got = chunk(ids.reshape(-1).contiguous(), one * n, torch.full((B,), n, dtype=torch.int32, device="cuda"), n)
+    got = got.view(B, n, V)
+    for i in range(n):
+        want = single(ids[:, i].contiguous(), one, torch.full((B,), i + 1, dtype=torch.int32, device="cuda"), 1)
+        # both round their activations to bf16 (2^-8) some twenty times along the two layers;
+        # such errors add up like their square root, and a logit is a sum over the row
+        size = want.norm(dim=1, keepdim=True) / V ** 0.5
+        assert ((got[:, i] - want).abs() <= 8 * 2.0 ** -8 * 20 ** 0.5 * size).all(), i
