@@ -120,13 +120,17 @@ template <int R, int K, int NT>
 __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit* u, int64_t* unit_begin) {
   using M = UnitMap<R, K>;
   __shared__ int64_t buf[NT / 32 + 1];
-  __shared__ int64_t found_rest;
-  __shared__ int found_b;
+  __shared__ Unit found;
+  __shared__ int64_t found_begin;
   const int tid = threadIdx.x, B = P.a.B;
-  int64_t total = 0, ex = 0, mine = 0;
+  // thread i has the sequences i, i + NT, ..; of up to NT they are read once
+  Seq s{0, 0, 0, false};
+  int64_t total = 0, ex = 0, per_head = 0;
   for (int base = 0; base < B; base += NT) {
-    mine = base + tid < B ? M::head_tiles(P, M::seq_of(P, base + tid)) * P.a.Hkv : 0;
-    total += block_scan<NT>(mine, buf, &ex);
+    s.n = 0;
+    if (base + tid < B) s = M::seq_of(P, base + tid);
+    per_head = M::head_tiles(P, s);
+    total += block_scan<NT>(per_head * P.a.Hkv, buf, &ex);
   }
   span->total = total;
   span->ctas = (int)min((int64_t)gridDim.x, total);
@@ -135,31 +139,33 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
   span->t1 = span_begin(total, span->ctas, blockIdx.x + 1);
   int64_t seen = 0;
   for (int base = 0; base < B; base += NT) {
+    int64_t sum = total;
     if (B > NT) {
-      mine = base + tid < B ? M::head_tiles(P, M::seq_of(P, base + tid)) * P.a.Hkv : 0;
+      s.n = 0;
+      if (base + tid < B) s = M::seq_of(P, base + tid);
+      per_head = M::head_tiles(P, s);
+      sum = block_scan<NT>(per_head * P.a.Hkv, buf, &ex);
     }
-    const int64_t sum = block_scan<NT>(mine, buf, &ex);
-    if (seen + ex <= span->t0 && span->t0 < seen + ex + mine) {
-      found_b = base + tid;
-      found_rest = span->t0 - (seen + ex);
+    int64_t rest = span->t0 - (seen + ex);
+    if (rest >= 0 && rest < per_head * P.a.Hkv) {  // in this thread's sequence
+      Unit v;
+      v.b = base + tid;
+      v.h = (int)quotient(rest, per_head);
+      rest -= v.h * per_head;
+      for (int qt = 0;; ++qt) {
+        M::fill(P, s, qt, &v);
+        if (rest < v.tiles) break;
+        rest -= v.tiles;
+      }
+      found = v;
+      found_begin = span->t0 - rest;
     }
     seen += sum;
     if (seen > span->t0) break;  // uniform
   }
   __syncthreads();
-  const int b = found_b;
-  const Seq s = M::seq_of(P, b);
-  const int64_t per_head = M::head_tiles(P, s);
-  int64_t rest = found_rest;
-  u->b = b;
-  u->h = (int)quotient(rest, per_head);
-  rest -= u->h * per_head;
-  for (int qt = 0;; ++qt) {
-    M::fill(P, s, qt, u);
-    if (rest < u->tiles) break;
-    rest -= u->tiles;
-  }
-  *unit_begin = span->t0 - rest;
+  *u = found;
+  *unit_begin = found_begin;
   return true;
 }
 
