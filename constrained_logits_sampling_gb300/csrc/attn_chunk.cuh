@@ -253,21 +253,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
           };
-          // the first half is computed before the tile's maximum is known, which hardly ever
-          // calls for another reference, so that the two overlap
-          sums[0] = sums[1] = 0;
-          weights(0);
-          float tops[4];
+          // The first half is computed before the tile's maximum is known, so that the two
+          // overlap; where the maximum calls for another reference (hardly ever after a unit's
+          // first tile), once more.
+          while (true) {
+            sums[0] = sums[1] = 0;
+            weights(0);
+            float tops[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tops[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+            for (int i = 0; i < 4; ++i) tops[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
 #pragma unroll
-          for (int c = 8; c < 128; c += 8)
+            for (int c = 8; c < 128; c += 8)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              tops[i] = max3(tops[i], __uint_as_float(x[c + i]), __uint_as_float(x[c + 4 + i]));
-          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * P.scale_log2;
-          const bool grow = top > m + kRescaleAt || (m == neg_inf && top > neg_inf);
-          if (__any_sync(~0u, grow)) {
+              for (int i = 0; i < 4; ++i)
+                tops[i] = max3(tops[i], __uint_as_float(x[c + i]), __uint_as_float(x[c + 4 + i]));
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * P.scale_log2;
+            const bool grow = top > m + kRescaleAt || (m == neg_inf && top > neg_inf);
+            if (!__any_sync(~0u, grow)) break;
             const float keep = grow ? exp2_fast(m - top) : 1.f;
             if (grow) m = top;
             l *= keep;
@@ -281,8 +283,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tmem_st16(o_tmem + c * 16, y);
               }
             }
-            sums[0] = sums[1] = 0;
-            weights(0);
           }
           hand_over(0, &sh.p_half[w]);  // the product starts on the first 64 keys
           weights(64);
