@@ -25,16 +25,26 @@ constexpr int kMaxVocab = 262144;
 
 // floor(2^40 p) for p in [0, 1], as hi 2^23 + lo, hi = floor(2^17 p) and lo = floor(2^23 times
 // the rest).  Adding 2^23 and truncating leaves an integer below 2^23 in a float's low bits;
-// the rest is exact.  Four float32 operations: a conversion to 64 bits would run in the
-// float64 unit, whose rate here bounds a call at four times the memory's time.
+// the rest is exact.  Four float32 operations, on two numbers at once: a conversion to 64 bits
+// would run in the float64 unit, whose rate here bounds a call at four times the memory's time.
 constexpr int kIntBits = 0x4b000000;  // of 2^23
-struct Mass {
-  int hi, lo;  // with kIntBits added to each
-  __device__ __forceinline__ explicit Mass(float p) {
-    const float y = __fmaf_rz(p, 131072.f, 8388608.f);
-    const float rest = fmaf(p, 131072.f, -(y - 8388608.f));
-    hi = __float_as_int(y);
-    lo = __float_as_int(__fmaf_rz(rest, 8388608.f, 8388608.f));
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+struct Mass2 {
+  int hi[2], lo[2];  // with kIntBits added to each
+  __device__ __forceinline__ Mass2(float p0, float p1) {
+    const uint64_t p = two(p0, p1), k17 = two(131072.f, 131072.f), k23 = two(8388608.f, 8388608.f);
+    const uint64_t minus = two(-1.f, -1.f);
+    uint64_t y, rest, z;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(p), "l"(k17), "l"(k23));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rest) : "l"(y), "l"(minus), "l"(k23));  // -hi
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rest) : "l"(p), "l"(k17), "l"(rest));
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(z) : "l"(rest), "l"(k23), "l"(k23));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(hi[0]), "=r"(hi[1]) : "l"(y));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo[0]), "=r"(lo[1]) : "l"(z));
   }
 };
 __device__ __forceinline__ int64_t mass_of(int hi, int lo) { return ((int64_t)hi << 23) + lo; }
@@ -44,13 +54,9 @@ __device__ __forceinline__ bool bad_prob(float p) { return !(p >= 0.f && p <= 1.
 // Whether any of the probabilities seen was outside [0, 1] or NaN.
 struct Range {
   float lo = 0.f, hi = 0.f;
-  __device__ __forceinline__ void see(float p) {
-    lo = fminf(lo, p);
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(p));  // keeps a NaN
-  }
   __device__ __forceinline__ void see(float p, float q) {
     asm("min.f32 %0, %0, %1, %2;" : "+f"(lo) : "f"(p), "f"(q));
-    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(p), "f"(q));
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(p), "f"(q));  // keeps a NaN
   }
   __device__ __forceinline__ bool bad() const { return !(lo >= 0.f && hi <= 1.f); }
 };
@@ -141,24 +147,29 @@ struct Weights {
     int hi = 0, lo = 0;  // of at most eight weights
     if (q) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
+      for (int i = 0; i < N; i += 2) {
         range->see(x[i], y[i]);
-        const Mass mp(x[i]), mq(y[i]);
-        if (x[i] > y[i]) {
-          hi += mp.hi - mq.hi;
-          lo += mp.lo - mq.lo;
-        }
+        range->see(x[i + 1], y[i + 1]);
+        const Mass2 mp(x[i], x[i + 1]), mq(y[i], y[i + 1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (x[i + e] > y[i + e]) {
+            hi += mp.hi[e] - mq.hi[e];
+            lo += mp.lo[e] - mq.lo[e];
+          }
       }
     } else {
       const int t0 = v * N - a;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        range->see(x[i]);
-        const Mass mp(x[i]);
-        if (t0 + i != hole) {
-          hi += mp.hi - kIntBits;
-          lo += mp.lo - kIntBits;
-        }
+      for (int i = 0; i < N; i += 2) {
+        range->see(x[i], x[i + 1]);
+        const Mass2 mp(x[i], x[i + 1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (t0 + i + e != hole) {
+            hi += mp.hi[e] - kIntBits;
+            lo += mp.lo[e] - kIntBits;
+          }
       }
     }
     return mass_of(hi, lo);
@@ -167,9 +178,13 @@ struct Weights {
     float x[N], y[N];
     values(v, x, y);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const Mass mp(x[i]), mq(q ? y[i] : 0.f);
-      w[i] = (q && x[i] <= y[i]) || v * N - a + i == hole ? 0 : mass_of(mp.hi - mq.hi, mp.lo - mq.lo);
+    for (int i = 0; i < N; i += 2) {
+      const Mass2 mp(x[i], x[i + 1]), mq(q ? y[i] : 0.f, q ? y[i + 1] : 0.f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        w[i + e] = (q && x[i + e] <= y[i + e]) || v * N - a + i + e == hole
+                       ? 0
+                       : mass_of(mp.hi[e] - mq.hi[e], mp.lo[e] - mq.lo[e]);
     }
   }
   // Sum over a warp's vectors first .. end - 1, kBatch at a time with four loads of each row in
