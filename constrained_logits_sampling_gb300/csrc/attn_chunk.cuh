@@ -17,7 +17,8 @@
 // it is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // time (P and its sum are then up to 2^8, which both types hold), so hardly ever.
 // A unit of at most 128 rows has one row tile: both halves of the CTA then take the same
-// queries and every other key tile, and their sums are joined at the end.
+// queries and every other key tile, and their sums are joined at the end, in the room of the
+// second row tile's queries.
 #pragma once
 
 #include <cuda.h>
@@ -85,11 +86,13 @@ struct ChunkShared {
   // the slot of the values before them are free
   unsigned long long k_landed[NS], v_landed[NV], k_full[NS], v_full[NV], tile_done[NS];
   unsigned long long q_full, q_empty, end, s_full[2], p_half[2], p_full[2], o_full[2];
+  unsigned long long unit_full[2], unit_done[2];  // of the units with even and odd numbers
   uint32_t tmem;
-  // where the softmax warps are: they have no registers to spare for it
-  Unit unit;
+  // The units that the softmax warps are at, by the load warps, which are ahead: those have no
+  // registers to spare for more than they need at a time.
+  Unit unit[2];
+  int64_t unit_begin[2];
   Span span;
-  int64_t unit_begin, at;
   volatile int dead;           // a bounded wait ran out: every other wait ends too
   alignas(16) uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
 };
@@ -168,12 +171,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.p_half[w], 4);
       mbar_init(&sh.p_full[w], 4);
       mbar_init(&sh.o_full[w], 1);
+      mbar_init(&sh.unit_full[w], 1);
+      mbar_init(&sh.unit_done[w], 1);
     }
     sh.dead = 0;
-    sh.unit = u;
     sh.span = span;
-    sh.unit_begin = unit_begin;
-    sh.at = span.t0;
     fence_mbar_init();
   }
   if (warp == 10) tmem_alloc512(&sh.tmem);
@@ -190,14 +192,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
     const uint32_t s_tmem = tmem + lane_base + w * 128, o_tmem = tmem + lane_base + 256 + w * 128;
     uint32_t s_phase = 0, o_phase = 0, tile = 0;
-    while (true) {
-      const Unit& u = sh.unit;
-      const int j0 = (int)(sh.at - sh.unit_begin);
-      const int cnt = (int)min((int64_t)(u.tiles - j0), sh.span.t1 - sh.at);
+    for (uint32_t seg = 0;; ++seg) {
+      chunk_wait(&sh.unit_full[seg & 1], (seg >> 1) & 1, &sh.dead);
+      const Unit& u = sh.unit[seg & 1];
+      const int j0 = (int)max(sh.span.t0 - sh.unit_begin[seg & 1], (int64_t)0);
+      const int cnt = (int)(min(sh.unit_begin[seg & 1] + u.tiles, sh.span.t1) - sh.unit_begin[seg & 1]) - j0;
       const bool split = u.rows <= 128;  // this half has the key tiles w, w + 2, ..
       const int step = split ? 2 : 1, jw = split ? w : 0;
-      const int place = w * 128 + (warp & 3) * 32 + lane;  // of this thread's sums in the scratch
-      const int r = split ? place & 127 : place;            // its row
+      const int r = (split ? 0 : w * 128) + (warp & 3) * 32 + lane;  // this thread's row
       const bool live = r < u.rows;
       float m = neg_inf, l = 0.f;  // reference maximum (log2 units) and weights' sum
       if (cnt > jw) {
@@ -294,102 +296,97 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         o_phase ^= 1;
         tc_fence_after();
       }
-      // A slot holds four sums of each row side by side, then the next four of each row, so that
-      // threads with a row each write whole lines.
+      // A slot of the scratch holds four sums of each row side by side, then the next four of
+      // each row, so that threads with a row each write whole lines.
       float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
-      float mine = 1.f, others = 0.f;  // weights of this half's sums and of the other's
-      if (split) {
-        // the second half's sums go through the scratch to the first, whose rows they belong to
-        if (w == 1 && cnt > 1) {
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t x[16];
-            __syncwarp();
-            tmem_ld16(x, o_tmem + c * 16);
-            if (live) {
+      const bool done = cnt == u.tiles;
+      const int row = u.row0 + r;
+      T* dst = (T*)a.out + (int64_t)(u.q0 + row / P.g) * a.o_stride_t +
+               (int64_t)(u.h * P.g + row % P.g) * a.o_stride_h;
+      // NC of this thread's row's sums, from column c on
+      auto put = [&](const auto& x, auto n, int c) {
+        constexpr int NC = decltype(n)::value;
+        if (!live) return;
+        if (done) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                __stcg(reinterpret_cast<uint4*>(slot + ((c * 16 + e) * kChunkRows + place * 4)),
-                       make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
-            }
+          for (int e = 0; e < NC; e += 8) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              y[i] = l == 0.f ? 0u
+                              : Pair<T>::narrow(__uint_as_float(x[e + 2 * i]) * inv,
+                                                __uint_as_float(x[e + 2 * i + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
           }
-          if (live) {
-            __stcg(slot + kChunkRows * D + place, m);
-            __stcg(slot + kChunkRows * D + kChunkRows + place, l);
-          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < NC; e += 4)
+            __stcg(reinterpret_cast<uint4*>(slot + (c + e) * kChunkRows + r * 4),
+                   make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
         }
+      };
+      if (split) {
+        // each half joins one half of the columns and hands the other its sums of the rest
+        float* const x_smem = reinterpret_cast<float*>(smem + kTile);
+        x_smem[w * 256 + r] = m;
+        x_smem[w * 256 + 128 + r] = l;
         SoftmaxSync::sync();
-        if (w == 0 && live && cnt > 1) {
-          const float mo = __ldcg(slot + kChunkRows * D + place + 128);
-          const float lo = __ldcg(slot + kChunkRows * D + kChunkRows + place + 128);
-          const float mn = fmaxf(m, mo);
-          mine = m == mn ? 1.f : exp2_fast(m - mn);
-          others = mo == mn ? 1.f : exp2_fast(mo - mn);
-          l = l * mine + lo * others;
-          m = mn;
+        const float mo = x_smem[(1 - w) * 256 + r], lo = x_smem[(1 - w) * 256 + 128 + r];
+        const float mn = fmaxf(m, mo);
+        const float mine = m == mn ? 1.f : exp2_fast(m - mn), others = mo == mn ? 1.f : exp2_fast(mo - mn);
+        l = l * mine + lo * others;
+        m = mn;
+        SoftmaxSync::sync();
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          uint32_t x[32];
+          __syncwarp();
+          tmem_ld32(x, o_tmem + (1 - w) * (D / 2) + c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)  // a half without a key tile has no sums
+            *reinterpret_cast<uint4*>(x_smem + w * 4096 + e * 128 + r * 4) =
+                cnt > w ? make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]) : make_uint4(0, 0, 0, 0);
+          SoftmaxSync::sync();
+          tmem_ld32(x, o_tmem + w * (D / 2) + c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(x_smem + (1 - w) * 4096 + e * 128 + r * 4);
+            const float ov[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              x[e + i] = __float_as_uint((cnt > w ? __uint_as_float(x[e + i]) * mine : 0.f) + ov[i] * others);
+          }
+          put(x, std::integral_constant<int, 32>(), w * (D / 2) + c);
+          SoftmaxSync::sync();
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t x[32];
+          __syncwarp();
+          tmem_ld32(x, o_tmem + c);
+          put(x, std::integral_constant<int, 32>(), c);
         }
       }
-      const bool done = cnt == u.tiles;
-      if (w == 0 || !split) {
-        const float inv = !done ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        const int row = u.row0 + r;
-        T* dst = (T*)a.out + (int64_t)(u.q0 + row / P.g) * a.o_stride_t +
-                 (int64_t)(u.h * P.g + row % P.g) * a.o_stride_h;
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t x[16];
-          __syncwarp();
-          tmem_ld16(x, o_tmem + c * 16);
-          if (live) {
-            if (split && cnt > 1) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 v =
-                    __ldcg(reinterpret_cast<const float4*>(slot + ((c * 16 + e) * kChunkRows + (place + 128) * 4)));
-                x[e] = __float_as_uint(__uint_as_float(x[e]) * mine + v.x * others);
-                x[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * mine + v.y * others);
-                x[e + 2] = __float_as_uint(__uint_as_float(x[e + 2]) * mine + v.z * others);
-                x[e + 3] = __float_as_uint(__uint_as_float(x[e + 3]) * mine + v.w * others);
-              }
-            }
-            if (done) {
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                y[e] = l == 0.f ? 0u
-                                : Pair<T>::narrow(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(dst + c * 16 + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                __stcg(reinterpret_cast<uint4*>(slot + ((c * 16 + e) * kChunkRows + place * 4)),
-                       make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
-            }
-          }
-        }
-        if (live && done) store_lse(P, u, r, m, l);
-        if (live && !done) {
-          __stcg(slot + kChunkRows * D + place, m);
-          __stcg(slot + kChunkRows * D + kChunkRows + place, l);
+      if (live && (w == 0 || !split)) {
+        if (done) {
+          store_lse(P, u, r, m, l);
+        } else {
+          __stcg(slot + kChunkRows * D + r, m);
+          __stcg(slot + kChunkRows * D + kChunkRows + r, l);
         }
       }
       tc_fence_before();  // O has been read: the next unit's products may overwrite it
       tile += cnt;
-      // (of two halves, the first has read here what the second may write again)
-      SoftmaxSync::sync();
-      if (tid == 0) {
-        sh.at += cnt;
-        if (sh.at < sh.span.t1) {
-          sh.unit_begin = sh.at;
-          next_unit<kChunkRows, kChunkKeys>(P, &sh.unit);
-        } else {
-          note_cut(P, sh.span, sh.unit, sh.unit_begin);
-          if (sh.dead) *P.gave_up = 1;
-        }
+      const bool last = sh.unit_begin[seg & 1] + u.tiles >= sh.span.t1;
+      if (last && tid == 0) {
+        note_cut(P, sh.span, u, sh.unit_begin[seg & 1]);
+        if (sh.dead) *P.gave_up = 1;
       }
       SoftmaxSync::sync();
-      if (sh.at >= sh.span.t1) break;
+      if (last) break;
+      if (tid == 0) mbar_arrive(&sh.unit_done[seg & 1]);
     }
   } else if (warp != 10) {
     // ------------------------------------------------------------------ loads
@@ -407,10 +404,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     };
     auto copy_queries = [&](uint32_t seg) {
+      // the unit's place is free when the softmax warps are done with the one before the last
+      if (seg >= 2) chunk_wait(&sh.unit_done[seg & 1], ((seg - 2) >> 1) & 1, &sh.dead);
+      if (lw == 0 && lane == 0) {
+        sh.unit[seg & 1] = u;
+        sh.unit_begin[seg & 1] = unit_begin;
+        mbar_arrive(&sh.unit_full[seg & 1]);
+      }
       chunk_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
       __syncwarp();
 #pragma unroll 1
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < (u.rows <= 128 ? 2 : 4); ++w) {
+        // the second row tile's room is where the halves of the last unit met
+        if (w == 2 && seg >= 1) chunk_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.dead);
+        __syncwarp();
         const int first = (w * 2 + lw) * 32;  // of 32 rows, one a lane, whose place it hands to the others
         const int mine = first + lane, row = u.row0 + mine;
         const bool live = mine < u.rows;
