@@ -19,13 +19,9 @@ constexpr int kStreamCtas = 2;  // per SM
 // The scratch, per SM: both kernels' slots (two per CTA, of rows of 128 sums, a maximum and a
 // sum), their cut units, and one word for all.
 constexpr size_t kChunkSlots = 2 * (size_t)kChunkRows * 130 * sizeof(float);
-constexpr size_t kStreamSlots = kStreamCtas * 2 * (size_t)32 * 130 * sizeof(float);
+constexpr size_t kStreamSlots = kStreamCtas * 2 * (size_t)kStreamRows * 130 * sizeof(float);
 constexpr size_t kCuts = (1 + kStreamCtas) * sizeof(CutUnit);
 constexpr size_t kScratch = kChunkSlots + kStreamSlots + kCuts;
-// Up to this many packed rows (a multiple of the stream kernel's tile) a sequence's keys are
-// read once by the stream kernel; above it, once per 256 rows by the chunk kernel.
-constexpr int kStreamRows = 32;
-
 // A launch that may start while the one before it ends.
 template <class Kernel, class... Args>
 cudaError_t launch_after(Kernel fn, int grid, int threads, int smem, cudaStream_t st, const Args&... args) {
@@ -42,19 +38,8 @@ cudaError_t launch_after(Kernel fn, int grid, int threads, int smem, cudaStream_
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-template <class T, int D, int MT>
-cudaError_t launch_stream(const AttnParams& P, int sms, bool first, cudaStream_t st) {
-  auto* fn = attn_stream_kernel<T, D, MT>;
-  const int bytes = StreamRing<D>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  if (!first) return launch_after(fn, sms * kStreamCtas, kStreamThreads, bytes, st, P);
-  fn<<<sms * kStreamCtas, kStreamThreads, bytes, st>>>(P);
-  return cudaGetLastError();
-}
-
 // The cache as a tensor of (element, slot, head, page), copied in boxes of 64 elements of the
-// slots of a page (of 128 at most).
+// slots of a page, of a tile's keys at most.
 bool cache_map(const AttnParams& P, const void* base, CUtensorMap* map) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -83,14 +68,37 @@ bool cache_map(const AttnParams& P, const void* base, CUtensorMap* map) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int D, bool kTma>
-cudaError_t launch_chunk(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap& v_map, int sms,
-                         cudaStream_t st) {
-  auto* fn = attn_chunk_kernel<T, D, kTma>;
+template <class Kernel>
+cudaError_t allow_smem(Kernel fn, int bytes) {
+  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <class T, int D>
+cudaError_t launch_chunk(const AttnParams& P, int sms, cudaStream_t st) {
+  // Boxes have to start on the eight rows of the swizzle and fill a tile.  2 x 2048 tokens over
+  // 14000 keys: 565 us with them, 1197 row by row.
+  const int page = P.a.page_size;
+  CUtensorMap k_map{}, v_map{};
+  const bool boxes = page >= 8 && (page % kChunkKeys == 0 || kChunkKeys % page == 0) &&
+                     cache_map(P, P.a.k_cache, &k_map) && cache_map(P, P.a.v_cache, &v_map);
   const int bytes = ChunkShape<D>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  auto* fn = boxes ? attn_chunk_kernel<T, D, true> : attn_chunk_kernel<T, D, false>;
+  const cudaError_t e = allow_smem(fn, bytes);
   if (e != cudaSuccess) return e;
   fn<<<sms, kChunkThreads, bytes, st>>>(P, k_map, v_map);
+  return cudaGetLastError();
+}
+
+// first: of the call
+template <class T, int D>
+cudaError_t launch_stream(const AttnParams& P, int sms, bool first, cudaStream_t st) {
+  const int grid = sms * kStreamCtas;
+  auto* fn = attn_stream_kernel<T, D>;
+  const int bytes = StreamRing<D>::kBytes;
+  const cudaError_t e = allow_smem(fn, bytes);
+  if (e != cudaSuccess) return e;
+  if (!first) return launch_after(fn, grid, kStreamThreads, bytes, st, P);
+  fn<<<grid, kStreamThreads, bytes, st>>>(P);
   return cudaGetLastError();
 }
 
@@ -103,34 +111,28 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
   CutUnit* const chunk_cut = reinterpret_cast<CutUnit*>(h->scratch + h->sms * (kChunkSlots + kStreamSlots));
   CutUnit* const stream_cut = chunk_cut + h->sms;
   P.gave_up = reinterpret_cast<int*>(stream_cut + h->sms * kStreamCtas);
+  // Sequences of up to 16 packed rows go to the stream kernel, longer ones to the chunk
+  // kernel.  256 sequences of 16 rows over 2.3 GB of keys and values: 404 us in the one, 445 in
+  // the other; of 24 rows, where the one would read keys twice or hold 32 rows: 541 and 422.
   const bool chunks = rows > kStreamRows;
-  // beside sequences with many rows, a few with few are not worth a launch of their own
-  const bool alone = chunks && (int64_t)P.a.B * P.a.Hkv <= 2 * h->sms;
+  // Beside longer sequences, a few short ones are not worth a launch of their own: 19 ragged
+  // sequences on 12 key heads take 40 us alone in the chunk kernel and 49 us in both; 240
+  // sequences of one token and 16 of 512, on 8 key heads, 803 and 725.
+  const bool alone = chunks && (int64_t)P.a.B * P.a.Hkv <= 4 * h->sms;
   cudaError_t e;
   if (chunks) {
     P.min_rows = alone ? 0 : kStreamRows + 1;
     P.max_rows = 0x7fffffff;
     P.partial = chunk_partial;
     P.cut = chunk_cut;
-    // boxes have to start on the eight rows of the swizzle and fill a tile
-    const int page = P.a.page_size;
-    const bool boxes = page >= 8 && (page % kChunkKeys == 0 || kChunkKeys % page == 0);
-    CUtensorMap k_map{}, v_map{};
-    e = boxes && cache_map(P, P.a.k_cache, &k_map) && cache_map(P, P.a.v_cache, &v_map)
-            ? launch_chunk<T, D, true>(P, k_map, v_map, h->sms, st)
-            : launch_chunk<T, D, false>(P, k_map, v_map, h->sms, st);
-    if (e != cudaSuccess) return e;
+    if ((e = launch_chunk<T, D>(P, h->sms, st)) != cudaSuccess) return e;
   }
   P.min_rows = 0;
   P.max_rows = chunks ? kStreamRows + 1 : 0x7fffffff;
   P.partial = stream_partial;
   P.cut = stream_cut;
-  const int tile = rows <= 16 ? 16 : 32;
-  if (!alone) {
-    e = tile == 16 ? launch_stream<T, D, 1>(P, h->sms, !chunks, st) : launch_stream<T, D, 2>(P, h->sms, !chunks, st);
-    if (e != cudaSuccess) return e;
-  }
-  const JoinParams J{P, chunk_partial, chunk_cut, chunks ? h->sms : 0, alone ? 0 : h->sms * kStreamCtas, tile};
+  if (!alone && (e = launch_stream<T, D>(P, h->sms, !chunks, st)) != cudaSuccess) return e;
+  const JoinParams J{P, chunk_partial, chunk_cut, chunks ? h->sms : 0, alone ? 0 : h->sms * kStreamCtas};
   return launch_after(attn_join_kernel<T, D>, h->sms * 2, kJoinThreads, 0, st, J);
 }
 
@@ -150,7 +152,7 @@ int clsample_attention_create(clsample_attention_t** out) {
   auto* h = new (std::nothrow) clsample_attention{dev, sms, nullptr};
   if (!h) return CLSAMPLE_ERR_CUDA;
   const size_t bytes = sms * kScratch + sizeof(int);
-  if (cudaMalloc(&h->scratch, bytes) != cudaSuccess || cudaMemset(h->scratch, 0, bytes) != cudaSuccess ||
+  if (cudaMalloc(&h->scratch, bytes) != cudaSuccess || cudaMemset(h->scratch + sms * kScratch, 0, sizeof(int)) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
     clsample_attention_destroy(h);
     cudaGetLastError();

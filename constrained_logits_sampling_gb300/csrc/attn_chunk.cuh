@@ -21,8 +21,6 @@
 // second row tile's queries.
 #pragma once
 
-#include <cuda.h>
-
 #include <type_traits>
 
 #include "attn_stream.cuh"
@@ -96,28 +94,6 @@ struct ChunkShared {
   volatile int dead;           // a bounded wait ran out: every other wait ends too
   alignas(16) uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
 };
-
-// One box of a tensor map of rank 4 to shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int x, int slot, int head, int page,
-                                          unsigned long long* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
-      : "memory");
-}
-
-// Bounded wait for a phase: about two seconds, then the CTA gives up.
-__device__ __forceinline__ bool chunk_wait(unsigned long long* bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long start = clock64();
-  for (uint32_t i = 1; i < kSpinLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0 && (*dead || clock64() - start > 4000000000ll)) break;
-  }
-  *dead = 1;
-  return false;
-}
 
 // Bits lo .. hi of a word, of which only 0 .. 31 exist.
 __device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
@@ -193,7 +169,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t s_tmem = tmem + lane_base + w * 128, o_tmem = tmem + lane_base + 256 + w * 128;
     uint32_t s_phase = 0, o_phase = 0, tile = 0;
     for (uint32_t seg = 0;; ++seg) {
-      chunk_wait(&sh.unit_full[seg & 1], (seg >> 1) & 1, &sh.dead);
+      bounded_wait(&sh.unit_full[seg & 1], (seg >> 1) & 1, &sh.dead);
       const Unit& u = sh.unit[seg & 1];
       const int j0 = (int)max(sh.span.t0 - sh.unit_begin[seg & 1], (int64_t)0);
       const int cnt = (int)(min(sh.unit_begin[seg & 1] + u.tiles, sh.span.t1) - sh.unit_begin[seg & 1]) - j0;
@@ -210,7 +186,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int pos_last = first_pos + (u.row0 + min(u.rows, half0 + 128) - 1) / P.g;
         for (int j = jw; j < cnt; j += step) {
           const int kb = kb0 + j * kChunkKeys;
-          chunk_wait(&sh.s_full[w], s_phase, &sh.dead);
+          bounded_wait(&sh.s_full[w], s_phase, &sh.dead);
           if (lane == 0) {
             if ((warp & 3) == 0 && (split || w == 1)) mbar_arrive(&sh.tile_done[(tile + j) % NS]);
           }
@@ -292,7 +268,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float2 s0 = split_pair(add2(sums[0], sums[1]));
           l += s0.x + s0.y;
         }
-        chunk_wait(&sh.o_full[w], o_phase, &sh.dead);
+        bounded_wait(&sh.o_full[w], o_phase, &sh.dead);
         o_phase ^= 1;
         tc_fence_after();
       }
@@ -405,18 +381,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     };
     auto copy_queries = [&](uint32_t seg) {
       // the unit's place is free when the softmax warps are done with the one before the last
-      if (seg >= 2) chunk_wait(&sh.unit_done[seg & 1], ((seg - 2) >> 1) & 1, &sh.dead);
+      if (seg >= 2) bounded_wait(&sh.unit_done[seg & 1], ((seg - 2) >> 1) & 1, &sh.dead);
       if (lw == 0 && lane == 0) {
         sh.unit[seg & 1] = u;
         sh.unit_begin[seg & 1] = unit_begin;
         mbar_arrive(&sh.unit_full[seg & 1]);
       }
-      chunk_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
+      bounded_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
       __syncwarp();
 #pragma unroll 1
       for (int w = 0; w < (u.rows <= 128 ? 2 : 4); ++w) {
         // the second row tile's room is where the halves of the last unit met
-        if (w == 2 && seg >= 1) chunk_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.dead);
+        if (w == 2 && seg >= 1) bounded_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.dead);
         __syncwarp();
         const int first = (w * 2 + lw) * 32;  // of 32 rows, one a lane, whose place it hands to the others
         const int mine = first + lane, row = u.row0 + mine;
@@ -435,12 +411,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // one: the keys' has been passed, and by now its barrier may be a phase further.
     auto key_slot = [&](uint32_t it) {
       const int64_t gate = (int64_t)it - NS;
-      if (gate >= 0) chunk_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
+      if (gate >= 0) bounded_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
       __syncwarp();
     };
     auto value_slot = [&](uint32_t it, int j) {
       const int64_t gate = (int64_t)it - NV + (u.rows <= 128 || j < NV ? 2 : 1);
-      if (gate >= 0 && gate > (int64_t)it - NS) chunk_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
+      if (gate >= 0 && gate > (int64_t)it - NS) bounded_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
       __syncwarp();
     };
     // a tile with values outside the unit's keys
@@ -514,7 +490,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
               if (i == st) parity = edges[i]++ & 1;
-            chunk_wait(&sh.v_landed[st], parity, &sh.dead);
+            bounded_wait(&sh.v_landed[st], parity, &sh.dead);
             __syncwarp();
             const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
             for (int i = lane; i < 128 * KC; i += 32) {  // a row's pieces may lie anywhere in it: all are cleared
@@ -597,10 +573,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // The copies are ordinary writes, the products read by the async proxy: the fence between
       // them costs a hundred cycles or so, which the issuing warp has not got.
       for (int i = 0; i < tiles; ++i) {
-        chunk_wait(&sh.k_landed[i % NS], (i / NS) & 1, &sh.dead);
+        bounded_wait(&sh.k_landed[i % NS], (i / NS) & 1, &sh.dead);
         fence_async_proxy();
         mbar_arrive(&sh.k_full[i % NS]);
-        chunk_wait(&sh.v_landed[i % NV], (i / NV) & 1, &sh.dead);
+        bounded_wait(&sh.v_landed[i % NV], (i / NV) & 1, &sh.dead);
         fence_async_proxy();
         mbar_arrive(&sh.v_full[i % NV]);
       }
@@ -619,7 +595,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       uint32_t it = 0, seg = 0, p_phase = 0;  // bit w of p_phase: half w
       bool alive = true;
       auto wait = [&](unsigned long long* bar, uint32_t parity) {
-        alive = __all_sync(~0u, chunk_wait(bar, parity, &sh.dead)) && alive;
+        alive = __all_sync(~0u, bounded_wait(bar, parity, &sh.dead)) && alive;
       };
       auto keys_ready = [&](uint32_t tile) { wait(&sh.k_full[tile % NS], (tile / NS) & 1); };
       auto values_ready = [&](uint32_t tile) { wait(&sh.v_full[tile % NV], (tile / NV) & 1); };

@@ -21,7 +21,7 @@ struct JoinParams {
   const float* chunk_partial;
   const CutUnit* chunk_cut;
   int chunk_ctas;      // 0: the chunk kernel was not launched
-  int stream_ctas, stream_rows;
+  int stream_ctas;
 };
 
 // Statuses: one CTA per sequence at a time looks at its lengths and at every page id that
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid
       const int sub = lane / kPer, d = lane % kPer * 4;
       const int r = few ? at * kStreamStep + warp * kRowsPerWarp + sub : at;
       const bool live = r < u.rows;
-      const int R = J.stream_rows;
+      constexpr int R = kStreamRows;
       auto load = [&](int part, float* m, float* l, float4 (&v)[1]) {
         const float* s = P.partial + (int64_t)((u.c0 + part) * 2 + (part == 0 ? 1 : 0)) * (R * (D + 2));
         *m = __ldcg(s + R * D + r);

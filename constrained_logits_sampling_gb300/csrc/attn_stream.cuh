@@ -1,12 +1,13 @@
 // Attention for few query rows per key head: bound by reading keys and values once.
 //
-// A unit is 16 MT packed rows (attn_units.cuh).  The four warps of a CTA share the rows and
-// split the keys: of each tile of 64 keys a warp takes 16, loads them itself (cp.async, its
-// own ring of stages) and keeps its own running maximum, sum and output in registers, so no
-// barrier stands between a load and its use and every byte passes shared memory once.  The
-// products are mma.m16n8k16: with so few rows the tensor cores are nearly idle either way,
-// and the row tile can be 16 where tcgen05 has 64 at least.  The four warps' results meet in
-// shared memory at the end of a unit's span.
+// A unit is 16 packed rows (attn_units.cuh).  Four warps share the rows and split the keys: of
+// each tile of 64 keys a warp takes 16, loads them itself (cp.async, its own ring of stages) and
+// keeps its own running maximum, sum and output in registers, so no barrier stands between a
+// load and its use and every byte passes shared memory once.  The products are mma.m16n8k16:
+// with so few rows the tensor cores are nearly idle either way, and the row tile can be 16 where
+// tcgen05 has 64 at least.  The four warps' results meet in shared memory at the end of a
+// unit's span.  A warp of its own that copied by TMA, on into the next unit while the others
+// ended one, was no faster (407 us against 404 below) and slower where a unit is one tile.
 #pragma once
 
 #include "attn_units.cuh"
@@ -71,10 +72,12 @@ constexpr int kStreamKeys = 64;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // Ring stages of a warp: two CTAs fit an SM, with about 190 KB of loads in flight.
+constexpr int kStreamRows = 16;
 template <int D>
 struct StreamRing {
   static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kBytes = 4 * kStages * 16 * D * 2 * 2;  // four warps, 16 keys and values a stage
+  static constexpr int kBytes = kStages * kStreamKeys * D * 2 * 2;  // keys and values
+  static_assert(kBytes >= 4 * kStreamRows * (D + 8) * 4, "room for four warps' sums");
 };
 
 // A scratch slot: R x D sums, then R maxima (log2 units) and R weights' sums.
@@ -99,18 +102,185 @@ __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, in
   if (P.a.lse) P.a.lse[(int64_t)(u.q0 + row / P.g) * P.a.Hq + u.h * P.g + row % P.g] = lse_of(m, l);
 }
 
-template <class T, int D, int MT>
+// The rows of a unit as one warp has them: queries as A operands, limits and running sums.  Lane
+// i has rows i / 4 and i / 4 + 8.
+template <class T, int D>
+struct StreamState {
+  uint32_t q[D / 16][4];
+  int pos[2];
+  int pos_first, pos_last;
+  float o[D / 8][4];
+  float m[2], l[2];
+
+  __device__ __forceinline__ void begin(const AttnParams& P, const Unit& u) {
+    const int lane = threadIdx.x & 31;
+    const float neg_inf = __int_as_float(0xff800000);
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = hf * 8 + (lane >> 2);
+      const bool live = r < u.rows;
+      const int row = u.row0 + r;
+      const T* src = (const T*)P.a.q + (int64_t)(u.q0 + (live ? row / P.g : 0)) * P.a.q_stride_t +
+                     (int64_t)(u.h * P.g + (live ? row % P.g : 0)) * P.a.q_stride_h + (lane & 3) * 2;
+      pos[hf] = live ? u.len - u.n + row / P.g : -1;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        q[ks][hf] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16)) : 0u;
+        q[ks][hf + 2] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16 + 8)) : 0u;
+      }
+      m[hf] = neg_inf;
+      l[hf] = 0.f;
+    }
+    pos_first = u.len - u.n + u.row0 / P.g;
+    pos_last = u.len - u.n + (u.row0 + u.rows - 1) / P.g;
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+  }
+
+  // 16 keys from position `key` on, of which those in `live` exist.  Rows of 64 elements in
+  // shared memory, 16-byte pieces swizzled by the row; the next 64 elements are `half` further.
+  __device__ __forceinline__ void step(const AttnParams& P, uint32_t kb, uint32_t vb, uint32_t half, int key,
+                                       unsigned live) {
+    const int lane = threadIdx.x & 31;
+    const float neg_inf = __int_as_float(0xff800000);
+    float s[2][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const int row = (lane & 7) + ((lane >> 4) << 3), ch = ks * 2 + ((lane >> 3) & 1);
+      uint32_t b[4];
+      ldmatrix4(b, kb + (ch >> 3) * half + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+      mma16816<T>(s[0], q[ks], b[0], b[1]);
+      mma16816<T>(s[1], q[ks], b[2], b[3]);
+    }
+    const int window = P.a.window;
+    // every key of the tile is seen by every row (rows past the unit's are never stored)
+    const bool whole = live == 0xffffu && key + 15 <= pos_first && (window <= 0 || key > pos_last - window);
+    bool moved = false;
+    float keep[2];
+    uint32_t p[4];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float x[4] = {s[0][hf * 2] * P.scale_log2, s[0][hf * 2 + 1] * P.scale_log2, s[1][hf * 2] * P.scale_log2,
+                    s[1][hf * 2 + 1] * P.scale_log2};
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = (e >> 1) * 8 + (lane & 3) * 2 + (e & 1);
+          const int kp = key + c;
+          if (!((live >> c) & 1) || kp > pos[hf] || (window > 0 && kp <= pos[hf] - window)) x[e] = neg_inf;
+        }
+      }
+      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      const float mn = fmaxf(m[hf], top);
+      const float base = mn == neg_inf ? 0.f : mn;  // a row that has seen no key yet
+      keep[hf] = exp2_fast(m[hf] - base);
+      moved |= mn != m[hf];
+      m[hf] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = exp2_fast(x[e] - base);
+        sum += x[e];
+      }
+      l[hf] = l[hf] * keep[hf] + sum;
+      p[hf] = Pair<T>::narrow(x[0], x[1]);
+      p[hf + 2] = Pair<T>::narrow(x[2], x[3]);
+    }
+    if (__any_sync(~0u, moved)) {
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d) {
+        o[d][0] *= keep[0];
+        o[d][1] *= keep[0];
+        o[d][2] *= keep[1];
+        o[d][3] *= keep[1];
+      }
+    }
+    // values of keys that do not exist may be anything, and 0 x NaN is NaN
+    const unsigned two = live >> ((lane & 3) * 2);
+    const uint32_t mask0 = (two & 1 ? 0xffffu : 0u) | (two & 2 ? 0xffff0000u : 0u);
+    const uint32_t mask1 = (two & 0x100 ? 0xffffu : 0u) | (two & 0x200 ? 0xffff0000u : 0u);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = d * 2 + (lane >> 4);
+      uint32_t b[4];
+      ldmatrix4_trans(b, vb + (ch >> 3) * half + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+      mma16816<T>(o[2 * d], p, b[0] & mask0, b[1] & mask1);
+      mma16816<T>(o[2 * d + 1], p, b[2] & mask0, b[3] & mask1);
+    }
+  }
+};
+
+// The warps' results of a unit's span meet: meet holds [warp][row][D + 8] (rows begin in different
+// banks), wm and wl the warps' maxima and sums.
+template <class T, int D>
+__device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u, StreamState<T, D>& st, float* meet,
+                                              float (&wm)[4][kStreamRows], float (&wl)[4][kStreamRows], bool done,
+                                              float* slot) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int R = kStreamRows;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    float sum = st.l[hf];
+    sum += __shfl_xor_sync(~0u, sum, 1);
+    sum += __shfl_xor_sync(~0u, sum, 2);
+    if ((lane & 3) == 0) {
+      wm[warp][hf * 8 + (lane >> 2)] = st.m[hf];
+      wl[warp][hf * 8 + (lane >> 2)] = sum;
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int col = d * 8 + (lane & 3) * 2, row = hf * 8 + (lane >> 2);
+      *reinterpret_cast<float2*>(meet + (warp * R + row) * (D + 8) + col) =
+          make_float2(st.o[d][hf * 2], st.o[d][hf * 2 + 1]);
+    }
+  __syncthreads();
+  for (int i = tid; i < u.rows * (D / 4); i += kStreamThreads) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    const float top = fmaxf(fmaxf(wm[0][r], wm[1][r]), fmaxf(wm[2][r], wm[3][r]));
+    const float base = top == __int_as_float(0xff800000) ? 0.f : top;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = exp2_fast(wm[w][r] - base);
+      const float4 v = *reinterpret_cast<const float4*>(meet + (w * R + r) * (D + 8) + d);
+      sum = make_float4(sum.x + v.x * f, sum.y + v.y * f, sum.z + v.z * f, sum.w + v.w * f);
+      lsum += wl[w][r] * f;
+    }
+    if (done) {
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+      store_out4<T>(P, u, r, d, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+      if (d == 0) store_lse(P, u, r, top, lsum);
+    } else {
+      __stcg(reinterpret_cast<float4*>(slot + r * D + d), sum);
+      if (d == 0) {
+        __stcg(slot + R * D + r, top);
+        __stcg(slot + R * D + R + r, lsum);
+      }
+    }
+  }
+  __syncthreads();  // for the next unit
+}
+
+template <class T, int D>
 __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __grid_constant__ AttnParams P) {
-  constexpr int R = 16 * MT, S = StreamRing<D>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
-  constexpr int kTileBytes = 16 * D * 2, kStageBytes = 2 * kTileBytes;
+  constexpr int R = kStreamRows, S = StreamRing<D>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
+  constexpr int kTileBytes = 16 * D * 2, kStageBytes = 2 * kTileBytes, kHalf = 16 * 128;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ unsigned key_ok[4][S];
   __shared__ float wm[4][R], wl[4][R];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const clsample_attention_args_t& a = P.a;
-  unsigned char* const ring = smem + warp * S * kStageBytes;
-  const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  const float neg_inf = __int_as_float(0xff800000);
+  const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(smem + warp * S * kStageBytes));
 
   let_next_grid_start();
   Span span;
@@ -154,7 +324,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
           const int row = (x * 32 + lane) / KC, ch = (x * 32 + lane) % KC;
           const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
           const bool live = (mask >> row) & 1;
-          const uint32_t dst = base + row * (D * 2) + ((ch ^ (row & 7)) << 4);
+          const uint32_t dst = base + (ch >> 3) * kHalf + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
           cp_async16(dst, kc + o, live);
           cp_async16(dst + kTileBytes, vc + o, live);
         }
@@ -170,41 +340,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
       issue(i, page);
       page = next;
     }
-
-    // queries as A operands, row limits
-    uint32_t q[MT][D / 16][4];
-    int pos[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = mt * 16 + hf * 8 + (lane >> 2);
-        const bool live = r < u.rows;
-        const int row = u.row0 + r;
-        const T* src = (const T*)a.q + (int64_t)(u.q0 + (live ? row / P.g : 0)) * a.q_stride_t +
-                       (int64_t)(u.h * P.g + (live ? row % P.g : 0)) * a.q_stride_h + (lane & 3) * 2;
-        pos[mt][hf] = live ? u.len - u.n + row / P.g : -1;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          q[mt][ks][hf] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16)) : 0u;
-          q[mt][ks][hf + 2] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16 + 8)) : 0u;
-        }
-      }
-    const int pos_first = u.len - u.n + u.row0 / P.g;
-    const int pos_last = u.len - u.n + (u.row0 + u.rows - 1) / P.g;
-
-    float o[MT][D / 8][4];
-    float m[MT][2], l[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][d][e] = 0.f;
-      m[mt][0] = m[mt][1] = neg_inf;
-      l[mt][0] = l[mt][1] = 0.f;
-    }
-
+    StreamState<T, D> st;
+    st.begin(P, u);
     for (int i = 0; i < cnt; ++i) {
       cp_async_wait<S - 2>();
       __syncwarp();
@@ -212,144 +349,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
       issue(i + S - 1, page);
       page = next;
       const int stage = i % S;
-      const unsigned live = key_ok[warp][stage];
-      const uint32_t kb = ring_addr + stage * kStageBytes, vb = kb + kTileBytes;
-      const int key = key0 + i * kStreamKeys;
-
-      float s[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][0][e] = s[mt][1][e] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int row = (lane & 7) + ((lane >> 4) << 3), ch = ks * 2 + ((lane >> 3) & 1);
-        uint32_t b[4];
-        ldmatrix4(b, kb + row * (D * 2) + ((ch ^ (row & 7)) << 4));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816<T>(s[mt][0], q[mt][ks], b[0], b[1]);
-          mma16816<T>(s[mt][1], q[mt][ks], b[2], b[3]);
-        }
-      }
-      // every key of the tile is seen by every row (rows past the unit's are never stored)
-      const bool whole = live == 0xffffu && key + 15 <= pos_first &&
-                         (a.window <= 0 || key > pos_last - a.window);
-      bool moved = false;
-      float keep[MT][2];
-      uint32_t p[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float x[4] = {s[mt][0][hf * 2] * P.scale_log2, s[mt][0][hf * 2 + 1] * P.scale_log2,
-                        s[mt][1][hf * 2] * P.scale_log2, s[mt][1][hf * 2 + 1] * P.scale_log2};
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = (e >> 1) * 8 + (lane & 3) * 2 + (e & 1);
-              const int kp = key + c;
-              const bool seen = ((live >> c) & 1) && kp <= pos[mt][hf] &&
-                                (a.window <= 0 || kp > pos[mt][hf] - a.window);
-              if (!seen) x[e] = neg_inf;
-            }
-          }
-          float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-          const float mn = fmaxf(m[mt][hf], top);
-          const float base = mn == neg_inf ? 0.f : mn;  // a row that has seen no key yet
-          keep[mt][hf] = exp2_fast(m[mt][hf] - base);
-          moved |= mn != m[mt][hf];
-          m[mt][hf] = mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = exp2_fast(x[e] - base);
-            sum += x[e];
-          }
-          l[mt][hf] = l[mt][hf] * keep[mt][hf] + sum;
-          p[mt][hf] = Pair<T>::narrow(x[0], x[1]);
-          p[mt][hf + 2] = Pair<T>::narrow(x[2], x[3]);
-        }
-      }
-      if (__any_sync(~0u, moved)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            o[mt][d][0] *= keep[mt][0];
-            o[mt][d][1] *= keep[mt][0];
-            o[mt][d][2] *= keep[mt][1];
-            o[mt][d][3] *= keep[mt][1];
-          }
-      }
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = d * 2 + (lane >> 4);
-        uint32_t b[4];
-        ldmatrix4_trans(b, vb + row * (D * 2) + ((ch ^ (row & 7)) << 4));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816<T>(o[mt][2 * d], p[mt], b[0], b[1]);
-          mma16816<T>(o[mt][2 * d + 1], p[mt], b[2], b[3]);
-        }
-      }
+      const uint32_t kb = ring_addr + stage * kStageBytes;
+      st.step(P, kb, kb + kTileBytes, kHalf, key0 + i * kStreamKeys, key_ok[warp][stage]);
     }
-
-    // the warps' results meet: each warp's sums go to its own ring, which is drained
     cp_async_wait<0>();
-    __syncwarp();
-    float* mine = reinterpret_cast<float*>(ring);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = mt * 16 + hf * 8 + (lane >> 2);
-        float sum = l[mt][hf];
-        sum += __shfl_xor_sync(~0u, sum, 1);
-        sum += __shfl_xor_sync(~0u, sum, 2);
-        if ((lane & 3) == 0) {
-          wm[warp][r] = m[mt][hf];
-          wl[warp][r] = sum;
-        }
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d)
-          *reinterpret_cast<float2*>(mine + r * D + d * 8 + (lane & 3) * 2) =
-              make_float2(o[mt][d][hf * 2], o[mt][d][hf * 2 + 1]);
-      }
-    __syncthreads();
-    const bool done = cnt == u.tiles;
-    float* slot = scratch_slot<R, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
-    for (int i = tid; i < u.rows * (D / 4); i += kStreamThreads) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      const float top = fmaxf(fmaxf(wm[0][r], wm[1][r]), fmaxf(wm[2][r], wm[3][r]));
-      const float base = top == neg_inf ? 0.f : top;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      float lsum = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = exp2_fast(wm[w][r] - base);
-        const float4 v =
-            *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * S * kStageBytes) + r * D + d);
-        sum = make_float4(sum.x + v.x * f, sum.y + v.y * f, sum.z + v.z * f, sum.w + v.w * f);
-        lsum += wl[w][r] * f;
-      }
-      if (done) {
-        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-        store_out4<T>(P, u, r, d, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
-        if (d == 0) store_lse(P, u, r, top, lsum);
-      } else {
-        __stcg(reinterpret_cast<float4*>(slot + r * D + d), sum);
-        if (d == 0) {
-          __stcg(slot + R * D + r, top);
-          __stcg(slot + R * D + R + r, lsum);
-        }
-      }
-    }
+    __syncthreads();  // the rings are drained: the first is where the warps meet
+    stream_finish<T, D>(P, u, st, reinterpret_cast<float*>(smem), wm, wl, cnt == u.tiles,
+                                   scratch_slot<R, D>(P, blockIdx.x, j0 == 0 ? 1 : 0));
     t += cnt;
     if (t >= span.t1) break;
-    __syncthreads();  // the rings and row sums have been read
     unit_begin = t;
     next_unit<R, kStreamKeys>(P, &u);
   }

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "bulk_copy.cuh"
+#include "tma.cuh"
 
 namespace clsample {
 
@@ -145,22 +146,6 @@ __device__ __forceinline__ void mma_commit(unsigned long long* bar) {
       : "memory");
 }
 
-// One look at a phase, without the pause that a poll may make.
-__device__ __forceinline__ bool mbar_test_wait(unsigned long long* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
 // Orders ordinary writes to shared memory that this thread has made or acquired before the
 // tensor cores' reads that it issues next.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

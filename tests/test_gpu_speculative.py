@@ -57,6 +57,13 @@ ATTEND = [
     ([65, 0, 129], [40, 3, 200], 5, 1, 64, 8, BF, 0, "nhd"),  # chunk longer than its keys
     ([257], [300], 2, 1, 128, 48, FP, 0, "hnd"),
     ([1] * 300, [(7 * i) % 90 for i in range(300)], 2, 1, 64, 16, BF, 0, "nhd"),
+    ([6, 7], [450, 200], 8, 2, 128, 16, FP, 0, "nhd"),  # 17 to 32 packed rows
+    ([40], [6000], 4, 1, 128, 64, BF, 0, "nhd"),  # a long unit in many parts
+    ([30, 2], [2500, 1200], 6, 2, 64, 256, FP, 700, "hnd"),  # pages longer than a tile, a window
+    ([100, 20], [2000, 40], 2, 1, 128, 48, BF, 0, "nhd"),  # pages that are no boxes
+    ([20 if i % 40 == 0 else 1 for i in range(310)], [25 + (11 * i) % 70 for i in range(310)], 4, 2, 64, 16, BF, 0,
+     "nhd"),  # many short sequences beside longer ones
+    ([300], [520], 1, 1, 64, 128, BF, 0, "nhd"),  # two row tiles, one head
 ]
 
 
@@ -137,17 +144,17 @@ def test_attention_in_a_graph(S):
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("n", [2, 50])
-def test_attention_bad_sequences(S, n):
+@pytest.mark.parametrize("n,page", [(2, 16), (50, 16), (50, 12)])
+def test_attention_bad_sequences(S, n, page):
     """A sequence that cannot be is INVALID and the others are what they were."""
     def problem():
-        return R.Problem([n] * 5, [80, 200, 150, 90, 64], 4, 2, 64, 16, BF, seed=11)
+        return R.Problem([n] * 5, [80, 200, 150, 90, 64], 4, 2, 64, page, BF, seed=11)
 
     pr = problem()
     ref, lse, tol, _ = R.attention(pr)
     pr.table[1, 3] = pr.pages  # a page past the cache
     pr.table[4, 0] = -1
-    pr.kv_lens[2] = pr.table.shape[1] * 16 + 1  # longer than its table
+    pr.kv_lens[2] = pr.table.shape[1] * page + 1  # longer than its table
     q = fused(pr)[0]
     got = S.ChunkAttention()(q, gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens), lse=True)
     assert got["status"].cpu().tolist() == [0, 2, 2, 0, 2]
@@ -249,6 +256,9 @@ APPEND = [
     ([8], [40], 40, 40, 64, 16, BF, 0, False, False, "nhd"),
     ([1] * 70, [i + 1 for i in range(70)], 2, 1, 64, 16, BF, 64, False, True, "nhd"),
     ([3] * 1100, [3 + i % 40 for i in range(1100)], 1, 1, 64, 16, BF, 64, False, False, "nhd"),
+    ([4, 3], [9, 60], 40, 20, 128, 16, FP, 128, False, True, "hnd"),  # more head rows than a block has at once
+    ([2], [7], 260, 2, 8, 16, BF, 8, True, True, "nhd"),  # more heads than the table holds
+    ([5, 1], [20, 33], 3, 2, 128, 16, BF, 64, False, True, "nhd"),  # half of each head rotated
 ]
 
 
@@ -377,18 +387,40 @@ def test_verify(S, V, dtype, has_draft, pad):
     assert np.array_equal(got["tokens"], tokens)
 
 
-def test_verify_full_vocabulary_split(S):
-    """Thresholds that fall in every slice and warp of a large row."""
-    V, B = 151936, 64
+@pytest.mark.parametrize("V,B,dtype", [(151936, 3, torch.float32), (151936, 64, torch.float32), (151936, 100, BF),
+                                       (50257, 200, torch.float32), (50257, 160, BF), (262144, 2, torch.float32)])
+def test_verify_full_vocabulary_split(S, V, B, dtype):
+    """Thresholds that fall in every slice and warp of a large row, for every cluster size; rows
+    that begin anywhere in a vector."""
     rng = np.random.default_rng(3)
-    p = softmax_rows(rng, 1, V, 1.0)
+    p = rounded(softmax_rows(rng, 1, V, 1.0), dtype)
     target = np.repeat(p, B, 0)
     ul = ((np.arange(B) + 0.5) / B).astype(np.float32)
-    got = run_verify(S, target, None, [], [0] * (B + 1), [], ul, 0)
+    got = run_verify(S, target, None, [], [0] * (B + 1), [], ul, 0, dtype)
     w = np.floor(p[0].astype(np.float64) * 2.0 ** 40).astype(np.int64)
     c = np.cumsum(w)
     want = [int(np.searchsorted(c, int(math.floor(float(a) * 2.0 ** 31)) * int(c[-1]) >> 31, side="right")) for a in ul]
     assert got["tokens"][:, 0].tolist() == want
+
+
+@pytest.mark.parametrize("V,dtype", [(151936, torch.float32), (50257, torch.float32), (50257, BF)])
+def test_verify_full_vocabulary_residual(S, V, dtype):
+    """The weights left above a draft's row, where the two rows are aligned differently."""
+    B = 6
+    rng = np.random.default_rng(4)
+    target, draft = (rounded(softmax_rows(rng, n, V, 1.0), dtype) for n in (2 * B, B))
+    x, u, ul = rng.integers(0, V, B), np.full(B, 0.99999, np.float32), rng.random(B, dtype=np.float32)
+    u[0] = 0.0
+    got = run_verify(S, target, draft, x, np.arange(B + 1), u, ul, 1, dtype)
+    P, Q = (np.floor(a.astype(np.float64) * 2.0 ** 40).astype(np.int64) for a in (target, draft))
+    for b in range(B):
+        # both factors have 24 bits: the product is exact in 64
+        ok = float(u[b]) * float(draft[b, x[b]]) < float(target[2 * b, x[b]])
+        w = P[2 * b + 1] if ok else np.maximum(P[2 * b] - Q[b], 0)
+        c = np.cumsum(w)
+        k = int(math.floor(float(ul[b]) * 2.0 ** 31)) * int(c[-1]) >> 31
+        t = int(np.searchsorted(c, k, side="right"))
+        assert got["tokens"][b].tolist() == ([int(x[b]), t] if ok else [t, -1]), b
 
 
 def test_verify_edges(S):
