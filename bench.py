@@ -90,14 +90,15 @@ def peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
+SAMPLER_SOURCES = ("bulk_copy.cuh", "clsample.cu", "sampler_math.cuh", "sweep.cuh")
+
+
 def kernel_source_hash():
-    """Hash of the CUDA sources and the C header (ties a committed ncu traffic figure
-    to the kernel it was measured on)."""
+    """Hash of the sampler's CUDA sources (ties a committed ncu traffic figure to the kernel it
+    was measured on)."""
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "constrained_logits_sampling_gb300", "csrc")
-    paths = sorted(os.path.join(csrc, n) for n in os.listdir(csrc) if n.endswith((".cu", ".cuh")))
-    for p in paths + [os.path.join(ROOT, "include", "clsample.h")]:
-        with open(p, "rb") as f:
+    for n in SAMPLER_SOURCES:
+        with open(os.path.join(ROOT, "constrained_logits_sampling_gb300", "csrc", n), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
 

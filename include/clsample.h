@@ -332,7 +332,7 @@ enum { CLSAMPLE_T_BF16 = 0, CLSAMPLE_T_F16 = 1 };
  * A token whose position is negative or not below max_pos (with rotation), or whose page
  * is not valid, is not written to the cache and its q_out row is zero; its sequence is
  * INVALID.  Two tokens of a call must not share a slot.
- * Limits: 1 <= D <= 256, rot_dim even and <= D, any strides.  Fast path: D, rot_dim (and
+ * Limits: 1 <= D <= 256, rot_dim even and <= D, any strides, lengths up to 2^30.  Fast path: D, rot_dim (and
  * rot_dim/2 in the half-split form) multiples of 8, arrays and strides multiples of 16 bytes,
  * at most 256 heads in all. */
 typedef struct {
@@ -382,9 +382,14 @@ int clsample_kv_append(const clsample_kv_append_args_t* args, clsample_stream_t 
  * Products are of `dtype` with float32 sums; the softmax is float32; its weights are
  * rounded to `dtype` for the product with the values, as the matrix instructions need.
  * The result of a call does not depend on timing: partial sums over a split key axis are
- * joined in key order.
+ * joined in key order.  A value that is not finite, of a key that a row does not see but another
+ * new row of the sequence does, may make the first row NaN (0 x NaN in a product).
+ * A wait inside the kernels that runs out (a GPU that stopped scheduling them) does not hang: all
+ * sequences of that call and of later calls on the handle are OVERFLOW.
  * Limits: D 64 or 128; Hq a multiple of Hkv; q, out and cache addresses and strides
- * multiples of 16 bytes (ERR_ALIGN). */
+ * multiples of 16 bytes (ERR_ALIGN); T Hq / Hkv below 2^31 - 1024; lengths up to 2^30.
+ * Speed: pages of 8, 16, 32, 64 or a multiple of 128 slots are copied by TMA for sequences of
+ * more than 16 packed rows (n_b Hq / Hkv); other sizes take about twice the time there. */
 typedef struct {
   int32_t B, T, Hq, Hkv, D;
   int32_t dtype;
@@ -412,7 +417,8 @@ typedef struct clsample_attention clsample_attention_t;
 int clsample_attention_create(clsample_attention_t** out);
 void clsample_attention_destroy(clsample_attention_t* handle);
 
-/* Enqueues one call on `stream`; nothing when B == 0. */
+/* Enqueues one call on `stream` (two or three launches, each of which may start while the one
+ * before it ends; they can be captured in a graph); nothing when B == 0. */
 int clsample_chunk_attention(clsample_attention_t* handle, const clsample_attention_args_t* args,
                              clsample_stream_t stream);
 
