@@ -35,6 +35,7 @@ __device__ __forceinline__ void attention_status(const AttnParams& P, bool gave_
     int bad = !s.ok;
     if (s.ok && s.n > 0 && s.len > 0) {
       const int lo = a.window > 0 ? max(0, s.len - s.n - a.window + 1) : 0;
+#pragma unroll 8
       for (int p = lo / a.page_size + threadIdx.x; p <= (s.len - 1) / a.page_size; p += NT) {
         const int id = __ldg(a.page_table + (int64_t)b * a.table_stride + p);
         bad |= id < 0 || id >= a.num_pages;

@@ -22,7 +22,8 @@ constexpr int kThreads = 256;
 constexpr int kCtasPerSm = 4;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBatch = 128;  // vectors of a warp between two marks
+constexpr int kLoad = 128;    // vectors that a warp loads at once
+constexpr int kBatch = 256;  // vectors of a warp between two marks: at most 32 batches, a thread a vector
 constexpr int kMaxVocab = 262144;
 
 // floor(2^40 p) for p in [0, 1], as hi 2^23 + lo, hi = floor(2^17 p) and lo = floor(2^23 times
@@ -189,14 +190,13 @@ struct Weights {
                        : mass_of(mp.hi[e] - mq.hi[e], mp.lo[e] - mq.lo[e]);
     }
   }
-  // Sum over a warp's vectors first .. end - 1, kBatch at a time with four loads of each row in
+  // Sum over a warp's vectors first .. end - 1, kLoad at a time with four loads of each row in
   // flight; the lane's sum of each batch is left in marks[batch * kThreads].
   __device__ __forceinline__ int64_t sum_range(int first, int end, Range* range, int64_t* marks) const {
     const int lane = threadIdx.x & 31, from = whole_from(), to = min(end, whole_to());
-    int64_t total = 0;
-    for (int v0 = first; v0 < end; v0 += kBatch) {  // uniform over the warp
-      int64_t sum = 0;
-      if (v0 >= from && v0 + kBatch <= to) {
+    int64_t total = 0, sum = 0;
+    for (int v0 = first; v0 < end; v0 += kLoad) {  // uniform over the warp
+      if (v0 >= from && v0 + kLoad <= to) {
         uint4 x4[4], y4[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) x4[k] = bits(p, (v0 + 32 * k + lane) * N - a, 0);
@@ -213,15 +213,18 @@ struct Weights {
         }
       } else {
 #pragma unroll 1
-        for (int v = v0 + lane; v < min(end, v0 + kBatch); v += 32) {
+        for (int v = v0 + lane; v < min(end, v0 + kLoad); v += 32) {
           float x[N], y[N];
           values(v, x, y);
           sum += sum_of(v, x, y, range);
         }
       }
-      *marks = sum;
-      marks += kThreads;
-      total += sum;
+      if (v0 + kLoad >= end || (v0 + kLoad - first) % kBatch == 0) {
+        *marks = sum;
+        marks += kThreads;
+        total += sum;
+        sum = 0;
+      }
     }
     return total;
   }
@@ -365,9 +368,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const __gr
   left -= __shfl_sync(~0u, run - batch_sum, batch);
   p0 += batch * kBatch;
   // the token, a vector a thread
+  static_assert(kBatch == kThreads, "one round");
   const int v = p0 + tid;
   int64_t x[N], mine = 0;
-  if (tid < kBatch && v < p1) {
+  if (v < p1) {
     w.vector(v, x);
 #pragma unroll
     for (int i = 0; i < N; ++i) mine += x[i];

@@ -17,6 +17,7 @@ limits are stated in include/clsample.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Dict, Optional
@@ -64,6 +65,11 @@ def _device() -> torch.device:
     if not torch.cuda.is_available():
         raise RuntimeError("the operators need a CUDA device")
     return torch.device("cuda", torch.cuda.current_device())
+
+
+def _on_stream(stream):
+    # outputs belong to the stream that writes them
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def _on(t: torch.Tensor, name: str, device: torch.device, dtype, dims: int):
@@ -177,10 +183,11 @@ class KVAppend:
                  **kw) -> Dict[str, torch.Tensor]:
         """Append, and return ``q`` (normed and rotated, a new tensor unless ``q_out`` is
         given) and ``status`` (int32 per sequence)."""
-        if kw.get("q_out") is None:
-            kw["q_out"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if kw.get("row_status") is None:
-            kw["row_status"] = torch.empty(kv_lens.numel(), dtype=torch.int32, device=q.device)
+        with _on_stream(stream):
+            if kw.get("q_out") is None:
+                kw["q_out"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if kw.get("row_status") is None:
+                kw["row_status"] = torch.empty(kv_lens.numel(), dtype=torch.int32, device=q.device)
         self.apply(self.make_args(q, k, v, k_cache, v_cache, page_table, cu_new, kv_lens, **kw), stream)
         return {"q": kw["q_out"], "status": kw["row_status"]}
 
@@ -241,11 +248,12 @@ class ChunkAttention:
                  **kw) -> Dict[str, torch.Tensor]:
         """Attend, and return ``out`` [T, Hq, D], ``status`` (int32 per sequence) and, with
         ``lse``, ``lse`` [T, Hq] (float32).  Rows that no sequence owns are not written."""
-        if kw.get("out") is None:
-            kw["out"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if kw.get("row_status") is None:
-            kw["row_status"] = torch.empty(kv_lens.numel(), dtype=torch.int32, device=q.device)
-        sums = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse else None
+        with _on_stream(stream):
+            if kw.get("out") is None:
+                kw["out"] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if kw.get("row_status") is None:
+                kw["row_status"] = torch.empty(kv_lens.numel(), dtype=torch.int32, device=q.device)
+            sums = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse else None
         self.apply(self.make_args(q, k_cache, v_cache, page_table, cu_new, kv_lens, lse=sums, **kw), stream)
         out = {"out": kw["out"], "status": kw["row_status"]}
         if lse:
@@ -316,9 +324,10 @@ class DraftVerifier:
         """Verify, and return ``tokens`` int32 [B, max_draft + 1] (accepted tokens, the drawn
         token, then -1), ``accepted`` and ``status`` (int32 per request)."""
         B, dev = u_sample.numel(), target_probs.device
-        out = {"tokens": torch.empty(B, int(max_draft) + 1, dtype=torch.int32, device=dev),
-               "accepted": torch.empty(B, dtype=torch.int32, device=dev),
-               "status": torch.empty(B, dtype=torch.int32, device=dev)}
+        with _on_stream(stream):
+            out = {"tokens": torch.empty(B, int(max_draft) + 1, dtype=torch.int32, device=dev),
+                   "accepted": torch.empty(B, dtype=torch.int32, device=dev),
+                   "status": torch.empty(B, dtype=torch.int32, device=dev)}
         self.apply(self.make_args(target_probs, draft_tokens, cu_draft, u_accept, u_sample, max_draft=max_draft,
                                   draft_probs=draft_probs, tokens=out["tokens"], accepted=out["accepted"],
                                   row_status=out["status"]), stream)

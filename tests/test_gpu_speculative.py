@@ -388,7 +388,8 @@ def test_verify(S, V, dtype, has_draft, pad):
 
 
 @pytest.mark.parametrize("V,B,dtype", [(151936, 3, torch.float32), (151936, 64, torch.float32), (151936, 100, BF),
-                                       (50257, 200, torch.float32), (50257, 160, BF), (262144, 2, torch.float32)])
+                                       (50257, 200, torch.float32), (50257, 160, BF), (262144, 2, torch.float32),
+                                       (262143, 160, torch.float32)])
 def test_verify_full_vocabulary_split(S, V, B, dtype):
     """Thresholds that fall in every slice and warp of a large row, for every cluster size; rows
     that begin anywhere in a vector."""
