@@ -38,9 +38,10 @@ cudaError_t launch_after(Kernel fn, int grid, int threads, int smem, cudaStream_
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// The cache as a tensor of (element, slot, head, page), copied in boxes of 64 elements of the
-// slots of a page, of a tile's keys at most.
-bool cache_map(const AttnParams& P, const void* base, CUtensorMap* map) {
+// A tensor map of 16-bit elements, 128-byte swizzle, zeros out of bounds; false if there is none.
+template <int N>
+bool make_map(const AttnParams& P, const void* base, const cuuint64_t (&dims)[N], const int64_t (&strides)[N - 1],
+              const cuuint32_t (&box)[N], CUtensorMap* map) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -53,19 +54,40 @@ bool cache_map(const AttnParams& P, const void* base, CUtensorMap* map) {
       fn = nullptr;
     return reinterpret_cast<Encode>(fn);
   }();
-  const clsample_attention_args_t& a = P.a;
-  if (!encode || a.num_pages == 0) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
-  // the stride of a dimension of one element is never used, but has to be valid
-  auto stride = [](int64_t s, int n) { return n > 1 ? (cuuint64_t)s * 2 : (cuuint64_t)16; };
-  const cuuint64_t strides[3] = {stride(a.slot_stride, a.page_size), stride(a.head_stride, a.Hkv),
-                                 stride(a.page_stride, a.num_pages)};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(a.page_size < kChunkKeys ? a.page_size : kChunkKeys), 1, 1};
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  return encode(map, a.dtype == CLSAMPLE_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  if (!encode) return false;
+  cuuint64_t bytes[N - 1];
+  cuuint32_t ones[N];
+  for (int i = 0; i < N; ++i) {
+    if (dims[i] == 0) return false;
+    // the stride of a dimension of one element is never used, but has to be valid
+    if (i > 0) bytes[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] * 2 : 16;
+    ones[i] = 1;
+  }
+  return encode(map, P.a.dtype == CLSAMPLE_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                N, const_cast<void*>(base), dims, bytes, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The cache as (element, slot, head, page), in boxes of 64 elements of the slots of a page, of a
+// tile's keys at most.
+bool cache_map(const AttnParams& P, const void* base, CUtensorMap* map) {
+  const clsample_attention_args_t& a = P.a;
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+  const int64_t strides[3] = {a.slot_stride, a.head_stride, a.page_stride};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(a.page_size < kChunkKeys ? a.page_size : kChunkKeys), 1, 1};
+  return make_map(P, base, dims, strides, box, map);
+}
+
+// The queries as (element, head, token), in boxes of 64 elements of a row tile: the heads of a key
+// head times as many tokens as make 128 rows.
+bool query_map(const AttnParams& P, CUtensorMap* map) {
+  const clsample_attention_args_t& a = P.a;
+  if (P.g > 128 || 128 % P.g != 0) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+  const int64_t strides[2] = {a.q_stride_h, a.q_stride_t};
+  const cuuint32_t box[3] = {64, (cuuint32_t)P.g, (cuuint32_t)(128 / P.g)};
+  return make_map(P, a.q, dims, strides, box, map);
 }
 
 template <class Kernel>
@@ -74,18 +96,19 @@ cudaError_t allow_smem(Kernel fn, int bytes) {
 }
 
 template <class T, int D>
-cudaError_t launch_chunk(const AttnParams& P, int sms, cudaStream_t st) {
+cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
   // Boxes have to start on the eight rows of the swizzle and fill a tile.  2 x 2048 tokens over
   // 14000 keys: 565 us with them, 1197 row by row.
   const int page = P.a.page_size;
-  CUtensorMap k_map{}, v_map{};
+  CUtensorMap k_map{}, v_map{}, q_map{};
   const bool boxes = page >= 8 && (page % kChunkKeys == 0 || kChunkKeys % page == 0) &&
                      cache_map(P, P.a.k_cache, &k_map) && cache_map(P, P.a.v_cache, &v_map);
+  P.q_box = boxes && query_map(P, &q_map);
   const int bytes = ChunkShape<D>::kBytes;
   auto* fn = boxes ? attn_chunk_kernel<T, D, true> : attn_chunk_kernel<T, D, false>;
   const cudaError_t e = allow_smem(fn, bytes);
   if (e != cudaSuccess) return e;
-  fn<<<sms, kChunkThreads, bytes, st>>>(P, k_map, v_map);
+  fn<<<sms, kChunkThreads, bytes, st>>>(P, k_map, v_map, q_map);
   return cudaGetLastError();
 }
 

@@ -5,9 +5,11 @@
 //   warps 8, 9, 11   loads (below);
 //   warp 10          issues the products.
 // Loads come in two forms.  Where pages are whole boxes of a tile (8, 16, 32, 64 or a
-// multiple of 128 slots) warp 8 copies keys and values by TMA, one box a page and 64
-// elements, an invalid page as zeros; warps 9 and 11 load the queries, and warp 9 clears the
-// value slots that lie outside the unit's keys (they may hold anything, and 0 x NaN is NaN).
+// multiple of 128 slots) warps 8 and 11 copy keys and values by TMA, one box a page and 64
+// elements, an invalid page as zeros (a box takes some 75 cycles to issue, so with pages of 16
+// slots one warp would not keep up: 771 us against 582); warp 9 loads the queries, in one box a
+// row tile where the query heads of a key head divide 128 and row by row otherwise, and clears
+// the value slots that lie outside the unit's keys (they may hold anything, and 0 x NaN is NaN).
 // Other page sizes are copied row by row with cp.async by warps 8 and 9, zeros where there
 // is no key, and warp 11 hands what has landed over to the tensor cores' proxy.
 // S = Q K^T goes to tensor memory (128 columns a tile), the softmax warps read it, write the
@@ -86,7 +88,7 @@ template <int NS, int NV>
 struct ChunkShared {
   // filled by the load warps; handed over; S of a tile complete, so that its keys' slot and
   // the slot of the values before them are free
-  unsigned long long k_landed[NS], v_landed[NV], k_full[NS], v_full[NV], tile_done[NS];
+  unsigned long long k_landed[NS], v_landed[NV], k_full[NS], v_full[NV], tile_done[2 * NS];
   unsigned long long q_full, q_empty, end, s_full[2], p_half[2], p_full[2], o_full[2];
   unsigned long long unit_full[2], unit_done[2];  // of the units with even and odd numbers
   uint32_t tmem;
@@ -112,10 +114,11 @@ struct SoftmaxSync {  // the 256 softmax threads
 template <class T, int D, bool kTma>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     attn_chunk_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap k_map,
-                      const __grid_constant__ CUtensorMap v_map) {
+                      const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
   using Shape = ChunkShape<D>;
   constexpr int NS = Shape::kKeySlots, NV = Shape::kValueSlots, kTile = Shape::kTile, KC = D / 8;
   constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 elements
+  constexpr int kRowWarps = kTma ? 1 : 2;  // that copy rows
   extern __shared__ unsigned char raw[];
   __shared__ ChunkShared<NS, NV> sh;
   unsigned char* const smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -138,12 +141,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.k_landed[i], 64 + 2);  // every load thread's copies, and each warp's words of key_ok
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.tile_done[i], 1);
+      mbar_init(&sh.tile_done[NS + i], 1);
     }
     for (int i = 0; i < NV; ++i) {
       mbar_init(&sh.v_landed[i], kTma ? 1 : 64);
       mbar_init(&sh.v_full[i], 1);
     }
-    mbar_init(&sh.q_full, 64);
+    mbar_init(&sh.q_full, kTma && P.q_box ? 1 : 32 * kRowWarps);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.end, 1);
     for (int w = 0; w < 2; ++w) {
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int kb = kb0 + j * kChunkKeys;
           bounded_wait(&sh.s_full[w], s_phase, &sh.dead);
           if (lane == 0) {
-            if ((warp & 3) == 0 && (split || w == 1)) mbar_arrive(&sh.tile_done[(tile + j) % NS]);
+            if ((warp & 3) == 0 && (split || w == 1)) mbar_arrive(&sh.tile_done[(tile + j) % (2 * NS)]);
           }
           __syncwarp();
           s_phase ^= 1;
@@ -364,6 +368,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         note_cut(P, sh.span, u, sh.unit_begin[seg & 1]);
         if (sh.dead) *P.gave_up = 1;
       }
+      if (split) fence_async_proxy();  // the room may next be written by a box copy
       SoftmaxSync::sync();
       if (last) break;
       if (tid == 0) mbar_arrive(&sh.unit_done[seg & 1]);
@@ -371,7 +376,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else if (warp != 10) {
     // ------------------------------------------------------------------ loads
     regs_down<kOtherRegs>();
-    const int lw = warp == 8 ? 0 : warp == 9 ? (kTma ? 0 : 1) : 1;  // of the two warps that copy rows
+    const int lw = kTma ? 0 : warp - 8;  // of the warps that copy rows
+    bool met = false;                    // the last unit's halves met in the second row tile's room
     const int tiles = (int)(span.t1 - span.t0);
     // 32 rows to rows r0.. of a tile; lane i has the place of row i, bit i of `live` tells
     // whether it is read or zero
@@ -384,6 +390,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     };
     auto copy_queries = [&](uint32_t seg) {
+      constexpr int kBlocks = 8 / kRowWarps;
+      const bool box = kTma && P.q_box;
+      int64_t off[kBlocks];
+      unsigned live[kBlocks];
+      if (!box) {  // each lane finds the places of its rows, one of 32, before it has to wait
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const int mine = (i * kRowWarps + lw) * 32 + lane, row = u.row0 + mine;
+          off[i] = mine < u.rows ? (int64_t)(u.q0 + row / P.g) * a.q_stride_t +
+                                       (int64_t)(u.h * P.g + row % P.g) * a.q_stride_h
+                                 : 0;
+          live[i] = __ballot_sync(~0u, mine < u.rows);
+        }
+      }
       // the unit's place is free when the softmax warps are done with the one before the last
       if (seg >= 2) bounded_wait(&sh.unit_done[seg & 1], ((seg - 2) >> 1) & 1, &sh.dead);
       if (lw == 0 && lane == 0) {
@@ -392,42 +412,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_arrive(&sh.unit_full[seg & 1]);
       }
       bounded_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
-      __syncwarp();
-#pragma unroll 1
-      for (int w = 0; w < (u.rows <= 128 ? 2 : 4); ++w) {
-        // the second row tile's room is where the halves of the last unit met
-        if (w == 2 && seg >= 1) bounded_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.dead);
+      const int tiles_of_rows = u.rows <= 128 ? 1 : 2;
+      auto second_tile = [&]() {
+        if (met) bounded_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.dead);
         __syncwarp();
-        const int first = (w * 2 + lw) * 32;  // of 32 rows, one a lane, whose place it hands to the others
-        const int mine = first + lane, row = u.row0 + mine;
-        const bool live = mine < u.rows;
-        const int64_t off = live ? (int64_t)(u.q0 + row / P.g) * a.q_stride_t +
-                                       (int64_t)(u.h * P.g + row % P.g) * a.q_stride_h
-                                 : 0;
-        copy_rows((const T*)a.q, off, __ballot_sync(~0u, live), q_smem + (first >> 7) * kTile, first & 127);
+      };
+      __syncwarp();
+      if (box) {
+        // (rows past the sequence's are other sequences' or zero, and are not stored)
+        if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, tiles_of_rows * kTile);
+        for (int w = 0; w < tiles_of_rows; ++w) {
+          if (w == 1) second_tile();
+          if (lane < D / 64 && !sh.dead)
+            tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, u.h * P.g, u.q0 + (u.row0 + w * 128) / P.g,
+                      &sh.q_full);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const int first = (i * kRowWarps + lw) * 32;
+          if (first >= 128 && tiles_of_rows == 1) break;
+          if (i == kBlocks / 2) second_tile();
+          if (first < u.rows) copy_rows((const T*)a.q, off[i], live[i], q_smem + (first >> 7) * kTile, first & 127);
+        }
+        cp_async_arrive(smem_addr(&sh.q_full));
       }
-      cp_async_arrive(smem_addr(&sh.q_full));
+      met = u.rows <= 128;
     };
     // The slot of a tile's keys is free when S of the tile that had it is complete, and the
     // slot of its values when O is, which a later tile's completion covers: the next one's if
     // both halves take each tile, the one after it otherwise (and across units, where either
-    // may have been the case).  The values' gate is only waited for where it is the later
-    // one: the keys' has been passed, and by now its barrier may be a phase further.
-    auto key_slot = [&](uint32_t it) {
-      const int64_t gate = (int64_t)it - NS;
-      if (gate >= 0) bounded_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
+    // may have been the case).  Of twice as many completions as there are key slots the one
+    // waited for is still the last on its barrier.
+    auto tile_done = [&](int64_t gate) {
+      if (gate >= 0) bounded_wait(&sh.tile_done[gate % (2 * NS)], (gate / (2 * NS)) & 1, &sh.dead);
       __syncwarp();
     };
-    auto value_slot = [&](uint32_t it, int j) {
-      const int64_t gate = (int64_t)it - NV + (u.rows <= 128 || j < NV ? 2 : 1);
-      if (gate >= 0 && gate > (int64_t)it - NS) bounded_wait(&sh.tile_done[gate % NS], (gate / NS) & 1, &sh.dead);
-      __syncwarp();
-    };
+    auto key_slot = [&](uint32_t it) { tile_done((int64_t)it - NS); };
+    auto value_slot = [&](uint32_t it, int j) { tile_done((int64_t)it - NV + (u.rows <= 128 || j < NV ? 2 : 1)); };
     // a tile with values outside the unit's keys
     auto edge = [&](int tile) { return tile * kChunkKeys < u.key_lo || tile * kChunkKeys + kChunkKeys > u.key_hi; };
 
-    if (kTma && warp == 8) {
-      // lane i has the i-th page (or 128 slots of one) of a tile
+    if (kTma && warp != 9) {
+      // lane i has the i-th page (or 128 slots of one) of a tile; warp 8 the keys, 11 the values
+      const bool keys = warp == 8;
+      const CUtensorMap* map = keys ? &k_map : &v_map;
       const int box = min(a.page_size, kChunkKeys), boxes = kChunkKeys / box;
       uint32_t it = 0;
       while (true) {
@@ -448,28 +477,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const unsigned bad = __ballot_sync(~0u, page < 0);
           const int from = page < 0 ? a.num_pages : page;
           page = page_of(j + 1);
-          key_slot(it);
-          if (lane < 4) {
-            uint32_t word = ~0u;
-            if (bad)
-              for (int e = 0; e < 32; ++e)
-                if ((bad >> ((lane * 32 + e) / box)) & 1) word &= ~(1u << e);
-            sh.key_ok[it % (2 * NS)][lane] = word;
+          unsigned long long* full;
+          uint32_t dst;
+          if (keys) {
+            key_slot(it);
+            if (lane < 4) {
+              uint32_t word = ~0u;
+              if (bad)
+                for (int e = 0; e < 32; ++e)
+                  if ((bad >> ((lane * 32 + e) / box)) & 1) word &= ~(1u << e);
+              sh.key_ok[it % (2 * NS)][lane] = word;
+            }
+            full = &sh.k_full[it % NS];
+            dst = k_smem + it % NS * kTile;
+          } else {
+            value_slot(it, j);
+            full = edge(tile) ? &sh.v_landed[it % NV] : &sh.v_full[it % NV];
+            dst = v_smem + it % NV * kTile;
           }
           __syncwarp();
-          unsigned long long* full = &sh.k_full[it % NS];
           if (lane == 0) mbar_arrive_expect_tx(full, kTile);
           __syncwarp();
           if (lane < boxes && !sh.dead)
             for (int x = 0; x < D / 64; ++x)
-              tma_load4(k_smem + it % NS * kTile + x * kHalf + lane * box * 128, &k_map, x * 64, slot, u.h, from, full);
-          value_slot(it, j);
-          full = edge(tile) ? &sh.v_landed[it % NV] : &sh.v_full[it % NV];
-          if (lane == 0) mbar_arrive_expect_tx(full, kTile);
-          __syncwarp();
-          if (lane < boxes && !sh.dead)
-            for (int x = 0; x < D / 64; ++x)
-              tma_load4(v_smem + it % NV * kTile + x * kHalf + lane * box * 128, &v_map, x * 64, slot, u.h, from, full);
+              tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h, from, full);
         }
         t += cnt;
         if (t >= span.t1) break;
@@ -485,28 +516,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int j0 = (int)(t - unit_begin);
         const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
         copy_queries(seg);
-        if (warp == 9) {
-          for (int j = 0; j < cnt; ++j) {
-            const int tile = u.tile0 + j0 + j;
-            if (!edge(tile)) continue;
-            const uint32_t st = (it + j) % NV;
-            uint32_t parity = 0;
+        for (int j = 0; j < cnt; ++j) {
+          const int tile = u.tile0 + j0 + j;
+          if (!edge(tile)) continue;
+          const uint32_t st = (it + j) % NV;
+          uint32_t parity = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-              if (i == st) parity = edges[i]++ & 1;
-            bounded_wait(&sh.v_landed[st], parity, &sh.dead);
-            __syncwarp();
-            const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
-            for (int i = lane; i < 128 * KC; i += 32) {  // a row's pieces may lie anywhere in it: all are cleared
-              const int row = i / KC, ch = i % KC;
-              if (row < lo || row >= hi)
-                *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.v_full[st]);
+          for (int i = 0; i < NV; ++i)
+            if (i == st) parity = edges[i]++ & 1;
+          bounded_wait(&sh.v_landed[st], parity, &sh.dead);
+          __syncwarp();
+          const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
+          for (int i = lane; i < 128 * KC; i += 32) {  // a row's pieces may lie anywhere in it: all are cleared
+            const int row = i / KC, ch = i % KC;
+            if (row < lo || row >= hi)
+              *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
           }
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.v_full[st]);
         }
         it += cnt;
         ++seg;

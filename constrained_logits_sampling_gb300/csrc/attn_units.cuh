@@ -20,6 +20,7 @@ struct AttnParams {
   int capacity;     // positions that the page table holds
   int min_rows;     // this launch takes the sequences with min_rows <= n g < max_rows
   int max_rows;
+  int q_box;        // queries may be copied in boxes of 128 rows
   float* partial;   // scratch: two slots per CTA
   struct CutUnit* cut;  // one per CTA: the unit that starts in its span and ends in another's
   int* gave_up;     // set when a bounded wait ran out

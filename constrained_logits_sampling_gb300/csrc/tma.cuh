@@ -25,6 +25,16 @@ __device__ __forceinline__ bool mbar_test_wait(unsigned long long* bar, uint32_t
 __device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// One box of a tensor map of rank 3 to shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int head, int token,
+                                          unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(head), "r"(token), "r"(smem_addr(bar))
+      : "memory");
+}
+
 // One box of a tensor map of rank 4 to shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int x, int slot, int head, int page,
                                           unsigned long long* bar) {
