@@ -216,6 +216,7 @@ int clsample_chunk_attention(clsample_attention_t* h, const clsample_attention_a
   P.a = *a;
   if (P.a.window > kMaxLen) P.a.window = kMaxLen;  // longer than any sequence
   P.g = a->Hq / a->Hkv;
+  P.g_shift = (P.g & (P.g - 1)) == 0 ? __builtin_ctz((unsigned)P.g) : -1;
   P.page_shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz((unsigned)a->page_size) : -1;
   P.capacity = capacity_of(a->max_pages, a->page_size);
   P.scale_log2 = a->scale * 1.44269504088896341f;

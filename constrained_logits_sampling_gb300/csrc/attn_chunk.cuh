@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       float m = neg_inf, l = 0.f;  // reference maximum (log2 units) and weights' sum
       if (cnt > jw) {
         const int first_pos = u.len - u.n, kb0 = (u.tile0 + j0) * kChunkKeys;
-        const int pos = live ? first_pos + (u.row0 + r) / P.g : -1;
+        const int pos = live ? first_pos + token_of(P, u.row0 + r) : -1;
         const int half0 = split ? 0 : w * 128;
-        const int pos_first = first_pos + (u.row0 + half0) / P.g;
-        const int pos_last = first_pos + (u.row0 + min(u.rows, half0 + 128) - 1) / P.g;
+        const int pos_first = first_pos + token_of(P, u.row0 + half0);
+        const int pos_last = first_pos + token_of(P, u.row0 + min(u.rows, half0 + 128) - 1);
         for (int j = jw; j < cnt; j += step) {
           const int kb = kb0 + j * kChunkKeys;
           bounded_wait(&sh.s_full[w], s_phase, &sh.dead);
@@ -284,28 +284,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // each row, so that threads with a row each write whole lines.
       float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
       const bool done = cnt == u.tiles;
-      const int row = u.row0 + r;
-      T* dst = (T*)a.out + (int64_t)(u.q0 + row / P.g) * a.o_stride_t +
-               (int64_t)(u.h * P.g + row % P.g) * a.o_stride_h;
-      // NC of this thread's row's sums, from column c on
-      auto put = [&](const auto& x, auto n, int c) {
-        constexpr int NC = decltype(n)::value;
-        if (!live) return;
+      // Four lanes have four rows; each stores a quarter of 32 columns of all four, so that a
+      // store is of 64 bytes a row and not of 16.
+      const int row = u.row0 + min(r, u.rows - 1);
+      const int64_t dst = (int64_t)(u.q0 + token_of(P, row)) * a.o_stride_t +
+                          (int64_t)(u.h * P.g + head_of(P, row)) * a.o_stride_h;
+      // 32 of this thread's row's sums, from column c on
+      auto put = [&](const uint32_t (&x)[32], int c) {
         if (done) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint32_t y[4][4];
 #pragma unroll
-          for (int e = 0; e < NC; e += 8) {
-            uint32_t y[4];
+          for (int i = 0; i < 16; ++i)
+            y[i >> 2][i & 3] = l == 0.f ? 0u
+                                        : Pair<T>::narrow(__uint_as_float(x[2 * i]) * inv,
+                                                          __uint_as_float(x[2 * i + 1]) * inv);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              y[i] = l == 0.f ? 0u
-                              : Pair<T>::narrow(__uint_as_float(x[e + 2 * i]) * inv,
-                                                __uint_as_float(x[e + 2 * i + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int s = 1; s <= 2; s *= 2) {
+            const bool upper = lane & s;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i & s) continue;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(~0u, upper ? y[i][e] : y[i + s][e], s);
+                if (upper)
+                  y[i][e] = got;
+                else
+                  y[i + s][e] = got;
+              }
+            }
           }
-        } else {
 #pragma unroll
-          for (int e = 0; e < NC; e += 4)
+          for (int i = 0; i < 4; ++i) {
+            const int64_t to = __shfl_sync(~0u, dst, (lane & ~3) + i);
+            if ((r & ~3) + i < u.rows)
+              *reinterpret_cast<uint4*>((T*)a.out + to + c + (lane & 3) * 8) =
+                  make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+          }
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
             __stcg(reinterpret_cast<uint4*>(slot + (c + e) * kChunkRows + r * 4),
                    make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
         }
@@ -341,7 +360,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int i = 0; i < 4; ++i)
               x[e + i] = __float_as_uint((cnt > w ? __uint_as_float(x[e + i]) * mine : 0.f) + ov[i] * others);
           }
-          put(x, std::integral_constant<int, 32>(), w * (D / 2) + c);
+          put(x, w * (D / 2) + c);
           SoftmaxSync::sync();
         }
       } else {
@@ -350,7 +369,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           uint32_t x[32];
           __syncwarp();
           tmem_ld32(x, o_tmem + c);
-          put(x, std::integral_constant<int, 32>(), c);
+          put(x, c);
         }
       }
       if (live && (w == 0 || !split)) {
@@ -398,8 +417,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
           const int mine = (i * kRowWarps + lw) * 32 + lane, row = u.row0 + mine;
-          off[i] = mine < u.rows ? (int64_t)(u.q0 + row / P.g) * a.q_stride_t +
-                                       (int64_t)(u.h * P.g + row % P.g) * a.q_stride_h
+          off[i] = mine < u.rows ? (int64_t)(u.q0 + token_of(P, row)) * a.q_stride_t +
+                                       (int64_t)(u.h * P.g + head_of(P, row)) * a.q_stride_h
                                  : 0;
           live[i] = __ballot_sync(~0u, mine < u.rows);
         }
@@ -424,7 +443,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int w = 0; w < tiles_of_rows; ++w) {
           if (w == 1) second_tile();
           if (lane < D / 64 && !sh.dead)
-            tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, u.h * P.g, u.q0 + (u.row0 + w * 128) / P.g,
+            tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, u.h * P.g, u.q0 + token_of(P, u.row0 + w * 128),
                       &sh.q_full);
         }
       } else {

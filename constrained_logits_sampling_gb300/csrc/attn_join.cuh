@@ -90,7 +90,7 @@ __device__ __forceinline__ void sum_parts(RowSum<NV>* r, int first, int step, in
 template <class T, int D, int NV>
 __device__ __forceinline__ void finish_row(const AttnParams& P, const CutUnit& u, int r, int d, const RowSum<NV>& s) {
   const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
-  const int row = u.row0 + r, token = u.q0 + row / P.g, head = u.h * P.g + row % P.g;
+  const int row = u.row0 + r, token = u.q0 + token_of(P, row), head = u.h * P.g + head_of(P, row);
   T* dst = (T*)P.a.out + (int64_t)token * P.a.o_stride_t + (int64_t)head * P.a.o_stride_h + d;
 #pragma unroll
   for (int i = 0; i < NV; ++i)

@@ -92,8 +92,8 @@ __device__ __forceinline__ float* scratch_slot(const AttnParams& P, int cta, int
 template <class T>
 __device__ __forceinline__ void store_out4(const AttnParams& P, const Unit& u, int r, int d, float4 o) {
   const int row = u.row0 + r;
-  T* dst = (T*)P.a.out + (int64_t)(u.q0 + row / P.g) * P.a.o_stride_t +
-           (int64_t)(u.h * P.g + row % P.g) * P.a.o_stride_h + d;
+  T* dst = (T*)P.a.out + (int64_t)(u.q0 + token_of(P, row)) * P.a.o_stride_t +
+           (int64_t)(u.h * P.g + head_of(P, row)) * P.a.o_stride_h + d;
   *reinterpret_cast<uint2*>(dst) = make_uint2(Pair<T>::narrow(o.x, o.y), Pair<T>::narrow(o.z, o.w));
 }
 __device__ __forceinline__ float lse_of(float m, float l) {  // m in log2 units
@@ -101,7 +101,7 @@ __device__ __forceinline__ float lse_of(float m, float l) {  // m in log2 units
 }
 __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, int r, float m, float l) {
   const int row = u.row0 + r;
-  if (P.a.lse) P.a.lse[(int64_t)(u.q0 + row / P.g) * P.a.Hq + u.h * P.g + row % P.g] = lse_of(m, l);
+  if (P.a.lse) P.a.lse[(int64_t)(u.q0 + token_of(P, row)) * P.a.Hq + u.h * P.g + head_of(P, row)] = lse_of(m, l);
 }
 
 // The rows of a unit as one warp has them: queries as A operands, limits and running sums.  Lane
@@ -122,9 +122,9 @@ struct StreamState {
       const int r = hf * 8 + (lane >> 2);
       const bool live = r < u.rows;
       const int row = u.row0 + r;
-      const T* src = (const T*)P.a.q + (int64_t)(u.q0 + (live ? row / P.g : 0)) * P.a.q_stride_t +
-                     (int64_t)(u.h * P.g + (live ? row % P.g : 0)) * P.a.q_stride_h + (lane & 3) * 2;
-      pos[hf] = live ? u.len - u.n + row / P.g : -1;
+      const T* src = (const T*)P.a.q + (int64_t)(u.q0 + (live ? token_of(P, row) : 0)) * P.a.q_stride_t +
+                     (int64_t)(u.h * P.g + (live ? head_of(P, row) : 0)) * P.a.q_stride_h + (lane & 3) * 2;
+      pos[hf] = live ? u.len - u.n + token_of(P, row) : -1;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         q[ks][hf] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16)) : 0u;
@@ -133,8 +133,8 @@ struct StreamState {
       m[hf] = neg_inf;
       l[hf] = 0.f;
     }
-    pos_first = u.len - u.n + u.row0 / P.g;
-    pos_last = u.len - u.n + (u.row0 + u.rows - 1) / P.g;
+    pos_first = u.len - u.n + token_of(P, u.row0);
+    pos_last = u.len - u.n + token_of(P, u.row0 + u.rows - 1);
 #pragma unroll
     for (int d = 0; d < D / 8; ++d)
 #pragma unroll

@@ -15,7 +15,7 @@ namespace clsample {
 
 struct AttnParams {
   clsample_attention_args_t a;
-  int g;            // query heads per key head
+  int g, g_shift;   // query heads per key head; log2, or -1
   int page_shift;   // log2(page_size), or -1
   int capacity;     // positions that the page table holds
   int min_rows;     // this launch takes the sequences with min_rows <= n g < max_rows
@@ -26,6 +26,12 @@ struct AttnParams {
   int* gave_up;     // set when a bounded wait ran out
   float scale_log2; // scale * log2(e)
 };
+
+// A packed row's token and its head among those of the key head.
+__device__ __forceinline__ int token_of(const AttnParams& P, int row) {
+  return P.g_shift >= 0 ? row >> P.g_shift : row / P.g;
+}
+__device__ __forceinline__ int head_of(const AttnParams& P, int row) { return row - token_of(P, row) * P.g; }
 
 struct CutUnit {
   int rows;          // 0: none
@@ -60,8 +66,8 @@ struct UnitMap {
     u->qt = qt;
     u->row0 = qt * R;
     u->rows = min(R, s.n * P.g - u->row0);
-    const int first = s.len - s.n + u->row0 / P.g;  // positions of the first and last row
-    const int last = s.len - s.n + (u->row0 + u->rows - 1) / P.g;
+    const int first = s.len - s.n + token_of(P, u->row0);  // positions of the first and last row
+    const int last = s.len - s.n + token_of(P, u->row0 + u->rows - 1);
     u->key_hi = max(0, min(last + 1, s.len));
     u->key_lo = P.a.window > 0 ? min(max(0, first - P.a.window + 1), u->key_hi) : 0;
     u->tile0 = u->key_lo / K;
