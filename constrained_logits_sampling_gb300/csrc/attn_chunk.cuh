@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const bool whole = (bits.x & bits.y & bits.z & bits.w) == ~0u && kb + 127 <= pos_first &&
                              (a.window <= 0 || kb > pos_last - a.window);
           uint32_t x[128];
-          tmem_ld128(x, s_tmem);
+          tmem_ld(x, s_tmem);
           if (!whole) {
             const int hi = pos - kb;  // columns lo .. hi are seen
             const int lo = a.window > 0 ? hi - a.window + 1 : 0;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t y[16];
-                tmem_ld16(y, o_tmem + c * 16);
+                tmem_ld(y, o_tmem + c * 16);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
                 tmem_st16(o_tmem + c * 16, y);
@@ -284,19 +284,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // each row, so that threads with a row each write whole lines.
       float* slot = scratch_slot<kChunkRows, D>(P, blockIdx.x, j0 == 0 ? 1 : 0);
       const bool done = cnt == u.tiles;
-      // Four lanes have four rows; each stores a quarter of 32 columns of all four, so that a
-      // store is of 64 bytes a row and not of 16.
+      // kCols columns at a time.  Four lanes have four rows; each stores a quarter of the columns
+      // of all four, so that a store is of four times as many bytes a row.
+      constexpr int kCols = D / 4, kWords = kCols / 8;
       const int row = u.row0 + min(r, u.rows - 1);
       const int64_t dst = (int64_t)(u.q0 + token_of(P, row)) * a.o_stride_t +
                           (int64_t)(u.h * P.g + head_of(P, row)) * a.o_stride_h;
-      // 32 of this thread's row's sums, from column c on
-      auto put = [&](const uint32_t (&x)[32], int c) {
+      // this thread's row's sums, from column c on
+      auto put = [&](const uint32_t (&x)[kCols], int c) {
         if (done) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint32_t y[4][4];
+          uint32_t y[4][kWords];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            y[i >> 2][i & 3] = l == 0.f ? 0u
+          for (int i = 0; i < kCols / 2; ++i)
+            y[i / kWords][i % kWords] = l == 0.f ? 0u
                                         : Pair<T>::narrow(__uint_as_float(x[2 * i]) * inv,
                                                           __uint_as_float(x[2 * i + 1]) * inv);
 #pragma unroll
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int i = 0; i < 4; ++i) {
               if (i & s) continue;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int e = 0; e < kWords; ++e) {
                 const uint32_t got = __shfl_xor_sync(~0u, upper ? y[i][e] : y[i + s][e], s);
                 if (upper)
                   y[i][e] = got;
@@ -318,13 +319,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int64_t to = __shfl_sync(~0u, dst, (lane & ~3) + i);
-            if ((r & ~3) + i < u.rows)
-              *reinterpret_cast<uint4*>((T*)a.out + to + c + (lane & 3) * 8) =
-                  make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+            T* at = (T*)a.out + to + c + (lane & 3) * (2 * kWords);
+            if ((r & ~3) + i >= u.rows) continue;
+            if constexpr (kWords == 4)
+              *reinterpret_cast<uint4*>(at) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+            else
+              *reinterpret_cast<uint2*>(at) = make_uint2(y[i][0], y[i][1]);
           }
         } else if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
+          for (int e = 0; e < kCols; e += 4)
             __stcg(reinterpret_cast<uint4*>(slot + (c + e) * kChunkRows + r * 4),
                    make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
         }
@@ -332,6 +336,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (split) {
         // each half joins one half of the columns and hands the other its sums of the rest
         float* const x_smem = reinterpret_cast<float*>(smem + kTile);
+        constexpr int kRoom = 128 * kCols;  // of a half
+        static_assert(2 * kRoom * 4 == kTile, "the second row tile's queries");
         x_smem[w * 256 + r] = m;
         x_smem[w * 256 + 128 + r] = l;
         SoftmaxSync::sync();
@@ -342,19 +348,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         m = mn;
         SoftmaxSync::sync();
 #pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
-          uint32_t x[32];
+        for (int c = 0; c < D / 2; c += kCols) {
+          uint32_t x[kCols];
           __syncwarp();
-          tmem_ld32(x, o_tmem + (1 - w) * (D / 2) + c);
+          tmem_ld(x, o_tmem + (1 - w) * (D / 2) + c);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)  // a half without a key tile has no sums
-            *reinterpret_cast<uint4*>(x_smem + w * 4096 + e * 128 + r * 4) =
+          for (int e = 0; e < kCols; e += 4)  // a half without a key tile has no sums
+            *reinterpret_cast<uint4*>(x_smem + w * kRoom + e * 128 + r * 4) =
                 cnt > w ? make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]) : make_uint4(0, 0, 0, 0);
           SoftmaxSync::sync();
-          tmem_ld32(x, o_tmem + w * (D / 2) + c);
+          tmem_ld(x, o_tmem + w * (D / 2) + c);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(x_smem + (1 - w) * 4096 + e * 128 + r * 4);
+          for (int e = 0; e < kCols; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(x_smem + (1 - w) * kRoom + e * 128 + r * 4);
             const float ov[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -365,10 +371,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t x[32];
+        for (int c = 0; c < D; c += kCols) {
+          uint32_t x[kCols];
           __syncwarp();
-          tmem_ld32(x, o_tmem + c);
+          tmem_ld(x, o_tmem + c);
           put(x, c);
         }
       }

@@ -25,7 +25,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 // Columns of this warp's 32 lanes (one row a thread), complete on return: load and wait are one
 // statement, so that nothing can use the registers in between.
-__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+__device__ __forceinline__ void tmem_ld(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
       "%14, %15}, [%16];"
@@ -35,7 +35,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+__device__ __forceinline__ void tmem_ld(uint32_t (&r)[32], uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
       "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -48,7 +48,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld128(uint32_t (&r)[128], uint32_t addr) {
+__device__ __forceinline__ void tmem_ld(uint32_t (&r)[128], uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
       "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, "

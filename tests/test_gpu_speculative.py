@@ -92,6 +92,46 @@ def test_attention(S, case):
     check_attention(S, R.Problem(new, lens, Hq, Hkv, D, page, dtype, seed=len(lens) + D, layout=layout), window)
 
 
+@pytest.mark.parametrize("D,page,dtype", [(64, 8, BF), (64, 16, FP), (128, 16, BF), (64, 24, BF)])
+def test_attention_units_in_a_row(S, D, page, dtype):
+    """CTAs that take several small and large units in a row, whose loads run ahead of the unit
+    that is being finished: against a product of all scores in float32 on the device, with the
+    bound of R.attention for weights of any distribution (|v| < 6, roundoff of the type)."""
+    g = torch.Generator(device="cuda").manual_seed(D + page)
+    B, n, Hq, Hkv = 60, 46, 9, 3  # 138 packed rows: a unit of both row tiles
+    lens = [n + (37 * b) % 400 for b in range(B)]
+    new = [n if b % 3 else 11 for b in range(B)]  # 33 rows: a unit of one
+    pages = [(m + page - 1) // page for m in lens]
+    table = torch.zeros(B, max(pages), dtype=torch.int32)
+    order, at = torch.randperm(sum(pages), generator=torch.Generator().manual_seed(1)).to(torch.int32), 0
+    for b, m in enumerate(pages):
+        table[b, :m] = order[at:at + m]
+        at += m
+    table = table.cuda()
+    k, v = (torch.randn(sum(pages), page, Hkv, D, device="cuda", generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(sum(new), Hq, D, device="cuda", generator=g).to(dtype)
+    cu = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32, device="cuda")
+    kv = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    att = S.ChunkAttention()
+    first = att(q, k, v, table, cu, kv, max_new=n)["out"]
+    u, at = R.ROUND[dtype], 0
+    for b in range(B):
+        m, c = lens[b], new[b]
+        ids = table[b, :pages[b]].long()
+        kb, vb = (x[ids].reshape(-1, Hkv, D)[:m].double().repeat_interleave(Hq // Hkv, 1) for x in (k, v))
+        y = torch.einsum("ihd,jhd->hij", q[at:at + c].double(), kb) / math.sqrt(D)
+        hide = torch.arange(m, device="cuda")[None, :] > torch.arange(m - c, m, device="cuda")[:, None]
+        w = torch.softmax(y.masked_fill(hide, -math.inf), -1)
+        want = torch.einsum("hij,jhd->ihd", w, vb)
+        mag = torch.einsum("hij,jhd->ihd", w, vb.abs())
+        # as in R.attention: scores are below 64 in size here, so a weight is off by 2^-24 (16 + 8 64) at most
+        tol = (u + 2.0 ** -23 * 528) * mag + u * want.abs() + 1e-7 + (m * 6 * 2.0 ** -25 if dtype == FP else 0)
+        assert ((first[at:at + c].double() - want).abs() <= tol).all(), b
+        at += c
+    for _ in range(3):
+        assert torch.equal(att(q, k, v, table, cu, kv, max_new=n)["out"], first)
+
+
 def test_attention_scale_and_large_scores(S):
     """Scores far above the exponent range: the running maximum has to hold them."""
     pr = R.Problem([3, 40], [90, 200], 4, 2, 64, 16, FP, seed=5)
