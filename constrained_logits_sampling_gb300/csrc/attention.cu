@@ -16,6 +16,7 @@ namespace clsample {
 namespace {
 
 constexpr int kStreamCtas = 2;  // per SM
+constexpr float kMaxScale = 2.0e38f;  // times log2(e) is still finite
 // The scratch, per SM: both kernels' slots (two per CTA, of rows of 128 sums, a maximum and a
 // sum), their cut units, and one word for all.
 constexpr size_t kChunkSlots = 2 * (size_t)kChunkRows * 130 * sizeof(float);
@@ -198,7 +199,7 @@ int clsample_chunk_attention(clsample_attention_t* h, const clsample_attention_a
   if (a->dtype != CLSAMPLE_T_BF16 && a->dtype != CLSAMPLE_T_F16) return CLSAMPLE_ERR_DTYPE;
   if (a->Hkv < 1 || a->Hq < a->Hkv || a->Hq > 65536 || a->Hq % a->Hkv != 0 || (a->D != 64 && a->D != 128) ||
       a->num_pages < 0 || a->page_size < 1 || a->max_pages < 0 || a->max_new < 0 || a->window < 0 ||
-      !(a->scale > 0.f && a->scale <= 3.0e38f) || (int64_t)a->T * (a->Hq / a->Hkv) > 0x7fffffff - 1024)
+      !(a->scale > 0.f && a->scale <= kMaxScale) || (int64_t)a->T * (a->Hq / a->Hkv) > 0x7fffffff - 1024)
     return CLSAMPLE_ERR_SHAPE;
   if (a->table_stride < a->max_pages) return CLSAMPLE_ERR_STRIDE;
   if (a->B == 0) return CLSAMPLE_SUCCESS;

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const __gr
         bad = true;
         continue;
       }
-      const float p = load_prob(target + (int64_t)(lo + b + i) * a.target_stride + x);
+      const float p = load_prob(target + ((int64_t)lo + b + i) * a.target_stride + x);
       const float q = draft ? load_prob(draft + (int64_t)(lo + i) * a.draft_stride + x) : 1.f;
       bad |= bad_prob(p) || bad_prob(q);
       // both factors have 24 bits, so the 64-bit product is exact
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const __gr
   int64_t total = 0, before = 0;
   int begin = 0, end = 0, part = 0;  // the slice's vectors, and how many of them a warp has
   if (!bad) {  // uniform over the cluster: every CTA took the same decisions
-    w.set(target + (int64_t)(lo + b + acc) * a.target_stride,
+    w.set(target + ((int64_t)lo + b + acc) * a.target_stride,
           refused && draft ? draft + (int64_t)(lo + acc) * a.draft_stride : nullptr,
           refused && !draft ? __ldg(a.draft_tokens + lo + acc) : -1, a.V);
     for (int pass = 0; pass < 2; ++pass) {

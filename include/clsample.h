@@ -376,7 +376,7 @@ int clsample_kv_append(const clsample_kv_append_args_t* args, clsample_stream_t 
  * lse               f32[T, Hq] output or NULL.
  * max_new           upper bound of n_b, known to the caller; a sequence above it is
  *                   INVALID and its out rows are 0.
- * scale             finite, > 0 (1 / sqrt(D) as a rule).
+ * scale             in (0, 2e38] (1 / sqrt(D) as a rule).
  * row_status        i32[B] output or NULL.  Keys on a page with an invalid id are left out.
  *
  * Products are of `dtype` with float32 sums; the softmax is float32; its weights are

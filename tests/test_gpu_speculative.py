@@ -279,6 +279,22 @@ def test_attention_refusals(S):
     assert e.value.code == -10
 
 
+@pytest.mark.parametrize("n", [1, 40])
+def test_attention_largest_scale(S, n):
+    """Scores of zero stay zero up to the largest scale; above it, where the scale in powers of
+    two is no longer finite, the call is refused."""
+    pr = R.Problem([n], [90], 2, 1, 64, 16, BF, seed=n)
+    att = S.ChunkAttention()
+    q = torch.zeros_like(fused(pr)[0])
+    args = (q, gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens))
+    got = att(*args, max_new=n, scale=2.0e38)["out"]
+    assert torch.isfinite(got.float()).all()
+    assert torch.equal(got, att(*args, max_new=n, scale=1.0)["out"])
+    with pytest.raises(Exception) as e:
+        att(*args, max_new=n, scale=2.5e38)
+    assert e.value.code == -9
+
+
 # ----------------------------------------------------------------------------- append
 
 APPEND = [
