@@ -7,7 +7,7 @@
 // Loads come in two forms.  Where pages are whole boxes of a tile (8, 16, 32, 64 or a
 // multiple of 128 slots) warps 8 and 11 copy keys and values by TMA, one box a page and 64
 // elements, an invalid page as zeros (a box takes some 75 cycles to issue, so with pages of 16
-// slots one warp would not keep up: 771 us against 582); warp 9 loads the queries, in one box a
+// slots one warp would not keep up: 771 us against 574); warp 9 loads the queries, in one box a
 // row tile where the query heads of a key head divide 128 and row by row otherwise, and clears
 // the value slots that lie outside the unit's keys (they may hold anything, and 0 x NaN is NaN).
 // Other page sizes are copied row by row with cp.async by warps 8 and 9, zeros where there
@@ -19,7 +19,7 @@
 // it is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // time (P and its sum are then up to 2^8, which both types hold), so hardly ever.
 // 2 x 2048 tokens on 32 / 8 heads of 128 over 14500 to 15600 keys (943 GFLOP): 565 us alone, 1.67
-// PFLOP/s, or 635 us in a row of calls that draw the power limit.  A tile of 128 keys takes
+// PFLOP/s, or 630 to 650 us in a row of calls that draw the power limit.  A tile of 128 keys takes
 // about 2500 cycles, of which the products are 2048: the rest is the way from a finished S over
 // the softmax (970 cycles) to the next product.
 // A unit of at most 128 rows has one row tile: both halves of the CTA then take the same
@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int w = 0; w < tiles_of_rows; ++w) {
           if (w == 1) second_tile();
           if (lane < D / 64 && !sh.dead)
-            tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, u.h * P.g, u.q0 + token_of(P, u.row0 + w * 128),
-                      &sh.q_full);
+            tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, u.h * P.g,
+                      u.q0 + token_of(P, u.row0 + w * 128), &sh.q_full);
         }
       } else {
 #pragma unroll
