@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uint32_t tmem = sh.tmem;
   int64_t t = span.t0;
 
+  // A whole warpgroup has to run the same register instruction, so warps 8 to 11 do before they part.
+  if (warp >= 8) regs_down<kOtherRegs>();
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax
     regs_up<kSoftmaxRegs>();
@@ -400,7 +402,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else if (warp != 10) {
     // ------------------------------------------------------------------ loads
-    regs_down<kOtherRegs>();
     const int lw = kTma ? 0 : warp - 8;  // of the warps that copy rows
     bool met = false;                    // the last unit's halves met in the second row tile's room
     const int tiles = (int)(span.t1 - span.t0);
@@ -641,7 +642,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ products
-    regs_down<kOtherRegs>();
     {
       // Everything here is uniform, and made known as such (uni): the operands of a product
       // have to be in uniform registers for the issue to keep up with the tensor cores.
