@@ -241,7 +241,8 @@ struct Shared {
   int slice_bad[kMaxCluster];
   int64_t warp_sum[kWarps], scan[kWarps];
   int first;  // first refused drafted token, or n
-  int bad;
+  int bad;    // of the request; not written after it has been read
+  int odd;    // a probability out of range in the CTA's slices: a warp may set it while another reads `bad`
 };
 
 template <class P, int C>
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const __gr
   bool bad = lo < 0 || hi < lo || hi > a.N || n > a.max_draft || !(u_last >= 0.f && u_last < 1.f);
   if (tid == 0) {
     sh.first = n;
-    sh.bad = 0;
+    sh.bad = sh.odd = 0;
   }
   __syncthreads();
   const P* target = reinterpret_cast<const P*>(a.target);
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const __gr
       const bool odd = __any_sync(~0u, range.bad());
       if (lane == 0) {
         sh.warp_sum[warp] = sum;
-        if (odd) atomicOr(&sh.bad, 1);
+        if (odd) atomicOr(&sh.odd, 1);
       }
       __syncthreads();
       if (tid < C) {
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const __gr
         for (int i = 0; i < kWarps; ++i) mine += sh.warp_sum[i];
         Shared* other = cluster.map_shared_rank(&sh, tid);
         other->slice_sum[rank] = mine;
-        other->slice_bad[rank] = sh.bad;
+        other->slice_bad[rank] = sh.odd;
       }
       cluster.sync();
       total = before = 0;

@@ -534,6 +534,26 @@ def test_verify_bad_requests(S):
     assert run_verify(S, target, draft, x, cu, u, ul, 1)["status"].tolist() == [2] * B
 
 
+@pytest.mark.parametrize("B", [3, 100, 300])  # every cluster size
+def test_verify_bad_first_and_last_probabilities(S, B):
+    """A probability out of range that a warp meets first of all, or last: the request is INVALID
+    as a whole and its neighbours are what they were, call after call."""
+    V = 5000
+    rng = np.random.default_rng(B)
+    target = softmax_rows(rng, B, V, 1.0)
+    ul = rng.random(B, dtype=np.float32)
+    good = run_verify(S, target, None, [], [0] * (B + 1), [], ul, 0)
+    assert good["status"].tolist() == [0] * B
+    broken = target.copy()
+    broken[0::3, 0] = 1.5
+    broken[1::3, V - 1] = np.nan
+    for _ in range(20):
+        got = run_verify(S, broken, None, [], [0] * (B + 1), [], ul, 0)
+        want = np.where(np.arange(B) % 3 == 2, good["tokens"][:, 0], -1)
+        assert got["status"].tolist() == [0 if b % 3 == 2 else 2 for b in range(B)]
+        assert np.array_equal(got["tokens"][:, 0], want)
+
+
 def test_verify_keeps_the_target_distribution(S):
     """First token of a verification, over many requests with one drafted token each drawn
     from q, is distributed as p: chi-square with 7 degrees of freedom below its 1e-6 point."""

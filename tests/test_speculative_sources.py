@@ -21,3 +21,12 @@ def test_a_warpgroup_sets_its_registers_at_one_place():
     assert sorted(sites) == ["down", "up"]
     assert re.search(r"if \(warp >= 8\) regs_down<kOtherRegs>\(\);\s*if \(warp < 8\) \{\s*regs_up<kSoftmaxRegs>\(\);",
                      code)
+
+
+def test_verification_writes_no_flag_that_warps_still_read():
+    """Every thread reads the request's flag after a barrier, and the next barrier of the block
+    comes only after the sums: a warp that is ahead must not write the word that a warp behind it
+    has yet to read, or the two would part before a barrier of all."""
+    code = code_of("verify.cu")
+    read = code.index("bad = sh.bad;")
+    assert "sh.bad" in code[:read] and "sh.bad" not in code[read + len("bad = sh.bad;"):]
