@@ -10,6 +10,8 @@
 struct clsample_attention {
   int dev, sms;
   unsigned char* scratch;
+  int stall;              // of AttnParams
+  long long wait_cycles;
 };
 
 namespace clsample {
@@ -173,7 +175,7 @@ int clsample_attention_create(clsample_attention_t** out) {
   const int rc = check_device(&dev, &sms);
   if (rc != CLSAMPLE_SUCCESS) return rc;
   if (sms * (1 + kStreamCtas) > kMaxCuts) return CLSAMPLE_ERR_DEVICE;
-  auto* h = new (std::nothrow) clsample_attention{dev, sms, nullptr};
+  auto* h = new (std::nothrow) clsample_attention{dev, sms, nullptr, 0, kWaitCycles};
   if (!h) return CLSAMPLE_ERR_CUDA;
   const size_t bytes = sms * kScratch + sizeof(int);
   if (cudaMalloc(&h->scratch, bytes) != cudaSuccess || cudaMemset(h->scratch + sms * kScratch, 0, sizeof(int)) != cudaSuccess ||
@@ -190,6 +192,16 @@ void clsample_attention_destroy(clsample_attention_t* h) {
   if (!h) return;
   if (h->scratch) cudaFree(h->scratch);
   delete h;
+}
+
+int clsample_debug_attention_stall(clsample_attention_t* h, int32_t barrier, int32_t slot, int64_t wait_cycles) {
+  using namespace clsample;
+  if (!h) return CLSAMPLE_ERR_NULL;
+  if (barrier < 0 || barrier > kStallSums || slot < 0 || slot > 255 || wait_cycles < 1 || wait_cycles > kWaitCycles)
+    return CLSAMPLE_ERR_SHAPE;
+  h->stall = barrier ? (barrier << 8) + slot : 0;
+  h->wait_cycles = barrier ? wait_cycles : kWaitCycles;
+  return CLSAMPLE_SUCCESS;
 }
 
 int clsample_chunk_attention(clsample_attention_t* h, const clsample_attention_args_t* a, clsample_stream_t stream) {
@@ -220,6 +232,8 @@ int clsample_chunk_attention(clsample_attention_t* h, const clsample_attention_a
   P.g_shift = (P.g & (P.g - 1)) == 0 ? __builtin_ctz((unsigned)P.g) : -1;
   P.page_shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz((unsigned)a->page_size) : -1;
   P.capacity = capacity_of(a->max_pages, a->page_size);
+  P.stall = h->stall;
+  P.wait_cycles = h->wait_cycles;
   P.scale_log2 = a->scale * 1.44269504088896341f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

@@ -97,7 +97,7 @@ struct ChunkShared {
   Unit unit[2];
   int64_t unit_begin[2];
   Span span;
-  volatile int dead;           // a bounded wait ran out: every other wait ends too
+  WaitLimit limit;
   alignas(16) uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
 };
 
@@ -109,7 +109,26 @@ __device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
 
 struct SoftmaxSync {  // the 256 softmax threads
   static __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+  static __device__ __forceinline__ bool all(bool yes) {  // and whether all of them say yes
+    uint32_t r;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)yes)
+        : "memory");
+    return r != 0;
+  }
 };
+
+// How a CTA ends when a wait has run out, so that nothing is left waiting or in flight and every
+// address stays one of the call's.  The wait's thread marks the CTA dead before it goes on, on
+// whatever is there.  Who waits for that one's arrivals goes on too, so the load warps look at the
+// mark after each wait: they announce and make no more copies, hand over no more units, and leave
+// after the unit that they have.  The warp of products issues none after a wait of its own that
+// failed.  The softmax threads finish the unit that they have, as its barriers take all 256 of
+// them, and go on to no other.  Then all pause while copies land.  The call's statuses tell that
+// its outputs are void.
 
 template <class T, int D, bool kTma>
 __global__ void __launch_bounds__(kChunkThreads, 1)
@@ -137,28 +156,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
 
   if (tid == 0) {
+    // for tests: a barrier that waits for one arrival more than it gets
+    auto init = [&](unsigned long long* bar, int count, int stall, int slot = 0) {
+      mbar_init(bar, count + (P.stall == (stall << 8) + slot ? 1 : 0));
+    };
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.k_landed[i], 64 + 2);  // every load thread's copies, and each warp's words of key_ok
-      mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.tile_done[i], 1);
-      mbar_init(&sh.tile_done[NS + i], 1);
+      init(&sh.k_landed[i], 64 + 2, kStallKeysLanded, i);  // every load thread's copies, and each warp's words of key_ok
+      init(&sh.k_full[i], 1, kStallKeys, i);
+      init(&sh.tile_done[i], 1, kStallTileDone, i);
+      init(&sh.tile_done[NS + i], 1, kStallTileDone, NS + i);
     }
     for (int i = 0; i < NV; ++i) {
-      mbar_init(&sh.v_landed[i], kTma ? 1 : 64);
-      mbar_init(&sh.v_full[i], 1);
+      init(&sh.v_landed[i], kTma ? 1 : 64, kStallValuesLanded, i);
+      init(&sh.v_full[i], 1, kStallValues, i);
     }
-    mbar_init(&sh.q_full, kTma && P.q_box ? 1 : 32 * kRowWarps);
-    mbar_init(&sh.q_empty, 1);
+    init(&sh.q_full, kTma && P.q_box ? 1 : 32 * kRowWarps, kStallQueries);
+    init(&sh.q_empty, 1, kStallQueriesDone);
     mbar_init(&sh.end, 1);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&sh.s_full[w], 1);
-      mbar_init(&sh.p_half[w], 4);
-      mbar_init(&sh.p_full[w], 4);
-      mbar_init(&sh.o_full[w], 1);
-      mbar_init(&sh.unit_full[w], 1);
-      mbar_init(&sh.unit_done[w], 1);
+      init(&sh.s_full[w], 1, kStallScores, w);
+      init(&sh.p_half[w], 4, kStallHalfWeights, w);
+      init(&sh.p_full[w], 4, kStallWeights, w);
+      init(&sh.o_full[w], 1, kStallSums, w);
+      init(&sh.unit_full[w], 1, kStallUnit, w);
+      init(&sh.unit_done[w], 1, kStallUnitDone, w);
     }
-    sh.dead = 0;
+    sh.limit.cycles = P.wait_cycles;
+    sh.limit.dead = 0;
     sh.span = span;
     fence_mbar_init();
   }
@@ -178,8 +202,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane in bits 16..
     const uint32_t s_tmem = tmem + lane_base + w * 128, o_tmem = tmem + lane_base + 256 + w * 128;
     uint32_t s_phase = 0, o_phase = 0, tile = 0;
-    for (uint32_t seg = 0;; ++seg) {
-      bounded_wait(&sh.unit_full[seg & 1], (seg >> 1) & 1, &sh.dead);
+    bool noted = false, go = SoftmaxSync::all(bounded_wait(&sh.unit_full[0], 0, &sh.limit));
+    for (uint32_t seg = 0; go; ++seg) {
       const Unit& u = sh.unit[seg & 1];
       const int j0 = (int)max(sh.span.t0 - sh.unit_begin[seg & 1], (int64_t)0);
       const int cnt = (int)(min(sh.unit_begin[seg & 1] + u.tiles, sh.span.t1) - sh.unit_begin[seg & 1]) - j0;
@@ -196,7 +220,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int pos_last = first_pos + token_of(P, u.row0 + min(u.rows, half0 + 128) - 1);
         for (int j = jw; j < cnt; j += step) {
           const int kb = kb0 + j * kChunkKeys;
-          bounded_wait(&sh.s_full[w], s_phase, &sh.dead);
+          bounded_wait(&sh.s_full[w], s_phase, &sh.limit);
           if (lane == 0) {
             if ((warp & 3) == 0 && (split || w == 1)) mbar_arrive(&sh.tile_done[(tile + j) % (2 * NS)]);
           }
@@ -278,7 +302,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float2 s0 = split_pair(add2(sums[0], sums[1]));
           l += s0.x + s0.y;
         }
-        bounded_wait(&sh.o_full[w], o_phase, &sh.dead);
+        bounded_wait(&sh.o_full[w], o_phase, &sh.limit);
         o_phase ^= 1;
         tc_fence_after();
       }
@@ -393,13 +417,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const bool last = sh.unit_begin[seg & 1] + u.tiles >= sh.span.t1;
       if (last && tid == 0) {
         note_cut(P, sh.span, u, sh.unit_begin[seg & 1]);
-        if (sh.dead) *P.gave_up = 1;
+        noted = true;
       }
       if (split) fence_async_proxy();  // the room may next be written by a box copy
-      SoftmaxSync::sync();
-      if (last) break;
-      if (tid == 0) mbar_arrive(&sh.unit_done[seg & 1]);
+      // (the next unit is published without this one's end)
+      go = SoftmaxSync::all(!last && bounded_wait(&sh.unit_full[(seg + 1) & 1], ((seg + 1) >> 1) & 1, &sh.limit) &&
+                            !sh.limit.dead);
+      if (go && tid == 0) mbar_arrive(&sh.unit_done[seg & 1]);
     }
+    if (tid == 0 && !noted) P.cut[blockIdx.x].rows = 0;  // what an earlier call left there is not joined
   } else if (warp != 10) {
     // ------------------------------------------------------------------ loads
     const int lw = kTma ? 0 : warp - 8;  // of the warps that copy rows
@@ -415,7 +441,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         cp_async16(dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + o, (live >> row) & 1);
       }
     };
-    auto copy_queries = [&](uint32_t seg) {
+    auto copy_queries = [&](uint32_t seg) -> bool {
       constexpr int kBlocks = 8 / kRowWarps;
       const bool box = kTma && P.q_box;
       int64_t off[kBlocks];
@@ -431,25 +457,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       // the unit's place is free when the softmax warps are done with the one before the last
-      if (seg >= 2) bounded_wait(&sh.unit_done[seg & 1], ((seg - 2) >> 1) & 1, &sh.dead);
-      if (lw == 0 && lane == 0) {
+      const bool free = seg < 2 || bounded_wait(&sh.unit_done[seg & 1], ((seg - 2) >> 1) & 1, &sh.limit);
+      if (lw == 0 && lane == 0 && free && !sh.limit.dead) {
         sh.unit[seg & 1] = u;
         sh.unit_begin[seg & 1] = unit_begin;
         mbar_arrive(&sh.unit_full[seg & 1]);
       }
-      bounded_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.dead);
+      bounded_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.limit);
+      if (__any_sync(~0u, sh.limit.dead)) return false;
       const int tiles_of_rows = u.rows <= 128 ? 1 : 2;
       auto second_tile = [&]() {
-        if (met) bounded_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.dead);
+        if (met) bounded_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.limit);
         __syncwarp();
       };
-      __syncwarp();
       if (box) {
         // (rows past the sequence's are other sequences' or zero, and are not stored)
         if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, tiles_of_rows * kTile);
         for (int w = 0; w < tiles_of_rows; ++w) {
           if (w == 1) second_tile();
-          if (lane < D / 64 && !sh.dead)
+          if (lane < D / 64 && !sh.limit.dead)
             tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, u.h * P.g,
                       u.q0 + token_of(P, u.row0 + w * 128), &sh.q_full);
         }
@@ -464,6 +490,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         cp_async_arrive(smem_addr(&sh.q_full));
       }
       met = u.rows <= 128;
+      return true;
     };
     // The slot of a tile's keys is free when S of the tile that had it is complete, and the
     // slot of its values when O is, which a later tile's completion covers: the next one's if
@@ -471,7 +498,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // may have been the case).  Of twice as many completions as there are key slots the one
     // waited for is still the last on its barrier.
     auto tile_done = [&](int64_t gate) {
-      if (gate >= 0) bounded_wait(&sh.tile_done[gate % (2 * NS)], (gate / (2 * NS)) & 1, &sh.dead);
+      if (gate >= 0) bounded_wait(&sh.tile_done[gate % (2 * NS)], (gate / (2 * NS)) & 1, &sh.limit);
       __syncwarp();
     };
     auto key_slot = [&](uint32_t it) { tile_done((int64_t)it - NS); };
@@ -521,27 +548,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             full = edge(tile) ? &sh.v_landed[it % NV] : &sh.v_full[it % NV];
             dst = v_smem + it % NV * kTile;
           }
+          const bool dead = sh.limit.dead;
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(full, kTile);
+          if (lane == 0 && !dead) mbar_arrive_expect_tx(full, kTile);
           __syncwarp();
-          if (lane < boxes && !sh.dead)
+          if (lane < boxes && !dead)
             for (int x = 0; x < D / 64; ++x)
               tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h, from, full);
         }
         t += cnt;
-        if (t >= span.t1) break;
+        if (t >= span.t1 || __any_sync(~0u, sh.limit.dead)) break;
         unit_begin = t;
         next_unit<kChunkRows, kChunkKeys>(P, &u);
       }
-      // copies still in flight when a wait gave up land before the CTA ends
-      if (sh.dead)
-        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     } else if (kTma) {
       uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
       while (true) {
         const int j0 = (int)(t - unit_begin);
         const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
-        copy_queries(seg);
+        if (!copy_queries(seg)) break;
         for (int j = 0; j < cnt; ++j) {
           const int tile = u.tile0 + j0 + j;
           if (!edge(tile)) continue;
@@ -550,7 +575,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int i = 0; i < NV; ++i)
             if (i == st) parity = edges[i]++ & 1;
-          bounded_wait(&sh.v_landed[st], parity, &sh.dead);
+          bounded_wait(&sh.v_landed[st], parity, &sh.limit);
+          const bool dead = sh.limit.dead;
           __syncwarp();
           const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
           for (int i = lane; i < 128 * KC; i += 32) {  // a row's pieces may lie anywhere in it: all are cleared
@@ -561,7 +587,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           fence_async_proxy();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.v_full[st]);
+          if (lane == 0 && !dead) mbar_arrive(&sh.v_full[st]);
         }
         it += cnt;
         ++seg;
@@ -576,7 +602,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       while (true) {
         const int j0 = (int)(t - unit_begin);
         const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
-        copy_queries(seg);
+        if (!copy_queries(seg)) break;
         const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
         const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
         const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
@@ -632,10 +658,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // The copies are ordinary writes, the products read by the async proxy: the fence between
       // them costs a hundred cycles or so, which the issuing warp has not got.
       for (int i = 0; i < tiles; ++i) {
-        bounded_wait(&sh.k_landed[i % NS], (i / NS) & 1, &sh.dead);
+        if (!bounded_wait(&sh.k_landed[i % NS], (i / NS) & 1, &sh.limit)) break;
         fence_async_proxy();
         mbar_arrive(&sh.k_full[i % NS]);
-        bounded_wait(&sh.v_landed[i % NV], (i / NV) & 1, &sh.dead);
+        if (!bounded_wait(&sh.v_landed[i % NV], (i / NV) & 1, &sh.limit)) break;
         fence_async_proxy();
         mbar_arrive(&sh.v_full[i % NV]);
       }
@@ -653,7 +679,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       uint32_t it = 0, seg = 0, p_phase = 0;  // bit w of p_phase: half w
       bool alive = true;
       auto wait = [&](unsigned long long* bar, uint32_t parity) {
-        alive = __all_sync(~0u, bounded_wait(bar, parity, &sh.dead)) && alive;
+        alive = __all_sync(~0u, bounded_wait(bar, parity, &sh.limit)) && alive;
       };
       auto keys_ready = [&](uint32_t tile) { wait(&sh.k_full[tile % NS], (tile / NS) & 1); };
       auto values_ready = [&](uint32_t tile) { wait(&sh.v_full[tile % NV], (tile / NV) & 1); };
@@ -745,13 +771,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!alive) {
         mma_commit(&sh.end);
         for (int i = 0; i < 1 << 16 && !mbar_try_wait(&sh.end, 0); ++i) __nanosleep(100);
+        __syncwarp();
       }
     }
   }
+  if (sh.limit.dead) {  // about a millisecond after a wait ran out every copy has landed
+    const long long start = clock64();
+    for (int i = 0; i < 1 << 16 && clock64() - start < 2000000; ++i) __nanosleep(1000);
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 10) tmem_free512(tmem);
+  if (tid == 0 && sh.limit.dead) *P.gave_up = 1;
 }
 
 }  // namespace clsample

@@ -13,6 +13,12 @@
 
 namespace clsample {
 
+// AttnParams.stall: a barrier of the chunk kernel, in bits 8 and up, and which of its slots.
+enum Stall {
+  kStallUnit = 1, kStallUnitDone, kStallQueries, kStallQueriesDone, kStallKeysLanded, kStallKeys, kStallValuesLanded,
+  kStallValues, kStallTileDone, kStallScores, kStallHalfWeights, kStallWeights, kStallSums
+};
+
 struct AttnParams {
   clsample_attention_args_t a;
   int g, g_shift;   // query heads per key head; log2, or -1
@@ -24,6 +30,8 @@ struct AttnParams {
   float* partial;   // scratch: two slots per CTA
   struct CutUnit* cut;  // one per CTA: the unit that starts in its span and ends in another's
   int* gave_up;     // set when a bounded wait ran out
+  long long wait_cycles;  // that a wait may take
+  int stall;        // where a wait of the chunk kernel is in vain, for tests; 0: nowhere
   float scale_log2; // scale * log2(e)
 };
 

@@ -45,15 +45,24 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// Bounded wait for a phase: about two seconds, then the CTA gives up.
-__device__ __forceinline__ bool bounded_wait(unsigned long long* bar, uint32_t parity, volatile int* dead) {
+// What the bounded waits of a CTA share: the cycles that one may take, and whether one has run
+// out, after which the others end too.
+struct WaitLimit {
+  long long cycles;
+  volatile int dead;
+};
+constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
+
+// Bounded wait for a phase: false if it ran out.  (A later wait of the same thread for the next
+// phase of that barrier would seem to succeed at once.)
+__device__ __forceinline__ bool bounded_wait(unsigned long long* bar, uint32_t parity, WaitLimit* limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long start = clock64();
   for (uint32_t i = 1; i < kSpinLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0 && (*dead || clock64() - start > 4000000000ll)) break;
+    if ((i & 63) == 0 && (limit->dead || clock64() - start > limit->cycles)) break;
   }
-  *dead = 1;
+  limit->dead = 1;
   return false;
 }
 

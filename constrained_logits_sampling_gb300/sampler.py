@@ -49,7 +49,7 @@ EXPORTS = ("clsample_create", "clsample_destroy", "clsample_apply", "clsample_pr
            "clsample_apply_static", "clsample_strerror", "clsample_geometry", "clsample_occupancy",
            "clsample_debug_weights", "clsample_debug_uniforms", "clsample_allowed_to_bitmask",
            "clsample_kv_append", "clsample_attention_create", "clsample_attention_destroy",
-           "clsample_chunk_attention", "clsample_verify")
+           "clsample_chunk_attention", "clsample_debug_attention_stall", "clsample_verify")
 
 
 def load_library(path: str = LIB_PATH):
@@ -94,6 +94,8 @@ def load_library(path: str = LIB_PATH):
             L.clsample_attention_destroy.restype = None
             L.clsample_chunk_attention.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
             L.clsample_chunk_attention.restype = ctypes.c_int
+            L.clsample_debug_attention_stall.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64]
+            L.clsample_debug_attention_stall.restype = ctypes.c_int
             _lib = L
         return _lib
 

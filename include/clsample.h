@@ -384,8 +384,9 @@ int clsample_kv_append(const clsample_kv_append_args_t* args, clsample_stream_t 
  * The result of a call does not depend on timing: partial sums over a split key axis are
  * joined in key order.  A value that is not finite, of a key that a row does not see but another
  * new row of the sequence does, may make the first row NaN (0 x NaN in a product).
- * A wait inside the kernels that runs out (a GPU that stopped scheduling them) does not hang: all
- * sequences of that call and of later calls on the handle are OVERFLOW.
+ * A wait inside the kernels that runs out (about two seconds; a GPU that stopped scheduling them)
+ * does not hang: the call ends, all sequences of that call and of later calls on the handle are
+ * OVERFLOW, and what that call wrote to its rows of out and lse is void.
  * Limits: D 64 or 128; Hq a multiple of Hkv; q, out and cache addresses and strides
  * multiples of 16 bytes (ERR_ALIGN); T Hq / Hkv below 2^31 - 1024; lengths up to 2^30.
  * Speed: pages of 8, 16, 32, 64 or a multiple of 128 slots are copied by TMA for sequences of
@@ -421,6 +422,14 @@ void clsample_attention_destroy(clsample_attention_t* handle);
  * before it ends; they can be captured in a graph); nothing when B == 0. */
 int clsample_chunk_attention(clsample_attention_t* handle, const clsample_attention_args_t* args,
                              clsample_stream_t stream);
+
+/* Test hook.  In later calls on the handle a barrier of the kernel for more than 16 packed rows
+ * waits for one arrival more than it gets, and no wait takes more than wait_cycles (1 to 4e9) SM
+ * cycles.  barrier: the unit of work (1) and its end (2), its queries (3) and their end (4), keys
+ * copied (5) and handed over (6), values copied (7) and handed over (8), a tile's end (9), its scores
+ * (10), half of its weights (11), all of them (12), the sums (13); slot: which of several.  0: none,
+ * which is also how a handle starts. */
+int clsample_debug_attention_stall(clsample_attention_t* handle, int32_t barrier, int32_t slot, int64_t wait_cycles);
 
 /* Arguments of clsample_verify.  Request b drafted n_b = cu_draft[b + 1] - cu_draft[b] >= 0
  * tokens (cu_draft int32[B + 1], within [0, N]).  Its n_b + 1 rows of target probabilities

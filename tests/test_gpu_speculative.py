@@ -222,6 +222,81 @@ def test_attention_bad_sequences(S, n, page):
     assert got["status"].cpu().tolist() == [2] * 5 and (got["out"] == 0).all()
 
 
+def batch(new, lens, Hq, Hkv, D, page, dtype, seed):
+    """q, caches, table, offsets and lengths, made on the device."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = [(m + page - 1) // page for m in lens]
+    order, at = torch.randperm(sum(need), generator=torch.Generator().manual_seed(seed)).to(torch.int32), 0
+    table = torch.zeros(len(new), max(need), dtype=torch.int32)
+    for b, m in enumerate(need):
+        table[b, :m] = order[at:at + m]
+        at += m
+    k, v = (torch.randn(sum(need), page, Hkv, D, device="cuda", generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(sum(new), Hq, D, device="cuda", generator=g).to(dtype)
+    cu = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32, device="cuda")
+    return q, k, v, table.cuda(), cu, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+STALLS = [(1, 0), (1, 1), (2, 0), (3, 0), (4, 0), (5, 1), (6, 0), (6, 1), (7, 0), (8, 0), (8, 2), (9, 0), (9, 3), (10, 0),
+          (10, 1), (11, 0), (12, 1), (13, 0), (13, 1)]
+
+
+@pytest.mark.parametrize("barrier,slot", STALLS)
+@pytest.mark.parametrize("D,page,dtype,Hq", [(128, 16, BF, 9), (64, 8, FP, 6), (64, 12, BF, 9), (128, 24, FP, 6)])
+def test_attention_wait_that_runs_out(S, D, page, dtype, Hq, barrier, slot):
+    """A barrier of the chunk kernel waits for what never comes, for a millisecond: the call ends,
+    all its sequences and those of later calls on the handle are OVERFLOW, nothing outside the
+    call's rows is written (the handle's scratch still holds the cuts of a larger call), and another
+    handle is not affected."""
+    import time
+    Hkv, OVERFLOW = 3, 1
+    att, fresh = S.ChunkAttention(), S.ChunkAttention()
+    big = batch([70] * 90, [70 + 31 * b % 500 for b in range(90)], Hq, Hkv, D, page, dtype, 1)
+    want_big = att(*big, max_new=70)
+    assert not want_big["status"].any()
+    # units of one row tile and of two (with 9 heads); some eight key tiles and two units a CTA
+    new = [46 if b % 3 else 11 for b in range(60)]
+    small = batch(new, [46 + 97 * b % 1500 for b in range(60)], Hq, Hkv, D, page, dtype, 2)
+    want = fresh(*small, max_new=46, lse=True)
+    assert not want["status"].any()
+    T, guard = sum(new), 300
+    room = torch.full((T + 2 * guard, Hq, D), 3.0, dtype=dtype, device="cuda")
+    sums = torch.full(((T + 2 * guard) * Hq,), 3.0, device="cuda")
+    status = torch.full((60,), -5, dtype=torch.int32, device="cuda")
+    args = att.make_args(*small, max_new=46, out=room[guard:guard + T], row_status=status,
+                         lse=sums[guard * Hq:(guard + T) * Hq])
+    assert att._L.clsample_debug_attention_stall(att._h, barrier, slot, 2_000_000) == 0
+    torch.cuda.synchronize()
+    start = time.time()
+    att.apply(args)
+    torch.cuda.synchronize()
+    assert time.time() - start < 10
+    # nobody waits for keys that TMA copies to land, for the end of a CTA's last units, or for half of
+    # the weights where all are there already
+    boxes = page % 8 == 0 and 128 % page == 0
+    if barrier in (2, 11) or (boxes and barrier == 5):
+        if not status.any():
+            assert barrier == 11 or torch.equal(room[guard:guard + T], want["out"])
+            return
+    assert (status == OVERFLOW).all()
+    assert (room[:guard] == 3).all() and (room[guard + T:] == 3).all()
+    assert (sums[:guard * Hq] == 3).all() and (sums[(guard + T) * Hq:] == 3).all()
+    assert att._L.clsample_debug_attention_stall(att._h, 0, 0, 1) == 0
+    later = att(*big, max_new=70)
+    assert (later["status"] == OVERFLOW).all() and torch.equal(later["out"], want_big["out"])
+    again = fresh(*small, max_new=46, lse=True)
+    assert not again["status"].any()
+    assert torch.equal(again["out"], want["out"]) and torch.equal(again["lse"], want["lse"])
+
+
+def test_attention_stall_refusals(S):
+    att = S.ChunkAttention()
+    stall = att._L.clsample_debug_attention_stall
+    assert stall(None, 0, 0, 1) == -1
+    for bad in ((-1, 0, 1), (14, 0, 1), (1, -1, 1), (1, 256, 1), (1, 0, 0), (1, 0, 4_000_000_001)):
+        assert stall(att._h, *bad) == -9
+
+
 def test_attention_far_offsets(S):
     """A cache whose last pages lie past 2^31 elements."""
     pages, page, Hkv, D = 1050, 128, 128, 128  # 2.2e9 elements, 4.4 GB each
