@@ -12,8 +12,9 @@ the drafted ones, or a chunk of a prompt) through
 As in ``sampler``, this is argument marshalling only: every step runs in libclsample.so, on
 CUDA tensors, without a CPU fallback.  ``make_args`` checks a call once and keeps its
 tensors alive; ``apply`` enqueues it, as often as wanted (the buffers' contents may change
-in between).  Calling an object does both and allocates the outputs.  The formulas and
-limits are stated in include/clsample.h.
+in between).  Calling an object does both and allocates the outputs.  An object belongs to the
+device that was current when it was made, and refuses calls while another one is.  The
+formulas and limits are stated in include/clsample.h.
 """
 from __future__ import annotations
 
@@ -24,9 +25,10 @@ from typing import Dict, Optional
 
 import torch
 
-from .sampler import LOGITS_BF16, LOGITS_F32, _check, _dptr, _stream_ptr, load_library
+from .sampler import LOGITS_BF16, LOGITS_F32, ClsampleError, _check, _dptr, _stream_ptr, load_library
 
 T_BF16, T_F16 = 0, 1
+ERR_DEVICE = -7
 _I32, _I64, _PTR = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
 
@@ -65,6 +67,12 @@ def _device() -> torch.device:
     if not torch.cuda.is_available():
         raise RuntimeError("the operators need a CUDA device")
     return torch.device("cuda", torch.cuda.current_device())
+
+
+def _current(device: torch.device):
+    # without a handle the library cannot know whose tensors a call has
+    if torch.cuda.current_device() != device.index:
+        raise ClsampleError(ERR_DEVICE)
 
 
 def _on_stream(stream):
@@ -177,6 +185,7 @@ class KVAppend:
 
     def apply(self, args: KVAppendArgs, stream: Optional[torch.cuda.Stream] = None):
         """Enqueue one call on ``stream`` (default: current)."""
+        _current(self.device)
         _check(self._L.clsample_kv_append(ctypes.byref(args), _stream_ptr(stream)))
 
     def __call__(self, q, k, v, k_cache, v_cache, page_table, cu_new, kv_lens, *, stream=None,
@@ -317,6 +326,7 @@ class DraftVerifier:
 
     def apply(self, args: VerifyArgs, stream: Optional[torch.cuda.Stream] = None):
         """Enqueue one call on ``stream`` (default: current)."""
+        _current(self.device)
         _check(self._L.clsample_verify(ctypes.byref(args), _stream_ptr(stream)))
 
     def __call__(self, target_probs, draft_tokens, cu_draft, u_accept, u_sample, *, max_draft: int,

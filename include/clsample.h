@@ -362,7 +362,8 @@ typedef struct {
 } clsample_kv_append_args_t;
 
 /* Enqueues one append on `stream` (one launch; none when T == 0 or B == 0, except that
- * the statuses of B sequences without tokens are written).  No handle, no scratch. */
+ * the statuses of B sequences without tokens are written).  No handle, no scratch; the arrays
+ * are the current device's. */
 int clsample_kv_append(const clsample_kv_append_args_t* args, clsample_stream_t stream);
 
 /* Arguments of clsample_chunk_attention.  Query head h reads key head h / (Hq / Hkv).  The
@@ -476,7 +477,8 @@ typedef struct {
   int32_t* row_status;
 } clsample_verify_args_t;
 
-/* Enqueues one verification on `stream` (one launch); nothing when B == 0. */
+/* Enqueues one verification on `stream` (one launch); nothing when B == 0.  No handle, no scratch;
+ * the arrays are the current device's. */
 int clsample_verify(const clsample_verify_args_t* args, clsample_stream_t stream);
 
 #ifdef __cplusplus

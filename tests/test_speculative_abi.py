@@ -100,3 +100,25 @@ def test_verify_refusals(lib, change, code):
 def test_verify_nothing_to_do(lib):
     assert lib.clsample_verify(None, None) == -1
     assert lib.clsample_verify(ctypes.byref(_verify(B=0)), None) == 0
+
+
+@pytest.mark.parametrize("name,function", [("KVAppend", "clsample_kv_append"), ("DraftVerifier", "clsample_verify")])
+def test_calls_while_another_device_is_current(lib, monkeypatch, name, function):
+    """An object's tensors are its own device's: with another device current nothing is launched."""
+    import types
+
+    import torch
+    from constrained_logits_sampling_gb300 import speculative as S
+    calls = []
+    op = getattr(S, name).__new__(getattr(S, name))
+    op._L = types.SimpleNamespace(**{function: lambda *a: calls.append(a) or 0})
+    op.device = torch.device("cuda", 0)
+    monkeypatch.setattr(S, "_stream_ptr", lambda stream: 0)
+    args = (S.KVAppendArgs if name == "KVAppend" else S.VerifyArgs)()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(RuntimeError) as e:
+        op.apply(args)
+    assert e.value.code == -7 and not calls
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    op.apply(args)
+    assert len(calls) == 1
