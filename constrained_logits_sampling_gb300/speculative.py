@@ -32,7 +32,19 @@ ERR_DEVICE = -7
 _I32, _I64, _PTR = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
 
-class KVAppendArgs(ctypes.Structure):
+class _Args(ctypes.Structure):
+    """Numbers that a 32-bit field cannot hold are refused: ctypes would keep their low bits."""
+
+    def __init_subclass__(cls):
+        cls._narrow = frozenset(n for n, t in cls._fields_ if t is _I32)
+
+    def __setattr__(self, name, value):
+        if name in self._narrow and not -(1 << 31) <= value < 1 << 31:
+            raise ValueError(f"{name} is {value}: out of the 32-bit range")
+        super().__setattr__(name, value)
+
+
+class KVAppendArgs(_Args):
     """Mirror of clsample_kv_append_args_t (include/clsample.h)."""
     _fields_ = [(n, _I32) for n in ("B", "T", "Hq", "Hkv", "D", "dtype", "num_pages", "page_size", "max_pages",
                                     "rot_dim", "max_pos", "interleaved")] + [
@@ -44,7 +56,7 @@ class KVAppendArgs(ctypes.Structure):
         ("cs_stride", _I64), ("q_weight", _PTR), ("k_weight", _PTR), ("row_status", _PTR)]
 
 
-class AttentionArgs(ctypes.Structure):
+class AttentionArgs(_Args):
     """Mirror of clsample_attention_args_t (include/clsample.h)."""
     _fields_ = [(n, _I32) for n in ("B", "T", "Hq", "Hkv", "D", "dtype", "num_pages", "page_size", "max_pages",
                                     "max_new", "window")] + [("scale", ctypes.c_float)] + [
@@ -55,7 +67,7 @@ class AttentionArgs(ctypes.Structure):
         ("row_status", _PTR)]
 
 
-class VerifyArgs(ctypes.Structure):
+class VerifyArgs(_Args):
     """Mirror of clsample_verify_args_t (include/clsample.h)."""
     _fields_ = [(n, _I32) for n in ("B", "N", "V", "dtype", "max_draft", "reserved0")] + [
         ("target", _PTR), ("target_stride", _I64), ("draft", _PTR), ("draft_stride", _I64), ("draft_tokens", _PTR),

@@ -354,6 +354,18 @@ def test_attention_refusals(S):
     assert e.value.code == -10
 
 
+def test_attention_numbers_past_32_bits(S):
+    pr = R.Problem([2], [40], 4, 2, 64, 16, BF, seed=13)
+    args = (fused(pr)[0], gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens))
+    att = S.ChunkAttention()
+    ref, _, tol, _ = R.attention(pr)
+    for kw in (dict(window=(1 << 31) - 1), dict(max_new=(1 << 31) - 1)):  # the bound chooses the kernel
+        assert ((att(*args, **kw)["out"].cpu().double() - ref).abs() <= tol).all()
+    for kw in (dict(window=(1 << 32) + 5), dict(max_new=(1 << 32) + 1)):
+        with pytest.raises(ValueError):
+            att(*args, **kw)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_attention_largest_scale(S, n):
     """Scores of zero stay zero up to the largest scale; above it, where the scale in powers of

@@ -122,3 +122,21 @@ def test_calls_while_another_device_is_current(lib, monkeypatch, name, function)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     op.apply(args)
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("cls,field", [("AttentionArgs", "window"), ("AttentionArgs", "max_new"), ("AttentionArgs", "T"),
+                                       ("KVAppendArgs", "rot_dim"), ("KVAppendArgs", "T"), ("VerifyArgs", "max_draft"),
+                                       ("VerifyArgs", "N")])
+def test_numbers_past_32_bits_are_refused(lib, cls, field):
+    """A window of 2^32 + 5 is not one of 5."""
+    from constrained_logits_sampling_gb300 import speculative as S
+    a = getattr(S, cls)()
+    for value in ((1 << 32) + 5, 1 << 31, -(1 << 31) - 1, 1 << 70):
+        with pytest.raises(ValueError):
+            setattr(a, field, value)
+        assert getattr(a, field) == 0
+    for value in ((1 << 31) - 1, -(1 << 31), 7):
+        setattr(a, field, value)
+        assert getattr(a, field) == value
+    a.page_stride = a.target_stride = 1 << 40  # 64-bit fields, or none of the structure's
+    assert getattr(a, "page_stride") == 1 << 40
