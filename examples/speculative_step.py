@@ -59,12 +59,12 @@ class Decoder:
         for w, (k_cache, v_cache) in zip(self.layers, self.caches):
             h = torch.nn.functional.rms_norm(x, x.shape[-1:])
             qkv = h @ w["qkv"]
-            q, k, v = (t.view(T, -1, self.D) for t in
-                       qkv.split([self.Hq * self.D, self.Hkv * self.D, self.Hkv * self.D], 1))
+            heads = (self.Hq, self.Hkv, self.Hkv)
+            q, k, v = (t.view(T, n, self.D) for n, t in zip(heads, qkv.split([n * self.D for n in heads], 1)))
             q = self.append(q, k, v, k_cache, v_cache, self.table, cu_new, kv_lens, cos_sin=self.cos_sin,
                             q_weight=w["q_norm"], k_weight=w["k_norm"])["q"]
             o = self.attend(q, k_cache, v_cache, self.table, cu_new, kv_lens, max_new=max_new)["out"]
-            x = x + o.view(T, -1) @ w["out"]
+            x = x + o.flatten(1) @ w["out"]
             up, gate = (torch.nn.functional.rms_norm(x, x.shape[-1:]) @ w["up"]).chunk(2, 1)
             x = x + (up * torch.nn.functional.silu(gate)) @ w["down"]
         return (torch.nn.functional.rms_norm(x, x.shape[-1:]) @ self.head).float()

@@ -714,3 +714,22 @@ def test_example_step(S):
         # such errors add up like their square root, and a logit is a sum over the row
         size = want.norm(dim=1, keepdim=True) / V ** 0.5
         assert ((got[:, i] - want).abs() <= 8 * 2.0 ** -8 * 20 ** 0.5 * size).all(), i
+
+
+def test_example_prompts_of_one_token(S):
+    """Prompts whose only token is left for the first step: nothing is prefilled."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "speculative_step.py")
+    spec = importlib.util.spec_from_file_location("speculative_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    B, V = 2, 300
+    shape = dict(vocab=V, Hq=4, Hkv=2, D=64, batch=B, max_len=64)
+    loop = ex.SpeculativeLoop(ex.Decoder(layers=2, **shape), ex.Decoder(layers=1, **shape), V, B, 2)
+    loop.prefill([[7], [11]])
+    for _ in range(3):
+        out = loop.step()
+        assert not out["status"].any()
+        assert ((out["tokens"] >= 0).sum(1) == out["accepted"] + 1).all()
+    assert (loop.lens >= 3).all()
