@@ -25,6 +25,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -90,15 +91,39 @@ def peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
-SAMPLER_SOURCES = ("bulk_copy.cuh", "clsample.cu", "sampler_math.cuh", "sweep.cuh")
+CSRC = os.path.join(ROOT, "constrained_logits_sampling_gb300", "csrc")
+HEADER = os.path.join(ROOT, "include", "clsample.h")
+OTHER_OPERATORS = "The other operators of a speculative-decoding step."  # where the header's sampler part ends
+
+
+def sampler_sources():
+    """The sampler's CUDA file and what it includes of its folder, in the order found."""
+    found, todo = [], ["clsample.cu"]
+    while todo:
+        n = todo.pop(0)
+        if n in found or not os.path.exists(os.path.join(CSRC, n)):
+            continue
+        found.append(n)
+        with open(os.path.join(CSRC, n)) as f:
+            todo += re.findall(r'^\s*#\s*include\s+"([^"]+)"', f.read(), re.M)
+    return found
+
+
+def sampler_header():
+    """The public header as far as the sampler goes: codes, argument layout, mode bits."""
+    with open(HEADER) as f:
+        head, mark, _ = f.read().partition(OTHER_OPERATORS)
+    if not mark:
+        raise RuntimeError(f"{HEADER}: no line says where the sampler's part ends")
+    return head
 
 
 def kernel_source_hash():
-    """Hash of the sampler's CUDA sources (ties a committed ncu traffic figure to the kernel it
-    was measured on)."""
-    h = hashlib.sha256()
-    for n in SAMPLER_SOURCES:
-        with open(os.path.join(ROOT, "constrained_logits_sampling_gb300", "csrc", n), "rb") as f:
+    """Hash of all that the sampler is compiled from (ties a committed ncu traffic figure to the
+    kernel it was measured on)."""
+    h = hashlib.sha256(sampler_header().encode())
+    for n in sorted(sampler_sources()):
+        with open(os.path.join(CSRC, n), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
 
