@@ -311,6 +311,62 @@ def test_attention_far_offsets(S):
     assert ((got["out"].cpu().double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("page", [128, 120])  # copied in boxes, and row by row
+def test_attention_far_offsets_of_chunks(S, page):
+    """More than 16 packed rows over a cache whose last pages lie past 2^31 elements."""
+    Hkv, D = 128, 128
+    pages = (1 << 31) // (page * Hkv * D) + 4
+    k = torch.zeros(pages, page, Hkv, D, dtype=BF, device="cuda")
+    v = torch.zeros(pages, page, Hkv, D, dtype=BF, device="cuda")
+    pr = R.Problem([24], [200], Hkv, Hkv, D, page, BF, seed=12)
+    for i, far in enumerate((pages - 1, pages - 2)):
+        k[far], v[far] = pr.k_cache[int(pr.table[0, i])].cuda(), pr.v_cache[int(pr.table[0, i])].cuda()
+    assert (pages - 2) * k.stride(0) > 1 << 31
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device="cuda")
+    got = S.ChunkAttention()(fused(pr)[0], k, v, table, gpu(pr.cu), gpu(pr.kv_lens))
+    ref, _, tol, _ = R.attention(pr)
+    assert ((got["out"].cpu().double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n,page", [(3, 16), (30, 16), (30, 12)])
+def test_attention_one_sequence_not_finite(S, n, page):
+    """Queries that are NaN or infinite, and keys and values of their sequence that are, concern
+    nobody else; the slots past each length hold NaN."""
+    pr = R.Problem([n] * 5, [90, n, 150, 200, 77], 6, 2, 64, page, BF, seed=17)
+    ref, lse, tol, lse_tol = R.attention(pr)
+    pr.q[n:2 * n] = math.nan
+    pr.q[3 * n:4 * n] = math.inf
+    for b, value in ((1, math.inf), (3, math.nan)):
+        p = int(pr.table[b, 0])
+        pr.k_cache[p, 0] = pr.v_cache[p, 0] = value
+    got = S.ChunkAttention()(fused(pr)[0], gpu(pr.k_cache), gpu(pr.v_cache), gpu(pr.table), gpu(pr.cu), gpu(pr.kv_lens),
+                             max_new=n, lse=True)
+    assert got["status"].cpu().tolist() == [0] * 5
+    for b in (0, 2, 4):
+        rows = slice(b * n, b * n + n)
+        assert ((got["out"].cpu().double() - ref).abs() <= tol)[rows].all()
+        assert ((got["lse"].cpu().double() - lse).abs() <= lse_tol)[rows].all()
+    assert torch.isnan(got["out"][n:2 * n].float()).all() and torch.isnan(got["out"][3 * n:4 * n].float()).all()
+
+
+def test_attention_two_handles_at_once(S):
+    """Calls of both kernels on two handles and two streams, side by side: the bits of calls alone."""
+    shapes = [batch([1 + 3 * (b % 3) for b in range(40)], [300 + 77 * b for b in range(40)], 8, 2, 128, 16, BF, 5),
+              batch([70 if b % 5 == 0 else 1 for b in range(400)], [100 + 13 * b % 900 for b in range(400)], 6, 3, 64, 32, FP, 6)]
+    most = [7, 70]
+    want = [S.ChunkAttention()(*a, max_new=m, lse=True) for a, m in zip(shapes, most)]
+    torch.cuda.synchronize()
+    handles, streams, got = [S.ChunkAttention() for _ in shapes], [torch.cuda.Stream() for _ in shapes], [[], []]
+    for _ in range(20):
+        for i, a in enumerate(shapes):
+            got[i].append(handles[i](*a, max_new=most[i], lse=True, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, calls in enumerate(got):
+        for c in calls:
+            assert not c["status"].any()
+            assert torch.equal(c["out"], want[i]["out"]) and torch.equal(c["lse"], want[i]["lse"])
+
+
 def test_attention_refusals(S):
     pr = R.Problem([2], [40], 4, 2, 64, 16, BF, seed=13)
     att = S.ChunkAttention()
@@ -468,6 +524,24 @@ def test_append_bad_tokens(S):
         assert torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
 
 
+@pytest.mark.parametrize("D", [128, 127])  # in 16-byte pieces, and element by element
+def test_append_far_offsets(S, D):
+    """Pages past 2^31 elements of a cache."""
+    page, Hkv = 128, 128
+    pages = (1 << 31) // (page * Hkv * D) + 4
+    kc, vc = (torch.zeros(pages, page, Hkv, D, dtype=BF, device="cuda") for _ in range(2))
+    pr = R.Problem([3], [130], 2, Hkv, D, page, BF, seed=3)
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device="cuda")
+    assert (pages - 2) * kc.stride(0) > 1 << 31
+    q, k, v = fused(pr)
+    got = S.KVAppend()(q, k, v, kc, vc, table, gpu(pr.cu), gpu(pr.kv_lens))
+    assert got["status"].tolist() == [0] and torch.equal(got["q"], q)
+    for t, (p, slot) in enumerate([(pages - 1, 127), (pages - 2, 0), (pages - 2, 1)]):
+        assert torch.equal(kc[p, slot], k[t]) and torch.equal(vc[p, slot], v[t])
+        kc[p, slot] = vc[p, slot] = 0
+    assert not kc.any() and not vc.any()
+
+
 def test_append_statuses_without_tokens(S):
     pr = R.Problem([0, 0, 0], [5, 0, 9], 2, 1, 64, 16, BF)
     q, k, v = fused(pr)
@@ -565,6 +639,32 @@ def test_verify_full_vocabulary_residual(S, V, dtype):
         k = int(math.floor(float(ul[b]) * 2.0 ** 31)) * int(c[-1]) >> 31
         t = int(np.searchsorted(c, k, side="right"))
         assert got["tokens"][b].tolist() == ([int(x[b]), t] if ok else [t, -1]), b
+
+
+@pytest.mark.parametrize("has_draft", [False, True])
+def test_verify_far_rows(S, has_draft):
+    """Rows of probabilities past 2^31 elements: the last requests of a batch draw from theirs."""
+    V, B = 131072, 8400
+    target = torch.zeros(2 * B, V, dtype=BF, device="cuda")  # 2.2e9 elements
+    x = torch.arange(B, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    rows = torch.arange(B, device="cuda")
+    target[2 * rows, rows + 5] = 1.0      # never the drafted token
+    target[2 * rows + 1, rows + 9] = 1.0
+    last = rows >= B - 3
+    target[2 * rows[last], rows[last] + 5] = 0.5  # the last three requests may keep theirs
+    target[2 * rows[last], rows[last]] = 0.5
+    draft = None
+    if has_draft:
+        draft = torch.zeros(B, V, dtype=BF, device="cuda")
+        draft[rows, rows] = 1.0
+    u = torch.full((B,), 0.25, device="cuda")
+    got = S.DraftVerifier()(target, x, cu, u, u.clone(), max_draft=1, draft_probs=draft)
+    assert not got["status"].any()
+    assert torch.equal(got["accepted"], last.to(torch.int32))
+    first = torch.where(last, rows, rows + 5)
+    second = torch.where(last, rows + 9, -torch.ones_like(rows))
+    assert torch.equal(got["tokens"].long(), torch.stack([first, second], 1))
 
 
 def test_verify_edges(S):
