@@ -142,7 +142,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __shared__ ChunkShared<NS, NV> sh;
   unsigned char* const smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_smem = smem_addr(smem), k_smem = q_smem + 2 * kTile, v_smem = k_smem + NS * kTile;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // The warp's number is made known as uniform, as its role's branches are: without it 2 x 1024 tokens
+  // over 7100 keys took 177 us instead of 157.
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   const clsample_attention_args_t& a = P.a;
   const float neg_inf = __int_as_float(0xff800000);
 
