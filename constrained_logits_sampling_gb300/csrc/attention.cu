@@ -101,7 +101,7 @@ cudaError_t allow_smem(Kernel fn, int bytes) {
 template <class T, int D>
 cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
   // Boxes have to start on the eight rows of the swizzle and fill a tile.  2 x 2048 tokens over
-  // 14000 keys: 565 us with them, 1197 row by row.
+  // 14500 to 15600 keys: 557 us with them, 1215 row by row.
   const int page = P.a.page_size;
   CUtensorMap k_map{}, v_map{}, q_map{};
   const bool boxes = page >= 8 && (page % kChunkKeys == 0 || kChunkKeys % page == 0) &&
@@ -138,12 +138,12 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
   CutUnit* const stream_cut = chunk_cut + h->sms;
   P.gave_up = reinterpret_cast<int*>(stream_cut + h->sms * kStreamCtas);
   // Sequences of up to 16 packed rows go to the stream kernel, longer ones to the chunk
-  // kernel.  256 sequences of 16 rows over 2.3 GB of keys and values: 404 us in the one, 445 in
-  // the other; of 24 rows, where the one would read keys twice or hold 32 rows: 541 and 422.
+  // kernel.  256 sequences of 16 rows over 2.3 GB of keys and values: 385 us in the one, 441 in
+  // the other; of 24 rows, where the one reads keys twice: 707 and 420.
   const bool chunks = rows > kStreamRows;
   // Beside longer sequences, a few short ones are not worth a launch of their own: 19 ragged
-  // sequences on 12 key heads take 40 us alone in the chunk kernel and 49 us in both; 240
-  // sequences of one token and 16 of 512, on 8 key heads, 803 and 725.
+  // sequences on 12 key heads take 31 us alone in the chunk kernel and 35 us in both; 240
+  // sequences of one token and 16 of 512, on 8 key heads, 708 and 590.
   const bool alone = chunks && (int64_t)P.a.B * P.a.Hkv <= 4 * h->sms;
   cudaError_t e;
   if (chunks) {

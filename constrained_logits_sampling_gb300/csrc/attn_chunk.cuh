@@ -7,9 +7,10 @@
 // Loads come in two forms.  Where pages are whole boxes of a tile (8, 16, 32, 64 or a
 // multiple of 128 slots) warps 8 and 11 copy keys and values by TMA, one box a page and 64
 // elements, an invalid page as zeros (a box takes some 75 cycles to issue, so with pages of 16
-// slots one warp would not keep up: 771 us against 574); warp 9 loads the queries, in one box a
-// row tile where the query heads of a key head divide 128 and row by row otherwise, and clears
-// the value slots that lie outside the unit's keys (they may hold anything, and 0 x NaN is NaN).
+// slots one warp would not keep up: on an earlier version 771 us against 574); warp 9 loads the
+// queries, in one box a row tile where the query heads of a key head divide 128 and row by row
+// otherwise, and clears the value slots that lie outside the unit's keys (they may hold anything,
+// and 0 x NaN is NaN).
 // Other page sizes are copied row by row with cp.async by warps 8 and 9, zeros where there
 // is no key, and warp 11 hands what has landed over to the tensor cores' proxy.
 // S = Q K^T goes to tensor memory (128 columns a tile), the softmax warps read it, write the
@@ -18,10 +19,10 @@
 // have the other's PV and next QK^T (2 x 128 x 128 x D each).  O stays in tensor memory;
 // it is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // time (P and its sum are then up to 2^8, which both types hold), so hardly ever.
-// 2 x 2048 tokens on 32 / 8 heads of 128 over 14500 to 15600 keys (943 GFLOP): 565 us alone, 1.67
-// PFLOP/s, or 630 to 650 us in a row of calls that draw the power limit.  A tile of 128 keys takes
-// about 2500 cycles, of which the products are 2048: the rest is the way from a finished S over
-// the softmax (970 cycles) to the next product.
+// 2 x 2048 tokens on 32 / 8 heads of 128 over 14500 to 15600 keys (943 GFLOP): 561 us a call with
+// L2 flushed in between (1.68 PFLOP/s), 615 to 635 in a row of calls that draw the power limit.
+// The products of a tile of 128 keys take 2048 cycles; a trace of an earlier version showed about
+// 2500 a tile, the rest of it the way from a finished S over the softmax (970) to the next product.
 // A unit of at most 128 rows has one row tile: both halves of the CTA then take the same
 // queries and every other key tile, and their sums are joined at the end, in the room of the
 // second row tile's queries.

@@ -8,8 +8,8 @@
 // tcgen05 has 64 at least.  The four warps' results meet in shared memory at the end of a
 // unit's span.  256 requests of 4 tokens on 32 / 8 heads of 128 over 200 to 4000 keys (2.27 GB):
 // 386 us, 5.9 TB/s, with rows of 256 bytes 2 KB apart in the cache; one token over 777 keys: 12 us.
-// A warp of its own that copied by TMA, on into the next unit while the others
-// ended one, was no faster (407 us against 404) and slower where a unit is one tile (19 and 15).
+// A warp of its own that copied by TMA, on into the next unit while the others ended one, was no
+// faster (on an earlier version, 407 us against 404) and slower where a unit is one tile (19 and 15).
 #pragma once
 
 #include "attn_units.cuh"
@@ -73,7 +73,8 @@ constexpr int kStreamThreads = 128;
 constexpr int kStreamKeys = 64;
 constexpr float kLn2 = 0.693147180559945309f;
 
-// Ring stages of a warp: two CTAs fit an SM, with about 190 KB of loads in flight.
+// Ring stages of a warp: two CTAs fit an SM, with up to 128 KB of loads in flight for heads of 128
+// and 160 KB for heads of 64 (all stages but the one that is worked on).
 constexpr int kStreamRows = 16;
 template <int D>
 struct StreamRing {

@@ -3,7 +3,7 @@
 //
 // Bound by memory: (Hq + 2 Hkv) D elements are read once and written once per token, with
 // about ten operations each.  8192 tokens of 32 + 8 heads of 128 bf16 elements (206 MB): 39 us,
-// 5.2 TB/s; 1024 tokens with norm (26 MB): 10.3 us; one token: 6.3 us, of which all is latency.
+// 5.2 TB/s; 1024 tokens with norm (26 MB): 10.3 us; one token: 6.3 to 6.9 us, all of it latency.
 #include "paged.cuh"
 
 namespace clsample {
@@ -163,9 +163,10 @@ struct HeadRow {
 // while the warps find its tokens' sequences, positions and pages; from then on a token's rows
 // are loaded while the one before it is worked on.  Addresses come from a table in shared
 // memory: with the selection between q, k and v in each row the instructions took longer than
-// the memory (8192 tokens: 68 us, 52 with the table).
+// the memory (8192 tokens, on an earlier version: 68 us, 52 with the table).
 // kPaired, for the usual case of a whole head rotated in halves: lane l has elements 4l .. 4l + 3
-// of both halves instead, so that pairs meet in a lane and nothing is exchanged (44 us against 48).
+// of both halves instead, so that pairs meet in a lane and nothing is exchanged (8192
+// tokens: 38 us against 43; 1024 with norm: 10.4 against 12.3).
 template <class T, int G, bool kPaired>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __grid_constant__ AppendParams P) {
   const clsample_kv_append_args_t& a = P.a;
@@ -342,8 +343,8 @@ void launch_append(AppendParams P, bool fast, int sms, cudaStream_t st) {
     append_any_kernel<T><<<P.a.T > 0 ? P.a.T : status_blocks, kThreads, 0, st>>>(P);
     return;
   }
-  // as many tokens a block as it takes for the blocks to fit the device at once (8192 tokens: 44 us,
-  // with one token a block 54)
+  // as many tokens a block as it takes for the blocks to fit the device at once (8192 tokens: 38 us,
+  // with one token a block 50)
   P.tokens = (P.a.T + sms * kBlocksPerSm - 1) / (sms * kBlocksPerSm);
   P.tokens = P.tokens < 1 ? 1 : P.tokens > kMaxTokens ? kMaxTokens : P.tokens;
   const int grid = P.a.T > 0 ? (P.a.T + P.tokens - 1) / P.tokens : status_blocks;

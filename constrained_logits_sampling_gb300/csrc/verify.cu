@@ -423,8 +423,8 @@ cudaError_t launch_verify(const clsample_verify_args_t& a, cudaStream_t st) {
 }
 
 // The largest cluster with which all requests are resident at once: one wave, each request
-// over as many SMs as that leaves it.  256 requests over 151936 tokens: 64 us on 2 CTAs each, 66
-// on 4, 74 on 8; one over 32000: 13 us on 8, 15 on 4, 17 on 2.
+// over as many SMs as that leaves it.  256 requests over 151936 tokens: 50 us on 2 CTAs each, 53
+// on 4, 61 on 8; one over 32000: 7.4 to 8.0 us on 8, 8.4 on 4, 10.3 on 2.
 template <class P>
 cudaError_t launch_verify(const clsample_verify_args_t& a, int sms, cudaStream_t st) {
   const int64_t slots = (int64_t)sms * kCtasPerSm;

@@ -241,8 +241,10 @@ class ChunkAttention:
                   scale: Optional[float] = None, window: int = 0, out: torch.Tensor,
                   lse: Optional[torch.Tensor] = None, row_status: Optional[torch.Tensor] = None) -> AttentionArgs:
         """q and out [T, Hq, D]; the cache and batch as in ``KVAppend``.  ``max_new``: no
-        sequence has more new tokens (None: T); ``scale`` None: 1 / sqrt(D); ``window`` > 0:
-        a token sees only that many keys, itself included; ``lse`` float32 [T, Hq]."""
+        sequence has more new tokens (None: T, a loose bound for a batch: with a bound of up to 16
+        packed rows, max_new Hq / Hkv, the kernel for few rows runs alone); ``scale`` None:
+        1 / sqrt(D); ``window`` > 0: a token sees only that many keys, itself included; ``lse``
+        float32 [T, Hq]."""
         dev, dt = self.device, q.dtype
         a = AttentionArgs()
         a.dtype = _type_of(q)

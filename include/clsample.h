@@ -371,12 +371,16 @@ int clsample_kv_append(const clsample_kv_append_args_t* args, clsample_stream_t 
  * window > 0:
  *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j).
  * A row that sees no key (kv_lens[b] < n_b) gets out 0 and lse -inf.  Slots that no row of
- * the sequence sees are never read: they may hold anything, and their page ids too.
+ * the sequence sees may hold anything: those of a page with others that are seen may be read, but
+ * nothing depends on them.  Ids of pages without a slot that is seen are not looked at.
  *
  * q, out            [T, Hq, D] of `dtype`, token and head strides (elements).
  * lse               f32[T, Hq] output or NULL.
  * max_new           upper bound of n_b, known to the caller; a sequence above it is
- *                   INVALID and its out rows are 0.
+ *                   INVALID and its out rows are 0.  It also chooses the kernels: only up to
+ *                   16 packed rows (max_new Hq / Hkv) does a call take the one for few rows
+ *                   alone, so a loose bound costs decoding batches time, and results of
+ *                   different bounds may differ in their rounding.
  * scale             in (0, 2e38] (1 / sqrt(D) as a rule).
  * row_status        i32[B] output or NULL.  Keys on a page with an invalid id are left out.
  *
