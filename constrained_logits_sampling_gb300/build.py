@@ -11,7 +11,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("clsample.cu", "attention.cu", "kv_append.cu", "verify.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("clsample.cu", "attention.cu", "tree_attention.cu", "kv_append.cu", "verify.cu",
+                                           "tree_plan.cu", "tree_verify.cu", "cache_pages.cu", "page_pool.cu")]
 HEADERS = [os.path.join(ROOT, "include", "clsample.h")] + sorted(
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
 LIB = os.path.join(PKG, "libclsample.so")

@@ -102,10 +102,24 @@ struct ChunkShared {
   alignas(16) uint32_t key_ok[2 * NS][4];  // keys of a tile that are on valid pages
 };
 
-// Bits lo .. hi of a word, of which only 0 .. 31 exist.
-__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
-  const uint32_t upto = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1;
-  return lo <= 0 ? upto : lo > 31 ? 0u : upto & (~0u << lo);
+// kTree: which of the keys kb .. kb + 127 any row of the unit sees, by one warp; keys before the
+// first new token count as seen.
+__device__ __forceinline__ uint4 seen_by_any(const AttnParams& P, const Unit& u, int kb) {
+  const int lane = threadIdx.x & 31, j0 = kb - (u.len - u.n);
+  const int last = token_of(P, u.row0 + u.rows - 1);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int i = token_of(P, u.row0) + lane; i <= last; i += 32) {
+    const uint32_t* row = mask_row(P, u.q0 + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] |= mask_word(row, min(u.n, u.len), j0 + 32 * k);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = __reduce_or_sync(~0u, w[k]) | column_bits(0, -j0 - 1 - 32 * k);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int k) {
+  return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
 }
 
 struct SoftmaxSync {  // the 256 softmax threads
@@ -131,7 +145,7 @@ struct SoftmaxSync {  // the 256 softmax threads
 // them, and go on to no other.  Then all pause while copies land.  The call's statuses tell that
 // its outputs are void.
 
-template <class T, int D, bool kTma>
+template <class T, int D, bool kTma, bool kTree = false>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     attn_chunk_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
@@ -153,7 +167,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   Span span;
   Unit u;
   int64_t unit_begin;
-  if (!find_span<kChunkRows, kChunkKeys, kChunkThreads>(P, &span, &u, &unit_begin)) {
+  if (!find_span<kChunkRows, kChunkKeys, kChunkThreads, kTree>(P, &span, &u, &unit_begin)) {
     if (tid == 0) P.cut[blockIdx.x].rows = 0;
     return;
   }
@@ -232,15 +246,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           tc_fence_after();
           const uint32_t* ok = sh.key_ok[(tile + j) % (2 * NS)];
           const uint4 bits = *reinterpret_cast<const uint4*>(ok);
-          const bool whole = (bits.x & bits.y & bits.z & bits.w) == ~0u && kb + 127 <= pos_first &&
-                             (a.window <= 0 || kb > pos_last - a.window);
+          // kTree: only cached keys, and nobody stands behind the last slot
+          const bool whole = (bits.x & bits.y & bits.z & bits.w) == ~0u &&
+                             (kTree ? kb + 127 < first_pos && (a.window <= 0 || kb > u.len - 1 - a.window)
+                                    : kb + 127 <= pos_first && (a.window <= 0 || kb > pos_last - a.window));
           uint32_t x[128];
           tmem_ld(x, s_tmem);
           if (!whole) {
-            const int hi = pos - kb;  // columns lo .. hi are seen
-            const int lo = a.window > 0 ? hi - a.window + 1 : 0;
-            const uint32_t shown[4] = {bits.x & column_bits(lo, hi), bits.y & column_bits(lo - 32, hi - 32),
-                                       bits.z & column_bits(lo - 64, hi - 64), bits.w & column_bits(lo - 96, hi - 96)};
+            int hi = pos - kb;  // columns lo .. hi are seen
+            int lo = a.window > 0 ? hi - a.window + 1 : 0;
+            uint32_t shown[4];
+            if constexpr (kTree) {
+              const int i = token_of(P, u.row0 + (live ? r : 0));
+              hi = first_pos - 1 - kb;
+              lo = a.window > 0 ? tree_position(P, u.q0 + i, i, u.len, u.n) - a.window + 1 - kb : 0;
+              const uint32_t* row = mask_row(P, u.q0 + i);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                shown[k] = column_bits(lo - 32 * k, hi - 32 * k);
+                if (kb + 127 >= first_pos) shown[k] |= mask_word(row, min(u.n, u.len), kb - first_pos + 32 * k);
+                shown[k] = live ? shown[k] & word_of(bits, k) : 0u;
+              }
+            } else {
+              shown[0] = bits.x & column_bits(lo, hi);
+              shown[1] = bits.y & column_bits(lo - 32, hi - 32);
+              shown[2] = bits.z & column_bits(lo - 64, hi - 64);
+              shown[3] = bits.w & column_bits(lo - 96, hi - 96);
+            }
 #pragma unroll
             for (int c = 0; c < 128; ++c)
               if (!(shown[c >> 5] & (1u << (c & 31)))) x[c] = 0xff800000u;
@@ -506,8 +538,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     };
     auto key_slot = [&](uint32_t it) { tile_done((int64_t)it - NS); };
     auto value_slot = [&](uint32_t it, int j) { tile_done((int64_t)it - NV + (u.rows <= 128 || j < NV ? 2 : 1)); };
-    // a tile with values outside the unit's keys
-    auto edge = [&](int tile) { return tile * kChunkKeys < u.key_lo || tile * kChunkKeys + kChunkKeys > u.key_hi; };
+    // a tile with values outside the unit's keys (kTree: or with values that perhaps no row sees)
+    auto edge = [&](int tile) {
+      return tile * kChunkKeys < u.key_lo || tile * kChunkKeys + kChunkKeys > (kTree ? u.len - u.n : u.key_hi);
+    };
 
     if (kTma && warp != 9) {
       // lane i has the i-th page (or 128 slots of one) of a tile; warp 8 the keys, 11 the values
@@ -562,7 +596,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         t += cnt;
         if (t >= span.t1 || __any_sync(~0u, sh.limit.dead)) break;
         unit_begin = t;
-        next_unit<kChunkRows, kChunkKeys>(P, &u);
+        next_unit<kChunkRows, kChunkKeys, kTree>(P, &u);
       }
     } else if (kTma) {
       uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
@@ -582,9 +616,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const bool dead = sh.limit.dead;
           __syncwarp();
           const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
+          uint4 any;
+          if (kTree) any = seen_by_any(P, u, tile * kChunkKeys);
           for (int i = lane; i < 128 * KC; i += 32) {  // a row's pieces may lie anywhere in it: all are cleared
             const int row = i / KC, ch = i % KC;
-            if (row < lo || row >= hi)
+            if (row < lo || row >= hi || (kTree && !((word_of(any, row >> 5) >> (row & 31)) & 1)))
               *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
           }
@@ -597,7 +633,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         t += cnt;
         if (t >= span.t1) break;
         unit_begin = t;
-        next_unit<kChunkRows, kChunkKeys>(P, &u);
+        next_unit<kChunkRows, kChunkKeys, kTree>(P, &u);
       }
       cp_async_wait_all();
     } else if (warp < 10) {
@@ -612,6 +648,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // warp lw has keys 64 lw .. 64 lw + 63 of a tile, two a lane
         auto page_of = [&](int j, int half) {
           const int key = (u.tile0 + j0 + j) * kChunkKeys + lw * 64 + half * 32 + lane;
+          if (kTree && j < cnt && (u.tile0 + j0 + j) * kChunkKeys + kChunkKeys > u.len - u.n) {  // uniform
+            const uint4 any = seen_by_any(P, u, (u.tile0 + j0 + j) * kChunkKeys);
+            if (!((word_of(any, lw * 2 + half) >> lane) & 1)) return -1;
+          }
           if (j >= cnt || key < u.key_lo || key >= u.key_hi) return -1;
           const int id = __ldg(table + (P.page_shift >= 0 ? key >> P.page_shift : key / a.page_size));
           return id < a.num_pages ? id : -1;
@@ -654,7 +694,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         t += cnt;
         if (t >= span.t1) break;
         unit_begin = t;
-        next_unit<kChunkRows, kChunkKeys>(P, &u);
+        next_unit<kChunkRows, kChunkKeys, kTree>(P, &u);
       }
       cp_async_wait_all();
     } else if (lane == 0) {
@@ -768,7 +808,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         t += cnt;
         if (uni(t >= span.t1)) break;
         unit_begin = t;
-        next_unit<kChunkRows, kChunkKeys>(P, &u);
+        next_unit<kChunkRows, kChunkKeys, kTree>(P, &u);
       }
       // products still running when a wait gave up end before their memory is freed
       if (!alive) {

@@ -28,13 +28,18 @@ struct JoinParams {
 
 // Statuses: one CTA per sequence at a time looks at its lengths and at every page id that
 // the call touches.
-template <int NT>
+template <int NT, bool kTree>
 __device__ __forceinline__ void attention_status(const AttnParams& P, bool gave_up) {
   const clsample_attention_args_t& a = P.a;
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const Seq s = load_seq(a.cu_new, a.kv_lens, b, a.T, P.capacity, a.max_new);
-    int bad = !s.ok;
-    if (s.ok && s.n > 0 && s.len > 0) {
+    int bad = !s.ok || (kTree && s.n > s.len);
+    if (kTree && !bad && P.tree.positions)
+      for (int i = threadIdx.x; i < s.n; i += NT) {
+        const int pos = __ldg(P.tree.positions + s.q0 + i);
+        bad |= pos < s.len - s.n || pos >= s.len;
+      }
+    if (s.ok && s.n > 0 && s.len > 0 && !(kTree && s.n > s.len)) {
       const int lo = a.window > 0 ? max(0, s.len - s.n - a.window + 1) : 0;
 #pragma unroll 8
       for (int p = lo / a.page_size + threadIdx.x; p <= (s.len - 1) / a.page_size; p += NT) {
@@ -100,7 +105,7 @@ __device__ __forceinline__ void finish_row(const AttnParams& P, const CutUnit& u
   if (d == 0 && P.a.lse) P.a.lse[(int64_t)token * P.a.Hq + head] = lse_of(s.m, s.l);
 }
 
-template <class T, int D>
+template <class T, int D, bool kTree = false>
 __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid_constant__ JoinParams J) {
   const AttnParams& P = J.p;
   constexpr int kCols = D / 16;                  // of 16 elements
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid
       }
     }
   }
-  if (P.a.row_status) attention_status<kJoinThreads>(P, *P.gave_up != 0);
+  if (P.a.row_status) attention_status<kJoinThreads, kTree>(P, *P.gave_up != 0);
 }
 
 }  // namespace clsample

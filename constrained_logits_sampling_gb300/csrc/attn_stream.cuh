@@ -107,10 +107,12 @@ __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, in
 
 // The rows of a unit as one warp has them: queries as A operands, limits and running sums.  Lane
 // i has rows i / 4 and i / 4 + 8.
-template <class T, int D>
+template <class T, int D, bool kTree = false>
 struct StreamState {
   uint32_t q[D / 16][4];
   int pos[2];
+  const uint32_t* mask[2];  // kTree: the rows' words, or null
+  int n;                    // kTree: the sequence's new tokens
   int pos_first, pos_last;
   float o[D / 8][4];
   float m[2], l[2];
@@ -125,7 +127,13 @@ struct StreamState {
       const int row = u.row0 + r;
       const T* src = (const T*)P.a.q + (int64_t)(u.q0 + (live ? token_of(P, row) : 0)) * P.a.q_stride_t +
                      (int64_t)(u.h * P.g + (live ? head_of(P, row) : 0)) * P.a.q_stride_h + (lane & 3) * 2;
-      pos[hf] = live ? u.len - u.n + token_of(P, row) : -1;
+      if constexpr (kTree) {
+        const int i = live ? token_of(P, row) : 0;
+        pos[hf] = tree_position(P, u.q0 + i, i, u.len, u.n);
+        mask[hf] = live ? mask_row(P, u.q0 + i) : nullptr;
+      } else {
+        pos[hf] = live ? u.len - u.n + token_of(P, row) : -1;
+      }
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         q[ks][hf] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16)) : 0u;
@@ -134,8 +142,10 @@ struct StreamState {
       m[hf] = neg_inf;
       l[hf] = 0.f;
     }
-    pos_first = u.len - u.n + token_of(P, u.row0);
-    pos_last = u.len - u.n + token_of(P, u.row0 + u.rows - 1);
+    // kTree: cached keys come before pos_first + 1, and nobody stands behind pos_last
+    pos_first = kTree ? u.len - u.n - 1 : u.len - u.n + token_of(P, u.row0);
+    pos_last = kTree ? u.len - 1 : u.len - u.n + token_of(P, u.row0 + u.rows - 1);
+    n = min(u.n, u.len);  // (no keys: none)
 #pragma unroll
     for (int d = 0; d < D / 8; ++d)
 #pragma unroll
@@ -162,6 +172,17 @@ struct StreamState {
     const int window = P.a.window;
     // every key of the tile is seen by every row (rows past the unit's are never stored)
     const bool whole = live == 0xffffu && key + 15 <= pos_first && (window <= 0 || key > pos_last - window);
+    uint32_t seen[2] = {0, 0};  // kTree: bit c, key + c
+    if (kTree && !whole) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+        if (mask[hf]) {
+          seen[hf] = column_bits(window > 0 ? pos[hf] - window + 1 - key : 0, pos_first - key);
+          if (key + 15 > pos_first) seen[hf] |= mask_word(mask[hf], n, key - pos_first - 1);
+          seen[hf] &= live;
+        }
+      live &= __reduce_or_sync(~0u, seen[0] | seen[1]);  // what no row sees may be anything
+    }
     bool moved = false;
     float keep[2];
     uint32_t p[4];
@@ -174,7 +195,9 @@ struct StreamState {
         for (int e = 0; e < 4; ++e) {
           const int c = (e >> 1) * 8 + (lane & 3) * 2 + (e & 1);
           const int kp = key + c;
-          if (!((live >> c) & 1) || kp > pos[hf] || (window > 0 && kp <= pos[hf] - window)) x[e] = neg_inf;
+          if (kTree) {
+            if (!((seen[hf] >> c) & 1)) x[e] = neg_inf;
+          } else if (!((live >> c) & 1) || kp > pos[hf] || (window > 0 && kp <= pos[hf] - window)) x[e] = neg_inf;
         }
       }
       float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
@@ -221,8 +244,8 @@ struct StreamState {
 
 // The warps' results of a unit's span meet: meet holds [warp][row][D + 8] (rows begin in different
 // banks), wm and wl the warps' maxima and sums.
-template <class T, int D>
-__device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u, StreamState<T, D>& st, float* meet,
+template <class T, int D, bool kTree>
+__device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u, StreamState<T, D, kTree>& st, float* meet,
                                               float (&wm)[4][kStreamRows], float (&wl)[4][kStreamRows], bool done,
                                               float* slot) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -274,7 +297,7 @@ __device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u
   __syncthreads();  // for the next unit
 }
 
-template <class T, int D>
+template <class T, int D, bool kTree = false>
 __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __grid_constant__ AttnParams P) {
   constexpr int R = kStreamRows, S = StreamRing<D>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
   constexpr int kTileBytes = 16 * D * 2, kStageBytes = 2 * kTileBytes, kHalf = 16 * 128;
@@ -289,7 +312,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
   Span span;
   Unit u;
   int64_t unit_begin;
-  if (!find_span<R, kStreamKeys, kStreamThreads>(P, &span, &u, &unit_begin)) {
+  if (!find_span<R, kStreamKeys, kStreamThreads, kTree>(P, &span, &u, &unit_begin)) {
     if (tid == 0) P.cut[blockIdx.x].rows = 0;
     wait_for_earlier_grids();  // this grid's end stands for theirs
     return;
@@ -343,7 +366,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
       issue(i, page);
       page = next;
     }
-    StreamState<T, D> st;
+    StreamState<T, D, kTree> st;
     st.begin(P, u);
     for (int i = 0; i < cnt; ++i) {
       cp_async_wait<S - 2>();
@@ -357,12 +380,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
     }
     cp_async_wait<0>();
     __syncthreads();  // the rings are drained: the first is where the warps meet
-    stream_finish<T, D>(P, u, st, reinterpret_cast<float*>(smem), wm, wl, cnt == u.tiles,
+    stream_finish<T, D, kTree>(P, u, st, reinterpret_cast<float*>(smem), wm, wl, cnt == u.tiles,
                                    scratch_slot<R, D>(P, blockIdx.x, j0 == 0 ? 1 : 0));
     t += cnt;
     if (t >= span.t1) break;
     unit_begin = t;
-    next_unit<R, kStreamKeys>(P, &u);
+    next_unit<R, kStreamKeys, kTree>(P, &u);
   }
   wait_for_earlier_grids();  // this grid's end stands for theirs
 }

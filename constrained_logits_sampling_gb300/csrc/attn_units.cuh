@@ -7,6 +7,10 @@
 // CTA, whatever the sequences' lengths: a unit that lies in one span is finished there, one
 // that a span boundary cuts leaves partial sums in the handle's scratch, which a last launch
 // joins in key order (attn_join.cuh).  Nothing waits for another CTA.
+//
+// With kTree the rows see the sequence's new tokens by mask instead of by position
+// (clsample_tree_attention): every unit of a sequence then has the same keys, and only the tiles
+// from the first new token on look at masks.
 #pragma once
 
 #include "paged.cuh"
@@ -33,6 +37,7 @@ struct AttnParams {
   long long wait_cycles;  // that a wait may take
   int stall;        // where a wait of the chunk kernel is in vain, for tests; 0: nowhere
   float scale_log2; // scale * log2(e)
+  clsample_tree_mask_t tree;  // with kTree
 };
 
 // A packed row's token and its head among those of the key head.
@@ -55,12 +60,35 @@ struct Unit {
   int tile0, tiles;   // key tiles, at least one
 };
 
-template <int R, int K>
+// Bits lo .. hi of a word, of which only 0 .. 31 exist.
+__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
+  const uint32_t upto = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1;
+  return lo <= 0 ? upto : lo > 31 ? 0u : upto & (~0u << lo);
+}
+
+// kTree: the words of row t, and which of the n new tokens (0 where the sequence has no keys) j0 ..
+// j0 + 31 a row sees; j0 may be negative, and tokens that there are not are not seen.
+__device__ __forceinline__ const uint32_t* mask_row(const AttnParams& P, int t) {
+  return P.tree.mask + (int64_t)t * P.tree.mask_stride;
+}
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* row, int n, int j0) {
+  const int w = j0 >> 5, words = (n + 31) >> 5;  // (w is rounded down)
+  const uint32_t lo = (unsigned)w < (unsigned)words ? __ldg(row + w) : 0u;
+  const uint32_t hi = (j0 & 31) && (unsigned)(w + 1) < (unsigned)words ? __ldg(row + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, j0 & 31) & column_bits(-j0, n - 1 - j0);
+}
+// Where row t, the sequence's new token i, stands for the window.
+__device__ __forceinline__ int tree_position(const AttnParams& P, int t, int i, int len, int n) {
+  return P.tree.positions ? min(max(__ldg(P.tree.positions + t), len - n), len - 1) : len - n + i;
+}
+
+template <int R, int K, bool kTree = false>
 struct UnitMap {
   static __device__ __forceinline__ Seq seq_of(const AttnParams& P, int b) {
     Seq s = load_seq(P.a.cu_new, P.a.kv_lens, b, P.a.T, P.capacity, P.a.max_new);
     const int64_t rows = (int64_t)s.n * P.g;
     if (rows < P.min_rows || rows >= P.max_rows) s.n = 0;  // another launch's
+    if (kTree && s.len < s.n) s.len = 0;  // no keys
     return s;
   }
   static __device__ __forceinline__ int row_tiles(const AttnParams& P, const Seq& s) {
@@ -74,6 +102,13 @@ struct UnitMap {
     u->qt = qt;
     u->row0 = qt * R;
     u->rows = min(R, s.n * P.g - u->row0);
+    if constexpr (kTree) {  // a row's window ends at the first new token or later
+      u->key_hi = s.len;
+      u->key_lo = P.a.window > 0 ? max(0, s.len - s.n - P.a.window + 1) : 0;
+      u->tile0 = u->key_lo / K;
+      u->tiles = max(1, (u->key_hi + K - 1) / K - u->tile0);
+      return;
+    }
     const int first = s.len - s.n + token_of(P, u->row0);  // positions of the first and last row
     const int last = s.len - s.n + token_of(P, u->row0 + u->rows - 1);
     u->key_hi = max(0, min(last + 1, s.len));
@@ -131,9 +166,9 @@ __device__ __forceinline__ int64_t span_begin(int64_t total, int ctas, int c) {
   return each * c + (uint32_t)((int)(total - each * ctas) * c) / (uint32_t)ctas;
 }
 
-template <int R, int K, int NT>
+template <int R, int K, int NT, bool kTree = false>
 __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit* u, int64_t* unit_begin) {
-  using M = UnitMap<R, K>;
+  using M = UnitMap<R, K, kTree>;
   __shared__ int64_t buf[NT / 32 + 1];
   __shared__ Unit found;
   __shared__ int64_t found_begin;
@@ -185,9 +220,9 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
 }
 
 // The unit after u (the caller has checked that the span goes on).
-template <int R, int K>
+template <int R, int K, bool kTree = false>
 __device__ __forceinline__ void next_unit(const AttnParams& P, Unit* u) {
-  using M = UnitMap<R, K>;
+  using M = UnitMap<R, K, kTree>;
   Seq s{u->q0, u->n, u->len, true};
   if (u->row0 + R < u->n * P.g) {
     M::fill(P, s, u->qt + 1, u);

@@ -18,10 +18,11 @@ constexpr int kMaxHeads = 256;   // Hq + 2 Hkv of the fast path
 struct AppendParams {
   clsample_kv_append_args_t a;
   int tokens;  // of a block of the fast path
+  const int32_t* positions;  // that tokens are rotated by; null: their places in the sequence
 };
 
 struct Token {
-  int b, pos, page, slot;
+  int b, turn, page, slot;  // turn: the position that it is rotated by
   bool ok;  // in a sequence, at a position with a cos/sin row and a valid page
 };
 
@@ -29,7 +30,8 @@ struct Token {
 // position, page and slot, by one warp: a 32-way search of the offsets, whose last step reads
 // the lengths along.  b is -1 when no sequence owns the row.  Offsets out of order can only
 // give a wrong owner or none: what is found is checked against them.
-__device__ __forceinline__ Token find_token(const clsample_kv_append_args_t& a, int t) {
+__device__ __forceinline__ Token find_token(const AppendParams& P, int t) {
+  const clsample_kv_append_args_t& a = P.a;
   const int lane = threadIdx.x & 31;
   Token k{-1, 0, 0, 0, false};
   int lo = 0, hi = a.B;  // the owner is in [lo, hi)
@@ -57,25 +59,32 @@ __device__ __forceinline__ Token find_token(const clsample_kv_append_args_t& a, 
   if (from < 0 || to > a.T || t < from || t >= to) return k;
   k.b = lo + src;
   if (len < 0 || len > capacity_of(a.max_pages, a.page_size)) return k;
-  k.pos = len - (to - from) + (t - from);
-  if (k.pos < 0 || (a.rot_dim > 0 && k.pos >= a.max_pos)) return k;
-  k.page = __ldg(a.page_table + (int64_t)k.b * a.table_stride + k.pos / a.page_size);
-  k.slot = k.pos % a.page_size;
+  const int pos = len - (to - from) + (t - from);
+  if (pos < 0) return k;
+  k.turn = P.positions ? __ldg(P.positions + t) : pos;
+  if (a.rot_dim > 0 && (k.turn < 0 || k.turn >= a.max_pos)) return k;
+  k.page = __ldg(a.page_table + (int64_t)k.b * a.table_stride + pos / a.page_size);
+  k.slot = pos % a.page_size;
   k.ok = k.page >= 0 && k.page < a.num_pages;
   return k;
 }
 
 // Statuses, one thread per sequence: the same checks as find_token for each of its tokens'
 // pages.  Runs in the first blocks of the launch, after their token.
-__device__ __forceinline__ void write_status(const clsample_kv_append_args_t& a, int b) {
+__device__ __forceinline__ void write_status(const AppendParams& P, int b) {
+  const clsample_kv_append_args_t& a = P.a;
   const int cap = capacity_of(a.max_pages, a.page_size);
   const Seq s = load_seq(a.cu_new, a.kv_lens, b, a.T, cap, a.T);
   bool ok = s.ok;
   if (ok && s.n > 0) {
     const int first = s.len - s.n;
-    if (first < 0 || (a.rot_dim > 0 && s.len > a.max_pos)) {
+    if (first < 0 || (a.rot_dim > 0 && !P.positions && s.len > a.max_pos)) {
       ok = false;
     } else {
+      for (int i = 0; ok && a.rot_dim > 0 && P.positions && i < s.n; ++i) {
+        const int at = __ldg(P.positions + s.q0 + i);
+        ok = at >= 0 && at < a.max_pos;
+      }
       for (int p = first / a.page_size; ok && p <= (s.len - 1) / a.page_size; ++p) {
         const int id = __ldg(a.page_table + (int64_t)b * a.table_stride + p);
         ok = id >= 0 && id < a.num_pages;
@@ -96,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) append_any_kernel(const __grid_const
   const int heads = a.Hq + 2 * a.Hkv;
   if ((int)blockIdx.x < a.T) {
     const int t = blockIdx.x;
-    const Token k = find_token(a, t);
+    const Token k = find_token(P, t);
     for (int r = warp; r < heads && k.b >= 0; r += kThreads / 32) {
       const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.Hkv;
       const int h = is_q ? r : is_v ? r - a.Hq - a.Hkv : r - a.Hq;
@@ -130,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) append_any_kernel(const __grid_const
       }
       __syncwarp();
       const int half = a.rot_dim / 2;
-      const float* cs = a.cos_sin + (int64_t)k.pos * a.cs_stride;
+      const float* cs = a.cos_sin + (int64_t)k.turn * a.cs_stride;
       for (int d = lane; d < D; d += 32) {
         float y = x[d];
         if (d < a.rot_dim) {
@@ -146,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) append_any_kernel(const __grid_const
     }
   }
   if (a.row_status)
-    for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += gridDim.x * kThreads) write_status(a, b);
+    for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += gridDim.x * kThreads) write_status(P, b);
 }
 
 // Where a head row comes from and goes to, for the block's first token.
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __
   };
   if (count > 0) fetch(0, 0);
   for (int i = warp; i < count; i += kThreads / 32) {
-    const Token k = find_token(a, t0 + i);
+    const Token k = find_token(P, t0 + i);
     if (lane == 0) tokens[i] = k;
   }
   __syncthreads();
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __
     const bool turns = k.ok && l * 8 < a.rot_dim;
     float c[8], s[8];  // cosines; sines, negative for the first elements of pairs
     if (turns) {
-      const float* cs = a.cos_sin + (int64_t)k.pos * a.cs_stride + turn_at;
+      const float* cs = a.cos_sin + (int64_t)k.turn * a.cs_stride + turn_at;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (e == 0 || (!kPaired && !a.interleaved)) {
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __
     }
   }
   if (a.row_status)
-    for (int b = blockIdx.x * kThreads + tid; b < a.B; b += gridDim.x * kThreads) write_status(a, b);
+    for (int b = blockIdx.x * kThreads + tid; b < a.B; b += gridDim.x * kThreads) write_status(P, b);
 }
 
 template <class T>
@@ -359,6 +368,11 @@ void launch_append(AppendParams P, bool fast, int sms, cudaStream_t st) {
 }  // namespace clsample
 
 extern "C" int clsample_kv_append(const clsample_kv_append_args_t* a, clsample_stream_t stream) {
+  return clsample_kv_append_at(a, nullptr, stream);
+}
+
+extern "C" int clsample_kv_append_at(const clsample_kv_append_args_t* a, const int32_t* positions,
+                                     clsample_stream_t stream) {
   using namespace clsample;
   if (!a) return CLSAMPLE_ERR_NULL;
   if (a->B < 0 || a->B > (1 << 24) - 1 || a->T < 0 || a->T > kMaxLen) return CLSAMPLE_ERR_BATCH;
@@ -383,7 +397,7 @@ extern "C" int clsample_kv_append(const clsample_kv_append_args_t* a, clsample_s
                     aligned16(a->q) && aligned16(a->k) && aligned16(a->v) && aligned16(a->q_out) &&
                     aligned16(a->k_cache) && aligned16(a->v_cache) && aligned16(a->q_weight) && aligned16(a->k_weight) &&
                     aligned16(a->cos_sin) && a->cs_stride % 4 == 0;
-  const AppendParams P{*a, 1};
+  const AppendParams P{*a, 1, positions};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a->dtype == CLSAMPLE_T_BF16)
     launch_append<__nv_bfloat16>(P, fast, sms, st);

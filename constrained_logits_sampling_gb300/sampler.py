@@ -49,7 +49,9 @@ EXPORTS = ("clsample_create", "clsample_destroy", "clsample_apply", "clsample_pr
            "clsample_apply_static", "clsample_strerror", "clsample_geometry", "clsample_occupancy",
            "clsample_debug_weights", "clsample_debug_uniforms", "clsample_allowed_to_bitmask",
            "clsample_kv_append", "clsample_attention_create", "clsample_attention_destroy",
-           "clsample_chunk_attention", "clsample_debug_attention_stall", "clsample_verify")
+           "clsample_chunk_attention", "clsample_debug_attention_stall", "clsample_verify", "clsample_tree_plan",
+           "clsample_kv_append_at", "clsample_tree_attention", "clsample_verify_tree", "clsample_keep_path",
+           "clsample_copy_pages", "clsample_pages_fork", "clsample_pages_reserve", "clsample_pages_trim")
 
 
 def load_library(path: str = LIB_PATH):
@@ -85,8 +87,17 @@ def load_library(path: str = LIB_PATH):
                                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
                                                       ctypes.c_void_p]
             L.clsample_allowed_to_bitmask.restype = ctypes.c_int
-            for name in ("clsample_kv_append", "clsample_verify"):
+            for name in ("clsample_kv_append", "clsample_verify", "clsample_tree_plan", "clsample_verify_tree",
+                         "clsample_keep_path", "clsample_copy_pages"):
                 getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+                getattr(L, name).restype = ctypes.c_int
+            L.clsample_kv_append_at.argtypes = [ctypes.c_void_p] * 3
+            L.clsample_tree_attention.argtypes = [ctypes.c_void_p] * 4
+            L.clsample_pages_fork.argtypes = [ctypes.c_void_p] * 4 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
+            L.clsample_pages_reserve.argtypes = [ctypes.c_void_p] * 7
+            L.clsample_pages_trim.argtypes = [ctypes.c_void_p] * 4
+            for name in ("clsample_kv_append_at", "clsample_tree_attention", "clsample_pages_fork",
+                         "clsample_pages_reserve", "clsample_pages_trim"):
                 getattr(L, name).restype = ctypes.c_int
             L.clsample_attention_create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
             L.clsample_attention_create.restype = ctypes.c_int

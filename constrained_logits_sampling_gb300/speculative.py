@@ -158,11 +158,14 @@ class KVAppend:
                   cos_sin: Optional[torch.Tensor] = None, rot_dim: Optional[int] = None, interleaved: bool = False,
                   q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
                   eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
-                  row_status: Optional[torch.Tensor] = None) -> KVAppendArgs:
+                  row_status: Optional[torch.Tensor] = None,
+                  positions: Optional[torch.Tensor] = None) -> KVAppendArgs:
         """q [T, Hq, D], k and v [T, Hkv, D]; caches [pages, page_size, Hkv, D] (any strides, so
         a transposed view of another layout will do); page_table int32 [B, max_pages], cu_new
         int32 [B + 1], kv_lens int32 [B] with the new tokens.  ``cos_sin`` float32 [positions,
-        rot_dim], cosines then sines; None: no rotation.  ``q_out`` None: q in place."""
+        rot_dim], cosines then sines; None: no rotation.  ``q_out`` None: q in place.  ``positions``
+        int32 [T]: what each token is rotated by, where that is not its place in the sequence (a tree of
+        drafted tokens, ``tree.TreePlan``)."""
         dev, dt = self.device, k.dtype
         a = KVAppendArgs()
         a.dtype = _type_of(k)
@@ -191,14 +194,19 @@ class KVAppend:
         a.q_weight = _dptr(q_weight, dt, a.D, "q_weight", dev)
         a.k_weight = _dptr(k_weight, dt, a.D, "k_weight", dev)
         a.row_status = _dptr(row_status, torch.int32, a.B, "row_status", dev)
+        a.positions = _dptr(positions, torch.int32, a.T, "positions", dev)
         a.keep = (q, k, v, k_cache, v_cache, page_table, cu_new, kv_lens, cos_sin, q_weight, k_weight, q_out,
-                  row_status)
+                  row_status, positions)
         return a
 
     def apply(self, args: KVAppendArgs, stream: Optional[torch.cuda.Stream] = None):
         """Enqueue one call on ``stream`` (default: current)."""
         _current(self.device)
-        _check(self._L.clsample_kv_append(ctypes.byref(args), _stream_ptr(stream)))
+        positions = getattr(args, "positions", None)
+        if positions is None:
+            _check(self._L.clsample_kv_append(ctypes.byref(args), _stream_ptr(stream)))
+        else:
+            _check(self._L.clsample_kv_append_at(ctypes.byref(args), positions, _stream_ptr(stream)))
 
     def __call__(self, q, k, v, k_cache, v_cache, page_table, cu_new, kv_lens, *, stream=None,
                  **kw) -> Dict[str, torch.Tensor]:

@@ -485,6 +485,242 @@ typedef struct {
  * the arrays are the current device's. */
 int clsample_verify(const clsample_verify_args_t* args, clsample_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * A step whose drafted tokens form a tree.  Request b drafted n_b = cu_draft[b + 1] -
+ * cu_draft[b] tokens (cu_draft int32[B + 1], within [0, N]); drafted token i (0 .. n_b - 1)
+ * continues token parents[cu_draft[b] + i]: -1 is the request's last accepted token, the root, and
+ * any other parent is a drafted token before it (< i).  The step's rows are, for each request, the
+ * root and then its drafted tokens: row cu_draft[b] + b is the root's, row cu_draft[b] + b + 1 + i
+ * that of drafted token i, N + B rows in all.
+ *
+ * clsample_tree_plan says what each row may see and where it stands; clsample_kv_append_at writes
+ * keys and values, each to the slot of its row (old_b + its place among the request's rows, old_b
+ * cached tokens before), rotated by its position in the text (old_b + its depth);
+ * clsample_tree_attention attends; clsample_verify_tree accepts a path; clsample_keep_path moves
+ * the path's keys and values together, behind the root's, and gives the new lengths. */
+
+/* Arguments of clsample_tree_plan.  kv_lens[b] counts the request's rows (old_b + n_b + 1).
+ *   mask       u32[N + B, mask_stride] output: bit j of a row's words (bit j & 31 of word j >> 5) is
+ *              set for the row itself and for the rows that it continues (j: place among the
+ *              request's rows), of those only the nearest `window` when window > 0.  The first
+ *              ceil((max_draft + 1) / 32) words of a row are written.
+ *   positions  i32[N + B] output or NULL: old_b + the row's depth (the root's is 0).
+ *   cu_new     i32[B + 1] output or NULL: cu_draft[b] + b, the rows' offsets.
+ *   row_status i32[B] output or NULL.  INVALID: offsets out of order or range (its rows are not
+ *              written), n_b > max_draft, a parent outside [-1, i), kv_lens[b] <= n_b or above 2^30
+ *              (mask and positions of its rows are 0).
+ * Limits: max_draft <= 1023. */
+typedef struct {
+  int32_t B, N, max_draft, window;
+  const int32_t* parents;
+  const int32_t* cu_draft;
+  const int32_t* kv_lens;
+  uint32_t* mask;
+  int64_t mask_stride;
+  int32_t* positions;
+  int32_t* cu_new;
+  int32_t* row_status;
+} clsample_tree_plan_args_t;
+
+/* Enqueues one plan on `stream` (one launch); nothing when B == 0.  No handle, no scratch. */
+int clsample_tree_plan(const clsample_tree_plan_args_t* args, clsample_stream_t stream);
+
+/* clsample_kv_append with the positions that tokens are rotated by: positions i32[T] (NULL: the
+ * same call).  Slots stay those of the tokens' rows.  A token whose positions[t] is negative or not
+ * below max_pos (with rotation) is not written and its sequence is INVALID. */
+int clsample_kv_append_at(const clsample_kv_append_args_t* args, const int32_t* positions, clsample_stream_t stream);
+
+/* What the rows of clsample_tree_attention see of the step's own tokens.
+ *   mask       u32[T, mask_stride]: row cu_new[b] + i sees the sequence's new token j if bit j of its
+ *              words is set (any mask, a row's own bit too; bits from n_b on are not looked at).
+ *              mask_stride >= ceil(max_new / 32).
+ *   positions  i32[T] or NULL (each row's place: kv_lens[b] - n_b + i), for the window alone. */
+typedef struct {
+  const uint32_t* mask;
+  int64_t mask_stride;
+  const int32_t* positions;
+} clsample_tree_mask_t;
+
+/* clsample_chunk_attention, except for what a row sees: of the cached tokens (positions below
+ * kv_lens[b] - n_b) all, or with window > 0 those above positions[row] - window; of the new ones
+ * those in its mask.  A row that sees nothing gets out 0 and lse -inf.  kv_lens[b] < n_b, or a
+ * position outside [kv_lens[b] - n_b, kv_lens[b]), makes the sequence INVALID.
+ * Slots of new tokens that no row sees may hold anything, as may those below kv_lens[b] - n_b -
+ * window + 1 with a window; the pages of all others have to be valid. */
+int clsample_tree_attention(clsample_attention_t* handle, const clsample_attention_args_t* args,
+                            const clsample_tree_mask_t* tree, clsample_stream_t stream);
+
+/* Arguments of clsample_verify_tree.  Drafted tokens are looked at in order, from the root: token
+ * i is tried if its parent is the last accepted token (the root at first).  With p the target's row
+ * of that parent, P = floor(p 2^40), q the draft's row that the token was drawn from, x its id, u =
+ * u_accept[cu_draft[b] + i], and in float32 s = 1 and c = 0 when a token is first accepted:
+ *   With a draft:    accepted if u (q(x) s) < p(x) for a parent's first child, and for a later one if
+ *                    u (q(x) s) < R(x) / 2^40, R(t) = max(P(t) - floor((q(t) c) 2^40), 0).  After a
+ *                    refusal c <- c + s, and s <- min(sum_t R(t) / 2^40, 1) with the new c.
+ *   Without (NULL):  the draft is certain of its tokens.  Accepted if u s < p(x) and no refused child of
+ *                    the same parent has the same id.  After a refusal s <- max(2^40 - sum of P over the
+ *                    ids of refused children, 0) / 2^40.
+ * (Products in parentheses, sums and quotients that leave s and c are rounded to float32; all
+ * else is exact.)  After the last accepted token one more is drawn with u_sample[b], from the weights
+ * R of its refused children (without a draft: P except at their ids), or from P if there are none or
+ * the weights are all 0; as clsample_verify draws, by floor(floor(u 2^31) W / 2^31).
+ * Of a request whose tokens have one child each the results are those of clsample_verify.  The kept
+ * tokens are distributed as the target's own: children drawn independently from q are refused with
+ * what q covered of p taken away, and a certain child is accepted with p(x) of what is left.
+ *
+ * target            [N + B, V] probabilities by row, as in clsample_verify.
+ * draft             [draft_rows_count, V] of the same type, or NULL.  Token i was drawn from row
+ *                   draft_rows[cu_draft[b] + i] (i32[N]; NULL: row cu_draft[b] + i).  Children of one
+ *                   parent must have the same row, unless there is one child only.
+ * tokens            i32[B, token_stride] output, token_stride > max_path: accepted tokens, the drawn
+ *                   one, then -1 up to place max_path.
+ * path              i32[B, path_stride] output or NULL, path_stride >= max_path: the accepted tokens'
+ *                   numbers i, then -1.
+ * max_path          after so many accepted tokens no more are tried.
+ * accepted          i32[B] output or NULL.
+ * row_status        i32[B] output or NULL.  INVALID as in clsample_verify (of all drafted tokens'
+ *                   probabilities, and those of rows that are summed), and for n_b > max_draft, a parent
+ *                   outside [-1, i), a draft row outside [0, draft_rows_count) or siblings' that differ.
+ * Limits: 0 < V <= 262144, max_draft <= 1023, 0 <= max_path <= max_draft. */
+typedef struct {
+  int32_t B, N, V;
+  int32_t dtype;
+  int32_t max_draft, max_path, draft_rows_count, reserved0;
+  const void* target;
+  int64_t target_stride;
+  const void* draft;
+  int64_t draft_stride;
+  const int32_t* draft_rows;
+  const int32_t* draft_tokens;
+  const int32_t* parents;
+  const int32_t* cu_draft;
+  const float* u_accept;
+  const float* u_sample;
+  int32_t* tokens;
+  int64_t token_stride;
+  int32_t* path;
+  int64_t path_stride;
+  int32_t* accepted;
+  int32_t* row_status;
+} clsample_verify_tree_args_t;
+
+/* Enqueues one verification on `stream` (one launch); nothing when B == 0.  No handle, no scratch. */
+int clsample_verify_tree(const clsample_verify_tree_args_t* args, clsample_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Pages of a cache.  The cache is that of the other operators, of `layers` layers with the same page
+ * table: layer l's arrays start l * layer_stride elements after the first's. */
+
+/* Arguments of clsample_keep_path: kv_lens[b] counts the root and n_b drafted tokens (as in the
+ * tree's step), so the root is at position r = kv_lens[b] - n_b - 1 and drafted token i at r + 1 + i.
+ * For i = 0 .. accepted[b] - 1 keys and values of position r + 1 + path[b, i] are moved to r + 1 + i,
+ * bit for bit, in all layers, and new_lens[b] = r + 1 + accepted[b].
+ *
+ * path              i32[B, path_stride], accepted i32[B]: as clsample_verify_tree leaves them; numbers
+ *                   of a path are increasing.
+ * new_lens          i32[B] output; not kv_lens itself.
+ * row_status        i32[B] output or NULL.  INVALID (nothing is moved, new_lens[b] = kv_lens[b]):
+ *                   offsets out of order or range, kv_lens[b] <= n_b or past the table, accepted[b]
+ *                   outside [0, min(n_b, max_path)], a path that does not increase within [0, n_b), or
+ *                   an invalid page among those that are moved between.
+ * The moved positions' slots must be the sequence's own.  Any strides and D up to 256; pieces of 16
+ * bytes are moved where addresses, strides and D allow it.
+ * Limits: max_path <= 1023. */
+typedef struct {
+  int32_t B, N, layers, Hkv, D;
+  int32_t dtype;
+  int32_t num_pages, page_size, max_pages, max_path;
+  void* k_cache;
+  void* v_cache;
+  int64_t layer_stride, page_stride, slot_stride, head_stride;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* cu_draft;
+  const int32_t* kv_lens;
+  const int32_t* path;
+  int64_t path_stride;
+  const int32_t* accepted;
+  int32_t* new_lens;
+  int32_t* row_status;
+} clsample_keep_path_args_t;
+
+/* Enqueues one call on `stream` (one launch); nothing when B == 0.  No handle, no scratch. */
+int clsample_keep_path(const clsample_keep_path_args_t* args, clsample_stream_t stream);
+
+/* Arguments of clsample_copy_pages: copies i32[n, 3], each (from, to, slots): the first `slots`
+ * slots of page `from` go to page `to`, keys and values of all layers.  A copy with from < 0 or slots
+ * 0 is none.  status i32[n] output or NULL: INVALID (nothing is copied) for a page outside
+ * [0, num_pages) or slots outside [0, page_size].  No page may be written by two copies, nor written by
+ * one and read by another.  Limits and strides as for clsample_keep_path. */
+typedef struct {
+  int32_t n, layers, Hkv, D;
+  int32_t dtype;
+  int32_t num_pages, page_size, reserved0;
+  void* k_cache;
+  void* v_cache;
+  int64_t layer_stride, page_stride, slot_stride, head_stride;
+  const int32_t* copies;
+  int32_t* status;
+} clsample_copy_pages_args_t;
+
+/* Enqueues the copies on `stream` (one launch); nothing when n == 0. */
+int clsample_copy_pages(const clsample_copy_pages_args_t* args, clsample_stream_t stream);
+
+/* A pool of pages that sequences may share, all of it on the device.  A batch of B sequences has
+ * page_table i32[B, table_stride], held i32[B] (the first held[b] entries of a row are pages that the
+ * sequence holds) and kv_lens i32[B].  A page is free when no sequence holds it.
+ *   refs       i32[num_pages]: how many sequences hold a page.
+ *   free_bits  u32[ceil(num_pages / 32)]: bit p & 31 of word p >> 5 is set where refs[p] is 0.
+ *   stamps     u64[num_pages], epoch u32[1], list i32[num_pages]: working room; stamps and epoch start
+ *              as 0 and belong to the pool.
+ * Calls on one pool have to be ordered; results do not depend on timing. */
+typedef struct {
+  int32_t num_pages, page_size;
+  int32_t* refs;
+  uint32_t* free_bits;
+  uint64_t* stamps;
+  uint32_t* epoch;
+  int32_t* list;
+} clsample_page_pool_t;
+
+typedef struct {
+  int32_t B, max_pages;
+  int32_t* page_table;
+  int64_t table_stride;
+  int32_t* held;
+  int32_t* kv_lens;
+} clsample_page_batch_t;
+
+/* Fork: for each pair i < n sequence dst[i] becomes one that shares the pages of sequence src[i] up to
+ * its length: row, held and length are set, references counted.  status i32[n] output or NULL.  INVALID
+ * (nothing is done for the pair): a sequence outside [0, B), held[dst] != 0, two pairs with the same dst,
+ * a dst that is a src of the call, a length of src that its held pages do not cover, or a page of it that
+ * is invalid or that nobody holds. */
+int clsample_pages_fork(const clsample_page_pool_t* pool, const clsample_page_batch_t* batch, const int32_t* src,
+                        const int32_t* dst, int32_t n, int32_t* status, clsample_stream_t stream);
+
+/* Reserve: sequence b is to write positions kv_lens[b] .. kv_lens[b] + new_tokens[b] - 1.  It gets
+ * the pages that it lacks for them, and a page of its own in place of each that it would write to and
+ * that others hold too; the last sequence of a call (in order) that would write to a page keeps it if
+ * nobody else holds it.  Free pages are given out from the lowest number on, in order of the sequences and
+ * of their positions.  copies i32[B, 3] output: for clsample_copy_pages, the written page with tokens
+ * before kv_lens[b] that was replaced: (old, new, kv_lens[b] % page_size), or (-1, -1, 0).
+ * row_status i32[B] output or NULL, free_pages i32[1] output or NULL (how many are free after the call).
+ * INVALID (and nothing done for the sequence): new_tokens[b] or kv_lens[b] negative, their sum past the
+ * table, held[b] out of range or less than the length needs, a page to write to that is invalid or that
+ * nobody holds.  If there are not enough free pages for all, nothing is done at all: every sequence that
+ * needs a page is OVERFLOW.  kv_lens is not changed. */
+int clsample_pages_reserve(const clsample_page_pool_t* pool, const clsample_page_batch_t* batch,
+                           const int32_t* new_tokens, int32_t* copies, int32_t* row_status, int32_t* free_pages,
+                           clsample_stream_t stream);
+
+/* Trim: the pages that sequence b holds beyond what kv_lens[b] needs go back (all, with length 0):
+ * their entries of the row become -1.  row_status i32[B] output or NULL.  INVALID: a length out of range or
+ * more than the held pages cover, held[b] out of range (nothing is done), or a page that is invalid or
+ * that nobody holds (it is dropped from the row alone). */
+int clsample_pages_trim(const clsample_page_pool_t* pool, const clsample_page_batch_t* batch, int32_t* row_status,
+                        clsample_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
