@@ -107,16 +107,16 @@ struct ChunkShared {
 __device__ __forceinline__ uint4 seen_by_any(const AttnParams& P, const Unit& u, int kb) {
   const int lane = threadIdx.x & 31, j0 = kb - (u.len - u.n);
   const int last = token_of(P, u.row0 + u.rows - 1);
-  uint32_t w[4] = {0, 0, 0, 0};
+  uint4 any = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
   for (int i = token_of(P, u.row0) + lane; i <= last; i += 32) {
-    const uint32_t* row = mask_row(P, u.q0 + i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] |= mask_word(row, min(u.n, u.len), j0 + 32 * k);
+    const uint4 w = mask_words(mask_row(P, u.q0 + i), min(u.n, u.len), j0);
+    any = make_uint4(any.x | w.x, any.y | w.y, any.z | w.z, any.w | w.w);
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = __reduce_or_sync(~0u, w[k]) | column_bits(0, -j0 - 1 - 32 * k);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(__reduce_or_sync(~0u, any.x) | column_bits(0, -j0 - 1),
+                    __reduce_or_sync(~0u, any.y) | column_bits(0, -j0 - 33),
+                    __reduce_or_sync(~0u, any.z) | column_bits(0, -j0 - 65),
+                    __reduce_or_sync(~0u, any.w) | column_bits(0, -j0 - 97));
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int k) {
   return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     attn_chunk_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
   using Shape = ChunkShape<D>;
+  using Map = UnitMap<kChunkRows, kChunkKeys, kTree>;
   constexpr int NS = Shape::kKeySlots, NV = Shape::kValueSlots, kTile = Shape::kTile, KC = D / 8;
   constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 elements
   constexpr int kRowWarps = kTma ? 1 : 2;  // that copy rows
@@ -237,6 +238,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int pos_last = first_pos + token_of(P, u.row0 + min(u.rows, half0 + 128) - 1);
         for (int j = jw; j < cnt; j += step) {
           const int kb = kb0 + j * kChunkKeys;
+          // kTree: what the row sees of the tile, while the scores are on their way
+          const bool cached = kTree && kb + 127 < first_pos && (a.window <= 0 || kb > u.len - 1 - a.window);
+          uint4 seen = make_uint4(0, 0, 0, 0);
+          if (kTree && !cached && live) {
+            const int i = token_of(P, u.row0 + r);
+            const int hi = first_pos - 1 - kb;
+            const int lo = a.window > 0 ? tree_position(P, u.q0 + i, i, u.len, u.n) - a.window + 1 - kb : 0;
+            if (kb + 127 >= first_pos) seen = mask_words(mask_row(P, u.q0 + i), min(u.n, u.len), kb - first_pos);
+            seen = make_uint4(seen.x | column_bits(lo, hi), seen.y | column_bits(lo - 32, hi - 32),
+                              seen.z | column_bits(lo - 64, hi - 64), seen.w | column_bits(lo - 96, hi - 96));
+          }
           bounded_wait(&sh.s_full[w], s_phase, &sh.limit);
           if (lane == 0) {
             if ((warp & 3) == 0 && (split || w == 1)) mbar_arrive(&sh.tile_done[(tile + j) % (2 * NS)]);
@@ -246,33 +258,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           tc_fence_after();
           const uint32_t* ok = sh.key_ok[(tile + j) % (2 * NS)];
           const uint4 bits = *reinterpret_cast<const uint4*>(ok);
-          // kTree: only cached keys, and nobody stands behind the last slot
           const bool whole = (bits.x & bits.y & bits.z & bits.w) == ~0u &&
-                             (kTree ? kb + 127 < first_pos && (a.window <= 0 || kb > u.len - 1 - a.window)
+                             (kTree ? cached
                                     : kb + 127 <= pos_first && (a.window <= 0 || kb > pos_last - a.window));
           uint32_t x[128];
           tmem_ld(x, s_tmem);
           if (!whole) {
-            int hi = pos - kb;  // columns lo .. hi are seen
-            int lo = a.window > 0 ? hi - a.window + 1 : 0;
-            uint32_t shown[4];
-            if constexpr (kTree) {
-              const int i = token_of(P, u.row0 + (live ? r : 0));
-              hi = first_pos - 1 - kb;
-              lo = a.window > 0 ? tree_position(P, u.q0 + i, i, u.len, u.n) - a.window + 1 - kb : 0;
-              const uint32_t* row = mask_row(P, u.q0 + i);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                shown[k] = column_bits(lo - 32 * k, hi - 32 * k);
-                if (kb + 127 >= first_pos) shown[k] |= mask_word(row, min(u.n, u.len), kb - first_pos + 32 * k);
-                shown[k] = live ? shown[k] & word_of(bits, k) : 0u;
-              }
-            } else {
-              shown[0] = bits.x & column_bits(lo, hi);
-              shown[1] = bits.y & column_bits(lo - 32, hi - 32);
-              shown[2] = bits.z & column_bits(lo - 64, hi - 64);
-              shown[3] = bits.w & column_bits(lo - 96, hi - 96);
-            }
+            const int hi = pos - kb;  // columns lo .. hi are seen
+            const int lo = a.window > 0 ? hi - a.window + 1 : 0;
+            const uint32_t all = kTree && cached && live ? ~0u : 0u;  // (a page of the tile is not valid)
+            const uint32_t shown[4] = {bits.x & (kTree ? seen.x | all : column_bits(lo, hi)),
+                                       bits.y & (kTree ? seen.y | all : column_bits(lo - 32, hi - 32)),
+                                       bits.z & (kTree ? seen.z | all : column_bits(lo - 64, hi - 64)),
+                                       bits.w & (kTree ? seen.w | all : column_bits(lo - 96, hi - 96))};
 #pragma unroll
             for (int c = 0; c < 128; ++c)
               if (!(shown[c >> 5] & (1u << (c & 31)))) x[c] = 0xff800000u;
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       tc_fence_before();  // O has been read: the next unit's products may overwrite it
       tile += cnt;
-      const bool last = sh.unit_begin[seg & 1] + u.tiles >= sh.span.t1;
+      const bool last = sh.unit_begin[seg & 1] + u.tiles + Map::kPad >= sh.span.t1;
       if (last && tid == 0) {
         note_cut(P, sh.span, u, sh.unit_begin[seg & 1]);
         noted = true;
@@ -465,7 +463,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // ------------------------------------------------------------------ loads
     const int lw = kTma ? 0 : warp - 8;  // of the warps that copy rows
     bool met = false;                    // the last unit's halves met in the second row tile's room
-    const int tiles = (int)(span.t1 - span.t0);
     // 32 rows to rows r0.. of a tile; lane i has the place of row i, bit i of `live` tells
     // whether it is read or zero
     auto copy_rows = [&](const T* src, int64_t off, unsigned live, uint32_t dst, int r0) {
@@ -550,8 +547,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int box = min(a.page_size, kChunkKeys), boxes = kChunkKeys / box;
       uint32_t it = 0;
       while (true) {
-        const int j0 = (int)(t - unit_begin);
-        const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+        const int j0 = tile_in_unit(t, unit_begin), cnt = tiles_here(span, u, unit_begin, t);
         const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
         auto page_of = [&](int j) {  // num_pages, which is out of bounds: zeros
           const int key = (u.tile0 + j0 + j) * kChunkKeys + lane * box;
@@ -593,16 +589,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int x = 0; x < D / 64; ++x)
               tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h, from, full);
         }
-        t += cnt;
-        if (t >= span.t1 || __any_sync(~0u, sh.limit.dead)) break;
-        unit_begin = t;
-        next_unit<kChunkRows, kChunkKeys, kTree>(P, &u);
+        if (!advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
       }
     } else if (kTma) {
       uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
       while (true) {
-        const int j0 = (int)(t - unit_begin);
-        const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+        const int j0 = tile_in_unit(t, unit_begin), cnt = tiles_here(span, u, unit_begin, t);
         if (!copy_queries(seg)) break;
         for (int j = 0; j < cnt; ++j) {
           const int tile = u.tile0 + j0 + j;
@@ -612,17 +604,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int i = 0; i < NV; ++i)
             if (i == st) parity = edges[i]++ & 1;
+          const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
+          uint4 keep = make_uint4(~0u, ~0u, ~0u, ~0u);
+          if (kTree) keep = seen_by_any(P, u, tile * kChunkKeys);
           bounded_wait(&sh.v_landed[st], parity, &sh.limit);
           const bool dead = sh.limit.dead;
           __syncwarp();
-          const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
-          uint4 any;
-          if (kTree) any = seen_by_any(P, u, tile * kChunkKeys);
-          for (int i = lane; i < 128 * KC; i += 32) {  // a row's pieces may lie anywhere in it: all are cleared
-            const int row = i / KC, ch = i % KC;
-            if (row < lo || row >= hi || (kTree && !((word_of(any, row >> 5) >> (row & 31)) & 1)))
-              *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
+          // a row's pieces may lie anywhere in it: all are cleared, of two rows at a time
+          static_assert(KC <= 16, "pieces of a row");
+          const int ch = lane & 15;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t gone = ~(word_of(keep, k) & column_bits(lo - 32 * k, hi - 1 - 32 * k));
+            while (gone) {  // uniform
+              const int r0 = __ffs(gone) - 1;
+              gone &= gone - 1;
+              const int r1 = gone ? __ffs(gone) - 1 : r0;
+              gone &= gone - 1;
+              const int row = 32 * k + (lane < 16 ? r0 : r1);
+              if (ch < KC)
+                *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
           }
           fence_async_proxy();
           __syncwarp();
@@ -630,17 +633,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         it += cnt;
         ++seg;
-        t += cnt;
-        if (t >= span.t1) break;
-        unit_begin = t;
-        next_unit<kChunkRows, kChunkKeys, kTree>(P, &u);
+        if (!advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (warp < 10) {
       uint32_t it = 0, seg = 0;
       while (true) {
-        const int j0 = (int)(t - unit_begin);
-        const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
+        const int j0 = tile_in_unit(t, unit_begin), cnt = tiles_here(span, u, unit_begin, t);
         if (!copy_queries(seg)) break;
         const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
         const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
@@ -691,23 +690,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        t += cnt;
-        if (t >= span.t1) break;
-        unit_begin = t;
-        next_unit<kChunkRows, kChunkKeys, kTree>(P, &u);
+        if (!advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (lane == 0) {
       // The copies are ordinary writes, the products read by the async proxy: the fence between
       // them costs a hundred cycles or so, which the issuing warp has not got.
-      for (int i = 0; i < tiles; ++i) {
-        if (!bounded_wait(&sh.k_landed[i % NS], (i / NS) & 1, &sh.limit)) break;
-        fence_async_proxy();
-        mbar_arrive(&sh.k_full[i % NS]);
-        if (!bounded_wait(&sh.v_landed[i % NV], (i / NV) & 1, &sh.limit)) break;
-        fence_async_proxy();
-        mbar_arrive(&sh.v_full[i % NV]);
-      }
+      uint32_t it = 0;
+      bool alive = true;
+      do {
+        for (const uint32_t end = it + tiles_here(span, u, unit_begin, t); alive && it < end; ++it) {
+          alive = bounded_wait(&sh.k_landed[it % NS], (it / NS) & 1, &sh.limit);
+          if (!alive) break;
+          fence_async_proxy();
+          mbar_arrive(&sh.k_full[it % NS]);
+          alive = bounded_wait(&sh.v_landed[it % NV], (it / NV) & 1, &sh.limit);
+          if (!alive) break;
+          fence_async_proxy();
+          mbar_arrive(&sh.v_full[it % NV]);
+        }
+      } while (alive && advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t));
     }
   } else {
     // ------------------------------------------------------------------ products
@@ -759,8 +761,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         p_phase ^= 1u << w;
       };
       while (true) {
-        const int j0 = (int)(t - unit_begin);
-        const int cnt = (int)uni((uint32_t)min((int64_t)(u.tiles - j0), span.t1 - t));
+        const int cnt = (int)uni((uint32_t)tiles_here(span, u, unit_begin, t));
         const bool split = uni(u.rows <= 128);
         wait(&sh.q_full, seg & 1);
         fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
@@ -805,10 +806,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        t += cnt;
-        if (uni(t >= span.t1)) break;
-        unit_begin = t;
-        next_unit<kChunkRows, kChunkKeys, kTree>(P, &u);
+        if (!uni(advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t))) break;
       }
       // products still running when a wait gave up end before their memory is freed
       if (!alive) {

@@ -320,9 +320,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
 
   int64_t t = span.t0;
   while (true) {
-    const int j0 = (int)(t - unit_begin);
-    const int cnt = (int)min((int64_t)(u.tiles - j0), span.t1 - t);
-    if (tid == 0 && t + cnt >= span.t1) note_cut(P, span, u, unit_begin);
+    const int j0 = tile_in_unit(t, unit_begin), cnt = tiles_here(span, u, unit_begin, t);
+    const bool last = unit_begin + u.tiles + UnitMap<R, kStreamKeys, kTree>::kPad >= span.t1;
+    if (tid == 0 && last) note_cut(P, span, u, unit_begin);
     const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
     const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
     const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
@@ -382,10 +382,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
     __syncthreads();  // the rings are drained: the first is where the warps meet
     stream_finish<T, D, kTree>(P, u, st, reinterpret_cast<float*>(smem), wm, wl, cnt == u.tiles,
                                    scratch_slot<R, D>(P, blockIdx.x, j0 == 0 ? 1 : 0));
-    t += cnt;
-    if (t >= span.t1) break;
-    unit_begin = t;
-    next_unit<R, kStreamKeys, kTree>(P, &u);
+    if (!advance<R, kStreamKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
   }
   wait_for_earlier_grids();  // this grid's end stands for theirs
 }

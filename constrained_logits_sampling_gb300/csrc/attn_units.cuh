@@ -46,6 +46,9 @@ __device__ __forceinline__ int token_of(const AttnParams& P, int row) {
 }
 __device__ __forceinline__ int head_of(const AttnParams& P, int row) { return row - token_of(P, row) * P.g; }
 
+// 64 trees of 24 to 32 rows over 200 to 4000 keys on 8 key heads: PADFIG
+constexpr int kChunkPad = 6, kStreamPad = 3;
+
 struct CutUnit {
   int rows;          // 0: none
   int row0, q0, h;   // as in Unit
@@ -77,13 +80,28 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t* row, int n, int j0
   const uint32_t hi = (j0 & 31) && (unsigned)(w + 1) < (unsigned)words ? __ldg(row + w + 1) : 0u;
   return __funnelshift_r(lo, hi, j0 & 31) & column_bits(-j0, n - 1 - j0);
 }
+// The same for 128 tokens from j0 on.
+__device__ __forceinline__ uint4 mask_words(const uint32_t* row, int n, int j0) {
+  const int w = j0 >> 5, words = (n + 31) >> 5;
+  uint32_t x[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) x[k] = (unsigned)(w + k) < (unsigned)words ? __ldg(row + w + k) : 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    x[k] = __funnelshift_r(x[k], x[k + 1], j0 & 31) & column_bits(-j0 - 32 * k, n - 1 - j0 - 32 * k);
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
 // Where row t, the sequence's new token i, stands for the window.
 __device__ __forceinline__ int tree_position(const AttnParams& P, int t, int i, int len, int n) {
   return P.tree.positions ? min(max(__ldg(P.tree.positions + t), len - n), len - 1) : len - n + i;
 }
 
+// What a unit costs beside its tiles, in tiles, where spans are made of the two (kTree): its end, and
+// the wait for masks and for the next one's first keys.  Sequences of very different lengths would
+// otherwise leave the CTAs with many short units far behind.
 template <int R, int K, bool kTree = false>
 struct UnitMap {
+  static constexpr int kPad = kTree ? (R > 16 ? kChunkPad : kStreamPad) : 0;
   static __device__ __forceinline__ Seq seq_of(const AttnParams& P, int b) {
     Seq s = load_seq(P.a.cu_new, P.a.kv_lens, b, P.a.T, P.capacity, P.a.max_new);
     const int64_t rows = (int64_t)s.n * P.g;
@@ -116,14 +134,14 @@ struct UnitMap {
     u->tile0 = u->key_lo / K;
     u->tiles = max(1, (u->key_hi + K - 1) / K - u->tile0);
   }
-  // key tiles of one key head of a sequence
+  // key tiles of one key head of a sequence, each unit's with kPad behind them
   static __device__ __forceinline__ int64_t head_tiles(const AttnParams& P, const Seq& s) {
     const int m = row_tiles(P, s);
     int64_t t = 0;
     Unit u;
     for (int qt = 0; qt < m; ++qt) {
       fill(P, s, qt, &u);
-      t += u.tiles;
+      t += u.tiles + kPad;
     }
     return t;
   }
@@ -152,8 +170,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* buf, int64_t* 
   return total;
 }
 
-// The whole call's key tiles, and where this CTA's span begins: u is the unit that holds
-// tile t0 = total * cta / ctas, *offset the tile's place in it.  Returns false without work.
+// The whole call's key tiles (with kPad behind each unit's), and where this CTA's span begins: u is
+// the unit that holds tile t0 = total * cta / ctas, or the next one if that lies behind its unit's
+// tiles (t0 is then that one's first).  Returns false without work.
 struct Span {
   int64_t total, t0, t1;
   int ctas;  // CTAs with work: those with the lower indices
@@ -165,6 +184,9 @@ __device__ __forceinline__ int64_t span_begin(int64_t total, int ctas, int c) {
   const int64_t each = quotient(total, ctas);
   return each * c + (uint32_t)((int)(total - each * ctas) * c) / (uint32_t)ctas;
 }
+
+template <int R, int K, bool kTree = false>
+__device__ __forceinline__ void next_unit(const AttnParams& P, Unit* u);
 
 template <int R, int K, int NT, bool kTree = false>
 __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit* u, int64_t* unit_begin) {
@@ -204,8 +226,8 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
       rest -= v.h * per_head;
       for (int qt = 0;; ++qt) {
         M::fill(P, s, qt, &v);
-        if (rest < v.tiles) break;
-        rest -= v.tiles;
+        if (rest < v.tiles + M::kPad) break;
+        rest -= v.tiles + M::kPad;
       }
       found = v;
       found_begin = span->t0 - rest;
@@ -216,11 +238,33 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
   __syncthreads();
   *u = found;
   *unit_begin = found_begin;
+  if (M::kPad > 0 && span->t0 >= found_begin + found.tiles) {  // the span begins behind the unit's tiles
+    *unit_begin += found.tiles + M::kPad;
+    if (*unit_begin >= span->t1) return false;
+    next_unit<R, K, kTree>(P, u);
+    span->t0 = *unit_begin;
+  }
+  return true;
+}
+
+// A CTA's way through its span: `t` tiles in, at unit u.  The place in the unit and how many of its tiles
+// are this CTA's.
+__device__ __forceinline__ int tile_in_unit(int64_t t, int64_t unit_begin) { return (int)(t - unit_begin); }
+__device__ __forceinline__ int tiles_here(const Span& span, const Unit& u, int64_t unit_begin, int64_t t) {
+  return (int)(min(unit_begin + u.tiles, span.t1) - t);
+}
+// On to the next unit; false if the span ends.
+template <int R, int K, bool kTree>
+__device__ __forceinline__ bool advance(const AttnParams& P, const Span& span, Unit* u, int64_t* unit_begin, int64_t* t) {
+  const int64_t next = *unit_begin + u->tiles + UnitMap<R, K, kTree>::kPad;
+  if (next >= span.t1) return false;
+  *t = *unit_begin = next;
+  next_unit<R, K, kTree>(P, u);
   return true;
 }
 
 // The unit after u (the caller has checked that the span goes on).
-template <int R, int K, bool kTree = false>
+template <int R, int K, bool kTree>
 __device__ __forceinline__ void next_unit(const AttnParams& P, Unit* u) {
   using M = UnitMap<R, K, kTree>;
   Seq s{u->q0, u->n, u->len, true};
