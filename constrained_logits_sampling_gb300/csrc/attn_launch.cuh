@@ -94,11 +94,6 @@ bool query_map(const AttnParams& P, CUtensorMap* map) {
   return make_map(P, a.q, dims, strides, box, map);
 }
 
-template <class Kernel>
-cudaError_t allow_smem(Kernel fn, int bytes) {
-  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <class T, int D, bool kTree>
 cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
   // Boxes have to start on the eight rows of the swizzle and fill a tile.  2 x 2048 tokens over
@@ -110,7 +105,8 @@ cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
   P.q_box = boxes && query_map(P, &q_map);
   const int bytes = ChunkShape<D>::kBytes;
   auto* fn = boxes ? attn_chunk_kernel<T, D, true, kTree> : attn_chunk_kernel<T, D, false, kTree>;
-  const cudaError_t e = allow_smem(fn, bytes);
+  static std::atomic<uint64_t> allowed[2];
+  const cudaError_t e = allow_smem_once(fn, bytes, &allowed[boxes]);
   if (e != cudaSuccess) return e;
   fn<<<sms, kChunkThreads, bytes, st>>>(P, k_map, v_map, q_map);
   return cudaGetLastError();
@@ -122,7 +118,8 @@ cudaError_t launch_stream(const AttnParams& P, int sms, bool first, cudaStream_t
   const int grid = sms * kStreamCtas;
   auto* fn = attn_stream_kernel<T, D, kTree>;
   const int bytes = StreamRing<D>::kBytes;
-  const cudaError_t e = allow_smem(fn, bytes);
+  static std::atomic<uint64_t> allowed;
+  const cudaError_t e = allow_smem_once(fn, bytes, &allowed);
   if (e != cudaSuccess) return e;
   if (!first) return launch_after(fn, grid, kStreamThreads, bytes, st, P);
   fn<<<grid, kStreamThreads, bytes, st>>>(P);

@@ -88,7 +88,7 @@ template <int kBytes>
 __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ clsample_copy_pages_args_t a,
                                                               const __grid_constant__ CacheShape c, int parts) {
   using T = typename Piece<kBytes>::T;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;  // pieces of a thread in flight
   const int planes = 2 * a.layers;
   const int i = blockIdx.x / (planes * parts), rest = blockIdx.x % (planes * parts);
   const int plane = rest / parts, part = rest % parts;
@@ -102,21 +102,30 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
   T* at = reinterpret_cast<T*>(plane < a.layers ? a.k_cache : a.v_cache) + layer * c.layer;
   const T* src = at + from * c.page;
   T* dst = at + to * c.page;
-  const int heads = c.per_head * a.Hkv;
-  const int64_t total = (int64_t)slots * heads;
-  for (int64_t e0 = part * kThreads + threadIdx.x; e0 < total; e0 += (int64_t)parts * kThreads * kAhead) {
+  // this thread's place (a slot, and a piece of it), which moves by the same step each time
+  const int heads = c.per_head * a.Hkv, step = parts * kThreads, step_slots = step / heads, step_rest = step % heads;
+  const int first = part * kThreads + threadIdx.x;
+  int slot = first / heads, piece = first % heads;
+  const bool flat = c.head == c.per_head;  // a slot's heads lie side by side
+  while (slot < slots) {
     T x[kAhead];
     int64_t off[kAhead];
+    bool live[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int64_t e = e0 + (int64_t)k * parts * kThreads;
-      const int slot = (int)(e / heads), at_head = (int)(e % heads);
-      off[k] = slot * c.slot + at_head / c.per_head * c.head + at_head % c.per_head;
-      if (e < total) x[k] = src[off[k]];
+      live[k] = slot < slots;
+      off[k] = slot * c.slot + (flat ? piece : piece / c.per_head * c.head + piece % c.per_head);
+      if (live[k]) x[k] = src[off[k]];
+      slot += step_slots;
+      piece += step_rest;
+      if (piece >= heads) {
+        piece -= heads;
+        ++slot;
+      }
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (e0 + (int64_t)k * parts * kThreads < total) dst[off[k]] = x[k];
+      if (live[k]) dst[off[k]] = x[k];
   }
 }
 
@@ -155,14 +164,16 @@ void launch_keep(const clsample_keep_path_args_t& a, cudaStream_t st) {
   keep_path_kernel<kBytes><<<(unsigned)(a.B * parts), kThreads, 0, st>>>(a, c, (int)parts);
 }
 
+// Enough CTAs for the device, but no more than a page's pieces take: most copies of a call may be none.
 template <int kBytes>
-int launch_copy(const clsample_copy_pages_args_t& a, cudaStream_t st) {
+int launch_copy(const clsample_copy_pages_args_t& a, int sms, cudaStream_t st) {
   const CacheShape c = shape_of(a, kBytes);
   const int64_t pieces = (int64_t)a.page_size * a.Hkv * c.per_head, planes = (int64_t)a.n * 2 * a.layers;
   if (planes > 0x7fffffff) return CLSAMPLE_ERR_BATCH;
-  int64_t parts = (pieces + 4 * kThreads - 1) / (4 * kThreads);
-  if (parts > 16) parts = 16;
-  if (parts > 0x7fffffff / planes) parts = 0x7fffffff / planes;
+  const int64_t most = (pieces + 8 * kThreads - 1) / (8 * kThreads);
+  int64_t parts = ((int64_t)sms * 16 + planes - 1) / planes;
+  if (parts > most) parts = most;
+  if (parts > 64) parts = 64;
   copy_pages_kernel<kBytes><<<(unsigned)(planes * parts), kThreads, 0, st>>>(a, c, (int)parts);
   return CLSAMPLE_SUCCESS;
 }
@@ -204,13 +215,14 @@ int clsample_copy_pages(const clsample_copy_pages_args_t* a, clsample_stream_t s
   if (rc != CLSAMPLE_SUCCESS) return rc;
   if (a->n == 0) return CLSAMPLE_SUCCESS;
   if (!a->copies || (a->num_pages > 0 && (!a->k_cache || !a->v_cache))) return CLSAMPLE_ERR_NULL;
-  if ((rc = check_device()) != CLSAMPLE_SUCCESS) return rc;
+  int sms = 0;
+  if ((rc = check_device(nullptr, &sms)) != CLSAMPLE_SUCCESS) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   switch (piece_bytes(*a)) {
-    case 16: rc = launch_copy<16>(*a, st); break;
-    case 8: rc = launch_copy<8>(*a, st); break;
-    case 4: rc = launch_copy<4>(*a, st); break;
-    default: rc = launch_copy<2>(*a, st);
+    case 16: rc = launch_copy<16>(*a, sms, st); break;
+    case 8: rc = launch_copy<8>(*a, sms, st); break;
+    case 4: rc = launch_copy<4>(*a, sms, st); break;
+    default: rc = launch_copy<2>(*a, sms, st);
   }
   if (rc != CLSAMPLE_SUCCESS) return rc;
   return cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;

@@ -6,23 +6,47 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "clsample.h"
 
 namespace clsample {
 
-// Host: success if the current device is an sm_103 part (`sms`: its SM count, if asked).
+// Host: success if the current device is an sm_103 part (`sms`: its SM count, if asked).  What a
+// device is does not change, so it is asked for once.
 inline int check_device(int* dev_out = nullptr, int* sms = nullptr) {
-  int dev = -1, major = 0, minor = 0;
+  constexpr int kDevices = 64, kOther = -1;
+  static std::atomic<int> known[kDevices];  // 0: not asked yet; SMs of an sm_103 part; kOther: another
+  int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return CLSAMPLE_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return CLSAMPLE_ERR_CUDA;
-  if (major != 10 || minor != 3) return CLSAMPLE_ERR_DEVICE;
-  if (sms && cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return CLSAMPLE_ERR_CUDA;
+  int count = dev >= 0 && dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (count == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return CLSAMPLE_ERR_CUDA;
+    if (major != 10 || minor != 3) count = kOther;
+    if (dev >= 0 && dev < kDevices) known[dev].store(count, std::memory_order_relaxed);
+  }
+  if (count == kOther) return CLSAMPLE_ERR_DEVICE;
+  if (sms) *sms = count;
   if (dev_out) *dev_out = dev;
   return CLSAMPLE_SUCCESS;
+}
+
+// Host: lets kernel fn have `bytes` of dynamic shared memory, which is asked for once a kernel and device.
+template <class Kernel>
+cudaError_t allow_smem_once(Kernel* fn, int bytes, std::atomic<uint64_t>* done) {
+  int dev = -1;
+  const cudaError_t got = cudaGetDevice(&dev);
+  if (got != cudaSuccess) return got;
+  const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

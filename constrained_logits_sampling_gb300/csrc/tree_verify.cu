@@ -310,8 +310,8 @@ cudaError_t launch_tree(const clsample_verify_tree_args_t& a, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaFuncSetAttribute(verify_tree_kernel<P, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem_bytes<P, C>(kMaxVocab));
+  static std::atomic<uint64_t> allowed;
+  const cudaError_t e = allow_smem_once(verify_tree_kernel<P, C>, smem_bytes<P, C>(kMaxVocab), &allowed);
   return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, verify_tree_kernel<P, C>, a) : e;
 }
 

@@ -130,7 +130,13 @@ def geometry(vocab: int):
     return {"slices": c.value, "chunk": k.value, "smem_bytes": s.value}
 
 
+# the current stream's handle without an object for it, which takes 3 us of a small call's 6 to make
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(s.cuda_stream)
 
