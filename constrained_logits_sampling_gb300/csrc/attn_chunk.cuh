@@ -165,14 +165,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const float neg_inf = __int_as_float(0xff800000);
 
   let_next_grid_start();
-  Span span;
-  Unit u;
-  int64_t unit_begin;
-  if (!find_span<kChunkRows, kChunkKeys, kChunkThreads, kTree>(P, &span, &u, &unit_begin)) {
-    if (tid == 0) P.cut[blockIdx.x].rows = 0;
-    return;
-  }
-
   if (tid == 0) {
     // for tests: a barrier that waits for one arrival more than it gets
     auto init = [&](unsigned long long* bar, int count, int stall, int slot = 0) {
@@ -201,13 +193,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     sh.limit.cycles = P.wait_cycles;
     sh.limit.dead = 0;
-    sh.span = span;
     fence_mbar_init();
+    if (kTma) {
+      prefetch_map(&k_map);
+      prefetch_map(&v_map);
+      if (P.q_box) prefetch_map(&q_map);
+    }
   }
   if (warp == 10) tmem_alloc512(&sh.tmem);
+  Span span;
+  Unit u;
+  int64_t unit_begin;
+  const bool work = find_span<kChunkRows, kChunkKeys, kChunkThreads, kTree>(P, &span, &u, &unit_begin);
+  if (tid == 0) sh.span = span;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (!work) {
+    if (tid == 0) P.cut[blockIdx.x].rows = 0;
+    if (warp == 10) tmem_free512(sh.tmem);
+    return;
+  }
   const uint32_t tmem = sh.tmem;
   int64_t t = span.t0;
 
@@ -223,8 +229,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     bool noted = false, go = SoftmaxSync::all(bounded_wait(&sh.unit_full[0], 0, &sh.limit));
     for (uint32_t seg = 0; go; ++seg) {
       const Unit& u = sh.unit[seg & 1];
-      const int j0 = (int)max(sh.span.t0 - sh.unit_begin[seg & 1], (int64_t)0);
-      const int cnt = (int)(min(sh.unit_begin[seg & 1] + u.tiles, sh.span.t1) - sh.unit_begin[seg & 1]) - j0;
+      const int64_t from = max(sh.span.t0, sh.unit_begin[seg & 1]);
+      const int j0 = tile_in_unit<Map>(from, u, sh.unit_begin[seg & 1]);
+      const int cnt = tiles_here<Map>(sh.span, u, sh.unit_begin[seg & 1], from);
       const bool split = u.rows <= 128;  // this half has the key tiles w, w + 2, ..
       const int step = split ? 2 : 1, jw = split ? w : 0;
       const int r = (split ? 0 : w * 128) + (warp & 3) * 32 + lane;  // this thread's row
@@ -447,9 +454,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       tc_fence_before();  // O has been read: the next unit's products may overwrite it
       tile += cnt;
-      const bool last = sh.unit_begin[seg & 1] + u.tiles + Map::kPad >= sh.span.t1;
+      const bool last = last_in_span<Map>(sh.span, u, sh.unit_begin[seg & 1]);
       if (last && tid == 0) {
-        note_cut(P, sh.span, u, sh.unit_begin[seg & 1]);
+        note_cut<Map>(P, sh.span, u, sh.unit_begin[seg & 1]);
         noted = true;
       }
       if (split) fence_async_proxy();  // the room may next be written by a box copy
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int box = min(a.page_size, kChunkKeys), boxes = kChunkKeys / box;
       uint32_t it = 0;
       while (true) {
-        const int j0 = tile_in_unit(t, unit_begin), cnt = tiles_here(span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(t, u, unit_begin), cnt = tiles_here<Map>(span, u, unit_begin, t);
         const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
         auto page_of = [&](int j) {  // num_pages, which is out of bounds: zeros
           const int key = (u.tile0 + j0 + j) * kChunkKeys + lane * box;
@@ -589,12 +596,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int x = 0; x < D / 64; ++x)
               tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h, from, full);
         }
-        if (!advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
+        if (!advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
       }
     } else if (kTma) {
       uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
       while (true) {
-        const int j0 = tile_in_unit(t, unit_begin), cnt = tiles_here(span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(t, u, unit_begin), cnt = tiles_here<Map>(span, u, unit_begin, t);
         if (!copy_queries(seg)) break;
         for (int j = 0; j < cnt; ++j) {
           const int tile = u.tile0 + j0 + j;
@@ -633,13 +640,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         it += cnt;
         ++seg;
-        if (!advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
+        if (!advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (warp < 10) {
       uint32_t it = 0, seg = 0;
       while (true) {
-        const int j0 = tile_in_unit(t, unit_begin), cnt = tiles_here(span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(t, u, unit_begin), cnt = tiles_here<Map>(span, u, unit_begin, t);
         if (!copy_queries(seg)) break;
         const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
         const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
@@ -690,7 +697,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        if (!advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
+        if (!advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (lane == 0) {
@@ -699,7 +706,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       uint32_t it = 0;
       bool alive = true;
       do {
-        for (const uint32_t end = it + tiles_here(span, u, unit_begin, t); alive && it < end; ++it) {
+        for (const uint32_t end = it + tiles_here<Map>(span, u, unit_begin, t); alive && it < end; ++it) {
           alive = bounded_wait(&sh.k_landed[it % NS], (it / NS) & 1, &sh.limit);
           if (!alive) break;
           fence_async_proxy();
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           fence_async_proxy();
           mbar_arrive(&sh.v_full[it % NV]);
         }
-      } while (alive && advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t));
+      } while (alive && advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t));
     }
   } else {
     // ------------------------------------------------------------------ products
@@ -761,7 +768,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         p_phase ^= 1u << w;
       };
       while (true) {
-        const int cnt = (int)uni((uint32_t)tiles_here(span, u, unit_begin, t));
+        const int cnt = (int)uni((uint32_t)tiles_here<Map>(span, u, unit_begin, t));
         const bool split = uni(u.rows <= 128);
         wait(&sh.q_full, seg & 1);
         fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
@@ -806,7 +813,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        if (!uni(advance<kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t))) break;
+        if (!uni(advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t))) break;
       }
       // products still running when a wait gave up end before their memory is freed
       if (!alive) {

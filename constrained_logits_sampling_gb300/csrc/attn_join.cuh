@@ -29,28 +29,24 @@ struct JoinParams {
 // Statuses: one CTA per sequence at a time looks at its lengths and at every page id that
 // the call touches.
 template <int NT, bool kTree>
-__device__ __forceinline__ void attention_status(const AttnParams& P, bool gave_up) {
+__device__ __forceinline__ bool attention_bad(const AttnParams& P, int b) {
   const clsample_attention_args_t& a = P.a;
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const Seq s = load_seq(a.cu_new, a.kv_lens, b, a.T, P.capacity, a.max_new);
-    int bad = !s.ok || (kTree && s.n > s.len);
-    if (kTree && !bad && P.tree.positions)
-      for (int i = threadIdx.x; i < s.n; i += NT) {
-        const int pos = __ldg(P.tree.positions + s.q0 + i);
-        bad |= pos < s.len - s.n || pos >= s.len;
-      }
-    if (s.ok && s.n > 0 && s.len > 0 && !(kTree && s.n > s.len)) {
-      const int lo = a.window > 0 ? max(0, s.len - s.n - a.window + 1) : 0;
-#pragma unroll 8
-      for (int p = lo / a.page_size + threadIdx.x; p <= (s.len - 1) / a.page_size; p += NT) {
-        const int id = __ldg(a.page_table + (int64_t)b * a.table_stride + p);
-        bad |= id < 0 || id >= a.num_pages;
-      }
+  const Seq s = load_seq(a.cu_new, a.kv_lens, b, a.T, P.capacity, a.max_new);
+  int bad = !s.ok || (kTree && s.n > s.len);
+  if (kTree && !bad && P.tree.positions)
+    for (int i = threadIdx.x; i < s.n; i += NT) {
+      const int pos = __ldg(P.tree.positions + s.q0 + i);
+      bad |= pos < s.len - s.n || pos >= s.len;
     }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0)
-      a.row_status[b] = bad ? CLSAMPLE_ROW_INVALID : gave_up ? CLSAMPLE_ROW_OVERFLOW : CLSAMPLE_ROW_OK;
+  if (s.ok && s.n > 0 && s.len > 0 && !(kTree && s.n > s.len)) {
+    const int lo = a.window > 0 ? max(0, s.len - s.n - a.window + 1) : 0;
+#pragma unroll 8
+    for (int p = lo / a.page_size + threadIdx.x; p <= (s.len - 1) / a.page_size; p += NT) {
+      const int id = __ldg(a.page_table + (int64_t)b * a.table_stride + p);
+      bad |= id < 0 || id >= a.num_pages;
+    }
   }
+  return __syncthreads_or(bad);
 }
 
 // NV times four sums of one row, over parts: o and l are relative to m.
@@ -118,6 +114,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid
   __shared__ float part_m[8][32], part_l[8][32];
   __shared__ float part_o[8][32][17];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the first status of each CTA rests on the call's inputs alone, and is found while the grids before end
+  bool bad = false;
+  if (P.a.row_status && (int)blockIdx.x < P.a.B) bad = attention_bad<kJoinThreads, kTree>(P, blockIdx.x);
   wait_for_earlier_grids();
   // Thread i has the cut units 4 i .. 4 i + 3, and how many block items they make.
   const int entries = J.chunk_ctas + J.stream_ctas;
@@ -250,7 +249,12 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid
       }
     }
   }
-  if (P.a.row_status) attention_status<kJoinThreads, kTree>(P, *P.gave_up != 0);
+  if (!P.a.row_status) return;
+  const bool gave_up = *P.gave_up != 0;
+  for (int b = blockIdx.x; b < P.a.B; b += gridDim.x) {
+    if (b >= (int)gridDim.x) bad = attention_bad<kJoinThreads, kTree>(P, b);
+    if (tid == 0) P.a.row_status[b] = bad ? CLSAMPLE_ROW_INVALID : gave_up ? CLSAMPLE_ROW_OVERFLOW : CLSAMPLE_ROW_OK;
+  }
 }
 
 }  // namespace clsample

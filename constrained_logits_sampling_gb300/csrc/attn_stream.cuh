@@ -299,6 +299,7 @@ __device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u
 
 template <class T, int D, bool kTree = false>
 __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __grid_constant__ AttnParams P) {
+  using Map = UnitMap<kStreamRows, kStreamKeys, kTree>;
   constexpr int R = kStreamRows, S = StreamRing<D>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
   constexpr int kTileBytes = 16 * D * 2, kStageBytes = 2 * kTileBytes, kHalf = 16 * 128;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -320,9 +321,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
 
   int64_t t = span.t0;
   while (true) {
-    const int j0 = tile_in_unit(t, unit_begin), cnt = tiles_here(span, u, unit_begin, t);
-    const bool last = unit_begin + u.tiles + UnitMap<R, kStreamKeys, kTree>::kPad >= span.t1;
-    if (tid == 0 && last) note_cut(P, span, u, unit_begin);
+    const int j0 = tile_in_unit<Map>(t, u, unit_begin), cnt = tiles_here<Map>(span, u, unit_begin, t);
+    if (tid == 0 && last_in_span<Map>(span, u, unit_begin)) note_cut<Map>(P, span, u, unit_begin);
     const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
     const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
     const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
     __syncthreads();  // the rings are drained: the first is where the warps meet
     stream_finish<T, D, kTree>(P, u, st, reinterpret_cast<float*>(smem), wm, wl, cnt == u.tiles,
                                    scratch_slot<R, D>(P, blockIdx.x, j0 == 0 ? 1 : 0));
-    if (!advance<R, kStreamKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
+    if (!advance<Map, R, kStreamKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
   }
   wait_for_earlier_grids();  // this grid's end stands for theirs
 }

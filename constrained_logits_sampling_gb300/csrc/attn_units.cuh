@@ -47,7 +47,8 @@ __device__ __forceinline__ int token_of(const AttnParams& P, int row) {
 __device__ __forceinline__ int head_of(const AttnParams& P, int row) { return row - token_of(P, row) * P.g; }
 
 // 64 trees of 24 to 32 rows over 200 to 4000 keys on 8 key heads: PADFIG
-constexpr int kChunkPad = 6, kStreamPad = 3;
+constexpr int kChunkPad = 18, kStreamPad = 3;
+constexpr int kMinSpan = 1;  // tiles
 
 struct CutUnit {
   int rows;          // 0: none
@@ -96,12 +97,17 @@ __device__ __forceinline__ int tree_position(const AttnParams& P, int t, int i, 
   return P.tree.positions ? min(max(__ldg(P.tree.positions + t), len - n), len - 1) : len - n + i;
 }
 
-// What a unit costs beside its tiles, in tiles, where spans are made of the two (kTree): its end, and
-// the wait for masks and for the next one's first keys.  Sequences of very different lengths would
-// otherwise leave the CTAs with many short units far behind.
+// How spans are measured.  A unit is kPad + tiles times its weight long; a tile belongs to the span
+// that holds its first position.  With kTree the weights are what tiles cost: of two row tiles 1.5 us, of
+// one 1 us; kPad is what a unit costs beside its tiles: its end, and the wait for masks and for the next
+// one's first keys.  Sequences of very different lengths would otherwise leave the CTAs with
+// many short units far behind.
 template <int R, int K, bool kTree = false>
 struct UnitMap {
-  static constexpr int kPad = kTree ? (R > 16 ? kChunkPad : kStreamPad) : 0;
+  static constexpr bool kWeighted = kTree && R > 128;
+  static constexpr int kPad = !kTree ? 0 : kWeighted ? kChunkPad : kStreamPad;
+  static constexpr int kMaxWeight = kWeighted ? 3 : 1;
+  static __device__ __forceinline__ int weight(const Unit& u) { return !kWeighted ? 1 : u.rows > 128 ? 3 : 2; }
   static __device__ __forceinline__ Seq seq_of(const AttnParams& P, int b) {
     Seq s = load_seq(P.a.cu_new, P.a.kv_lens, b, P.a.T, P.capacity, P.a.max_new);
     const int64_t rows = (int64_t)s.n * P.g;
@@ -134,14 +140,14 @@ struct UnitMap {
     u->tile0 = u->key_lo / K;
     u->tiles = max(1, (u->key_hi + K - 1) / K - u->tile0);
   }
-  // key tiles of one key head of a sequence, each unit's with kPad behind them
+  // length of one key head's units
   static __device__ __forceinline__ int64_t head_tiles(const AttnParams& P, const Seq& s) {
     const int m = row_tiles(P, s);
     int64_t t = 0;
     Unit u;
     for (int qt = 0; qt < m; ++qt) {
       fill(P, s, qt, &u);
-      t += u.tiles + kPad;
+      t += u.tiles * weight(u) + kPad;
     }
     return t;
   }
@@ -170,9 +176,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* buf, int64_t* 
   return total;
 }
 
-// The whole call's key tiles (with kPad behind each unit's), and where this CTA's span begins: u is
-// the unit that holds tile t0 = total * cta / ctas, or the next one if that lies behind its unit's
-// tiles (t0 is then that one's first).  Returns false without work.
+// The length of the whole call's units, and where this CTA's span begins: u is the unit that holds
+// position t0 = total * cta / ctas, or the next one if no tile of that begins there or later (t0 is then
+// the next one's first).  Returns false without work.
 struct Span {
   int64_t total, t0, t1;
   int ctas;  // CTAs with work: those with the lower indices
@@ -183,6 +189,27 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // of numbe
 __device__ __forceinline__ int64_t span_begin(int64_t total, int ctas, int c) {
   const int64_t each = quotient(total, ctas);
   return each * c + (uint32_t)((int)(total - each * ctas) * c) / (uint32_t)ctas;
+}
+
+// At position t of a span, at unit u: the place in the unit, how many of its tiles are this CTA's, and
+// whether the span ends with it.
+template <class M>
+__device__ __forceinline__ int tiles_before(int64_t at, const Unit& u) {  // tiles that begin before `at` of a unit
+  if (!M::kWeighted) return (int)min(at, (int64_t)u.tiles);
+  const uint32_t x = (uint32_t)min(at, (int64_t)u.tiles * 3);  // (below 2^26)
+  return min(u.tiles, (int)(M::weight(u) == 3 ? (x + 2) / 3 : (x + 1) / 2));
+}
+template <class M>
+__device__ __forceinline__ int tile_in_unit(int64_t t, const Unit& u, int64_t unit_begin) {
+  return tiles_before<M>(t - unit_begin, u);
+}
+template <class M>
+__device__ __forceinline__ int tiles_here(const Span& span, const Unit& u, int64_t unit_begin, int64_t t) {
+  return tiles_before<M>(span.t1 - unit_begin, u) - tile_in_unit<M>(t, u, unit_begin);
+}
+template <class M>
+__device__ __forceinline__ bool last_in_span(const Span& span, const Unit& u, int64_t unit_begin) {
+  return unit_begin + (int64_t)u.tiles * M::weight(u) + M::kPad >= span.t1;
 }
 
 template <int R, int K, bool kTree = false>
@@ -205,7 +232,9 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
     total += block_scan<NT>(per_head * P.a.Hkv, buf, &ex);
   }
   span->total = total;
-  span->ctas = (int)min((int64_t)gridDim.x, total);
+  // every span holds a tile of the unit that it lies in
+  span->ctas = (int)min((int64_t)gridDim.x, kTree ? max((int64_t)1, quotient(total, kMinSpan * M::kMaxWeight)) : total);
+  if (total == 0) return false;
   if ((int)blockIdx.x >= span->ctas) return false;
   span->t0 = span_begin(total, span->ctas, blockIdx.x);
   span->t1 = span_begin(total, span->ctas, blockIdx.x + 1);
@@ -226,8 +255,9 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
       rest -= v.h * per_head;
       for (int qt = 0;; ++qt) {
         M::fill(P, s, qt, &v);
-        if (rest < v.tiles + M::kPad) break;
-        rest -= v.tiles + M::kPad;
+        const int64_t length = (int64_t)v.tiles * M::weight(v) + M::kPad;
+        if (rest < length) break;
+        rest -= length;
       }
       found = v;
       found_begin = span->t0 - rest;
@@ -238,8 +268,8 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
   __syncthreads();
   *u = found;
   *unit_begin = found_begin;
-  if (M::kPad > 0 && span->t0 >= found_begin + found.tiles) {  // the span begins behind the unit's tiles
-    *unit_begin += found.tiles + M::kPad;
+  if (M::kPad > 0 && tile_in_unit<M>(span->t0, found, found_begin) >= found.tiles) {  // behind the unit's tiles
+    *unit_begin += (int64_t)found.tiles * M::weight(found) + M::kPad;
     if (*unit_begin >= span->t1) return false;
     next_unit<R, K, kTree>(P, u);
     span->t0 = *unit_begin;
@@ -247,18 +277,12 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
   return true;
 }
 
-// A CTA's way through its span: `t` tiles in, at unit u.  The place in the unit and how many of its tiles
-// are this CTA's.
-__device__ __forceinline__ int tile_in_unit(int64_t t, int64_t unit_begin) { return (int)(t - unit_begin); }
-__device__ __forceinline__ int tiles_here(const Span& span, const Unit& u, int64_t unit_begin, int64_t t) {
-  return (int)(min(unit_begin + u.tiles, span.t1) - t);
-}
 // On to the next unit; false if the span ends.
-template <int R, int K, bool kTree>
+template <class M, int R, int K, bool kTree>
 __device__ __forceinline__ bool advance(const AttnParams& P, const Span& span, Unit* u, int64_t* unit_begin, int64_t* t) {
-  const int64_t next = *unit_begin + u->tiles + UnitMap<R, K, kTree>::kPad;
-  if (next >= span.t1) return false;
-  *t = *unit_begin = next;
+  if (last_in_span<M>(span, *u, *unit_begin)) return false;
+  *unit_begin += (int64_t)u->tiles * M::weight(*u) + M::kPad;
+  *t = *unit_begin;
   next_unit<R, K, kTree>(P, u);
   return true;
 }
@@ -291,10 +315,12 @@ __device__ __forceinline__ int cta_of_tile(const Span& sp, int64_t t) {
 
 // Called by one thread of each CTA, with the unit that its span ends with: whether the rest of
 // it is another's.
+template <class M>
 __device__ __forceinline__ void note_cut(const AttnParams& P, const Span& span, const Unit& u, int64_t unit_begin) {
   CutUnit c{0, 0, 0, 0, 0, 0};
-  if (unit_begin >= span.t0 && unit_begin + u.tiles > span.t1)
-    c = CutUnit{u.rows, u.row0, u.q0, u.h, (int)blockIdx.x, cta_of_tile(span, unit_begin + u.tiles - 1)};
+  const int64_t last = unit_begin + (int64_t)(u.tiles - 1) * M::weight(u);  // where the last tile is
+  if (unit_begin >= span.t0 && last >= span.t1)
+    c = CutUnit{u.rows, u.row0, u.q0, u.h, (int)blockIdx.x, cta_of_tile(span, last)};
   P.cut[blockIdx.x] = c;
 }
 

@@ -25,6 +25,9 @@ __device__ __forceinline__ bool mbar_test_wait(unsigned long long* bar, uint32_t
 __device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // One box of a tensor map of rank 3 to shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int head, int token,
                                           unsigned long long* bar) {
