@@ -25,7 +25,8 @@
 // 2500 a tile, the rest of it the way from a finished S over the softmax (970) to the next product.
 // A unit of at most 128 rows has one row tile: both halves of the CTA then take the same
 // queries and every other key tile, and their sums are joined at the end, in the room of the
-// second row tile's queries.
+// second row tile's queries.  With kTree two key heads make such a unit (a pair, attn_units.cuh): each half
+// takes the queries of one and all key tiles of it, copied in turns, and nothing is joined.
 #pragma once
 
 #include <type_traits>
@@ -230,19 +231,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (uint32_t seg = 0; go; ++seg) {
       const Unit& u = sh.unit[seg & 1];
       const int64_t from = max(sh.span.t0, sh.unit_begin[seg & 1]);
-      const int j0 = tile_in_unit<Map>(from, u, sh.unit_begin[seg & 1]);
-      const int cnt = tiles_here<Map>(sh.span, u, sh.unit_begin[seg & 1], from);
-      const bool split = u.rows <= 128;  // this half has the key tiles w, w + 2, ..
-      const int step = split ? 2 : 1, jw = split ? w : 0;
-      const int r = (split ? 0 : w * 128) + (warp & 3) * 32 + lane;  // this thread's row
+      const int j0 = tile_in_unit<Map>(P, from, u, sh.unit_begin[seg & 1]);
+      const int cnt = tiles_here<Map>(P, sh.span, u, sh.unit_begin[seg & 1], from);
+      const bool pair = Map::is_pair(P, u);       // this half has the key head h + w
+      const bool split = !pair && u.rows <= 128;  // this half has the key tiles w, w + 2, ..
+      const int step = split ? 2 : 1, jw = split ? w : 0, other = pair ? w : 0;
+      const int at_row = (split ? 0 : w * 128) + (warp & 3) * 32 + lane;  // in the scratch
+      const int r = pair ? at_row & 127 : at_row;                         // this thread's row
       const bool live = r < u.rows;
       float m = neg_inf, l = 0.f;  // reference maximum (log2 units) and weights' sum
       if (cnt > jw) {
         const int first_pos = u.len - u.n, kb0 = (u.tile0 + j0) * kChunkKeys;
         const int pos = live ? first_pos + token_of(P, u.row0 + r) : -1;
-        const int half0 = split ? 0 : w * 128;
+        const int half0 = split || pair ? 0 : w * 128;
         const int pos_first = first_pos + token_of(P, u.row0 + half0);
         const int pos_last = first_pos + token_of(P, u.row0 + min(u.rows, half0 + 128) - 1);
+        auto copy = [&](int j) { return pair ? 2 * j + w : j; };  // the place of tile j among the unit's copies
         for (int j = jw; j < cnt; j += step) {
           const int kb = kb0 + j * kChunkKeys;
           // kTree: what the row sees of the tile, while the scores are on their way
@@ -258,12 +262,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           bounded_wait(&sh.s_full[w], s_phase, &sh.limit);
           if (lane == 0) {
-            if ((warp & 3) == 0 && (split || w == 1)) mbar_arrive(&sh.tile_done[(tile + j) % (2 * NS)]);
+            if ((warp & 3) == 0 && (split || pair || w == 1)) mbar_arrive(&sh.tile_done[(tile + copy(j)) % (2 * NS)]);
           }
           __syncwarp();
           s_phase ^= 1;
           tc_fence_after();
-          const uint32_t* ok = sh.key_ok[(tile + j) % (2 * NS)];
+          const uint32_t* ok = sh.key_ok[(tile + copy(j)) % (2 * NS)];
           const uint4 bits = *reinterpret_cast<const uint4*>(ok);
           const bool whole = (bits.x & bits.y & bits.z & bits.w) == ~0u &&
                              (kTree ? cached
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       constexpr int kCols = D / 4, kWords = kCols / 8;
       const int row = u.row0 + min(r, u.rows - 1);
       const int64_t dst = (int64_t)(u.q0 + token_of(P, row)) * a.o_stride_t +
-                          (int64_t)(u.h * P.g + head_of(P, row)) * a.o_stride_h;
+                          (int64_t)((u.h + other) * P.g + head_of(P, row)) * a.o_stride_h;
       // this thread's row's sums, from column c on
       auto put = [&](const uint32_t (&x)[kCols], int c) {
         if (done) {
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         } else if (live) {
 #pragma unroll
           for (int e = 0; e < kCols; e += 4)
-            __stcg(reinterpret_cast<uint4*>(slot + (c + e) * kChunkRows + r * 4),
+            __stcg(reinterpret_cast<uint4*>(slot + (c + e) * kChunkRows + at_row * 4),
                    make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]));
         }
       };
@@ -446,15 +450,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       if (live && (w == 0 || !split)) {
         if (done) {
-          store_lse(P, u, r, m, l);
+          store_lse(P, u, r, m, l, other);
         } else {
-          __stcg(slot + kChunkRows * D + r, m);
-          __stcg(slot + kChunkRows * D + kChunkRows + r, l);
+          __stcg(slot + kChunkRows * D + at_row, m);
+          __stcg(slot + kChunkRows * D + kChunkRows + at_row, l);
         }
       }
       tc_fence_before();  // O has been read: the next unit's products may overwrite it
-      tile += cnt;
-      const bool last = last_in_span<Map>(sh.span, u, sh.unit_begin[seg & 1]);
+      tile += pair ? 2 * cnt : cnt;
+      const bool last = last_in_span<Map>(P, sh.span, u, sh.unit_begin[seg & 1]);
       if (last && tid == 0) {
         note_cut<Map>(P, sh.span, u, sh.unit_begin[seg & 1]);
         noted = true;
@@ -482,15 +486,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     };
     auto copy_queries = [&](uint32_t seg) -> bool {
       constexpr int kBlocks = 8 / kRowWarps;
-      const bool box = kTma && P.q_box;
+      const bool box = kTma && P.q_box, pair = Map::is_pair(P, u), split = !pair && u.rows <= 128;
       int64_t off[kBlocks];
       unsigned live[kBlocks];
       if (!box) {  // each lane finds the places of its rows, one of 32, before it has to wait
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
-          const int mine = (i * kRowWarps + lw) * 32 + lane, row = u.row0 + mine;
+          const int at = (i * kRowWarps + lw) * 32 + lane, mine = pair ? at & 127 : at, row = u.row0 + mine;
           off[i] = mine < u.rows ? (int64_t)(u.q0 + token_of(P, row)) * a.q_stride_t +
-                                       (int64_t)(u.h * P.g + head_of(P, row)) * a.q_stride_h
+                                       (int64_t)((u.h + (pair ? at >> 7 : 0)) * P.g + head_of(P, row)) * a.q_stride_h
                                  : 0;
           live[i] = __ballot_sync(~0u, mine < u.rows);
         }
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       bounded_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.limit);
       if (__any_sync(~0u, sh.limit.dead)) return false;
-      const int tiles_of_rows = u.rows <= 128 ? 1 : 2;
+      const int tiles_of_rows = split ? 1 : 2;
       auto second_tile = [&]() {
         if (met) bounded_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.limit);
         __syncwarp();
@@ -515,8 +519,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int w = 0; w < tiles_of_rows; ++w) {
           if (w == 1) second_tile();
           if (lane < D / 64 && !sh.limit.dead)
-            tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, u.h * P.g,
-                      u.q0 + token_of(P, u.row0 + w * 128), &sh.q_full);
+            tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, (u.h + (pair ? w : 0)) * P.g,
+                      u.q0 + token_of(P, u.row0 + (pair ? 0 : w * 128)), &sh.q_full);
         }
       } else {
 #pragma unroll
@@ -524,17 +528,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int first = (i * kRowWarps + lw) * 32;
           if (first >= 128 && tiles_of_rows == 1) break;
           if (i == kBlocks / 2) second_tile();
-          if (first < u.rows) copy_rows((const T*)a.q, off[i], live[i], q_smem + (first >> 7) * kTile, first & 127);
+          if ((pair ? first & 127 : first) < u.rows) copy_rows((const T*)a.q, off[i], live[i], q_smem + (first >> 7) * kTile, first & 127);
         }
         cp_async_arrive(smem_addr(&sh.q_full));
       }
-      met = u.rows <= 128;
+      met = split;
       return true;
     };
     // The slot of a tile's keys is free when S of the tile that had it is complete, and the
     // slot of its values when O is, which a later tile's completion covers: the next one's if
     // both halves take each tile, the one after it otherwise (and across units, where either
-    // may have been the case).  Of twice as many completions as there are key slots the one
+    // may have been the case; a pair's copies are taken in turns).  Of twice as many completions as there are key slots the one
     // waited for is still the last on its barrier.
     auto tile_done = [&](int64_t gate) {
       if (gate >= 0) bounded_wait(&sh.tile_done[gate % (2 * NS)], (gate / (2 * NS)) & 1, &sh.limit);
@@ -554,7 +558,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int box = min(a.page_size, kChunkKeys), boxes = kChunkKeys / box;
       uint32_t it = 0;
       while (true) {
-        const int j0 = tile_in_unit<Map>(t, u, unit_begin), cnt = tiles_here<Map>(span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, span, u, unit_begin, t);
         const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
         auto page_of = [&](int j) {  // num_pages, which is out of bounds: zeros
           const int key = (u.tile0 + j0 + j) * kChunkKeys + lane * box;
@@ -562,83 +566,91 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int id = __ldg(table + (P.page_shift >= 0 ? key >> P.page_shift : key / a.page_size));
           return id >= 0 && id < a.num_pages ? id : -1;
         };
+        const int copies = Map::is_pair(P, u) ? 2 : 1;  // of a tile: of one head after the other
         int page = page_of(0);
-        for (int j = 0; j < cnt; ++j, ++it) {
+        for (int j = 0; j < cnt; ++j) {
           const int tile = u.tile0 + j0 + j;
           const int key = tile * kChunkKeys + lane * box;
           const int slot = a.page_size > kChunkKeys ? key % a.page_size : 0;
           const unsigned bad = __ballot_sync(~0u, page < 0);
           const int from = page < 0 ? a.num_pages : page;
           page = page_of(j + 1);
-          unsigned long long* full;
-          uint32_t dst;
-          if (keys) {
-            key_slot(it);
-            if (lane < 4) {
-              uint32_t word = ~0u;
-              if (bad)
-                for (int e = 0; e < 32; ++e)
-                  if ((bad >> ((lane * 32 + e) / box)) & 1) word &= ~(1u << e);
-              sh.key_ok[it % (2 * NS)][lane] = word;
+#pragma unroll 1
+          for (int head = 0; head < copies; ++head, ++it) {
+            unsigned long long* full;
+            uint32_t dst;
+            if (keys) {
+              key_slot(it);
+              if (lane < 4) {
+                uint32_t word = ~0u;
+                if (bad)
+                  for (int e = 0; e < 32; ++e)
+                    if ((bad >> ((lane * 32 + e) / box)) & 1) word &= ~(1u << e);
+                sh.key_ok[it % (2 * NS)][lane] = word;
+              }
+              full = &sh.k_full[it % NS];
+              dst = k_smem + it % NS * kTile;
+            } else {
+              value_slot(it, j);
+              full = edge(tile) ? &sh.v_landed[it % NV] : &sh.v_full[it % NV];
+              dst = v_smem + it % NV * kTile;
             }
-            full = &sh.k_full[it % NS];
-            dst = k_smem + it % NS * kTile;
-          } else {
-            value_slot(it, j);
-            full = edge(tile) ? &sh.v_landed[it % NV] : &sh.v_full[it % NV];
-            dst = v_smem + it % NV * kTile;
+            const bool dead = sh.limit.dead;
+            __syncwarp();
+            if (lane == 0 && !dead) mbar_arrive_expect_tx(full, kTile);
+            __syncwarp();
+            if (lane < boxes && !dead)
+              for (int x = 0; x < D / 64; ++x)
+                tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h + head, from, full);
           }
-          const bool dead = sh.limit.dead;
-          __syncwarp();
-          if (lane == 0 && !dead) mbar_arrive_expect_tx(full, kTile);
-          __syncwarp();
-          if (lane < boxes && !dead)
-            for (int x = 0; x < D / 64; ++x)
-              tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h, from, full);
         }
         if (!advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
       }
     } else if (kTma) {
       uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
       while (true) {
-        const int j0 = tile_in_unit<Map>(t, u, unit_begin), cnt = tiles_here<Map>(span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, span, u, unit_begin, t);
         if (!copy_queries(seg)) break;
+        const int copies = Map::is_pair(P, u) ? 2 : 1;
         for (int j = 0; j < cnt; ++j) {
           const int tile = u.tile0 + j0 + j;
           if (!edge(tile)) continue;
-          const uint32_t st = (it + j) % NV;
-          uint32_t parity = 0;
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (i == st) parity = edges[i]++ & 1;
           const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
           uint4 keep = make_uint4(~0u, ~0u, ~0u, ~0u);
-          if (kTree) keep = seen_by_any(P, u, tile * kChunkKeys);
-          bounded_wait(&sh.v_landed[st], parity, &sh.limit);
-          const bool dead = sh.limit.dead;
-          __syncwarp();
-          // a row's pieces may lie anywhere in it: all are cleared, of two rows at a time
-          static_assert(KC <= 16, "pieces of a row");
-          const int ch = lane & 15;
+          if (kTree && tile * kChunkKeys + kChunkKeys > u.len - u.n) keep = seen_by_any(P, u, tile * kChunkKeys);
+#pragma unroll 1
+          for (int head = 0; head < copies; ++head) {
+            const uint32_t st = (it + j * copies + head) % NV;
+            uint32_t parity = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t gone = ~(word_of(keep, k) & column_bits(lo - 32 * k, hi - 1 - 32 * k));
-            while (gone) {  // uniform
-              const int r0 = __ffs(gone) - 1;
-              gone &= gone - 1;
-              const int r1 = gone ? __ffs(gone) - 1 : r0;
-              gone &= gone - 1;
-              const int row = 32 * k + (lane < 16 ? r0 : r1);
-              if (ch < KC)
-                *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < NV; ++i)
+              if (i == st) parity = edges[i]++ & 1;
+            bounded_wait(&sh.v_landed[st], parity, &sh.limit);
+            const bool dead = sh.limit.dead;
+            __syncwarp();
+            // a row's pieces may lie anywhere in it: all are cleared, of two rows at a time
+            static_assert(KC <= 16, "pieces of a row");
+            const int ch = lane & 15;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t gone = ~(word_of(keep, k) & column_bits(lo - 32 * k, hi - 1 - 32 * k));
+              while (gone) {  // uniform
+                const int r0 = __ffs(gone) - 1;
+                gone &= gone - 1;
+                const int r1 = gone ? __ffs(gone) - 1 : r0;
+                gone &= gone - 1;
+                const int row = 32 * k + (lane < 16 ? r0 : r1);
+                if (ch < KC)
+                  *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+              }
             }
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0 && !dead) mbar_arrive(&sh.v_full[st]);
           }
-          fence_async_proxy();
-          __syncwarp();
-          if (lane == 0 && !dead) mbar_arrive(&sh.v_full[st]);
         }
-        it += cnt;
+        it += cnt * copies;
         ++seg;
         if (!advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
       }
@@ -646,10 +658,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     } else if (warp < 10) {
       uint32_t it = 0, seg = 0;
       while (true) {
-        const int j0 = tile_in_unit<Map>(t, u, unit_begin), cnt = tiles_here<Map>(span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, span, u, unit_begin, t);
         if (!copy_queries(seg)) break;
-        const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
-        const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
+        const int copies = Map::is_pair(P, u) ? 2 : 1;
         const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
         // warp lw has keys 64 lw .. 64 lw + 63 of a tile, two a lane
         auto page_of = [&](int j, int half) {
@@ -663,7 +674,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           return id < a.num_pages ? id : -1;
         };
         int page[2] = {page_of(0, 0), page_of(0, 1)};
-        for (int j = 0; j < cnt; ++j, ++it) {
+        for (int j = 0; j < cnt; ++j) {
           int64_t off[2];
           unsigned live[2], shown[2];
 #pragma unroll
@@ -678,22 +689,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             page[half] = page_of(j + 1, half);
           }
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            if (kv)
-              value_slot(it, j);
-            else
-              key_slot(it);
-            unsigned long long* landed = kv ? &sh.v_landed[it % NV] : &sh.k_landed[it % NS];
-            if (kv == 0 && lane == 0) {
-              sh.key_ok[it % (2 * NS)][lw * 2] = shown[0];
-              sh.key_ok[it % (2 * NS)][lw * 2 + 1] = shown[1];
-              mbar_arrive(landed);
+          for (int head = 0; head < copies; ++head, ++it) {
+            const T* const kc = (const T*)a.k_cache + (int64_t)(u.h + head) * a.head_stride;
+            const T* const vc = (const T*)a.v_cache + (int64_t)(u.h + head) * a.head_stride;
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+              if (kv)
+                value_slot(it, j);
+              else
+                key_slot(it);
+              unsigned long long* landed = kv ? &sh.v_landed[it % NV] : &sh.k_landed[it % NS];
+              if (kv == 0 && lane == 0) {
+                sh.key_ok[it % (2 * NS)][lw * 2] = shown[0];
+                sh.key_ok[it % (2 * NS)][lw * 2 + 1] = shown[1];
+                mbar_arrive(landed);
+              }
+              const T* src = kv ? vc : kc;
+              const uint32_t dst = kv ? v_smem + it % NV * kTile : k_smem + it % NS * kTile;
+              copy_rows(src, off[0], live[0], dst, lw * 64);
+              copy_rows(src, off[1], live[1], dst, lw * 64 + 32);
+              cp_async_arrive(smem_addr(landed));
             }
-            const T* src = kv ? vc : kc;
-            const uint32_t dst = kv ? v_smem + it % NV * kTile : k_smem + it % NS * kTile;
-            copy_rows(src, off[0], live[0], dst, lw * 64);
-            copy_rows(src, off[1], live[1], dst, lw * 64 + 32);
-            cp_async_arrive(smem_addr(landed));
           }
         }
         ++seg;
@@ -706,7 +722,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       uint32_t it = 0;
       bool alive = true;
       do {
-        for (const uint32_t end = it + tiles_here<Map>(span, u, unit_begin, t); alive && it < end; ++it) {
+        const uint32_t copies = Map::is_pair(P, u) ? 2 : 1;
+        for (const uint32_t end = it + copies * tiles_here<Map>(P, span, u, unit_begin, t); alive && it < end; ++it) {
           alive = bounded_wait(&sh.k_landed[it % NS], (it / NS) & 1, &sh.limit);
           if (!alive) break;
           fence_async_proxy();
@@ -768,12 +785,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         p_phase ^= 1u << w;
       };
       while (true) {
-        const int cnt = (int)uni((uint32_t)tiles_here<Map>(span, u, unit_begin, t));
-        const bool split = uni(u.rows <= 128);
+        const int cnt = (int)uni((uint32_t)tiles_here<Map>(P, span, u, unit_begin, t));
+        const bool turns = uni(u.rows <= 128);  // the halves take copies in turns, of one head or of a pair's
+        const uint32_t pair = uni(Map::is_pair(P, u));
         wait(&sh.q_full, seg & 1);
         fence_async_proxy();  // the copies were ordinary writes; the products read by the async proxy
         keys_ready(it);
-        if (!split) {
+        if (!turns) {
           qk(0, 0, it);
           qk(1, 1, it);
           if (cnt == 1) mma_commit(&sh.q_empty);
@@ -793,20 +811,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           mma_commit(&sh.o_full[1]);
           ++it;
         } else {
+          const int n = pair ? 2 * cnt : cnt;
           qk(0, 0, it);
-          if (cnt > 1) {
+          if (n > 1) {
             keys_ready(it + 1);
-            qk(1, 0, it + 1);
+            qk(1, pair, it + 1);
           }
-          if (cnt <= 2) mma_commit(&sh.q_empty);
-          for (int j = 0; j < cnt; ++j, ++it) {
+          if (n <= 2) mma_commit(&sh.q_empty);
+          for (int j = 0; j < n; ++j, ++it) {
             const uint32_t w = j & 1;
             values_ready(it);
             pv(w, it, j > 1);
-            if (j + 2 < cnt) {
+            if (j + 2 < n) {
               keys_ready(it + 2);
-              qk(w, 0, it + 2);
-              if (j + 3 == cnt) mma_commit(&sh.q_empty);
+              qk(w, pair ? w : 0, it + 2);
+              if (j + 3 == n) mma_commit(&sh.q_empty);
             } else {
               mma_commit(&sh.o_full[w]);
             }

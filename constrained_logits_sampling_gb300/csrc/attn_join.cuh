@@ -92,7 +92,8 @@ __device__ __forceinline__ void sum_parts(RowSum<NV>* r, int first, int step, in
 template <class T, int D, int NV>
 __device__ __forceinline__ void finish_row(const AttnParams& P, const CutUnit& u, int r, int d, const RowSum<NV>& s) {
   const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
-  const int row = u.row0 + r, token = u.q0 + token_of(P, row), head = u.h * P.g + head_of(P, row);
+  const int row = u.row0 + (u.pair ? r & 127 : r), token = u.q0 + token_of(P, row);
+  const int head = (u.h + (u.pair ? r >> 7 : 0)) * P.g + head_of(P, row);
   T* dst = (T*)P.a.out + (int64_t)token * P.a.o_stride_t + (int64_t)head * P.a.o_stride_h + d;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -129,8 +130,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid
       const CutUnit u = e < J.chunk_ctas ? J.chunk_cut[e] : P.cut[e - J.chunk_ctas];
       cuts[e] = u;
       const bool few = u.c1 - u.c0 < kFewParts;
+      const int rows = u.pair ? 128 + u.rows : u.rows;  // (a pair's second rows begin at 128)
       if (e < J.chunk_ctas)
-        items[k] = few ? (u.rows + kChunkStep - 1) / kChunkStep : (u.rows + 31) / 32 * kCols;
+        items[k] = few ? (rows + kChunkStep - 1) / kChunkStep : (rows + 31) / 32 * kCols;
       else
         items[k] = few ? (u.rows + kStreamStep - 1) / kStreamStep : u.rows;
     }
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid
       // a slot: four sums of each of 256 rows, the next four of each, ..; one lane a row
       const int r = few ? at * kChunkStep + warp / kCols * 32 + lane : at / kCols * 32 + lane;
       const int d = (few ? warp % kCols : at % kCols) * 16;
-      const bool live = r < u.rows;
+      const bool live = u.pair ? r < 256 && (r & 127) < u.rows : r < u.rows;
       auto load = [&](int part, float* m, float* l, float4 (&v)[4]) {
         const float* s = J.chunk_partial + (int64_t)((u.c0 + part) * 2 + (part == 0 ? 1 : 0)) * (kChunkRows * (D + 2));
         *m = __ldcg(s + kChunkRows * D + r);

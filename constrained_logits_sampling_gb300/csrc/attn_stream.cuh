@@ -100,9 +100,10 @@ __device__ __forceinline__ void store_out4(const AttnParams& P, const Unit& u, i
 __device__ __forceinline__ float lse_of(float m, float l) {  // m in log2 units
   return l > 0.f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xff800000);
 }
-__device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, int r, float m, float l) {
-  const int row = u.row0 + r;
-  if (P.a.lse) P.a.lse[(int64_t)(u.q0 + token_of(P, row)) * P.a.Hq + u.h * P.g + head_of(P, row)] = lse_of(m, l);
+__device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, int r, float m, float l, int other = 0) {
+  const int row = u.row0 + r;  // of head h + other
+  if (P.a.lse)
+    P.a.lse[(int64_t)(u.q0 + token_of(P, row)) * P.a.Hq + (u.h + other) * P.g + head_of(P, row)] = lse_of(m, l);
 }
 
 // The rows of a unit as one warp has them: queries as A operands, limits and running sums.  Lane
@@ -321,8 +322,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
 
   int64_t t = span.t0;
   while (true) {
-    const int j0 = tile_in_unit<Map>(t, u, unit_begin), cnt = tiles_here<Map>(span, u, unit_begin, t);
-    if (tid == 0 && last_in_span<Map>(span, u, unit_begin)) note_cut<Map>(P, span, u, unit_begin);
+    const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, span, u, unit_begin, t);
+    if (tid == 0 && last_in_span<Map>(P, span, u, unit_begin)) note_cut<Map>(P, span, u, unit_begin);
     const T* kc = (const T*)a.k_cache + (int64_t)u.h * a.head_stride;
     const T* vc = (const T*)a.v_cache + (int64_t)u.h * a.head_stride;
     const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;

@@ -54,6 +54,7 @@ struct CutUnit {
   int rows;          // 0: none
   int row0, q0, h;   // as in Unit
   int c0, c1;        // the CTAs that have its parts: c0 in its second slot, the others in the first
+  int pair;          // of two key heads
 };
 
 struct Unit {
@@ -98,16 +99,31 @@ __device__ __forceinline__ int tree_position(const AttnParams& P, int t, int i, 
 }
 
 // How spans are measured.  A unit is kPad + tiles times its weight long; a tile belongs to the span
-// that holds its first position.  With kTree the weights are what tiles cost: of two row tiles 1.5 us, of
-// one 1 us; kPad is what a unit costs beside its tiles: its end, and the wait for masks and for the next
+// that holds its first position.  With kTree the weights are what tiles cost (of two row tiles 1.5 us, of
+// one 1 us); kPad is what a unit costs beside its tiles: its end, and the wait for masks and for the next
 // one's first keys.  Sequences of very different lengths would otherwise leave the CTAs with
 // many short units far behind.
+//
+// With kTree, where a key head has one row tile, a unit is two key heads with one row tile each
+// (a pair: heads h and h + 1; the last of an odd number is alone).
 template <int R, int K, bool kTree = false>
 struct UnitMap {
   static constexpr bool kWeighted = kTree && R > 128;
   static constexpr int kPad = !kTree ? 0 : kWeighted ? kChunkPad : kStreamPad;
-  static constexpr int kMaxWeight = kWeighted ? 3 : 1;
-  static __device__ __forceinline__ int weight(const Unit& u) { return !kWeighted ? 1 : u.rows > 128 ? 3 : 2; }
+  static constexpr int kMaxWeight = kWeighted ? 4 : 1;
+  static __device__ __forceinline__ bool pairs(const AttnParams& P, int n) {
+    return kWeighted && P.a.Hkv > 1 && (int64_t)n * P.g <= 128;
+  }
+  static __device__ __forceinline__ bool is_pair(const AttnParams& P, const Unit& u) {
+    return pairs(P, u.n) && u.h + 1 < P.a.Hkv;
+  }
+  static __device__ __forceinline__ int weight(const AttnParams& P, const Unit& u) {
+    return !kWeighted ? 1 : u.rows > 128 ? 3 : P.a.Hkv > 1 ? 4 : 2;
+  }
+  // units of one row tile of a sequence with n rows
+  static __device__ __forceinline__ int groups(const AttnParams& P, int n) {
+    return pairs(P, n) ? (P.a.Hkv + 1) / 2 : P.a.Hkv;
+  }
   static __device__ __forceinline__ Seq seq_of(const AttnParams& P, int b) {
     Seq s = load_seq(P.a.cu_new, P.a.kv_lens, b, P.a.T, P.capacity, P.a.max_new);
     const int64_t rows = (int64_t)s.n * P.g;
@@ -140,14 +156,14 @@ struct UnitMap {
     u->tile0 = u->key_lo / K;
     u->tiles = max(1, (u->key_hi + K - 1) / K - u->tile0);
   }
-  // length of one key head's units
+  // length of the units of one key head, or of a pair
   static __device__ __forceinline__ int64_t head_tiles(const AttnParams& P, const Seq& s) {
     const int m = row_tiles(P, s);
     int64_t t = 0;
     Unit u;
     for (int qt = 0; qt < m; ++qt) {
       fill(P, s, qt, &u);
-      t += u.tiles * weight(u) + kPad;
+      t += u.tiles * weight(P, u) + kPad;
     }
     return t;
   }
@@ -194,22 +210,24 @@ __device__ __forceinline__ int64_t span_begin(int64_t total, int ctas, int c) {
 // At position t of a span, at unit u: the place in the unit, how many of its tiles are this CTA's, and
 // whether the span ends with it.
 template <class M>
-__device__ __forceinline__ int tiles_before(int64_t at, const Unit& u) {  // tiles that begin before `at` of a unit
+__device__ __forceinline__ int tiles_before(const AttnParams& P, int64_t at, const Unit& u) {  // that begin before `at`
   if (!M::kWeighted) return (int)min(at, (int64_t)u.tiles);
-  const uint32_t x = (uint32_t)min(at, (int64_t)u.tiles * 3);  // (below 2^26)
-  return min(u.tiles, (int)(M::weight(u) == 3 ? (x + 2) / 3 : (x + 1) / 2));
+  const uint32_t x = (uint32_t)min(at, (int64_t)u.tiles * M::kMaxWeight);  // (below 2^26)
+  const int w = M::weight(P, u);
+  return min(u.tiles, (int)(w == 3 ? (x + 2) / 3 : w == 4 ? (x + 3) / 4 : (x + 1) / 2));
 }
 template <class M>
-__device__ __forceinline__ int tile_in_unit(int64_t t, const Unit& u, int64_t unit_begin) {
-  return tiles_before<M>(t - unit_begin, u);
+__device__ __forceinline__ int tile_in_unit(const AttnParams& P, int64_t t, const Unit& u, int64_t unit_begin) {
+  return tiles_before<M>(P, t - unit_begin, u);
 }
 template <class M>
-__device__ __forceinline__ int tiles_here(const Span& span, const Unit& u, int64_t unit_begin, int64_t t) {
-  return tiles_before<M>(span.t1 - unit_begin, u) - tile_in_unit<M>(t, u, unit_begin);
+__device__ __forceinline__ int tiles_here(const AttnParams& P, const Span& span, const Unit& u, int64_t unit_begin,
+                                          int64_t t) {
+  return tiles_before<M>(P, span.t1 - unit_begin, u) - tile_in_unit<M>(P, t, u, unit_begin);
 }
 template <class M>
-__device__ __forceinline__ bool last_in_span(const Span& span, const Unit& u, int64_t unit_begin) {
-  return unit_begin + (int64_t)u.tiles * M::weight(u) + M::kPad >= span.t1;
+__device__ __forceinline__ bool last_in_span(const AttnParams& P, const Span& span, const Unit& u, int64_t unit_begin) {
+  return unit_begin + (int64_t)u.tiles * M::weight(P, u) + M::kPad >= span.t1;
 }
 
 template <int R, int K, bool kTree = false>
@@ -229,7 +247,7 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
     s.n = 0;
     if (base + tid < B) s = M::seq_of(P, base + tid);
     per_head = M::head_tiles(P, s);
-    total += block_scan<NT>(per_head * P.a.Hkv, buf, &ex);
+    total += block_scan<NT>(per_head * M::groups(P, s.n), buf, &ex);
   }
   span->total = total;
   // every span holds a tile of the unit that it lies in
@@ -245,17 +263,18 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
       s.n = 0;
       if (base + tid < B) s = M::seq_of(P, base + tid);
       per_head = M::head_tiles(P, s);
-      sum = block_scan<NT>(per_head * P.a.Hkv, buf, &ex);
+      sum = block_scan<NT>(per_head * M::groups(P, s.n), buf, &ex);
     }
     int64_t rest = span->t0 - (seen + ex);
-    if (rest >= 0 && rest < per_head * P.a.Hkv) {  // in this thread's sequence
+    if (rest >= 0 && rest < per_head * M::groups(P, s.n)) {  // in this thread's sequence
       Unit v;
       v.b = base + tid;
-      v.h = (int)quotient(rest, per_head);
-      rest -= v.h * per_head;
+      const int group = (int)quotient(rest, per_head);
+      v.h = M::pairs(P, s.n) ? 2 * group : group;
+      rest -= group * per_head;
       for (int qt = 0;; ++qt) {
         M::fill(P, s, qt, &v);
-        const int64_t length = (int64_t)v.tiles * M::weight(v) + M::kPad;
+        const int64_t length = (int64_t)v.tiles * M::weight(P, v) + M::kPad;
         if (rest < length) break;
         rest -= length;
       }
@@ -268,8 +287,8 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
   __syncthreads();
   *u = found;
   *unit_begin = found_begin;
-  if (M::kPad > 0 && tile_in_unit<M>(span->t0, found, found_begin) >= found.tiles) {  // behind the unit's tiles
-    *unit_begin += (int64_t)found.tiles * M::weight(found) + M::kPad;
+  if (M::kPad > 0 && tile_in_unit<M>(P, span->t0, found, found_begin) >= found.tiles) {  // behind the unit's tiles
+    *unit_begin += (int64_t)found.tiles * M::weight(P, found) + M::kPad;
     if (*unit_begin >= span->t1) return false;
     next_unit<R, K, kTree>(P, u);
     span->t0 = *unit_begin;
@@ -280,8 +299,8 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
 // On to the next unit; false if the span ends.
 template <class M, int R, int K, bool kTree>
 __device__ __forceinline__ bool advance(const AttnParams& P, const Span& span, Unit* u, int64_t* unit_begin, int64_t* t) {
-  if (last_in_span<M>(span, *u, *unit_begin)) return false;
-  *unit_begin += (int64_t)u->tiles * M::weight(*u) + M::kPad;
+  if (last_in_span<M>(P, span, *u, *unit_begin)) return false;
+  *unit_begin += (int64_t)u->tiles * M::weight(P, *u) + M::kPad;
   *t = *unit_begin;
   next_unit<R, K, kTree>(P, u);
   return true;
@@ -296,7 +315,8 @@ __device__ __forceinline__ void next_unit(const AttnParams& P, Unit* u) {
     M::fill(P, s, u->qt + 1, u);
     return;
   }
-  if (++u->h >= P.a.Hkv) {
+  u->h += M::pairs(P, u->n) ? 2 : 1;
+  if (u->h >= P.a.Hkv) {
     u->h = 0;
     do {
       s = M::seq_of(P, ++u->b);
@@ -317,10 +337,10 @@ __device__ __forceinline__ int cta_of_tile(const Span& sp, int64_t t) {
 // it is another's.
 template <class M>
 __device__ __forceinline__ void note_cut(const AttnParams& P, const Span& span, const Unit& u, int64_t unit_begin) {
-  CutUnit c{0, 0, 0, 0, 0, 0};
-  const int64_t last = unit_begin + (int64_t)(u.tiles - 1) * M::weight(u);  // where the last tile is
+  CutUnit c{0, 0, 0, 0, 0, 0, 0};
+  const int64_t last = unit_begin + (int64_t)(u.tiles - 1) * M::weight(P, u);  // where the last tile is
   if (unit_begin >= span.t0 && last >= span.t1)
-    c = CutUnit{u.rows, u.row0, u.q0, u.h, (int)blockIdx.x, cta_of_tile(span, last)};
+    c = CutUnit{u.rows, u.row0, u.q0, u.h, (int)blockIdx.x, cta_of_tile(span, last), M::is_pair(P, u)};
   P.cut[blockIdx.x] = c;
 }
 
