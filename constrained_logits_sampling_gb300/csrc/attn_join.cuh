@@ -102,7 +102,8 @@ __device__ __forceinline__ void finish_row(const AttnParams& P, const CutUnit& u
   if (d == 0 && P.a.lse) P.a.lse[(int64_t)token * P.a.Hq + head] = lse_of(s.m, s.l);
 }
 
-template <class T, int D, bool kTree = false>
+// R: rows of a unit of the stream kernel
+template <class T, int D, bool kTree = false, int R = kStreamRows>
 __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid_constant__ JoinParams J) {
   const AttnParams& P = J.p;
   constexpr int kCols = D / 16;                  // of 16 elements
@@ -216,7 +217,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid
       const int sub = lane / kPer, d = lane % kPer * 4;
       const int r = few ? at * kStreamStep + warp * kRowsPerWarp + sub : at;
       const bool live = r < u.rows;
-      constexpr int R = kStreamRows;
       auto load = [&](int part, float* m, float* l, float4 (&v)[1]) {
         const float* s = P.partial + (int64_t)((u.c0 + part) * 2 + (part == 0 ? 1 : 0)) * (R * (D + 2));
         *m = __ldcg(s + R * D + r);

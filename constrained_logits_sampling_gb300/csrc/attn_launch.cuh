@@ -19,11 +19,12 @@ namespace clsample {
 namespace {  // each source that includes this has kernels of its own
 
 constexpr int kStreamCtas = 2;  // per SM
+constexpr int kTreeStreamRows = 32;
 constexpr float kMaxScale = 2.0e38f;  // times log2(e) is still finite
 // The scratch, per SM: both kernels' slots (two per CTA, of rows of 128 sums, a maximum and a
 // sum), their cut units, and one word for all.
 constexpr size_t kChunkSlots = 2 * (size_t)kChunkRows * 130 * sizeof(float);
-constexpr size_t kStreamSlots = kStreamCtas * 2 * (size_t)kStreamRows * 130 * sizeof(float);
+constexpr size_t kStreamSlots = kStreamCtas * 2 * (size_t)kMaxStreamRows * 130 * sizeof(float);
 constexpr size_t kCuts = (1 + kStreamCtas) * sizeof(CutUnit);
 constexpr size_t kScratch = kChunkSlots + kStreamSlots + kCuts;
 // A launch that may start while the one before it ends.
@@ -113,11 +114,11 @@ cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
 }
 
 // first: of the call
-template <class T, int D, bool kTree>
+template <class T, int D, bool kTree, int RB>
 cudaError_t launch_stream(const AttnParams& P, int sms, bool first, cudaStream_t st) {
   const int grid = sms * kStreamCtas;
-  auto* fn = attn_stream_kernel<T, D, kTree>;
-  const int bytes = StreamRing<D>::kBytes;
+  auto* fn = attn_stream_kernel<T, D, kTree, RB>;
+  const int bytes = StreamRing<D, RB>::kBytes;
   static std::atomic<uint64_t> allowed;
   const cudaError_t e = allow_smem_once(fn, bytes, &allowed);
   if (e != cudaSuccess) return e;
@@ -126,8 +127,9 @@ cudaError_t launch_stream(const AttnParams& P, int sms, bool first, cudaStream_t
   return cudaGetLastError();
 }
 
-template <class T, int D, bool kTree>
-cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
+template <class T, int D, bool kTree, int RB>
+cudaError_t launch(const clsample_attention* h, AttnParams P, int64_t most_rows, cudaStream_t st) {
+  constexpr int kRows = RB * kStreamRows;
   // no valid sequence has more rows than this; one that breaks the bound has no keys
   const int64_t rows = P.a.max_new * (int64_t)P.g;
   float* const chunk_partial = reinterpret_cast<float*>(h->scratch);
@@ -135,29 +137,41 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, cudaStream_t st) {
   CutUnit* const chunk_cut = reinterpret_cast<CutUnit*>(h->scratch + h->sms * (kChunkSlots + kStreamSlots));
   CutUnit* const stream_cut = chunk_cut + h->sms;
   P.gave_up = reinterpret_cast<int*>(stream_cut + h->sms * kStreamCtas);
-  // Sequences of up to 16 packed rows go to the stream kernel, longer ones to the chunk
-  // kernel.  256 sequences of 16 rows over 2.3 GB of keys and values: 385 us in the one, 441 in
-  // the other; of 24 rows, where the one reads keys twice: 707 and 420.
-  const bool chunks = rows > kStreamRows;
+  const bool chunks = rows > most_rows;
   // Beside longer sequences, a few short ones are not worth a launch of their own: 19 ragged
   // sequences on 12 key heads take 31 us alone in the chunk kernel and 35 us in both; 240
   // sequences of one token and 16 of 512, on 8 key heads, 708 and 590.
   const bool alone = chunks && (int64_t)P.a.B * P.a.Hkv <= 4 * h->sms;
   cudaError_t e;
   if (chunks) {
-    P.min_rows = alone ? 0 : kStreamRows + 1;
+    P.min_rows = alone ? 0 : (int)most_rows + 1;
     P.max_rows = 0x7fffffff;
     P.partial = chunk_partial;
     P.cut = chunk_cut;
     if ((e = launch_chunk<T, D, kTree>(P, h->sms, st)) != cudaSuccess) return e;
   }
   P.min_rows = 0;
-  P.max_rows = chunks ? kStreamRows + 1 : 0x7fffffff;
+  P.max_rows = chunks ? (int)most_rows + 1 : 0x7fffffff;
   P.partial = stream_partial;
   P.cut = stream_cut;
-  if (!alone && (e = launch_stream<T, D, kTree>(P, h->sms, !chunks, st)) != cudaSuccess) return e;
+  if (!alone && (e = launch_stream<T, D, kTree, RB>(P, h->sms, !chunks, st)) != cudaSuccess) return e;
   const JoinParams J{P, chunk_partial, chunk_cut, chunks ? h->sms : 0, alone ? 0 : h->sms * kStreamCtas};
-  return launch_after(attn_join_kernel<T, D, kTree>, h->sms * 2, kJoinThreads, 0, st, J);
+  return launch_after(attn_join_kernel<T, D, kTree, kRows>, h->sms * 2, kJoinThreads, 0, st, J);
+}
+
+// Sequences of up to `most_rows` packed rows go to the stream kernel, longer ones to the chunk
+// kernel.  By position: 256 sequences of 16 rows over 2.3 GB of keys and values take 385 us in the
+// one and 441 in the other; of 24 rows, where the one reads keys twice, 707 and 420.  By mask, where the
+// stream kernel has units of 32 rows if any sequence may have more than 16: THRESHOLDS
+template <class T, int D, bool kTree>
+cudaError_t launch(const clsample_attention* h, const AttnParams& P, cudaStream_t st) {
+  if constexpr (!kTree) {
+    return launch<T, D, false, 1>(h, P, kStreamRows, st);
+  } else {
+    const int64_t rows = P.a.max_new * (int64_t)P.g;
+    if (rows <= kStreamRows) return launch<T, D, true, 1>(h, P, kStreamRows, st);
+    return launch<T, D, true, 2>(h, P, kTreeStreamRows, st);
+  }
 }
 
 // The checks of a call's arguments.

@@ -10,6 +10,11 @@
 // 386 us, 5.9 TB/s, with rows of 256 bytes 2 KB apart in the cache; one token over 777 keys: 12 us.
 // A warp of its own that copied by TMA, on into the next unit while the others ended one, was no
 // faster (on an earlier version, 407 us against 404) and slower where a unit is one tile (19 and 15).
+//
+// RB = 2 (with kTree): a unit is 32 rows, each warp has both halves of them, and a piece of keys or
+// values is read from shared memory once for the two.  There the queries stay in shared memory, as the
+// sums take the registers.  mma.sync bounds what rows cost: 16 rows of 64 requests over 2000 keys take
+// 35 us of it, beside 80 us of memory.
 #pragma once
 
 #include "attn_units.cuh"
@@ -76,11 +81,13 @@ constexpr float kLn2 = 0.693147180559945309f;
 // Ring stages of a warp: two CTAs fit an SM, with up to 128 KB of loads in flight for heads of 128
 // and 160 KB for heads of 64 (all stages but the one that is worked on).
 constexpr int kStreamRows = 16;
-template <int D>
+constexpr int kMaxStreamRows = 2 * kStreamRows;
+template <int D, int RB = 1>
 struct StreamRing {
   static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kBytes = kStages * kStreamKeys * D * 2 * 2;  // keys and values
-  static_assert(kBytes >= 4 * kStreamRows * (D + 8) * 4, "room for four warps' sums");
+  static constexpr int kRing = kStages * kStreamKeys * D * 2 * 2;  // keys and values
+  static constexpr int kBytes = kRing + (RB > 1 ? RB * kStreamRows * D * 2 : 0);  // and queries
+  static_assert(kRing >= 4 * RB * kStreamRows * (D + 8) * 4, "room for four warps' sums");
 };
 
 // A scratch slot: R x D sums, then R maxima (log2 units) and R weights' sums.
@@ -106,28 +113,27 @@ __device__ __forceinline__ void store_lse(const AttnParams& P, const Unit& u, in
     P.a.lse[(int64_t)(u.q0 + token_of(P, row)) * P.a.Hq + (u.h + other) * P.g + head_of(P, row)] = lse_of(m, l);
 }
 
-// The rows of a unit as one warp has them: queries as A operands, limits and running sums.  Lane
-// i has rows i / 4 and i / 4 + 8.
-template <class T, int D, bool kTree = false>
+// The rows of a unit as one warp has them: queries as A operands (RB 1), limits and running sums.  Lane
+// i has rows i / 4 and i / 4 + 8 of each 16.
+template <class T, int D, bool kTree = false, int RB = 1>
 struct StreamState {
-  uint32_t q[D / 16][4];
-  int pos[2];
-  const uint32_t* mask[2];  // kTree: the rows' words, or null
-  int n;                    // kTree: the sequence's new tokens
+  uint32_t q[RB == 1 ? D / 16 : 1][4];
+  uint32_t q_smem;              // RB > 1: rows of 64 elements, swizzled as keys are
+  int pos[2 * RB];
+  const uint32_t* mask[2 * RB];  // kTree: the rows' words, or null
+  int n;                         // kTree: the sequence's new tokens
   int pos_first, pos_last;
-  float o[D / 8][4];
-  float m[2], l[2];
+  float o[RB][D / 8][4];
+  float m[2 * RB], l[2 * RB];
 
   __device__ __forceinline__ void begin(const AttnParams& P, const Unit& u) {
     const int lane = threadIdx.x & 31;
     const float neg_inf = __int_as_float(0xff800000);
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+    for (int hf = 0; hf < 2 * RB; ++hf) {
       const int r = hf * 8 + (lane >> 2);
       const bool live = r < u.rows;
       const int row = u.row0 + r;
-      const T* src = (const T*)P.a.q + (int64_t)(u.q0 + (live ? token_of(P, row) : 0)) * P.a.q_stride_t +
-                     (int64_t)(u.h * P.g + (live ? head_of(P, row) : 0)) * P.a.q_stride_h + (lane & 3) * 2;
       if constexpr (kTree) {
         const int i = live ? token_of(P, row) : 0;
         pos[hf] = tree_position(P, u.q0 + i, i, u.len, u.n);
@@ -135,10 +141,14 @@ struct StreamState {
       } else {
         pos[hf] = live ? u.len - u.n + token_of(P, row) : -1;
       }
+      if constexpr (RB == 1) {
+        const T* src = (const T*)P.a.q + (int64_t)(u.q0 + (live ? token_of(P, row) : 0)) * P.a.q_stride_t +
+                       (int64_t)(u.h * P.g + (live ? head_of(P, row) : 0)) * P.a.q_stride_h + (lane & 3) * 2;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        q[ks][hf] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16)) : 0u;
-        q[ks][hf + 2] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16 + 8)) : 0u;
+        for (int ks = 0; ks < D / 16; ++ks) {
+          q[ks][hf] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16)) : 0u;
+          q[ks][hf + 2] = live ? __ldg(reinterpret_cast<const unsigned*>(src + ks * 16 + 8)) : 0u;
+        }
       }
       m[hf] = neg_inf;
       l[hf] = 0.f;
@@ -148,9 +158,26 @@ struct StreamState {
     pos_last = kTree ? u.len - 1 : u.len - u.n + token_of(P, u.row0 + u.rows - 1);
     n = min(u.n, u.len);  // (no keys: none)
 #pragma unroll
-    for (int d = 0; d < D / 8; ++d)
+    for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+      for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[rb][d][e] = 0.f;
+  }
+
+  // RB > 1: the unit's queries to shared memory, by all threads; rows past the unit's are zero.
+  __device__ __forceinline__ void load_queries(const AttnParams& P, const Unit& u, unsigned char* smem) {
+    constexpr int kRows = RB * kStreamRows, KC = D / 8;
+    q_smem = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    for (int i = threadIdx.x; i < kRows * KC; i += kStreamThreads) {
+      const int r = i / KC, ch = i % KC, row = u.row0 + r;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < u.rows)
+        x = __ldg(reinterpret_cast<const uint4*>((const T*)P.a.q + (int64_t)(u.q0 + token_of(P, row)) * P.a.q_stride_t +
+                                                 (int64_t)(u.h * P.g + head_of(P, row)) * P.a.q_stride_h + ch * 8));
+      *reinterpret_cast<uint4*>(smem + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+    }
+    __syncthreads();
   }
 
   // 16 keys from position `key` on, of which those in `live` exist.  Rows of 64 elements in
@@ -159,38 +186,54 @@ struct StreamState {
                                        unsigned live) {
     const int lane = threadIdx.x & 31;
     const float neg_inf = __int_as_float(0xff800000);
-    float s[2][4];
+    float s[RB][2][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[rb][0][e] = s[rb][1][e] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       const int row = (lane & 7) + ((lane >> 4) << 3), ch = ks * 2 + ((lane >> 3) & 1);
       uint32_t b[4];
       ldmatrix4(b, kb + (ch >> 3) * half + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-      mma16816<T>(s[0], q[ks], b[0], b[1]);
-      mma16816<T>(s[1], q[ks], b[2], b[3]);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        uint32_t qa[4];
+        if constexpr (RB == 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qa[e] = q[ks][e];
+        } else {
+          const int qr = rb * 16 + (lane & 15), qc = ks * 2 + (lane >> 4);
+          ldmatrix4(qa, q_smem + (qc >> 3) * (RB * kStreamRows * 128) + qr * 128 + (((qc & 7) ^ (qr & 7)) << 4));
+        }
+        mma16816<T>(s[rb][0], qa, b[0], b[1]);
+        mma16816<T>(s[rb][1], qa, b[2], b[3]);
+      }
     }
     const int window = P.a.window;
     // every key of the tile is seen by every row (rows past the unit's are never stored)
     const bool whole = live == 0xffffu && key + 15 <= pos_first && (window <= 0 || key > pos_last - window);
-    uint32_t seen[2] = {0, 0};  // kTree: bit c, key + c
+    uint32_t seen[2 * RB] = {};  // kTree: bit c, key + c
     if (kTree && !whole) {
+      uint32_t any = 0;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+      for (int hf = 0; hf < 2 * RB; ++hf)
         if (mask[hf]) {
           seen[hf] = column_bits(window > 0 ? pos[hf] - window + 1 - key : 0, pos_first - key);
           if (key + 15 > pos_first) seen[hf] |= mask_word(mask[hf], n, key - pos_first - 1);
           seen[hf] &= live;
+          any |= seen[hf];
         }
-      live &= __reduce_or_sync(~0u, seen[0] | seen[1]);  // what no row sees may be anything
+      live &= __reduce_or_sync(~0u, any);  // what no row sees may be anything
     }
     bool moved = false;
-    float keep[2];
-    uint32_t p[4];
+    float keep[2 * RB];
+    uint32_t p[RB][4];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float x[4] = {s[0][hf * 2] * P.scale_log2, s[0][hf * 2 + 1] * P.scale_log2, s[1][hf * 2] * P.scale_log2,
-                    s[1][hf * 2 + 1] * P.scale_log2};
+    for (int hf = 0; hf < 2 * RB; ++hf) {
+      const int rb = hf >> 1, e0 = (hf & 1) * 2;
+      float x[4] = {s[rb][0][e0] * P.scale_log2, s[rb][0][e0 + 1] * P.scale_log2, s[rb][1][e0] * P.scale_log2,
+                    s[rb][1][e0 + 1] * P.scale_log2};
       if (!whole) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -216,17 +259,19 @@ struct StreamState {
         sum += x[e];
       }
       l[hf] = l[hf] * keep[hf] + sum;
-      p[hf] = Pair<T>::narrow(x[0], x[1]);
-      p[hf + 2] = Pair<T>::narrow(x[2], x[3]);
+      p[rb][hf & 1] = Pair<T>::narrow(x[0], x[1]);
+      p[rb][(hf & 1) + 2] = Pair<T>::narrow(x[2], x[3]);
     }
     if (__any_sync(~0u, moved)) {
 #pragma unroll
-      for (int d = 0; d < D / 8; ++d) {
-        o[d][0] *= keep[0];
-        o[d][1] *= keep[0];
-        o[d][2] *= keep[1];
-        o[d][3] *= keep[1];
-      }
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          o[rb][d][0] *= keep[2 * rb];
+          o[rb][d][1] *= keep[2 * rb];
+          o[rb][d][2] *= keep[2 * rb + 1];
+          o[rb][d][3] *= keep[2 * rb + 1];
+        }
     }
     // values of keys that do not exist may be anything, and 0 x NaN is NaN
     const unsigned two = live >> ((lane & 3) * 2);
@@ -237,22 +282,25 @@ struct StreamState {
       const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = d * 2 + (lane >> 4);
       uint32_t b[4];
       ldmatrix4_trans(b, vb + (ch >> 3) * half + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-      mma16816<T>(o[2 * d], p, b[0] & mask0, b[1] & mask1);
-      mma16816<T>(o[2 * d + 1], p, b[2] & mask0, b[3] & mask1);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        mma16816<T>(o[rb][2 * d], p[rb], b[0] & mask0, b[1] & mask1);
+        mma16816<T>(o[rb][2 * d + 1], p[rb], b[2] & mask0, b[3] & mask1);
+      }
     }
   }
 };
 
 // The warps' results of a unit's span meet: meet holds [warp][row][D + 8] (rows begin in different
 // banks), wm and wl the warps' maxima and sums.
-template <class T, int D, bool kTree>
-__device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u, StreamState<T, D, kTree>& st, float* meet,
-                                              float (&wm)[4][kStreamRows], float (&wl)[4][kStreamRows], bool done,
-                                              float* slot) {
+template <class T, int D, bool kTree, int RB>
+__device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u, StreamState<T, D, kTree, RB>& st,
+                                              float* meet, float (&wm)[4][RB * kStreamRows],
+                                              float (&wl)[4][RB * kStreamRows], bool done, float* slot) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int R = kStreamRows;
+  constexpr int R = RB * kStreamRows;
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
+  for (int hf = 0; hf < 2 * RB; ++hf) {
     float sum = st.l[hf];
     sum += __shfl_xor_sync(~0u, sum, 1);
     sum += __shfl_xor_sync(~0u, sum, 2);
@@ -264,10 +312,10 @@ __device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u
 #pragma unroll
   for (int d = 0; d < D / 8; ++d)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+    for (int hf = 0; hf < 2 * RB; ++hf) {
       const int col = d * 8 + (lane & 3) * 2, row = hf * 8 + (lane >> 2);
       *reinterpret_cast<float2*>(meet + (warp * R + row) * (D + 8) + col) =
-          make_float2(st.o[d][hf * 2], st.o[d][hf * 2 + 1]);
+          make_float2(st.o[hf >> 1][d][(hf & 1) * 2], st.o[hf >> 1][d][(hf & 1) * 2 + 1]);
     }
   __syncthreads();
   for (int i = tid; i < u.rows * (D / 4); i += kStreamThreads) {
@@ -298,11 +346,11 @@ __device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u
   __syncthreads();  // for the next unit
 }
 
-template <class T, int D, bool kTree = false>
+template <class T, int D, bool kTree = false, int RB = 1>
 __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __grid_constant__ AttnParams P) {
-  using Map = UnitMap<kStreamRows, kStreamKeys, kTree>;
-  constexpr int R = kStreamRows, S = StreamRing<D>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
+  constexpr int R = RB * kStreamRows, S = StreamRing<D, RB>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
   constexpr int kTileBytes = 16 * D * 2, kStageBytes = 2 * kTileBytes, kHalf = 16 * 128;
+  using Map = UnitMap<R, kStreamKeys, kTree>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ unsigned key_ok[4][S];
   __shared__ float wm[4][R], wl[4][R];
@@ -367,7 +415,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
       issue(i, page);
       page = next;
     }
-    StreamState<T, D, kTree> st;
+    StreamState<T, D, kTree, RB> st;
+    if constexpr (RB > 1) st.load_queries(P, u, smem + StreamRing<D, RB>::kRing);
     st.begin(P, u);
     for (int i = 0; i < cnt; ++i) {
       cp_async_wait<S - 2>();
@@ -381,7 +430,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
     }
     cp_async_wait<0>();
     __syncthreads();  // the rings are drained: the first is where the warps meet
-    stream_finish<T, D, kTree>(P, u, st, reinterpret_cast<float*>(smem), wm, wl, cnt == u.tiles,
+    stream_finish<T, D, kTree, RB>(P, u, st, reinterpret_cast<float*>(smem), wm, wl, cnt == u.tiles,
                                    scratch_slot<R, D>(P, blockIdx.x, j0 == 0 ? 1 : 0));
     if (!advance<Map, R, kStreamKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
   }

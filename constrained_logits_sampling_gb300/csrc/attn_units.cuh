@@ -108,7 +108,7 @@ __device__ __forceinline__ int tree_position(const AttnParams& P, int t, int i, 
 // (a pair: heads h and h + 1; the last of an odd number is alone).
 template <int R, int K, bool kTree = false>
 struct UnitMap {
-  static constexpr bool kWeighted = kTree && R > 128;
+  static constexpr bool kWeighted = kTree && R > 128;  // the chunk kernel's
   static constexpr int kPad = !kTree ? 0 : kWeighted ? kChunkPad : kStreamPad;
   static constexpr int kMaxWeight = kWeighted ? 4 : 1;
   static __device__ __forceinline__ bool pairs(const AttnParams& P, int n) {
