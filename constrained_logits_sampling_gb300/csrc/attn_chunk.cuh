@@ -25,7 +25,7 @@
 // 2500 a tile, the rest of it the way from a finished S over the softmax (970) to the next product.
 // A unit of at most 128 rows has one row tile: both halves of the CTA then take the same
 // queries and every other key tile, and their sums are joined at the end, in the room of the
-// second row tile's queries.  With kTree two key heads make such a unit (a pair, attn_units.cuh): each half
+// second row tile's queries.  With kPairs two key heads make such a unit (attn_units.cuh): each half
 // takes the queries of one and all key tiles of it, copied in turns, and nothing is joined.
 #pragma once
 
@@ -42,9 +42,14 @@ constexpr int kChunkKeys = 128;
 constexpr float kRescaleAt = 8.f;  // log2
 
 // Registers a thread: the two softmax warpgroups, and the one of loads and products.  They
-// add up to what the block is launched with (3 x 168).
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168 && 168 * kChunkThreads <= 65536, "the launch's registers");
+// add up to what the block is launched with (3 x 168).  With kTree the loads look at masks and at units of
+// other kinds, and take more; what does not stay in registers goes a long way here, as shared memory
+// leaves L1 little room (64 trees of up to 32 rows: 117 us with 200 and 104, 114 so).
+template <bool kTree>
+struct ChunkRegs {
+  static constexpr int kSoftmax = kTree ? 192 : 200, kOther = kTree ? 120 : 104;
+  static_assert(2 * kSoftmax + kOther == 3 * 168 && 168 * kChunkThreads <= 65536, "the launch's registers");
+};
 
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -146,12 +151,13 @@ struct SoftmaxSync {  // the 256 softmax threads
 // them, and go on to no other.  Then all pause while copies land.  The call's statuses tell that
 // its outputs are void.
 
-template <class T, int D, bool kTma, bool kTree = false>
+template <class T, int D, bool kTma, bool kTree = false, bool kPairs = false>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     attn_chunk_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
   using Shape = ChunkShape<D>;
-  using Map = UnitMap<kChunkRows, kChunkKeys, kTree>;
+  using Map = UnitMap<kChunkRows, kChunkKeys, kTree, kPairs>;
+  constexpr int kSoftmaxRegs = ChunkRegs<kTree>::kSoftmax, kOtherRegs = ChunkRegs<kTree>::kOther;
   constexpr int NS = Shape::kKeySlots, NV = Shape::kValueSlots, kTile = Shape::kTile, KC = D / 8;
   constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 elements
   constexpr int kRowWarps = kTma ? 1 : 2;  // that copy rows
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   Span span;
   Unit u;
   int64_t unit_begin;
-  const bool work = find_span<kChunkRows, kChunkKeys, kChunkThreads, kTree>(P, &span, &u, &unit_begin);
+  const bool work = find_span<Map, kChunkThreads>(P, &span, &u, &unit_begin);
   if (tid == 0) sh.span = span;
   tc_fence_before();
   __syncthreads();
@@ -537,9 +543,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     };
     // The slot of a tile's keys is free when S of the tile that had it is complete, and the
     // slot of its values when O is, which a later tile's completion covers: the next one's if
-    // both halves take each tile, the one after it otherwise (and across units, where either
-    // may have been the case; a pair's copies are taken in turns).  Of twice as many completions as there are key slots the one
-    // waited for is still the last on its barrier.
+    // both halves take each tile, the one after it otherwise (a pair's copies are taken in turns; and
+    // across units, where either may have been the case).  Of twice as many completions as there are key
+    // slots the one waited for is still the last on its barrier.
     auto tile_done = [&](int64_t gate) {
       if (gate >= 0) bounded_wait(&sh.tile_done[gate % (2 * NS)], (gate / (2 * NS)) & 1, &sh.limit);
       __syncwarp();
@@ -604,7 +610,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h + head, from, full);
           }
         }
-        if (!advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
+        if (!advance<Map>(P, span, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
       }
     } else if (kTma) {
       uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
@@ -652,7 +658,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         it += cnt * copies;
         ++seg;
-        if (!advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
+        if (!advance<Map>(P, span, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (warp < 10) {
@@ -713,7 +719,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        if (!advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
+        if (!advance<Map>(P, span, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (lane == 0) {
@@ -733,7 +739,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           fence_async_proxy();
           mbar_arrive(&sh.v_full[it % NV]);
         }
-      } while (alive && advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t));
+      } while (alive && advance<Map>(P, span, &u, &unit_begin, &t));
     }
   } else {
     // ------------------------------------------------------------------ products
@@ -832,7 +838,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        if (!uni(advance<Map, kChunkRows, kChunkKeys, kTree>(P, span, &u, &unit_begin, &t))) break;
+        if (!uni(advance<Map>(P, span, &u, &unit_begin, &t))) break;
       }
       // products still running when a wait gave up end before their memory is freed
       if (!alive) {

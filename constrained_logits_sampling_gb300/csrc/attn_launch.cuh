@@ -19,7 +19,6 @@ namespace clsample {
 namespace {  // each source that includes this has kernels of its own
 
 constexpr int kStreamCtas = 2;  // per SM
-constexpr int kTreeStreamRows = 32;
 constexpr float kMaxScale = 2.0e38f;  // times log2(e) is still finite
 // The scratch, per SM: both kernels' slots (two per CTA, of rows of 128 sums, a maximum and a
 // sum), their cut units, and one word for all.
@@ -105,9 +104,15 @@ cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
                      cache_map(P, P.a.k_cache, &k_map) && cache_map(P, P.a.v_cache, &v_map);
   P.q_box = boxes && query_map(P, &q_map);
   const int bytes = ChunkShape<D>::kBytes;
+  // By mask, many units a CTA go in pairs, which end and begin side by side: 256 requests of 48 rows over 300
+  // keys on 8 key heads take 141 us so and 177 one by one; 64 requests of 96 to 128 rows over 200 to 4000 keys
+  // 119 and 114, as the kernel's loops are longer.
+  const bool pairs = kTree && (int64_t)P.a.B * P.a.Hkv >= 6 * (int64_t)sms;
   auto* fn = boxes ? attn_chunk_kernel<T, D, true, kTree> : attn_chunk_kernel<T, D, false, kTree>;
-  static std::atomic<uint64_t> allowed[2];
-  const cudaError_t e = allow_smem_once(fn, bytes, &allowed[boxes]);
+  if constexpr (kTree)
+    if (pairs) fn = boxes ? attn_chunk_kernel<T, D, true, true, true> : attn_chunk_kernel<T, D, false, true, true>;
+  static std::atomic<uint64_t> allowed[4];
+  const cudaError_t e = allow_smem_once(fn, bytes, &allowed[2 * pairs + boxes]);
   if (e != cudaSuccess) return e;
   fn<<<sms, kChunkThreads, bytes, st>>>(P, k_map, v_map, q_map);
   return cudaGetLastError();
@@ -161,16 +166,24 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, int64_t most_rows,
 
 // Sequences of up to `most_rows` packed rows go to the stream kernel, longer ones to the chunk
 // kernel.  By position: 256 sequences of 16 rows over 2.3 GB of keys and values take 385 us in the
-// one and 441 in the other; of 24 rows, where the one reads keys twice, 707 and 420.  By mask, where the
-// stream kernel has units of 32 rows if any sequence may have more than 16: THRESHOLDS
+// one and 441 in the other; of 24 rows, where the one reads keys twice, 707 and 420.
+// By mask the stream kernel has units of 32 rows if any sequence may have more than 16.  64 requests of
+// 24 rows over 2000 keys on 8 key heads of 128: 107 us there and 112 in the chunk kernel, over 300 keys 37 and
+// 48; on 4 heads of 64: 42 and 52, 19 and 26.  Up to 64 rows, which read their keys twice, where those are
+// few: 8 requests of 48 rows over 300 keys 19 and 23 us (heads of 64: 12 and 18); with heads of 128
+// only where a CTA has few units (64 requests: 57 and 52).
 template <class T, int D, bool kTree>
 cudaError_t launch(const clsample_attention* h, const AttnParams& P, cudaStream_t st) {
   if constexpr (!kTree) {
     return launch<T, D, false, 1>(h, P, kStreamRows, st);
   } else {
-    const int64_t rows = P.a.max_new * (int64_t)P.g;
+    const int64_t rows = P.a.max_new * (int64_t)P.g, units = (int64_t)P.a.B * P.a.Hkv;
     if (rows <= kStreamRows) return launch<T, D, true, 1>(h, P, kStreamRows, st);
-    return launch<T, D, true, 2>(h, P, kTreeStreamRows, st);
+    const int64_t keys = P.a.window > 0 && (int64_t)P.a.window + P.a.max_new < P.capacity
+                             ? (int64_t)P.a.window + P.a.max_new
+                             : P.capacity;
+    const bool twice = keys <= 512 && (D == 64 || units <= h->sms);
+    return launch<T, D, true, 2>(h, P, twice ? 2 * kMaxStreamRows : kMaxStreamRows, st);
   }
 }
 

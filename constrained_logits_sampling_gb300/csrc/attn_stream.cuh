@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
   Span span;
   Unit u;
   int64_t unit_begin;
-  if (!find_span<R, kStreamKeys, kStreamThreads, kTree>(P, &span, &u, &unit_begin)) {
+  if (!find_span<Map, kStreamThreads>(P, &span, &u, &unit_begin)) {
     if (tid == 0) P.cut[blockIdx.x].rows = 0;
     wait_for_earlier_grids();  // this grid's end stands for theirs
     return;
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
     __syncthreads();  // the rings are drained: the first is where the warps meet
     stream_finish<T, D, kTree, RB>(P, u, st, reinterpret_cast<float*>(smem), wm, wl, cnt == u.tiles,
                                    scratch_slot<R, D>(P, blockIdx.x, j0 == 0 ? 1 : 0));
-    if (!advance<Map, R, kStreamKeys, kTree>(P, span, &u, &unit_begin, &t)) break;
+    if (!advance<Map>(P, span, &u, &unit_begin, &t)) break;
   }
   wait_for_earlier_grids();  // this grid's end stands for theirs
 }

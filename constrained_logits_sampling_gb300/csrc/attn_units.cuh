@@ -46,9 +46,9 @@ __device__ __forceinline__ int token_of(const AttnParams& P, int row) {
 }
 __device__ __forceinline__ int head_of(const AttnParams& P, int row) { return row - token_of(P, row) * P.g; }
 
-// 64 trees of 24 to 32 rows over 200 to 4000 keys on 8 key heads: PADFIG
+// 64 trees of 24 to 32 tokens over 200 to 4000 keys on 8 key heads, in the chunk kernel: 125 us with 8, 121
+// with 12, 117 with 18, 120 with 24 (and 197 with spans of equal tiles).
 constexpr int kChunkPad = 18, kStreamPad = 3;
-constexpr int kMinSpan = 1;  // tiles
 
 struct CutUnit {
   int rows;          // 0: none
@@ -87,7 +87,11 @@ __device__ __forceinline__ uint4 mask_words(const uint32_t* row, int n, int j0) 
   const int w = j0 >> 5, words = (n + 31) >> 5;
   uint32_t x[5];
 #pragma unroll
-  for (int k = 0; k < 5; ++k) x[k] = (unsigned)(w + k) < (unsigned)words ? __ldg(row + w + k) : 0u;
+  for (int k = 0; k < 5; ++k) {  // (volatile: loaded here, not where it is first looked at)
+    x[k] = 0;
+    if ((unsigned)(w + k) < (unsigned)words)
+      asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x[k]) : "l"(row + w + k));
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     x[k] = __funnelshift_r(x[k], x[k + 1], j0 & 31) & column_bits(-j0 - 32 * k, n - 1 - j0 - 32 * k);
@@ -104,21 +108,22 @@ __device__ __forceinline__ int tree_position(const AttnParams& P, int t, int i, 
 // one's first keys.  Sequences of very different lengths would otherwise leave the CTAs with
 // many short units far behind.
 //
-// With kTree, where a key head has one row tile, a unit is two key heads with one row tile each
-// (a pair: heads h and h + 1; the last of an odd number is alone).
-template <int R, int K, bool kTree = false>
+// kPairs: where a key head has one row tile of 128, a unit is two key heads with one row tile each (a
+// pair: heads h and h + 1; the last of an odd number is alone).
+template <int R, int K, bool kTree = false, bool kPairs = false>
 struct UnitMap {
-  static constexpr bool kWeighted = kTree && R > 128;  // the chunk kernel's
+  static constexpr int kRows = R, kKeys = K;
+  static constexpr bool kByMask = kTree, kWeighted = kTree && R > 128;  // weighted: the chunk kernel's
   static constexpr int kPad = !kTree ? 0 : kWeighted ? kChunkPad : kStreamPad;
-  static constexpr int kMaxWeight = kWeighted ? 4 : 1;
+  static constexpr int kMaxWeight = kPairs ? 4 : kWeighted ? 3 : 1;
   static __device__ __forceinline__ bool pairs(const AttnParams& P, int n) {
-    return kWeighted && P.a.Hkv > 1 && (int64_t)n * P.g <= 128;
+    return kPairs && P.a.Hkv > 1 && (int64_t)n * P.g <= 128;
   }
   static __device__ __forceinline__ bool is_pair(const AttnParams& P, const Unit& u) {
-    return pairs(P, u.n) && u.h + 1 < P.a.Hkv;
+    return kPairs && pairs(P, u.n) && u.h + 1 < P.a.Hkv;
   }
   static __device__ __forceinline__ int weight(const AttnParams& P, const Unit& u) {
-    return !kWeighted ? 1 : u.rows > 128 ? 3 : P.a.Hkv > 1 ? 4 : 2;
+    return !kWeighted ? 1 : u.rows > 128 ? 3 : kPairs && P.a.Hkv > 1 ? 4 : 2;
   }
   // units of one row tile of a sequence with n rows
   static __device__ __forceinline__ int groups(const AttnParams& P, int n) {
@@ -230,12 +235,11 @@ __device__ __forceinline__ bool last_in_span(const AttnParams& P, const Span& sp
   return unit_begin + (int64_t)u.tiles * M::weight(P, u) + M::kPad >= span.t1;
 }
 
-template <int R, int K, bool kTree = false>
+template <class M>
 __device__ __forceinline__ void next_unit(const AttnParams& P, Unit* u);
 
-template <int R, int K, int NT, bool kTree = false>
+template <class M, int NT>
 __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit* u, int64_t* unit_begin) {
-  using M = UnitMap<R, K, kTree>;
   __shared__ int64_t buf[NT / 32 + 1];
   __shared__ Unit found;
   __shared__ int64_t found_begin;
@@ -251,7 +255,7 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
   }
   span->total = total;
   // every span holds a tile of the unit that it lies in
-  span->ctas = (int)min((int64_t)gridDim.x, kTree ? max((int64_t)1, quotient(total, kMinSpan * M::kMaxWeight)) : total);
+  span->ctas = (int)min((int64_t)gridDim.x, M::kByMask ? max((int64_t)1, quotient(total, M::kMaxWeight)) : total);
   if (total == 0) return false;
   if ((int)blockIdx.x >= span->ctas) return false;
   span->t0 = span_begin(total, span->ctas, blockIdx.x);
@@ -290,28 +294,27 @@ __device__ __forceinline__ bool find_span(const AttnParams& P, Span* span, Unit*
   if (M::kPad > 0 && tile_in_unit<M>(P, span->t0, found, found_begin) >= found.tiles) {  // behind the unit's tiles
     *unit_begin += (int64_t)found.tiles * M::weight(P, found) + M::kPad;
     if (*unit_begin >= span->t1) return false;
-    next_unit<R, K, kTree>(P, u);
+    next_unit<M>(P, u);
     span->t0 = *unit_begin;
   }
   return true;
 }
 
 // On to the next unit; false if the span ends.
-template <class M, int R, int K, bool kTree>
+template <class M>
 __device__ __forceinline__ bool advance(const AttnParams& P, const Span& span, Unit* u, int64_t* unit_begin, int64_t* t) {
   if (last_in_span<M>(P, span, *u, *unit_begin)) return false;
   *unit_begin += (int64_t)u->tiles * M::weight(P, *u) + M::kPad;
   *t = *unit_begin;
-  next_unit<R, K, kTree>(P, u);
+  next_unit<M>(P, u);
   return true;
 }
 
 // The unit after u (the caller has checked that the span goes on).
-template <int R, int K, bool kTree>
+template <class M>
 __device__ __forceinline__ void next_unit(const AttnParams& P, Unit* u) {
-  using M = UnitMap<R, K, kTree>;
   Seq s{u->q0, u->n, u->len, true};
-  if (u->row0 + R < u->n * P.g) {
+  if (u->row0 + M::kRows < u->n * P.g) {
     M::fill(P, s, u->qt + 1, u);
     return;
   }
