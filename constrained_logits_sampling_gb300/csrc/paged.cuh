@@ -36,17 +36,21 @@ inline int check_device(int* dev_out = nullptr, int* sms = nullptr) {
   return CLSAMPLE_SUCCESS;
 }
 
-// Host: lets kernel fn have `bytes` of dynamic shared memory, which is asked for once a kernel and device.
+// Host: sets an attribute of kernel fn, which is asked for once a kernel and device.
 template <class Kernel>
-cudaError_t allow_smem_once(Kernel* fn, int bytes, std::atomic<uint64_t>* done) {
+cudaError_t allow_once(Kernel* fn, cudaFuncAttribute what, int value, std::atomic<uint64_t>* done) {
   int dev = -1;
   const cudaError_t got = cudaGetDevice(&dev);
   if (got != cudaSuccess) return got;
   const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
   if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = cudaFuncSetAttribute(fn, what, value);
   if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
   return e;
+}
+template <class Kernel>
+cudaError_t allow_smem_once(Kernel* fn, int bytes, std::atomic<uint64_t>* done) {
+  return allow_once(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

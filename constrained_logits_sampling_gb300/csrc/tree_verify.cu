@@ -1,15 +1,18 @@
 // clsample_verify_tree: a walk down a tree of drafted tokens (rule in include/clsample.h).
 //
 // One cluster of CTAs per request, as for clsample_verify.  Every CTA gathers what the walk needs of
-// all drafted tokens at once (parents, ids, random numbers, p and q at the ids) and takes every
-// decision for itself, each warp for itself: a token is tried if its parent is the last accepted one, so
-// the next to try is found by a ballot over the parents.  A refusal by a draft with probabilities needs
+// all drafted tokens at once (parents, ids, random numbers, p and q at the ids).  Its first warp then
+// takes the decisions: a token is tried if its parent is the last accepted one, so the next to try is found
+// by a ballot over the parents.  (All CTAs of a cluster take the same ones.  By all warps they cost 2 us a
+// refusal, as exact comparisons run in the float64 unit.)  A refusal by a draft with probabilities needs
 // the sum of what is left of the row: one pass of the cluster over p and q, whose sums meet in
 // distributed shared memory; the last such pass is also the one that the token is drawn from.  As all
 // refused children of a token came from one row q, what is left is max(P - Q c, 0) with one
-// number c, and a pass costs the same after any number of refusals.
+// number c, and a pass costs the same after any number of refusals.  No pass is needed where the next
+// child is accepted whatever the sum: s does not grow.
 // A draft that is certain needs one pass, over the last token's row, with its refused ids as
-// holes in a bitmap.  Bound by memory: p and q once for each refusal on the path.
+// holes in a bitmap.  Bound by memory where requests are many: p and q once for each refusal on the
+// path; else by the chain of passes, FIGV each.
 #include <cooperative_groups.h>
 
 #include "draw_weights.cuh"
@@ -21,16 +24,24 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = kDrawThreads;
 constexpr int kMaxNodes = 1023;
+constexpr int kMaxCtas = 16;  // of a cluster
 
 struct Shared {
-  int64_t slice_sum[2][kMaxCluster];  // written by the cluster's CTAs, in passes by turns
-  int slice_bad[2][kMaxCluster];
+  int64_t slice_sum[2][kMaxCtas];  // written by the cluster's CTAs, in passes by turns
+  int slice_bad[2][kMaxCtas];
   int64_t warp_sum[kWarps], scan[kWarps];
   int bad;  // of the request; not written after it has been read
   int odd;  // a probability out of range in the CTA's slices
   int x[kMaxNodes + 1], row[kMaxNodes + 1], of_parent[kMaxNodes + 1];  // of_parent: the row of a token's children
   float u[kMaxNodes + 1], p[kMaxNodes + 1], q[kMaxNodes + 1];
   short parent[kMaxNodes + 1], path[kMaxNodes + 1];
+  bool as_first[kMaxNodes + 1];  // accepted if it is its parent's first child
+  // What the first warp has found: whose row to sum (or to draw from, if `end`), less which row how often.
+  struct Step {
+    int node, acc, refused, row;
+    float taken;
+    bool end;
+  } step;
 };
 
 __device__ __forceinline__ int64_t warp_total(int64_t v) {
@@ -93,6 +104,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     sh.u[i] = u;
     sh.p[i] = p;
     sh.q[i] = q;
+    // both factors have 24 bits, so the 64-bit product is exact
+    sh.as_first[i] = (double)u * (double)q < (double)p;
   }
   if (bad) atomicOr(&sh.bad, 1);
   __syncthreads();
@@ -136,70 +149,92 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
   };
 
-  // The walk, the same in every warp of the cluster.
-  int node = -1, acc = 0, refused = 0;  // the last accepted token, how many, refused children of it
-  float share = 1.f, taken = 0.f;       // s and c
-  int64_t removed = 0;                  // without a draft: P of the refused ids
-  bool summed = false;                  // `at` is of the node's row and what has been taken from it
-  // the first token from i on whose parent is `node`, or n
+  // The walk, by the first warp of each CTA of the cluster, up to the next sum that it needs.
+  int node = -1, acc = 0, refused = 0, at_token = -1;  // the last accepted token, how many, refused children of it
+  float share = 1.f, taken = 0.f;                      // s and c
+  int64_t removed = 0;                                 // without a draft: P of the refused ids
+  // the first token after i whose parent is `node`, or n
   auto next_child = [&](int i) {
-    for (int base = i & ~31; base < n; base += 32) {
-      const unsigned m = __ballot_sync(~0u, base + lane >= i && base + lane < n && sh.parent[min(base + lane, n - 1)] == node);
+    for (int base = (i + 1) & ~31; base < n; base += 32) {
+      const int j = base + lane;
+      const unsigned m = __ballot_sync(~0u, j > i && j < n && sh.parent[min(j, n - 1)] == node);
       if (m) return base + __ffs(m) - 1;
     }
     return n;
   };
-  for (int i = bad ? n : next_child(0); i < n && !bad && acc < a.max_path; i = next_child(i + 1)) {
-    const float p = sh.p[i], q = sh.q[i];
-    const double u = sh.u[i];
-    bool ok;
-    if (draft) {
-      double left = p;
-      if (refused) {
-        const float cut = q * taken;
-        left = p > cut ? (double)(mass_at(p) - mass_at(cut)) * 9.094947017729282379150390625e-13 : 0.0;
-      }
-      // both factors have 24 bits, so the 64-bit product is exact
-      ok = u * (double)(q * share) < left;
-    } else {
-      bool again = false;  // a refused child of the same parent has the same id
-      if (refused) {
-        const int x = sh.x[i];
-        for (int base = 0; base < i && !again; base += 32) {
-          const int j = min(base + lane, n - 1);
-          again = __any_sync(~0u, base + lane < i && sh.parent[j] == node && sh.x[j] == x);
+  // Whether token i is accepted with share s; for a draft with probabilities.
+  auto accepts = [&](int i, float s) {
+    if (!refused) return (bool)sh.as_first[i];
+    const float p = sh.p[i], q = sh.q[i], cut = q * taken;
+    const double left = p > cut ? (double)(mass_at(p) - mass_at(cut)) * 9.094947017729282379150390625e-13 : 0.0;
+    return (double)sh.u[i] * (double)(q * s) < left;
+  };
+  auto accept = [&](int i) {
+    if (lane == 0) sh.path[acc] = (short)i;
+    ++acc;
+    node = i;
+    refused = 0;
+    share = 1.f;
+    taken = 0.f;
+    removed = 0;
+  };
+  auto walk = [&]() {  // true: a sum is needed
+    while (true) {
+      const int i = acc < a.max_path ? next_child(at_token) : n;
+      if (i >= n) return false;
+      at_token = i;
+      if (draft) {
+        if (accepts(i, share)) {
+          accept(i);
+          continue;
         }
+        ++refused;
+        taken += share;
+        if (share == 0.f) continue;  // nothing is left, and nothing will be
+        // the next one, should it be accepted with a share that can only be too large
+        const int next = next_child(i);
+        if (next >= n || !accepts(next, share)) return true;
+        at_token = next;
+        accept(next);
+      } else {
+        bool again = false;  // a refused child of the same parent has the same id
+        if (refused) {
+          const int x = sh.x[i];
+          for (int base = 0; base < i && !again; base += 32) {
+            const int j = min(base + lane, n - 1);
+            again = __any_sync(~0u, base + lane < i && sh.parent[j] == node && sh.x[j] == x);
+          }
+        }
+        const float p = sh.p[i];
+        const bool ok = !again && (refused ? (double)sh.u[i] * (double)share < (double)p : (bool)sh.as_first[i]);
+        if (ok) {
+          accept(i);
+          continue;
+        }
+        ++refused;
+        if (!again) removed += mass_at(p);
+        share = share_of(max(((int64_t)1 << 40) - removed, (int64_t)0));
       }
-      ok = !again && u * (double)share < (double)p;
-      if (!ok && !again) removed += mass_at(p);
     }
-    if (ok) {
-      if (tid == 0) sh.path[acc] = (short)i;
-      ++acc;
-      node = i;
-      refused = 0;
-      share = 1.f;
-      taken = 0.f;
-      removed = 0;
-      summed = false;
-      continue;
+  };
+  while (!bad) {
+    if (warp == 0) {
+      const bool more = walk();
+      if (lane == 0) sh.step = {node, acc, refused, refused && draft ? sh.row[at_token] : 0, taken, !more};
     }
-    ++refused;
-    if (!draft) {
-      share = share_of(max(((int64_t)1 << 40) - removed, (int64_t)0));
-      continue;
-    }
-    taken += share;
-    if (summed && at.total == 0) continue;  // nothing is left, and nothing will be
-    w.set(target + (row0 + node + 1) * a.target_stride, draft + sh.row[i] * a.draft_stride, -1, a.V);
-    w.taken = taken;
+    __syncthreads();
+    node = sh.step.node;
+    acc = sh.step.acc;
+    refused = sh.step.refused;
+    if (sh.step.end) break;
+    w.set(target + (row0 + node + 1) * a.target_stride, draft + sh.step.row * a.draft_stride, -1, a.V);
+    w.taken = sh.step.taken;
     sum();
-    summed = true;
     share = fminf(share_of(at.total), 1.f);
   }
 
   if (!bad) {  // uniform over the cluster
-    if (!summed) {
+    if (!draft || !refused) {  // else the last sum is that of what is left
       w.set(target + (row0 + node + 1) * a.target_stride, nullptr, -1, a.V);
       w.holes = nullptr;
       if (refused) {  // a certain draft's
@@ -311,14 +346,20 @@ cudaError_t launch_tree(const clsample_verify_tree_args_t& a, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   static std::atomic<uint64_t> allowed;
-  const cudaError_t e = allow_smem_once(verify_tree_kernel<P, C>, smem_bytes<P, C>(kMaxVocab), &allowed);
+  cudaError_t e = allow_smem_once(verify_tree_kernel<P, C>, smem_bytes<P, C>(kMaxVocab), &allowed);
+  if (C > 8 && e == cudaSuccess) {
+    static std::atomic<uint64_t> large;
+    e = allow_once(verify_tree_kernel<P, C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, &large);
+  }
   return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, verify_tree_kernel<P, C>, a) : e;
 }
 
-// As for clsample_verify: the largest cluster with which all requests are resident at once.
+// As for clsample_verify: the largest cluster with which all requests are resident at once.  One
+// request of 6 refusals over 151936 tokens: FIG16 us on 16 CTAs, FIG8 on 8.
 template <class P>
 cudaError_t launch_tree(const clsample_verify_tree_args_t& a, int sms, cudaStream_t st) {
   const int64_t slots = (int64_t)sms * kCtasPerSm;
+  if (a.B * (int64_t)16 <= slots) return launch_tree<P, 16>(a, st);
   if (a.B * (int64_t)8 <= slots) return launch_tree<P, 8>(a, st);
   if (a.B * (int64_t)4 <= slots) return launch_tree<P, 4>(a, st);
   return launch_tree<P, 2>(a, st);
