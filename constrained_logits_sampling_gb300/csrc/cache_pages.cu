@@ -83,49 +83,53 @@ __global__ void __launch_bounds__(kThreads) keep_path_kernel(const __grid_consta
   }
 }
 
-// A CTA has a share of one copy's pieces in one plane (keys or values of a layer).
+// An item is a share of one copy's pieces in one plane (keys or values of a layer).  A CTA takes several
+// where there are many, as most copies of a call may be none (3840 CTAs of nothing took 7.4 us).
 template <int kBytes>
 __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ clsample_copy_pages_args_t a,
                                                               const __grid_constant__ CacheShape c, int parts) {
   using T = typename Piece<kBytes>::T;
   constexpr int kAhead = 8;  // pieces of a thread in flight
-  const int planes = 2 * a.layers;
-  const int i = blockIdx.x / (planes * parts), rest = blockIdx.x % (planes * parts);
-  const int plane = rest / parts, part = rest % parts;
-  const int from = __ldg(a.copies + 3 * (int64_t)i), to = __ldg(a.copies + 3 * (int64_t)i + 1),
-            slots = __ldg(a.copies + 3 * (int64_t)i + 2);
-  const bool none = from < 0 || slots == 0;
-  const bool bad = !none && (from >= a.num_pages || to < 0 || to >= a.num_pages || slots < 0 || slots > a.page_size);
-  if (a.status && rest == 0 && threadIdx.x == 0) a.status[i] = bad ? CLSAMPLE_ROW_INVALID : CLSAMPLE_ROW_OK;
-  if (none || bad || from == to) return;
-  const int layer = plane < a.layers ? plane : plane - a.layers;
-  T* at = reinterpret_cast<T*>(plane < a.layers ? a.k_cache : a.v_cache) + layer * c.layer;
-  const T* src = at + from * c.page;
-  T* dst = at + to * c.page;
-  // this thread's place (a slot, and a piece of it), which moves by the same step each time
+  const int planes = 2 * a.layers, per_copy = planes * parts;
+  const int64_t items = (int64_t)a.n * per_copy;
   const int heads = c.per_head * a.Hkv, step = parts * kThreads, step_slots = step / heads, step_rest = step % heads;
-  const int first = part * kThreads + threadIdx.x;
-  int slot = first / heads, piece = first % heads;
   const bool flat = c.head == c.per_head;  // a slot's heads lie side by side
-  while (slot < slots) {
-    T x[kAhead];
-    int64_t off[kAhead];
-    bool live[kAhead];
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int i = (int)(item / per_copy), rest = (int)(item - (int64_t)i * per_copy);
+    const int plane = rest / parts, part = rest % parts;
+    const int from = __ldg(a.copies + 3 * (int64_t)i), to = __ldg(a.copies + 3 * (int64_t)i + 1),
+              slots = __ldg(a.copies + 3 * (int64_t)i + 2);
+    const bool none = from < 0 || slots == 0;
+    const bool bad = !none && (from >= a.num_pages || to < 0 || to >= a.num_pages || slots < 0 || slots > a.page_size);
+    if (a.status && rest == 0 && threadIdx.x == 0) a.status[i] = bad ? CLSAMPLE_ROW_INVALID : CLSAMPLE_ROW_OK;
+    if (none || bad || from == to) continue;
+    const int layer = plane < a.layers ? plane : plane - a.layers;
+    T* at = reinterpret_cast<T*>(plane < a.layers ? a.k_cache : a.v_cache) + layer * c.layer;
+    const T* src = at + from * c.page;
+    T* dst = at + to * c.page;
+    // this thread's place (a slot, and a piece of it), which moves by the same step each time
+    const int first = part * kThreads + threadIdx.x;
+    int slot = first / heads, piece = first % heads;
+    while (slot < slots) {
+      T x[kAhead];
+      int64_t off[kAhead];
+      bool live[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      live[k] = slot < slots;
-      off[k] = slot * c.slot + (flat ? piece : piece / c.per_head * c.head + piece % c.per_head);
-      if (live[k]) x[k] = src[off[k]];
-      slot += step_slots;
-      piece += step_rest;
-      if (piece >= heads) {
-        piece -= heads;
-        ++slot;
+      for (int k = 0; k < kAhead; ++k) {
+        live[k] = slot < slots;
+        off[k] = slot * c.slot + (flat ? piece : piece / c.per_head * c.head + piece % c.per_head);
+        if (live[k]) x[k] = src[off[k]];
+        slot += step_slots;
+        piece += step_rest;
+        if (piece >= heads) {
+          piece -= heads;
+          ++slot;
+        }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (live[k]) dst[off[k]] = x[k];
+      for (int k = 0; k < kAhead; ++k)
+        if (live[k]) dst[off[k]] = x[k];
+    }
   }
 }
 
@@ -158,23 +162,25 @@ template <int kBytes>
 void launch_keep(const clsample_keep_path_args_t& a, cudaStream_t st) {
   const CacheShape c = shape_of(a, kBytes);
   const int64_t columns = (int64_t)2 * a.layers * a.Hkv * c.per_head;
-  int64_t parts = (columns + kThreads - 1) / kThreads;
+  // two columns a thread: 192 requests' paths in 8 layers (2 x 7.8 MB) 5.5 us, with one 6.6
+  int64_t parts = (columns + 2 * kThreads - 1) / (2 * kThreads);
   const int64_t most = (1 << 30) / (int64_t)a.B;
   if (parts > most) parts = most;
   keep_path_kernel<kBytes><<<(unsigned)(a.B * parts), kThreads, 0, st>>>(a, c, (int)parts);
 }
 
-// Enough CTAs for the device, but no more than a page's pieces take: most copies of a call may be none.
+// Few copies are shared out among as many CTAs as their pieces take, up to the device's room.
 template <int kBytes>
 int launch_copy(const clsample_copy_pages_args_t& a, int sms, cudaStream_t st) {
+  constexpr int kPerSm = 6;
   const CacheShape c = shape_of(a, kBytes);
   const int64_t pieces = (int64_t)a.page_size * a.Hkv * c.per_head, planes = (int64_t)a.n * 2 * a.layers;
-  if (planes > 0x7fffffff) return CLSAMPLE_ERR_BATCH;
-  const int64_t most = (pieces + 8 * kThreads - 1) / (8 * kThreads);
-  int64_t parts = ((int64_t)sms * 16 + planes - 1) / planes;
+  const int64_t most = (pieces + 8 * kThreads - 1) / (8 * kThreads), room = (int64_t)sms * kPerSm;
+  int64_t parts = (room + planes - 1) / planes;
   if (parts > most) parts = most;
   if (parts > 64) parts = 64;
-  copy_pages_kernel<kBytes><<<(unsigned)(planes * parts), kThreads, 0, st>>>(a, c, (int)parts);
+  const int64_t items = planes * parts;
+  copy_pages_kernel<kBytes><<<(unsigned)(items < room ? items : room), kThreads, 0, st>>>(a, c, (int)parts);
   return CLSAMPLE_SUCCESS;
 }
 

@@ -196,7 +196,7 @@ def test_calls_while_another_device_is_current(lib, monkeypatch, where, name, fu
     monkeypatch.setattr(M, "_stream_ptr", lambda stream: 0)
     if name == "PagePool":
         op._args = M.PoolArgs()
-        args = M._PoolCall(function, M.BatchArgs(), (None,), ())
+        args = M._PoolCall(function, op._args, M.BatchArgs(), (None,), ())
     else:
         args = {"TreePlan": plan, "TreeVerifier": verify, "KeepPath": keep, "CopyPages": copy}[name]()
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
