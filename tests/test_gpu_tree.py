@@ -677,3 +677,140 @@ def test_verify_streams_graphs_and_refusals(S):
     with pytest.raises(Exception) as e:
         v(*args, **dict(kw, max_path=10))
     assert e.value.code == -9
+
+
+# ----------------------------------------------------------------------------- together
+
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "tree_step.py")
+    spec = importlib.util.spec_from_file_location("tree_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    return ex
+
+
+def test_example_step(S):
+    """The example's loop: kept tokens are those of the rule on the probabilities that the step used, each
+    row's logits are those of its line of tokens run as a chain on a cache of its own, and after the steps
+    the cache holds what a plain pass over the kept tokens writes, both within the rounding of the
+    activations (bf16)."""
+    ex = example()
+    B, V, width, depth = 3, 300, 3, 3
+    shape = dict(vocab=V, Hq=4, Hkv=2, D=64, max_len=192)
+    target, draft = ex.TreeDecoder(layers=2, seed=0, pages=60, **shape), ex.TreeDecoder(layers=1, seed=0, pages=60, **shape)
+    loop = ex.TreeLoop(target, draft, B, 192, width, depth)
+    prompt = [5 * i % V for i in range(1, 42)]
+    loop.prefill(prompt)
+    page0 = loop.target.table[0, 0]
+    kept = [list(prompt) for _ in range(B)]
+    for _ in range(6):
+        before = loop.target.lens.clone()
+        out = loop.step()
+        used = {n: t.cpu().numpy() if torch.is_tensor(t) else t for n, t in loop.used.items()}
+        tokens, path, accepted = TR.verify_tree(used["target_probs"], None, None, used["draft_tokens"], used["parents"],
+                                                used["cu_draft"], used["u_accept"], used["u_sample"], depth)
+        assert np.array_equal(out["tokens"].cpu().numpy(), tokens)
+        assert np.array_equal(out["path"].cpu().numpy(), path)
+        assert np.array_equal(out["accepted"].cpu().numpy(), accepted)
+        assert torch.equal(loop.target.lens[1:].cpu(), before[1:].cpu() + 1 + torch.from_numpy(accepted))
+        # every row's probabilities against its own line of tokens, run alone
+        x = used["draft_tokens"].reshape(B, -1)
+        for b in range(B):
+            for i, p in enumerate(used["parents"][:x.shape[1]]):
+                line, at = [x[b, i]], p
+                while at >= 0:
+                    line, at = [x[b, at]] + line, used["parents"][at]
+                if i % 4 == 1:
+                    want = alone(ex, shape, kept[b] + [int(t) for t in line])
+                    got = torch.from_numpy(used["target_probs"][b * (x.shape[1] + 1) + 1 + i]).log() * loop.T
+                    want = want - want.logsumexp(0)
+                    got = got - got.logsumexp(0)
+                    # activations are rounded to bf16 (2^-8) some twenty times along the two layers; such errors
+                    # add up like their square root, and a logit is a sum over the row
+                    size = want.std()
+                    assert ((got - want).abs() <= 2 * 8 * 2.0 ** -8 * 20 ** 0.5 * size).all()
+            kept[b] += [int(t) for t in tokens[b, :accepted[b] + 1]]
+    assert int(loop.target.pool.refs[int(page0)]) == B + 1  # the prompt's first page is still everybody's
+    held = loop.target.held.tolist()
+    assert held == [-(-n // 16) for n in loop.target.lens.tolist()]
+    used_pages = {int(p) for b in range(B + 1) for p in loop.target.table[b, :held[b]]}
+    assert int((loop.target.pool.refs > 0).sum()) == len(used_pages)
+    # keys and values of all layers: of the first layer they depend on the token and its position alone
+    fresh = ex.TreeDecoder(layers=2, seed=0, pages=60, **shape)
+    for b in range(B):
+        n = int(loop.target.lens[b + 1])
+        assert n == len(kept[b]) - 1
+        table = torch.arange(12, dtype=I32, device="cuda")[None]
+        fresh(i32(kept[b][:n]), table, i32([0, n]), i32([n]), n)
+        row = loop.target.table[b + 1]
+        for c, w in ((target.k_cache, fresh.k_cache), (target.v_cache, fresh.v_cache)):
+            got = torch.stack([c[0, int(row[j // 16]), j % 16] for j in range(n)]).float()
+            want = torch.stack([w[0, j // 16, j % 16] for j in range(n)]).float()
+            # one product of bf16 numbers in float32, in other orders, rounded once
+            assert (got - want).abs().max() <= 2 * 2.0 ** -8 * want.abs().max()
+
+
+def alone(ex, shape, tokens):
+    """Logits after a line of tokens, by ChunkAttention on a cache of its own."""
+    key = tuple(sorted(shape.items()))
+    if key not in alone.models:
+        alone.models[key] = ex.TreeDecoder(layers=2, seed=0, pages=12, **shape)
+    n = len(tokens)
+    table = torch.arange(12, dtype=I32, device="cuda")[None]
+    return alone.models[key](i32(tokens), table, i32([0, n]), i32([n]), n)[-1].cpu()
+
+
+alone.models = {}
+
+
+def test_example_runs(S):
+    example().main(steps=2, batch=2, vocab=500)
+
+
+STALLS = [(1, 0), (1, 1), (2, 0), (3, 0), (4, 0), (5, 1), (6, 0), (6, 1), (7, 0), (8, 0), (8, 2), (9, 0), (9, 3), (10, 0),
+          (10, 1), (11, 0), (12, 1), (13, 0), (13, 1)]
+
+
+@pytest.mark.parametrize("barrier,slot", STALLS)
+@pytest.mark.parametrize("D,page,dtype,G,Hkv,B", [(128, 16, BF, 4, 3, 60), (64, 8, FP, 2, 4, 260), (64, 12, BF, 4, 4, 260),
+                                                  (128, 24, FP, 8, 3, 40)])
+def test_attention_wait_that_runs_out(S, D, page, dtype, G, Hkv, B, barrier, slot):
+    """A barrier of the chunk kernel, one by one and in pairs, waits for what never comes, for a
+    millisecond: the call ends, its sequences and those of later calls on the handle are OVERFLOW, nothing
+    outside its rows is written, and another handle is not affected."""
+    import time
+
+    import test_gpu_speculative as G0
+    OVERFLOW = 1
+    att, fresh = S.TreeAttention(), S.TreeAttention()
+    new = [46 if b % 3 else 21 for b in range(B)]
+    q, k, v, table, cu, lens = G0.batch(new, [46 + 97 * b % 700 for b in range(B)], G * Hkv, Hkv, D, page, dtype, 2)
+    T, guard = sum(new), 200
+    mask = torch.full((T, 2), -1, dtype=I32, device="cuda")
+    want = fresh(q, k, v, table, cu, lens, mask=mask, max_new=46, lse=True)
+    assert not want["status"].any()
+    room = torch.full((T + 2 * guard, G * Hkv, D), 3.0, dtype=dtype, device="cuda")
+    status = torch.full((B,), -5, dtype=I32, device="cuda")
+    args = att.make_args(q, k, v, table, cu, lens, mask=mask, max_new=46, out=room[guard:guard + T], row_status=status)
+    assert att._L.clsample_debug_attention_stall(att._h, barrier, slot, 2_000_000) == 0
+    torch.cuda.synchronize()
+    start = time.time()
+    att.apply(args)
+    torch.cuda.synchronize()
+    assert time.time() - start < 10
+    # nobody waits for keys that TMA copies to land, for the end of a CTA's last units, for half of the
+    # weights where all are there already, or for a second unit where a CTA has one
+    boxes = page % 8 == 0 and 128 % page == 0
+    if barrier in (1, 2, 11) or (boxes and barrier in (5, 7)):
+        if not status.any():
+            assert barrier == 11 or torch.equal(room[guard:guard + T], want["out"])
+            return
+    assert (status == OVERFLOW).all()
+    assert (room[:guard] == 3).all() and (room[guard + T:] == 3).all()
+    assert att._L.clsample_debug_attention_stall(att._h, 0, 0, 1) == 0
+    later = att(q, k, v, table, cu, lens, mask=mask, max_new=46)
+    assert (later["status"] == OVERFLOW).all() and torch.equal(later["out"], want["out"])
+    again = fresh(q, k, v, table, cu, lens, mask=mask, max_new=46, lse=True)
+    assert not again["status"].any() and torch.equal(again["out"], want["out"])
