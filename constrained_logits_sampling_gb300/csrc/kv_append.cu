@@ -70,21 +70,18 @@ __device__ __forceinline__ Token find_token(const AppendParams& P, int t) {
 }
 
 // Statuses, one thread per sequence: the same checks as find_token for each of its tokens'
-// pages.  Runs in the first blocks of the launch, after their token.
-__device__ __forceinline__ void write_status(const AppendParams& P, int b) {
+// pages (and positions: `turns`).  Runs in the first blocks of the launch, after their token.
+__device__ __forceinline__ void write_status(const AppendParams& P, int b, bool turns = true) {
   const clsample_kv_append_args_t& a = P.a;
   const int cap = capacity_of(a.max_pages, a.page_size);
   const Seq s = load_seq(a.cu_new, a.kv_lens, b, a.T, cap, a.T);
-  bool ok = s.ok;
+  bool ok = s.ok && turns;
   if (ok && s.n > 0) {
     const int first = s.len - s.n;
     if (first < 0 || (a.rot_dim > 0 && !P.positions && s.len > a.max_pos)) {
       ok = false;
     } else {
-      for (int i = 0; ok && a.rot_dim > 0 && P.positions && i < s.n; ++i) {
-        const int at = __ldg(P.positions + s.q0 + i);
-        ok = at >= 0 && at < a.max_pos;
-      }
+
       for (int p = first / a.page_size; ok && p <= (s.len - 1) / a.page_size; ++p) {
         const int id = __ldg(a.page_table + (int64_t)b * a.table_stride + p);
         ok = id >= 0 && id < a.num_pages;
@@ -92,6 +89,26 @@ __device__ __forceinline__ void write_status(const AppendParams& P, int b) {
     }
   }
   a.row_status[b] = ok ? CLSAMPLE_ROW_OK : CLSAMPLE_ROW_INVALID;
+}
+
+// Statuses by all blocks; where positions are given, a warp a sequence, whose lanes look at them.
+__device__ __forceinline__ void write_statuses(const AppendParams& P) {
+  const int B = P.a.B, first = blockIdx.x * kThreads + threadIdx.x, all = gridDim.x * kThreads;
+  if (!P.positions || P.a.rot_dim == 0) {
+    for (int b = first; b < B; b += all) write_status(P, b);
+    return;
+  }
+  const int lane = threadIdx.x & 31, cap = capacity_of(P.a.max_pages, P.a.page_size);
+  for (int b = first >> 5; b < B; b += all >> 5) {
+    const Seq s = load_seq(P.a.cu_new, P.a.kv_lens, b, P.a.T, cap, P.a.T);
+    bool turns = true;
+    for (int i = lane; s.ok && i < s.n; i += 32) {
+      const int at = __ldg(P.positions + s.q0 + i);
+      turns &= at >= 0 && at < P.a.max_pos;
+    }
+    turns = __all_sync(~0u, turns);
+    if (lane == 0) write_status(P, b, turns);
+  }
 }
 
 // Any head size, strides and rotation: one warp per head row, elements one by one through
@@ -154,8 +171,7 @@ __global__ void __launch_bounds__(kThreads) append_any_kernel(const __grid_const
       __syncwarp();
     }
   }
-  if (a.row_status)
-    for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += gridDim.x * kThreads) write_status(P, b);
+  if (a.row_status) write_statuses(P);
 }
 
 // Where a head row comes from and goes to, for the block's first token.
@@ -340,8 +356,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const __
       }
     }
   }
-  if (a.row_status)
-    for (int b = blockIdx.x * kThreads + tid; b < a.B; b += gridDim.x * kThreads) write_status(P, b);
+  if (a.row_status) write_statuses(P);
 }
 
 template <class T>
