@@ -634,21 +634,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             bounded_wait(&sh.v_landed[st], parity, &sh.limit);
             const bool dead = sh.limit.dead;
             __syncwarp();
-            // a row's pieces may lie anywhere in it: all are cleared, of two rows at a time
-            static_assert(KC <= 16, "pieces of a row");
-            const int ch = lane & 15;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t gone = ~(word_of(keep, k) & column_bits(lo - 32 * k, hi - 1 - 32 * k));
-              while (gone) {  // uniform
-                const int r0 = __ffs(gone) - 1;
-                gone &= gone - 1;
-                const int r1 = gone ? __ffs(gone) - 1 : r0;
-                gone &= gone - 1;
-                const int row = 32 * k + (lane < 16 ? r0 : r1);
-                if (ch < KC)
+            // a row's pieces may lie anywhere in it: all are cleared
+            if constexpr (!kTree) {
+              for (int i = lane; i < 128 * KC; i += 32) {
+                const int row = i / KC, ch = i % KC;
+                if (row < lo || row >= hi)
                   *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) =
                       make_uint4(0, 0, 0, 0);
+              }
+            } else {
+#pragma unroll 1
+              for (int k = 0; k < 4; ++k) {  // 32 rows
+                const uint32_t gone = ~(word_of(keep, k) & column_bits(lo - 32 * k, hi - 1 - 32 * k));
+                if (gone == 0) continue;
+#pragma unroll 4
+                for (int x = 0; x < KC; ++x) {
+                  const int i = x * 32 + lane, row = i / KC, ch = i % KC;
+                  if ((gone >> row) & 1)
+                    *reinterpret_cast<uint4*>(smem + (2 + NS + st) * kTile + (ch >> 3) * kHalf + (32 * k + row) * 128 +
+                                              (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
               }
             }
             fence_async_proxy();
