@@ -42,14 +42,11 @@ constexpr int kChunkKeys = 128;
 constexpr float kRescaleAt = 8.f;  // log2
 
 // Registers a thread: the two softmax warpgroups, and the one of loads and products.  They
-// add up to what the block is launched with (3 x 168).  With kTree the loads look at masks and at units of
-// other kinds, and take more; what does not stay in registers goes a long way here, as shared memory
-// leaves L1 little room (64 trees of up to 32 rows: 117 us with 200 and 104, 114 so).
-template <bool kTree>
-struct ChunkRegs {
-  static constexpr int kSoftmax = kTree ? 192 : 200, kOther = kTree ? 120 : 104;
-  static_assert(2 * kSoftmax + kOther == 3 * 168 && 168 * kChunkThreads <= 65536, "the launch's registers");
-};
+// add up to what the block is launched with (3 x 168).  (What does not stay in them goes a long way
+// here, as shared memory leaves L1 little room.  With kTree the loads look at masks and at units of other
+// kinds; 256 requests of 48 rows over 300 keys took 133 us when they did not fit, and 118 since.)
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168 && 168 * kChunkThreads <= 65536, "the launch's registers");
 
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -157,7 +154,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
   using Shape = ChunkShape<D>;
   using Map = UnitMap<kChunkRows, kChunkKeys, kTree, kPairs>;
-  constexpr int kSoftmaxRegs = ChunkRegs<kTree>::kSoftmax, kOtherRegs = ChunkRegs<kTree>::kOther;
   constexpr int NS = Shape::kKeySlots, NV = Shape::kValueSlots, kTile = Shape::kTile, KC = D / 8;
   constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 elements
   constexpr int kRowWarps = kTma ? 1 : 2;  // that copy rows
@@ -223,6 +219,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
   const uint32_t tmem = sh.tmem;
   int64_t t = span.t0;
+
+  const Span& ours = kTree ? sh.span : span;  // (one of them costs registers, the other loads)
 
   // A whole warpgroup has to run the same register instruction, so warps 8 to 11 do before they part.
   if (warp >= 8) regs_down<kOtherRegs>();
@@ -483,7 +481,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // 32 rows to rows r0.. of a tile; lane i has the place of row i, bit i of `live` tells
     // whether it is read or zero
     auto copy_rows = [&](const T* src, int64_t off, unsigned live, uint32_t dst, int r0) {
-#pragma unroll
+#pragma unroll kTree ? 2 : KC
       for (int x = 0; x < KC; ++x) {
         const int i = x * 32 + lane, row = i / KC, ch = i % KC, r = r0 + row;
         const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
@@ -564,7 +562,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int box = min(a.page_size, kChunkKeys), boxes = kChunkKeys / box;
       uint32_t it = 0;
       while (true) {
-        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, ours, u, unit_begin, t);
         const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
         auto page_of = [&](int j) {  // num_pages, which is out of bounds: zeros
           const int key = (u.tile0 + j0 + j) * kChunkKeys + lane * box;
@@ -610,12 +608,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h + head, from, full);
           }
         }
-        if (!advance<Map>(P, span, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
+        if (!advance<Map>(P, ours, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
       }
     } else if (kTma) {
       uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
       while (true) {
-        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, ours, u, unit_begin, t);
         if (!copy_queries(seg)) break;
         const int copies = Map::is_pair(P, u) ? 2 : 1;
         for (int j = 0; j < cnt; ++j) {
@@ -663,13 +661,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         it += cnt * copies;
         ++seg;
-        if (!advance<Map>(P, span, &u, &unit_begin, &t)) break;
+        if (!advance<Map>(P, ours, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (warp < 10) {
       uint32_t it = 0, seg = 0;
       while (true) {
-        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, span, u, unit_begin, t);
+        const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, ours, u, unit_begin, t);
         if (!copy_queries(seg)) break;
         const int copies = Map::is_pair(P, u) ? 2 : 1;
         const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
@@ -724,7 +722,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        if (!advance<Map>(P, span, &u, &unit_begin, &t)) break;
+        if (!advance<Map>(P, ours, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (lane == 0) {
@@ -734,7 +732,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       bool alive = true;
       do {
         const uint32_t copies = Map::is_pair(P, u) ? 2 : 1;
-        for (const uint32_t end = it + copies * tiles_here<Map>(P, span, u, unit_begin, t); alive && it < end; ++it) {
+        for (const uint32_t end = it + copies * tiles_here<Map>(P, ours, u, unit_begin, t); alive && it < end; ++it) {
           alive = bounded_wait(&sh.k_landed[it % NS], (it / NS) & 1, &sh.limit);
           if (!alive) break;
           fence_async_proxy();
@@ -744,7 +742,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           fence_async_proxy();
           mbar_arrive(&sh.v_full[it % NV]);
         }
-      } while (alive && advance<Map>(P, span, &u, &unit_begin, &t));
+      } while (alive && advance<Map>(P, ours, &u, &unit_begin, &t));
     }
   } else {
     // ------------------------------------------------------------------ products
@@ -796,7 +794,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         p_phase ^= 1u << w;
       };
       while (true) {
-        const int cnt = (int)uni((uint32_t)tiles_here<Map>(P, span, u, unit_begin, t));
+        const int cnt = (int)uni((uint32_t)tiles_here<Map>(P, ours, u, unit_begin, t));
         const bool turns = uni(u.rows <= 128);  // the halves take copies in turns, of one head or of a pair's
         const uint32_t pair = uni(Map::is_pair(P, u));
         wait(&sh.q_full, seg & 1);
@@ -843,7 +841,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        if (!uni(advance<Map>(P, span, &u, &unit_begin, &t))) break;
+        if (!uni(advance<Map>(P, ours, &u, &unit_begin, &t))) break;
       }
       // products still running when a wait gave up end before their memory is freed
       if (!alive) {

@@ -167,23 +167,27 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, int64_t most_rows,
 // Sequences of up to `most_rows` packed rows go to the stream kernel, longer ones to the chunk
 // kernel.  By position: 256 sequences of 16 rows over 2.3 GB of keys and values take 385 us in the
 // one and 441 in the other; of 24 rows, where the one reads keys twice, 707 and 420.
-// By mask the stream kernel has units of 32 rows if any sequence may have more than 16.  64 requests of
-// 24 rows over 2000 keys on 8 key heads of 128: 107 us there and 112 in the chunk kernel, over 300 keys 37 and
-// 48; on 4 heads of 64: 42 and 52, 19 and 26.  Up to 64 rows, which read their keys twice, where those are
-// few: 8 requests of 48 rows over 300 keys 19 and 23 us (heads of 64: 12 and 18); with heads of 128
-// only where a CTA has few units (64 requests: 57 and 52).
+// By mask the stream kernel alone, in units of 16 rows that read their keys again, takes calls of
+// little work: `steps` is how many pieces of 64 keys that would be at most.  One request over 1500 keys on 8
+// key heads of 128 takes 14 us there with 96 rows and 20 in the chunk kernel (with 256: 26 and 19); 95
+// requests of 3 to 42 rows with a window of 300 on 4 heads of 64 take 30 and 47.  Otherwise it has units of 32
+// rows.  64 requests of 24 rows over 2000 keys on 8 key heads of 128: 107 us there and 112 in the chunk
+// kernel, over 300 keys 37 and 48; on 4 heads of 64: 42 and 52, 19 and 26.  With heads of 64 and few keys up to
+// 64 rows, read twice: 64 requests of 48 rows over 300 keys 24 and 28 us (of 128: 57 and 52).
 template <class T, int D, bool kTree>
 cudaError_t launch(const clsample_attention* h, const AttnParams& P, cudaStream_t st) {
   if constexpr (!kTree) {
     return launch<T, D, false, 1>(h, P, kStreamRows, st);
   } else {
     const int64_t rows = P.a.max_new * (int64_t)P.g, units = (int64_t)P.a.B * P.a.Hkv;
-    if (rows <= kStreamRows) return launch<T, D, true, 1>(h, P, kStreamRows, st);
     const int64_t keys = P.a.window > 0 && (int64_t)P.a.window + P.a.max_new < P.capacity
                              ? (int64_t)P.a.window + P.a.max_new
                              : P.capacity;
-    const bool twice = keys <= 512 && (D == 64 || units <= h->sms);
-    return launch<T, D, true, 2>(h, P, twice ? 2 * kMaxStreamRows : kMaxStreamRows, st);
+    const double steps = (double)units * ((rows + 15) / 16) * ((keys + kStreamKeys - 1) / kStreamKeys);
+    const int few = rows <= 64 ? 20 : D == 64 ? 8 : 4;  // a CTA
+    if (rows <= kStreamRows || steps <= (double)few * kStreamCtas * h->sms)
+      return launch<T, D, true, 1>(h, P, rows, st);
+    return launch<T, D, true, 2>(h, P, keys <= 512 && D == 64 ? 2 * kMaxStreamRows : kMaxStreamRows, st);
   }
 }
 
