@@ -185,6 +185,49 @@ def test_attention(S, case):
     check_attention(S, pr, rows, [o + d for o, t in zip(old, depth) for d in t], window)
 
 
+@pytest.mark.parametrize("Hkv,G,D,page,dtype", [(3, 1, 128, 16, BF), (5, 2, 64, 12, FP), (7, 1, 64, 64, BF)])
+def test_attention_of_many_units(S, Hkv, G, D, page, dtype):
+    """So many that key heads go in pairs, of an odd number of them; some sequences have one row or none."""
+    B = 6 * torch.cuda.get_device_properties(0).multi_processor_count // Hkv + 1
+    drafted = [(70 if i % 80 == 3 else 45) if i % 40 == 3 else i % 2 for i in range(B)]
+    old = [(37 * i) % 60 + (400 if i % 160 == 3 else 0) for i in range(B)]
+    pr = problem(drafted, old, Hkv * G, Hkv, D, page, dtype, seed=Hkv)
+    _, rows, depth = trees_of(drafted, Hkv)
+    check_attention(S, pr, rows, [o + d for o, t in zip(old, depth) for d in t])
+
+
+@pytest.mark.parametrize("n", [17, 33, 64, 65])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("wide", [0, 400])
+def test_attention_whatever_the_table_holds(S, n, D, wide):
+    """The same results from tables of few and of many pages, which the choice of kernels rests on."""
+    pr = problem([n - 1, 0, n // 2], [150, 700, 3], 4, 2, D, 64, BF, seed=n + D)
+    _, rows, depth = trees_of([n - 1, 0, n // 2], n)
+    if wide:
+        pr.table = torch.cat([pr.table, torch.full((3, wide), -1, dtype=I32)], 1)
+    check_attention(S, pr, rows, [o + d for o, t in zip((150, 700, 3), depth) for d in t], window=90 if n == 33 else 0)
+
+
+def test_attention_two_handles_at_once(S):
+    """Calls of two objects on two streams do not meet."""
+    cases = []
+    for seed, drafted, old in ((1, [60, 3], [3000, 900]), (2, [100, 30], [2000, 4000])):
+        pr = problem(drafted, old, 8, 2, 128, 16, BF, seed=seed)
+        _, rows, _ = trees_of(drafted, seed)
+        handle = S.TreeAttention()
+        alone = check_attention(S, pr, rows, handle=handle)["out"]
+        args, mask = tensors(pr), TR.words_of(rows, 4).cuda()
+        cases.append((handle, args, mask, max(pr.new), alone, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (handle, args, mask, most, _, stream) in enumerate(cases):
+            got[i].append(handle(*args, mask=mask, max_new=most, stream=stream)["out"])
+    torch.cuda.synchronize()
+    for i, case in enumerate(cases):
+        assert all(torch.equal(o, case[4]) for o in got[i])
+
+
 def test_attention_takes_the_plan(S):
     drafted, old = [30, 0, 17], [100, 7, 640]
     pr = problem(drafted, old, 8, 2, 64, 16, BF, seed=3)
