@@ -18,7 +18,7 @@ struct clsample_attention {
 namespace clsample {
 namespace {  // each source that includes this has kernels of its own
 
-constexpr int kStreamCtas = 2;  // per SM
+constexpr int kStreamCtas = 3;  // per SM, at most
 constexpr float kMaxScale = 2.0e38f;  // times log2(e) is still finite
 // The scratch, per SM: both kernels' slots (two per CTA, of rows of 128 sums, a maximum and a
 // sum), their cut units, and one word for all.
@@ -94,6 +94,11 @@ bool query_map(const AttnParams& P, CUtensorMap* map) {
   return make_map(P, a.q, dims, strides, box, map);
 }
 
+// By mask, many units a CTA go in pairs in the chunk kernel, which end and begin side by side: 256 requests
+// of 48 rows over 300 keys on 8 key heads take 118 us so and 177 one by one (the latter on an earlier version);
+// 64 requests of 96 to 128 rows over 200 to 4000 keys 119 and 114, as the kernel's loops are longer.
+inline bool in_pairs(int64_t units, int sms) { return units >= 6 * (int64_t)sms; }
+
 template <class T, int D, bool kTree>
 cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
   // Boxes have to start on the eight rows of the swizzle and fill a tile.  2 x 2048 tokens over
@@ -104,10 +109,7 @@ cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
                      cache_map(P, P.a.k_cache, &k_map) && cache_map(P, P.a.v_cache, &v_map);
   P.q_box = boxes && query_map(P, &q_map);
   const int bytes = ChunkShape<D>::kBytes;
-  // By mask, many units a CTA go in pairs, which end and begin side by side: 256 requests of 48 rows over 300
-  // keys on 8 key heads take 141 us so and 177 one by one; 64 requests of 96 to 128 rows over 200 to 4000 keys
-  // 119 and 114, as the kernel's loops are longer.
-  const bool pairs = kTree && (int64_t)P.a.B * P.a.Hkv >= 6 * (int64_t)sms;
+  const bool pairs = kTree && in_pairs((int64_t)P.a.B * P.a.Hkv, sms);
   auto* fn = boxes ? attn_chunk_kernel<T, D, true, kTree> : attn_chunk_kernel<T, D, false, kTree>;
   if constexpr (kTree)
     if (pairs) fn = boxes ? attn_chunk_kernel<T, D, true, true, true> : attn_chunk_kernel<T, D, false, true, true>;
@@ -121,9 +123,10 @@ cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
 // first: of the call
 template <class T, int D, bool kTree, int RB>
 cudaError_t launch_stream(const AttnParams& P, int sms, bool first, cudaStream_t st) {
-  const int grid = sms * kStreamCtas;
+  using Ring = StreamRing<D, RB, kTree>;
+  const int grid = sms * Ring::kCtas;
   auto* fn = attn_stream_kernel<T, D, kTree, RB>;
-  const int bytes = StreamRing<D, RB>::kBytes;
+  const int bytes = Ring::kBytes;
   static std::atomic<uint64_t> allowed;
   const cudaError_t e = allow_smem_once(fn, bytes, &allowed);
   if (e != cudaSuccess) return e;
@@ -160,7 +163,7 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, int64_t most_rows,
   P.partial = stream_partial;
   P.cut = stream_cut;
   if (!alone && (e = launch_stream<T, D, kTree, RB>(P, h->sms, !chunks, st)) != cudaSuccess) return e;
-  const JoinParams J{P, chunk_partial, chunk_cut, chunks ? h->sms : 0, alone ? 0 : h->sms * kStreamCtas};
+  const JoinParams J{P, chunk_partial, chunk_cut, chunks ? h->sms : 0, alone ? 0 : h->sms * StreamRing<D, RB, kTree>::kCtas};
   return launch_after(attn_join_kernel<T, D, kTree, kRows>, h->sms * 2, kJoinThreads, 0, st, J);
 }
 
@@ -170,10 +173,11 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, int64_t most_rows,
 // By mask the stream kernel alone, in units of 16 rows that read their keys again, takes calls of
 // little work: `steps` is how many pieces of 64 keys that would be at most.  One request over 1500 keys on 8
 // key heads of 128 takes 14 us there with 96 rows and 20 in the chunk kernel (with 256: 26 and 19); 95
-// requests of 3 to 42 rows with a window of 300 on 4 heads of 64 take 30 and 47.  Otherwise it has units of 32
-// rows.  64 requests of 24 rows over 2000 keys on 8 key heads of 128: 107 us there and 112 in the chunk
-// kernel, over 300 keys 37 and 48; on 4 heads of 64: 42 and 52, 19 and 26.  With heads of 64 and few keys up to
-// 64 rows, read twice: 64 requests of 48 rows over 300 keys 24 and 28 us (of 128: 57 and 52).
+// requests of 3 to 42 rows with a window of 300 on 4 heads of 64 take 25, and 46 in both kernels by row
+// counts.  Otherwise it has units of 32 rows.  64 requests of 24 rows over 2000 keys on 8 key heads of 128: 107
+// us there and 112 in the chunk kernel, over 300 keys 37 and 48; on 4 heads of 64: 41 and 52, 18 and 26.  With
+// heads of 64 and few keys up to 64 rows, read twice: 64 requests of 48 rows over 300 keys 24 and 28 us (of 128:
+// 57 and 52), but not where the chunk kernel has pairs: 256 requests of 48 rows 70 and 58.
 template <class T, int D, bool kTree>
 cudaError_t launch(const clsample_attention* h, const AttnParams& P, cudaStream_t st) {
   if constexpr (!kTree) {
@@ -185,9 +189,10 @@ cudaError_t launch(const clsample_attention* h, const AttnParams& P, cudaStream_
                              : P.capacity;
     const double steps = (double)units * ((rows + 15) / 16) * ((keys + kStreamKeys - 1) / kStreamKeys);
     const int few = rows <= 64 ? 20 : D == 64 ? 8 : 4;  // a CTA
-    if (rows <= kStreamRows || steps <= (double)few * kStreamCtas * h->sms)
+    if (rows <= kStreamRows || steps <= (double)few * 2 * h->sms)
       return launch<T, D, true, 1>(h, P, rows, st);
-    return launch<T, D, true, 2>(h, P, keys <= 512 && D == 64 ? 2 * kMaxStreamRows : kMaxStreamRows, st);
+    const bool twice = keys <= 512 && D == 64 && !in_pairs(units, h->sms);
+    return launch<T, D, true, 2>(h, P, twice ? 2 * kMaxStreamRows : kMaxStreamRows, st);
   }
 }
 

@@ -79,12 +79,17 @@ constexpr int kStreamKeys = 64;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // Ring stages of a warp: two CTAs fit an SM, with up to 128 KB of loads in flight for heads of 128
-// and 160 KB for heads of 64 (all stages but the one that is worked on).
+// and 160 KB for heads of 64 (all stages but the one that is worked on).  By mask with heads of 64 three
+// fit, with 144 KB: units are short there, and while one CTA ends a unit or waits for the next one's pages
+// the others work.  95 requests of 3 to 42 rows with a window of 300 on 4 heads: 25 us so and 30 with two; 300
+// requests of 32 rows over 450 keys 58 and 65 (16 of them over 8000: 47 and 43, as sums leave in more parts).
+// With heads of 128 the registers do not allow it.
 constexpr int kStreamRows = 16;
 constexpr int kMaxStreamRows = 2 * kStreamRows;
-template <int D, int RB = 1>
+template <int D, int RB = 1, bool kTree = false>
 struct StreamRing {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kCtas = kTree && D == 64 ? 3 : 2;  // per SM
+  static constexpr int kStages = D == 128 ? 3 : kCtas == 3 ? 4 : 6;
   static constexpr int kRing = kStages * kStreamKeys * D * 2 * 2;  // keys and values
   static constexpr int kBytes = kRing + (RB > 1 ? RB * kStreamRows * D * 2 : 0);  // and queries
   static_assert(kRing >= 4 * RB * kStreamRows * (D + 8) * 4, "room for four warps' sums");
@@ -347,8 +352,9 @@ __device__ __forceinline__ void stream_finish(const AttnParams& P, const Unit& u
 }
 
 template <class T, int D, bool kTree = false, int RB = 1>
-__global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __grid_constant__ AttnParams P) {
-  constexpr int R = RB * kStreamRows, S = StreamRing<D, RB>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
+__global__ void __launch_bounds__(kStreamThreads, StreamRing<D, RB, kTree>::kCtas)
+    attn_stream_kernel(const __grid_constant__ AttnParams P) {
+  constexpr int R = RB * kStreamRows, S = StreamRing<D, RB, kTree>::kStages, KC = D / 8;  // KC: 16-byte pieces of a key
   constexpr int kTileBytes = 16 * D * 2, kStageBytes = 2 * kTileBytes, kHalf = 16 * 128;
   using Map = UnitMap<R, kStreamKeys, kTree>;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) attn_stream_kernel(const __
       page = next;
     }
     StreamState<T, D, kTree, RB> st;
-    if constexpr (RB > 1) st.load_queries(P, u, smem + StreamRing<D, RB>::kRing);
+    if constexpr (RB > 1) st.load_queries(P, u, smem + StreamRing<D, RB, kTree>::kRing);
     st.begin(P, u);
     for (int i = 0; i < cnt; ++i) {
       cp_async_wait<S - 2>();
