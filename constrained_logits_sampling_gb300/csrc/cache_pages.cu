@@ -65,9 +65,10 @@ __global__ void __launch_bounds__(kThreads) keep_path_kernel(const __grid_consta
   if (bad) return;
   const int begin = stays;
   if (begin >= count) return;
-  const int heads = c.per_head * a.Hkv, columns = 2 * a.layers * heads;
-  for (int col = part * kThreads + tid; col < columns; col += parts * kThreads) {
-    const int plane = col / heads, rest = col % heads;  // planes: keys of all layers, then values
+  // (below 2^31; a step is about half of them, so the first column past them needs 32 bits)
+  const unsigned heads = (unsigned)(c.per_head * a.Hkv), columns = 2 * a.layers * heads;
+  for (unsigned col = part * kThreads + tid; col < columns; col += (unsigned)parts * kThreads) {
+    const int plane = (int)(col / heads), rest = (int)(col % heads);  // planes: keys of all layers, then values
     const int layer = plane < a.layers ? plane : plane - a.layers;
     T* at = reinterpret_cast<T*>(plane < a.layers ? a.k_cache : a.v_cache) + layer * c.layer +
             rest / c.per_head * c.head + rest % c.per_head;

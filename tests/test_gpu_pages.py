@@ -353,6 +353,19 @@ def test_moves_far_offsets(G, D):
         assert not c.any()
 
 
+def test_keep_path_of_the_most_columns(G):
+    """Columns close to 2^31, where a thread's next one may lie past it."""
+    Hkv, D = 4194303, 255
+    k, v = (torch.zeros(1, 3, Hkv, D, dtype=BF, device="cuda") for _ in range(2))
+    for c, add in ((k, 1), (v, 2)):
+        c.view(torch.int16)[0, 2] = (torch.arange(Hkv * D, device="cuda") % 31991 + add).view(Hkv, D).to(torch.int16)
+    got = G.KeepPath()(k, v, i32([[0]]), i32([0, 2]), i32([3]), i32([[1]]), i32([1]))
+    assert got["status"].tolist() == [0] and got["kv_lens"].tolist() == [2]
+    for c in (k, v):
+        bits16 = c.view(torch.int16)
+        assert torch.equal(bits16[0, 1], bits16[0, 2]) and not bits16[0, 0].any()
+
+
 @pytest.mark.parametrize("layers,Hkv,D,page,dtype,layout", [
     (3, 2, 128, 16, BF, "nhd"), (2, 3, 64, 7, FP, "hnd"), (0, 2, 33, 5, BF, "nhd"), (2, 1, 20, 64, BF, "hnd"), (1, 5, 6, 3, FP, "nhd"),
     (30, 8, 256, 32, BF, "nhd")])
