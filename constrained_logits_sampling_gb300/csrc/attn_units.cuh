@@ -46,8 +46,8 @@ __device__ __forceinline__ int token_of(const AttnParams& P, int row) {
 }
 __device__ __forceinline__ int head_of(const AttnParams& P, int row) { return row - token_of(P, row) * P.g; }
 
-// 64 trees of 24 to 32 tokens over 200 to 4000 keys on 8 key heads, in the chunk kernel: 125 us with 8, 121
-// with 12, 117 with 18, 120 with 24 (and 197 with spans of equal tiles).
+// 64 trees of 24 to 32 tokens over 200 to 4000 keys on 8 key heads, in the chunk kernel, on an earlier version:
+// 125 us with 8, 121 with 12, 117 with 18, 120 with 24 (and 197 with spans of equal tiles).
 constexpr int kChunkPad = 18, kStreamPad = 3;
 
 struct CutUnit {

@@ -12,7 +12,8 @@
 // child is accepted whatever the sum: s does not grow.
 // A draft that is certain needs one pass, over the last token's row, with its refused ids as
 // holes in a bitmap.  Bound by memory where requests are many: p and q once for each refusal on the
-// path; else by the chain of passes, each 4 us over 151936 tokens on 16 CTAs.
+// path (256 requests of 6 refusals over 151936 tokens, 1.87 GB: 347 us, 5.4 TB/s); else by the chain of
+// passes, each 4 us over 151936 tokens on 16 CTAs.
 #include <cooperative_groups.h>
 
 #include "draw_weights.cuh"
@@ -42,6 +43,14 @@ struct Shared {
     float taken;
     bool end;
   } step;
+  // Where the walk stands between sums.  Here and not in registers, of which a thread has 64: what did not fit
+  // went through local memory in every pass (256 requests of 6 refusals 375 us, 347 since).
+  struct Walk {
+    int at;        // the last token looked at
+    float s, c;
+    int64_t removed;
+  } walk;
+  int64_t total;  // of the last pass
 };
 
 __device__ __forceinline__ int64_t warp_total(int64_t v) {
@@ -55,10 +64,16 @@ __device__ __forceinline__ int64_t mass_at(float p) { return (int64_t)((double)p
 // m / 2^40 rounded to float32
 __device__ __forceinline__ float share_of(int64_t m) { return __ll2float_rn(m) * 9.094947017729282379150390625e-13f; }
 
-// The sums of a pass over a row's weights, and where its slices lie.
-struct Pass {
-  int64_t total, before;  // of all slices; of those before this CTA's
-  int begin, end, part;   // this CTA's vectors, and how many of them a warp has
+// A CTA's share of a row's vectors, and how many of them a warp has.
+template <int C>
+struct Share {
+  int begin, end, part;
+  __device__ __forceinline__ Share(int vectors, int rank) {
+    const int share = (vectors + C - 1) / C;
+    begin = min(vectors, rank * share);
+    end = min(vectors, begin + share);
+    part = (share + kWarps - 1) / kWarps;
+  }
 };
 
 template <class P, int C>
@@ -79,7 +94,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const float u_last = __ldg(a.u_sample + b);
   bool bad = lo < 0 || hi < lo || hi > a.N || hi - lo > a.max_draft || !(u_last >= 0.f && u_last < 1.f);
   const int n = bad ? 0 : hi - lo;  // at most kMaxNodes
-  if (tid == 0) sh.bad = sh.odd = 0;
+  if (tid == 0) {
+    sh.bad = sh.odd = 0;
+    sh.step = {-1, 0, 0, 0, 0.f, false};
+    sh.walk = {-1, 1.f, 0.f, 0};
+  }
   for (int i = tid; i <= n; i += kThreads) sh.of_parent[i] = -1;
   __syncthreads();
   const P* target = reinterpret_cast<const P*>(a.target);
@@ -113,15 +132,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   cluster.barrier_wait();
 
   W w{};
-  Pass at{};
   int passes = 0;
   uint32_t* const holes = reinterpret_cast<uint32_t*>(marks + marks_words<P, C>(a.V));
   // Sums the weights w over the cluster.  All CTAs take part, and all learn of bad probabilities.
   auto sum = [&]() {
-    const int share = (w.vectors() + C - 1) / C;
-    at.begin = min(w.vectors(), rank * share);
-    at.end = min(w.vectors(), at.begin + share);
-    at.part = (share + kWarps - 1) / kWarps;
+    const Share<C> at(w.vectors(), rank);
     const int w0 = min(at.end, at.begin + warp * at.part), w1 = min(at.end, w0 + at.part);
     Range range;
     const int64_t mine = warp_total(w.sum_range(w0, w1, &range, marks + tid));
@@ -141,99 +156,108 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     cluster.sync();
     ++passes;
-    at.total = at.before = 0;
+    int64_t total = 0;
     for (int i = 0; i < C; ++i) {
-      if (i < rank) at.before += sh.slice_sum[turn][i];
-      at.total += sh.slice_sum[turn][i];
+      total += sh.slice_sum[turn][i];
       bad |= sh.slice_bad[turn][i] != 0;
     }
+    return total;
   };
 
   // The walk, by the first warp of each CTA of the cluster, up to the next sum that it needs.
-  int node = -1, acc = 0, refused = 0, at_token = -1;  // the last accepted token, how many, refused children of it
-  float share = 1.f, taken = 0.f;                      // s and c
-  int64_t removed = 0;                                 // without a draft: P of the refused ids
-  // the first token after i whose parent is `node`, or n
-  auto next_child = [&](int i) {
-    for (int base = (i + 1) & ~31; base < n; base += 32) {
-      const int j = base + lane;
-      const unsigned m = __ballot_sync(~0u, j > i && j < n && sh.parent[min(j, n - 1)] == node);
-      if (m) return base + __ffs(m) - 1;
-    }
-    return n;
-  };
-  // Whether token i is accepted with share s; for a draft with probabilities.
-  auto accepts = [&](int i, float s) {
-    if (!refused) return (bool)sh.as_first[i];
-    const float p = sh.p[i], q = sh.q[i], cut = q * taken;
-    const double left = p > cut ? (double)(mass_at(p) - mass_at(cut)) * 9.094947017729282379150390625e-13 : 0.0;
-    return (double)sh.u[i] * (double)(q * s) < left;
-  };
-  auto accept = [&](int i) {
-    if (lane == 0) sh.path[acc] = (short)i;
-    ++acc;
-    node = i;
-    refused = 0;
-    share = 1.f;
-    taken = 0.f;
-    removed = 0;
-  };
-  auto walk = [&]() {  // true: a sum is needed
-    while (true) {
-      const int i = acc < a.max_path ? next_child(at_token) : n;
-      if (i >= n) return false;
-      at_token = i;
-      if (draft) {
-        if (accepts(i, share)) {
-          accept(i);
-          continue;
-        }
-        ++refused;
-        taken += share;
-        if (share == 0.f) continue;  // nothing is left, and nothing will be
-        // the next one, should it be accepted with a share that can only be too large
-        const int next = next_child(i);
-        if (next >= n || !accepts(next, share)) return true;
-        at_token = next;
-        accept(next);
-      } else {
-        bool again = false;  // a refused child of the same parent has the same id
-        if (refused) {
-          const int x = sh.x[i];
-          for (int base = 0; base < i && !again; base += 32) {
-            const int j = min(base + lane, n - 1);
-            again = __any_sync(~0u, base + lane < i && sh.parent[j] == node && sh.x[j] == x);
-          }
-        }
-        const float p = sh.p[i];
-        const bool ok = !again && (refused ? (double)sh.u[i] * (double)share < (double)p : (bool)sh.as_first[i]);
-        if (ok) {
-          accept(i);
-          continue;
-        }
-        ++refused;
-        if (!again) removed += mass_at(p);
-        share = share_of(max(((int64_t)1 << 40) - removed, (int64_t)0));
-      }
-    }
-  };
   while (!bad) {
     if (warp == 0) {
+      __syncwarp();
+      // the last accepted token, how many, refused children of it
+      int node = sh.step.node, acc = sh.step.acc, refused = sh.step.refused, at_token = sh.walk.at;
+      float share = sh.walk.s, taken = sh.walk.c;  // s and c
+      int64_t removed = sh.walk.removed;           // without a draft: P of the refused ids
+      // the first token after i whose parent is `node`, or n
+      auto next_child = [&](int i) {
+        for (int base = (i + 1) & ~31; base < n; base += 32) {
+          const int j = base + lane;
+          const unsigned m = __ballot_sync(~0u, j > i && j < n && sh.parent[min(j, n - 1)] == node);
+          if (m) return base + __ffs(m) - 1;
+        }
+        return n;
+      };
+      // Whether token i is accepted with share s; for a draft with probabilities.
+      auto accepts = [&](int i, float s) {
+        if (!refused) return (bool)sh.as_first[i];
+        const float p = sh.p[i], q = sh.q[i], cut = q * taken;
+        const double left = p > cut ? (double)(mass_at(p) - mass_at(cut)) * 9.094947017729282379150390625e-13 : 0.0;
+        return (double)sh.u[i] * (double)(q * s) < left;
+      };
+      auto accept = [&](int i) {
+        if (lane == 0) sh.path[acc] = (short)i;
+        ++acc;
+        node = i;
+        refused = 0;
+        share = 1.f;
+        taken = 0.f;
+        removed = 0;
+      };
+      auto walk = [&]() {  // true: a sum is needed
+        while (true) {
+          const int i = acc < a.max_path ? next_child(at_token) : n;
+          if (i >= n) return false;
+          at_token = i;
+          if (draft) {
+            if (accepts(i, share)) {
+              accept(i);
+              continue;
+            }
+            ++refused;
+            taken += share;
+            if (share == 0.f) continue;  // nothing is left, and nothing will be
+            // the next one, should it be accepted with a share that can only be too large
+            const int next = next_child(i);
+            if (next >= n || !accepts(next, share)) return true;
+            at_token = next;
+            accept(next);
+          } else {
+            bool again = false;  // a refused child of the same parent has the same id
+            if (refused) {
+              const int x = sh.x[i];
+              for (int base = 0; base < i && !again; base += 32) {
+                const int j = min(base + lane, n - 1);
+                again = __any_sync(~0u, base + lane < i && sh.parent[j] == node && sh.x[j] == x);
+              }
+            }
+            const float p = sh.p[i];
+            const bool ok = !again && (refused ? (double)sh.u[i] * (double)share < (double)p : (bool)sh.as_first[i]);
+            if (ok) {
+              accept(i);
+              continue;
+            }
+            ++refused;
+            if (!again) removed += mass_at(p);
+            share = share_of(max(((int64_t)1 << 40) - removed, (int64_t)0));
+          }
+        }
+      };
       const bool more = walk();
-      if (lane == 0) sh.step = {node, acc, refused, refused && draft ? sh.row[at_token] : 0, taken, !more};
+      __syncwarp();
+      if (lane == 0) {
+        sh.step = {node, acc, refused, refused && draft ? sh.row[at_token] : 0, taken, !more};
+        sh.walk = {at_token, share, taken, removed};
+      }
     }
     __syncthreads();
-    node = sh.step.node;
-    acc = sh.step.acc;
-    refused = sh.step.refused;
     if (sh.step.end) break;
-    w.set(target + (row0 + node + 1) * a.target_stride, draft + sh.step.row * a.draft_stride, -1, a.V);
+    w.set(target + (row0 + sh.step.node + 1) * a.target_stride, draft + sh.step.row * a.draft_stride, -1, a.V);
     w.taken = sh.step.taken;
-    sum();
-    share = fminf(share_of(at.total), 1.f);
+    const int64_t total = sum();
+    if (tid == 0) {
+      sh.total = total;
+      sh.walk.s = fminf(share_of(total), 1.f);
+    }
   }
+  const int node = sh.step.node, acc = sh.step.acc, refused = sh.step.refused;
 
+  int64_t total = 0;
   if (!bad) {  // uniform over the cluster
+    total = sh.total;
     if (!draft || !refused) {  // else the last sum is that of what is left
       w.set(target + (row0 + node + 1) * a.target_stride, nullptr, -1, a.V);
       w.holes = nullptr;
@@ -249,14 +273,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         __syncthreads();
         w.holes = holes;
       }
-      sum();
+      total = sum();
     }
-    if (!bad && at.total == 0 && refused) {  // nothing is left: draw from p itself
+    if (!bad && total == 0 && refused) {  // nothing is left: draw from p itself
       w.set(w.p, nullptr, -1, a.V);
       w.holes = nullptr;
-      sum();
+      total = sum();
     }
-    bad |= at.total == 0;
+    bad |= total == 0;
   }
 
   int32_t* out = a.tokens + (int64_t)b * a.token_stride;
@@ -275,9 +299,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (bad) return;
   // floor(u31 total / 2^31) with total below 2^58
   const int64_t u31 = __float2ll_rz(u_last * 2147483648.f);
-  const int64_t k = u31 * (at.total >> 31) + ((u31 * (at.total & 0x7fffffff)) >> 31);
-  int64_t left = k - at.before;
-  if (left < 0 || left >= sh.slice_sum[(passes - 1) & 1][rank]) return;  // another slice's
+  int64_t left = u31 * (total >> 31) + ((u31 * (total & 0x7fffffff)) >> 31);
+  const int64_t* const slices = sh.slice_sum[(passes - 1) & 1];
+  for (int i = 0; i < rank; ++i) left -= slices[i];
+  if (left < 0 || left >= slices[rank]) return;  // another slice's
+  const Share<C> at(w.vectors(), rank);
   int part = 0;  // the warp whose part holds the threshold
   while (left >= sh.warp_sum[part]) left -= sh.warp_sum[part++];
   // the batch of that warp: lane i adds up batch i
@@ -355,9 +381,10 @@ cudaError_t launch_tree(const clsample_verify_tree_args_t& a, cudaStream_t st) {
 }
 
 // As for clsample_verify: the largest cluster with which all requests are resident at once.  One
-// request of 6 refusals over 151936 tokens: 30 us on 16 CTAs, 41 on 8.  (64 requests on 16 CTAs each, not
-// all resident: 47 us instead of 51 where one of them has far more refusals than the others, but 110
-// instead of 82 where all have 6.)
+// request of 6 refusals over 151936 tokens: 29 us on 16 CTAs, 40 on 8.  (On an earlier version 64 requests
+// on 16 CTAs each, not all resident: 47 us instead of 51 where one of them has far more refusals than the
+// others, but 110 instead of 82 where all have 6; now 48 and 77 on 8.  Three CTAs a multiprocessor of 80
+// registers, not all resident either: 41 and 98.)
 template <class P>
 cudaError_t launch_tree(const clsample_verify_tree_args_t& a, int sms, cudaStream_t st) {
   const int64_t slots = (int64_t)sms * kCtasPerSm;
