@@ -41,12 +41,6 @@ constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 128;
 constexpr float kRescaleAt = 8.f;  // log2
 
-// Registers a thread: the two softmax warpgroups, and the one of loads and products.  They
-// add up to what the block is launched with (3 x 168).  (What does not stay in them goes a long way
-// here, as shared memory leaves L1 little room.  With kTree the loads look at masks and at units of other
-// kinds; 256 requests of 48 rows over 300 keys took 133 us when they did not fit, and 118 since.)
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168 && 168 * kChunkThreads <= 65536, "the launch's registers");
 
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -222,6 +216,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   const Span& ours = kTree ? sh.span : span;  // (one of them costs registers, the other loads)
 
+  // Registers a thread: the two softmax warpgroups, and the one of loads and products.  They add up to what
+  // the block is launched with (3 x 168).  (What does not stay in them goes a long way here, as shared memory
+  // leaves L1 little room.  With kTree the loads look at masks and at units of other kinds; 256 requests of 48 rows
+  // over 300 keys took 133 us when they did not fit, 119 with 60 bytes of them left and 117 so; 64 requests of
+  // 192 rows 66 with 200 and 68 with 192.)
+  constexpr int kSoftmaxRegs = kPairs ? 192 : 200, kOtherRegs = kPairs ? 120 : 104;
+  static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168 && 168 * kChunkThreads <= 65536, "the launch's registers");
   // A whole warpgroup has to run the same register instruction, so warps 8 to 11 do before they part.
   if (warp >= 8) regs_down<kOtherRegs>();
   if (warp < 8) {

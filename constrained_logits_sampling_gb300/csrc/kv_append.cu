@@ -81,7 +81,6 @@ __device__ __forceinline__ void write_status(const AppendParams& P, int b, bool 
     if (first < 0 || (a.rot_dim > 0 && !P.positions && s.len > a.max_pos)) {
       ok = false;
     } else {
-
       for (int p = first / a.page_size; ok && p <= (s.len - 1) / a.page_size; ++p) {
         const int id = __ldg(a.page_table + (int64_t)b * a.table_stride + p);
         ok = id >= 0 && id < a.num_pages;
