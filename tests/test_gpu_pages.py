@@ -423,6 +423,82 @@ def test_moves_streams_graphs_and_refusals(G):
     assert e.value.code == -9
 
 
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_that_follow_one_another(G, graph):
+    """Fork, reserve, copy, a write, a kept path and trim, each of what the one before has left."""
+    page, B, pages = 16, 40, 400
+    old, n = 500, 6
+    pool, keep, copy = G.PagePool(pages, page), G.KeepPath(), G.CopyPages()
+    k, v = (torch.randn(3, pages, page, 2, 64, device="cuda").to(BF) for _ in range(2))
+    table = torch.full((B, 40), -1, dtype=I32, device="cuda")
+    held, lens, more = (torch.zeros(B, dtype=I32, device="cuda") for _ in range(3))
+    more[0] = old
+    first = pool.reserve(table, held, lens, more)
+    lens[0] = old
+    assert first["status"].tolist() == [0] * B
+    src, dst = i32([0] * (B - 1)), i32(list(range(1, B)))
+    new, cu = i32([n + 1] * B), i32([n * b for b in range(B + 1)])
+    path, accepted = i32([[1, 3, 5]] * B), i32([b % 4 for b in range(B)])
+    copies, after, free = (torch.zeros(s, dtype=I32, device="cuda") for s in ((B, 3), (B,), (1,)))
+    status = [torch.full((B,), -1, dtype=I32, device="cuda") for _ in range(5)]
+    fork = pool.fork_args(table, held, lens, src, dst, row_status=status[0][1:])
+    reserve = pool.reserve_args(table, held, lens, new, copies=copies, row_status=status[1], free_pages=free)
+    moved = copy.make_args(k, v, copies, status=status[2])
+    kept = keep.make_args(k, v, table, cu, lens, path, accepted, new_lens=after, row_status=status[3])
+    trim = pool.trim_args(table, held, lens, row_status=status[4])
+    rows = torch.arange(n + 1, device="cuda")
+    values = torch.randn(2, 3, B, n + 1, 2, 64, device="cuda").to(BF)
+    who = torch.arange(B, device="cuda").view(B, 1)
+    start = [t.clone() for t in (table, held, lens, pool.refs, pool.free_bits)]
+    before = k[:, table[0, (old - 1) // page].long(), :old % page].clone()
+
+    def work():
+        for t, s in zip((table, held, lens, pool.refs, pool.free_bits), start):
+            t.copy_(s)
+        pool.apply(fork)
+        pool.apply(reserve)
+        copy.apply(moved)
+        at = old + rows
+        ids = table[who, (at // page).view(1, -1)].long()
+        k[:, ids, at % page], v[:, ids, at % page] = values[0], values[1]
+        lens.add_(n + 1)
+        keep.apply(kept)
+        lens.copy_(after)
+        pool.apply(trim)
+
+    def check():
+        assert all(s.tolist()[i == 0:] == [0] * (B - (i == 0)) for i, s in enumerate(status))
+        assert lens.tolist() == [old + 1 + b % 4 for b in range(B)]
+        for b in range(B):
+            ids = table[b].tolist()
+            last = ids[(old - 1) // page]
+            assert torch.equal(k[:, last, :old % page], before)
+            for i, j in enumerate([0] + [p + 1 for p in (1, 3, 5)][:b % 4]):
+                x = old + i
+                assert torch.equal(k[:, ids[x // page], x % page], values[0][:, b, j])
+                assert torch.equal(v[:, ids[x // page], x % page], values[1][:, b, j])
+        own = (old - 1) // page
+        assert len({int(t) for t in table[:, own]}) == B  # written to, so each has its own
+        assert held.tolist() == [-(-int(m) // page) for m in lens]
+
+    if graph:
+        work()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            work()
+        for _ in range(3):
+            k[:, table[:, (old - 1) // page].long(), old % page:] = 0
+            g.replay()
+            torch.cuda.synchronize()
+            check()
+    else:
+        for _ in range(3):
+            work()
+            torch.cuda.synchronize()
+            check()
+
+
 def test_forked_sequences_attend_as_their_own(G):
     """A prompt forked twice, each child given a token of its own: attention over the shared pages
     equals attention over caches that share nothing, bit for bit."""

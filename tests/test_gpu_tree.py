@@ -94,6 +94,62 @@ def test_plan_strides_stream_and_graph(S):
     assert torch.equal(wide[:, 1:3], want["mask"]) and torch.equal(pos, want["positions"] + 5)
 
 
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("kind", ["kernel", "host", "device", "fill", "streams", "first"])
+def test_plan_behind_other_work(S, kind, graph):
+    """Whatever the work before it is, a call takes what that leaves; the work after it takes the call's."""
+    r = random.Random(8)
+    trees = [TR.tree(r, n) for n in (20, 0, 45, 63)]
+    parents, cu, lens = i32([p for t in trees for p in t]), offsets([len(t) for t in trees]), i32([30, 9, 99, 70])
+    if kind == "fill":
+        parents.fill_(-1)
+    want = S.TreePlan()(parents, cu, lens, max_draft=63)
+    host = parents.cpu().pin_memory()
+    given, side, plan = torch.empty_like(parents), torch.cuda.Stream(), S.TreePlan()
+    out = {n: torch.empty_like(want[n]) for n in ("mask", "positions", "status")}
+    copies = {n: torch.empty_like(t) for n, t in out.items()}
+    args = plan.make_args(given, cu, lens, max_draft=63, mask=out["mask"], positions=out["positions"],
+                          row_status=out["status"])
+
+    def work():
+        if kind == "streams":  # behind two of them
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(300000)
+                given.copy_(parents)
+            torch.cuda._sleep(1000)
+            torch.cuda.current_stream().wait_stream(side)
+        elif kind != "first":
+            torch.cuda._sleep(300000)
+            if kind == "kernel":
+                torch.add(parents, 0, out=given)
+            elif kind == "fill":
+                given.fill_(-1)
+            else:
+                given.copy_(host if kind == "host" else parents, non_blocking=True)
+        plan.apply(args)
+        for n, t in out.items():
+            copies[n].copy_(t)
+
+    main = torch.cuda.Stream()
+    for _ in range(3):
+        given.copy_(parents) if kind == "first" else given.fill_(-7)
+        for t in list(out.values()) + list(copies.values()):
+            t.fill_(-3)
+        torch.cuda.synchronize()
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                work()
+            g.replay()
+        else:
+            with torch.cuda.stream(main):
+                work()
+        torch.cuda.synchronize()
+        for n in out:
+            assert torch.equal(copies[n], want[n]), n
+
+
 def test_plan_bad_requests(S):
     """Requests that cannot be are INVALID with empty masks; the others are what they were."""
     good = [-1, 0, 0]
