@@ -264,6 +264,47 @@ def test_attention_whatever_the_table_holds(S, n, D, wide):
     check_attention(S, pr, rows, [o + d for o, t in zip((150, 700, 3), depth) for d in t], window=90 if n == 33 else 0)
 
 
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("drafted,old,Hkv,D", [([3, 9], [700, 90], 2, 64), ([70, 5], [2500, 2000], 8, 128),
+                                              ([60 if i % 50 == 1 else i % 3 for i in range(320)], [300] * 320, 2, 128)])
+def test_attention_behind_other_work(S, drafted, old, Hkv, D, graph):
+    """A call takes what the work before it leaves, of each of its inputs (in one kernel, another, or both)."""
+    pr = problem(drafted, old, 4 * Hkv, Hkv, D, 16, BF, seed=6)
+    _, rows, depth = trees_of(drafted, 6, 200)
+    good = tensors(pr) + [TR.words_of(rows, 3).cuda(), i32([o + d for o, t in zip(old, depth) for d in t])]
+    att, kw = S.TreeAttention(), dict(window=200, max_new=max(pr.new))
+    want = att(*good[:6], mask=good[6], positions=good[7], lse=True, **kw)
+    given = [torch.empty_like(t) for t in good]
+    out, status = torch.empty_like(want["out"]), torch.empty_like(want["status"])
+    args = att.make_args(*given[:6], mask=given[6], positions=given[7], out=out, row_status=status, **kw)
+    seen, ok = torch.empty_like(out), torch.empty_like(status)
+
+    def work(last):
+        for i, (t, g) in enumerate(zip(given, good)):
+            if i != last:
+                t.copy_(g)
+        torch.cuda._sleep(300000)
+        torch.add(good[last], 0, out=given[last])
+        att.apply(args)
+        seen.copy_(out)
+        ok.copy_(status)
+
+    for last in range(len(good)):
+        for t in given:
+            t.fill_(-1)
+        seen.fill_(7)
+        torch.cuda.synchronize()
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                work(last)
+            g.replay()
+        else:
+            work(last)
+        torch.cuda.synchronize()
+        assert torch.equal(seen, want["out"]) and torch.equal(ok, want["status"]), last
+
+
 def test_attention_two_handles_at_once(S):
     """Calls of two objects on two streams do not meet."""
     cases = []
