@@ -161,7 +161,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const clsample_attention_args_t& a = P.a;
   const float neg_inf = __int_as_float(0xff800000);
 
-  if (kTree && P.behind) wait_for_earlier_grids();  // before the next may start, which then need not
   let_next_grid_start();
   if (tid == 0) {
     // for tests: a barrier that waits for one arrival more than it gets

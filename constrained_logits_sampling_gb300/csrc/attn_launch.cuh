@@ -101,15 +101,13 @@ cudaError_t launch_chunk(AttnParams P, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> allowed[4];
   const cudaError_t e = allow_smem_once(fn, bytes, &allowed[2 * pairs + boxes]);
   if (e != cudaSuccess) return e;
-  if (P.behind) return launch_after(fn, sms, kChunkThreads, bytes, st, P, k_map, v_map, q_map);
   fn<<<sms, kChunkThreads, bytes, st>>>(P, k_map, v_map, q_map);
   return cudaGetLastError();
 }
 
 // first: of the call
 template <class T, int D, bool kTree, int RB>
-cudaError_t launch_stream(AttnParams P, int sms, bool first, cudaStream_t st) {
-  P.behind = kTree && first;
+cudaError_t launch_stream(const AttnParams& P, int sms, bool first, cudaStream_t st) {
   using Ring = StreamRing<D, RB, kTree>;
   const int grid = sms * Ring::kCtas;
   auto* fn = attn_stream_kernel<T, D, kTree, RB>;
@@ -117,7 +115,7 @@ cudaError_t launch_stream(AttnParams P, int sms, bool first, cudaStream_t st) {
   static std::atomic<uint64_t> allowed;
   const cudaError_t e = allow_smem_once(fn, bytes, &allowed);
   if (e != cudaSuccess) return e;
-  if (!first || P.behind) return launch_after(fn, grid, kStreamThreads, bytes, st, P);
+  if (!first) return launch_after(fn, grid, kStreamThreads, bytes, st, P);
   fn<<<grid, kStreamThreads, bytes, st>>>(P);
   return cudaGetLastError();
 }
@@ -139,7 +137,6 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, int64_t most_rows,
   const bool alone = chunks && (int64_t)P.a.B * P.a.Hkv <= 4 * h->sms;
   cudaError_t e;
   if (chunks) {
-    P.behind = kTree;
     P.min_rows = alone ? 0 : (int)most_rows + 1;
     P.max_rows = 0x7fffffff;
     P.partial = chunk_partial;
@@ -160,7 +157,7 @@ cudaError_t launch(const clsample_attention* h, AttnParams P, int64_t most_rows,
 // one and 441 in the other; of 24 rows, where the one reads keys twice, 707 and 420.
 // By mask the stream kernel alone, in units of 16 rows that read their keys again, takes calls of
 // little work: `steps` is how many pieces of 64 keys that would be at most.  One request over 1500 keys on 8
-// key heads of 128 takes 14 us there with 96 rows and 20 in the chunk kernel (with 256: 25 and 18); 95
+// key heads of 128 takes 14 us there with 96 rows and 20 in the chunk kernel (with 256: 26 and 19); 95
 // requests of 3 to 42 rows with a window of 300 on 4 heads of 64 take 25, and 46 in both kernels by row
 // counts.  Otherwise it has units of 32 rows.  64 requests of 24 rows over 2000 keys on 8 key heads of 128: 107
 // us there and 112 in the chunk kernel, over 300 keys 37 and 48; on 4 heads of 64: 41 and 52, 18 and 26.  With

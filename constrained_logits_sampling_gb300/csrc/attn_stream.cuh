@@ -364,7 +364,6 @@ __global__ void __launch_bounds__(kStreamThreads, StreamRing<D, RB, kTree>::kCta
   const clsample_attention_args_t& a = P.a;
   const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(smem + warp * S * kStageBytes));
 
-  if (kTree && P.behind) wait_for_earlier_grids();  // before the next may start, which then need not
   let_next_grid_start();
   Span span;
   Unit u;

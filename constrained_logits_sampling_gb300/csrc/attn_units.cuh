@@ -31,7 +31,6 @@ struct AttnParams {
   int min_rows;     // this launch takes the sequences with min_rows <= n g < max_rows
   int max_rows;
   int q_box;        // queries may be copied in boxes of 128 rows
-  int behind;       // kTree: the call's first launch, which may start while the grid before it ends
   float* partial;   // scratch: two slots per CTA
   struct CutUnit* cut;  // one per CTA: the unit that starts in its span and ends in another's
   int* gave_up;     // set when a bounded wait ran out
@@ -131,7 +130,7 @@ struct UnitMap {
     return pairs(P, n) ? (P.a.Hkv + 1) / 2 : P.a.Hkv;
   }
   static __device__ __forceinline__ Seq seq_of(const AttnParams& P, int b) {
-    Seq s = load_seq<kTree>(P.a.cu_new, P.a.kv_lens, b, P.a.T, P.capacity, P.a.max_new);
+    Seq s = load_seq(P.a.cu_new, P.a.kv_lens, b, P.a.T, P.capacity, P.a.max_new);
     const int64_t rows = (int64_t)s.n * P.g;
     if (rows < P.min_rows || rows >= P.max_rows) s.n = 0;  // another launch's
     if (kTree && s.len < s.n) s.len = 0;  // no keys

@@ -114,17 +114,14 @@ __host__ __device__ inline int capacity_of(int max_pages, int page_size) {
 }
 
 // Rows and length of one sequence, as the arrays state them; ok is false when offsets or
-// length cannot be (then n is 0 unless the offsets themselves are in order).  kPlain: by loads that stay
-// behind wait_for_earlier_grids().
+// length cannot be (then n is 0 unless the offsets themselves are in order).
 struct Seq {
   int q0, n, len;
   bool ok;
 };
-template <bool kPlain = false>
 __device__ __forceinline__ Seq load_seq(const int32_t* cu, const int32_t* lens, int b, int T, int capacity,
                                         int max_new) {
-  const int lo = kPlain ? cu[b] : __ldg(cu + b), hi = kPlain ? cu[b + 1] : __ldg(cu + b + 1);
-  const int len = kPlain ? lens[b] : __ldg(lens + b);
+  const int lo = __ldg(cu + b), hi = __ldg(cu + b + 1), len = __ldg(lens + b);
   Seq s{lo, hi - lo, len, true};
   if (lo < 0 || hi < lo || hi > T) return Seq{0, 0, 0, false};
   if (len < 0 || len > capacity || s.n > max_new) {
