@@ -26,6 +26,21 @@ constexpr size_t kChunkSlots = 2 * (size_t)kChunkRows * 130 * sizeof(float);
 constexpr size_t kStreamSlots = kStreamCtas * 2 * (size_t)kMaxStreamRows * 130 * sizeof(float);
 constexpr size_t kCuts = (1 + kStreamCtas) * sizeof(CutUnit);
 constexpr size_t kScratch = kChunkSlots + kStreamSlots + kCuts;
+// A launch that may start while the one before it ends.
+template <class Kernel, class... Args>
+cudaError_t launch_after(Kernel fn, int grid, int threads, int smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
 
 // A tensor map of 16-bit elements, 128-byte swizzle, zeros out of bounds; false if there is none.
 template <int N>

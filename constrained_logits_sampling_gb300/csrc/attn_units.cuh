@@ -347,4 +347,9 @@ __device__ __forceinline__ void note_cut(const AttnParams& P, const Span& span, 
   P.cut[blockIdx.x] = c;
 }
 
+// Launches that follow one another without a gap: the next grid may start as this one's blocks
+// leave, and takes no result before wait_for_earlier_grids().
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_earlier_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace clsample

@@ -32,9 +32,8 @@ __global__ void __launch_bounds__(kThreads) keep_path_kernel(const __grid_consta
   __shared__ int64_t from[kMaxPath + 1], to[kMaxPath + 1];
   __shared__ int stays;  // tokens that are in their places: the first ones
   const int b = blockIdx.x / parts, part = blockIdx.x % parts, tid = threadIdx.x;
-  wait_for_earlier_grids();
-  const int lo = a.cu_draft[b], hi = a.cu_draft[b + 1], len = a.kv_lens[b];
-  const int count = a.accepted[b], n = hi - lo;
+  const int lo = __ldg(a.cu_draft + b), hi = __ldg(a.cu_draft + b + 1), len = __ldg(a.kv_lens + b);
+  const int count = __ldg(a.accepted + b), n = hi - lo;
   bool bad = lo < 0 || hi < lo || hi > a.N || len <= n || len > capacity_of(a.max_pages, a.page_size) || count < 0 ||
              count > min(n, a.max_path);
   const int first = len - n;  // the first place of the path
@@ -44,14 +43,14 @@ __global__ void __launch_bounds__(kThreads) keep_path_kernel(const __grid_consta
     const int32_t* path = a.path + (int64_t)b * a.path_stride;
     const int32_t* table = a.page_table + (int64_t)b * a.table_stride;
     for (int i = tid; i < count; i += kThreads) {
-      const int x = path[i], before = i ? path[i - 1] : -1;
+      const int x = __ldg(path + i), before = i ? __ldg(path + i - 1) : -1;
       if (x <= before || x >= n) {
         bad = true;
       } else if (x == i) {
         atomicAdd(&stays, 1);
       } else {
         const int src = first + x, dst = first + i;
-        const int src_page = table[src / a.page_size], dst_page = table[dst / a.page_size];
+        const int src_page = __ldg(table + src / a.page_size), dst_page = __ldg(table + dst / a.page_size);
         bad |= src_page < 0 || src_page >= a.num_pages || dst_page < 0 || dst_page >= a.num_pages;
         from[i] = src_page * c.page + src % a.page_size * c.slot;
         to[i] = dst_page * c.page + dst % a.page_size * c.slot;
@@ -92,7 +91,6 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
                                                               const __grid_constant__ CacheShape c, int parts) {
   using T = typename Piece<kBytes>::T;
   constexpr int kAhead = 8;  // pieces of a thread in flight
-  wait_for_earlier_grids();
   const int planes = 2 * a.layers, per_copy = planes * parts;
   const int64_t items = (int64_t)a.n * per_copy;
   const int heads = c.per_head * a.Hkv, step = parts * kThreads, step_slots = step / heads, step_rest = step % heads;
@@ -100,8 +98,8 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int i = (int)(item / per_copy), rest = (int)(item - (int64_t)i * per_copy);
     const int plane = rest / parts, part = rest % parts;
-    const int32_t* const copy = a.copies + 3 * (int64_t)i;
-    const int from = copy[0], to = copy[1], slots = copy[2];
+    const int from = __ldg(a.copies + 3 * (int64_t)i), to = __ldg(a.copies + 3 * (int64_t)i + 1),
+              slots = __ldg(a.copies + 3 * (int64_t)i + 2);
     const bool none = from < 0 || slots == 0;
     const bool bad = !none && (from >= a.num_pages || to < 0 || to >= a.num_pages || slots < 0 || slots > a.page_size);
     if (a.status && rest == 0 && threadIdx.x == 0) a.status[i] = bad ? CLSAMPLE_ROW_INVALID : CLSAMPLE_ROW_OK;
@@ -162,20 +160,19 @@ int check_cache(const Args& a) {
 }
 
 template <int kBytes>
-cudaError_t launch_keep(const clsample_keep_path_args_t& a, cudaStream_t st) {
+void launch_keep(const clsample_keep_path_args_t& a, cudaStream_t st) {
   const CacheShape c = shape_of(a, kBytes);
   const int64_t columns = (int64_t)2 * a.layers * a.Hkv * c.per_head;
-  // two columns a thread: 192 requests' paths in 8 layers (2 x 7.8 MB) 5.2 us; on an earlier version 5.5, with
-  // one 6.6
+  // two columns a thread: 192 requests' paths in 8 layers (2 x 7.8 MB) 5.5 us, with one 6.6
   int64_t parts = (columns + 2 * kThreads - 1) / (2 * kThreads);
   const int64_t most = (1 << 30) / (int64_t)a.B;
   if (parts > most) parts = most;
-  return launch_after(keep_path_kernel<kBytes>, (int)(a.B * parts), kThreads, 0, st, a, c, (int)parts);
+  keep_path_kernel<kBytes><<<(unsigned)(a.B * parts), kThreads, 0, st>>>(a, c, (int)parts);
 }
 
 // Few copies are shared out among as many CTAs as their pieces take, up to the device's room.
 template <int kBytes>
-cudaError_t launch_copy(const clsample_copy_pages_args_t& a, int sms, cudaStream_t st) {
+int launch_copy(const clsample_copy_pages_args_t& a, int sms, cudaStream_t st) {
   constexpr int kPerSm = 6;
   const CacheShape c = shape_of(a, kBytes);
   const int64_t pieces = (int64_t)a.page_size * a.Hkv * c.per_head, planes = (int64_t)a.n * 2 * a.layers;
@@ -184,7 +181,8 @@ cudaError_t launch_copy(const clsample_copy_pages_args_t& a, int sms, cudaStream
   if (parts > most) parts = most;
   if (parts > 64) parts = 64;
   const int64_t items = planes * parts;
-  return launch_after(copy_pages_kernel<kBytes>, (int)(items < room ? items : room), kThreads, 0, st, a, c, (int)parts);
+  copy_pages_kernel<kBytes><<<(unsigned)(items < room ? items : room), kThreads, 0, st>>>(a, c, (int)parts);
+  return CLSAMPLE_SUCCESS;
 }
 
 }  // namespace
@@ -207,14 +205,13 @@ int clsample_keep_path(const clsample_keep_path_args_t* a, clsample_stream_t str
   if (a->new_lens == a->kv_lens) return CLSAMPLE_ERR_SHAPE;
   if ((rc = check_device()) != CLSAMPLE_SUCCESS) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
   switch (piece_bytes(*a)) {
-    case 16: e = launch_keep<16>(*a, st); break;
-    case 8: e = launch_keep<8>(*a, st); break;
-    case 4: e = launch_keep<4>(*a, st); break;
-    default: e = launch_keep<2>(*a, st);
+    case 16: launch_keep<16>(*a, st); break;
+    case 8: launch_keep<8>(*a, st); break;
+    case 4: launch_keep<4>(*a, st); break;
+    default: launch_keep<2>(*a, st);
   }
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
 }
 
 int clsample_copy_pages(const clsample_copy_pages_args_t* a, clsample_stream_t stream) {
@@ -228,14 +225,14 @@ int clsample_copy_pages(const clsample_copy_pages_args_t* a, clsample_stream_t s
   int sms = 0;
   if ((rc = check_device(nullptr, &sms)) != CLSAMPLE_SUCCESS) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
   switch (piece_bytes(*a)) {
-    case 16: e = launch_copy<16>(*a, sms, st); break;
-    case 8: e = launch_copy<8>(*a, sms, st); break;
-    case 4: e = launch_copy<4>(*a, sms, st); break;
-    default: e = launch_copy<2>(*a, sms, st);
+    case 16: rc = launch_copy<16>(*a, sms, st); break;
+    case 8: rc = launch_copy<8>(*a, sms, st); break;
+    case 4: rc = launch_copy<4>(*a, sms, st); break;
+    default: rc = launch_copy<2>(*a, sms, st);
   }
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
+  if (rc != CLSAMPLE_SUCCESS) return rc;
+  return cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -4,7 +4,7 @@
 // Counting references needs no order, and free pages are a set of bits, so whatever order
 // atomics take, the state after a call is the same.  What has an order, the giving out of free
 // pages, is one CTA's work: it needs a prefix sum over the sequences and one over the bits.  All of it is
-// latency: a few dependent loads and barriers.  Behind one another: fork 1.5 to 2 us, reserve 3.7 to 3.9, trim 1.3.
+// latency: a few dependent loads and barriers.
 #include "paged.cuh"
 
 namespace clsample {
@@ -29,10 +29,9 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   const clsample_page_pool_t& pool = P.pool;
   const clsample_page_batch_t& q = P.batch;
   const int i = blockIdx.x, tid = threadIdx.x;
-  wait_for_earlier_grids();
-  const int src = src_of[i], dst = dst_of[i];
+  const int src = __ldg(src_of + i), dst = __ldg(dst_of + i);
   int bad = src < 0 || src >= q.B || dst < 0 || dst >= q.B;
-  for (int k = tid; k < n; k += kThreads) bad |= src_of[k] == dst || (k != i && dst_of[k] == dst);
+  for (int k = tid; k < n; k += kThreads) bad |= __ldg(src_of + k) == dst || (k != i && __ldg(dst_of + k) == dst);
   bad = __syncthreads_or(bad);
   int len = 0, need = 0;
   if (!bad) {  // (src is no dst and dst is this pair's: neither changes meanwhile)
@@ -70,7 +69,6 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(const __grid_constant__ 
   const clsample_page_pool_t& pool = P.pool;
   const clsample_page_batch_t& q = P.batch;
   const int b = blockIdx.x, tid = threadIdx.x;
-  wait_for_earlier_grids();
   const int len = q.kv_lens[b], held = q.held[b];
   bool bad = len < 0 || len > capacity_of(q.max_pages, pool.page_size) || held < 0 || held > q.max_pages;
   const int keep = bad ? 0 : pages_of(len, pool.page_size);
@@ -133,7 +131,7 @@ struct Writes {
 // One CTA, a thread a sequence.  A page that sequences of the call would write to, where any of
 // them is shared: each takes its reference back first, and if none is left nobody else holds it; the last
 // of them, by a maximum over stamps, then keeps it.  Stamps carry the call's number, so they need not be
-// cleared.  Without a shared page none of that is done (on an earlier version 7.3 us to 4.3 for 240 sequences).
+// cleared.  Without a shared page none of that is done (7.3 us to 4.3 for 240 sequences).
 // Of up to 1024 sequences, a thread keeps what it has read of its one; beyond that copies tells it from
 // one pass to the next whether it is INVALID (-2), where its pages start in the list and how many it needs.
 __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_constant__ PoolParams P,
@@ -146,7 +144,6 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
   __shared__ int buf[32], near[kReserveThreads];  // near: the first pages of the list
   __shared__ Long longs[kReserveThreads];
   __shared__ int long_count;
-  wait_for_earlier_grids();
   const int tid = threadIdx.x, page = pool.page_size, cap = capacity_of(q.max_pages, page);
   const bool one = q.B <= kReserveThreads;
   const uint64_t call = (uint64_t)(*pool.epoch + 1) << 32;
@@ -162,7 +159,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
     mine += __popc(bits);
   }
   auto load = [&](int b) {
-    Writes w{q.kv_lens[b], new_tokens[b], q.held[b], 0, -1};
+    Writes w{q.kv_lens[b], __ldg(new_tokens + b), q.held[b], 0, -1};
     if (w.count > 0) {
       w.first = w.len / page;
       w.last = (int)(((int64_t)w.len + w.count - 1) / page);
@@ -351,9 +348,8 @@ int clsample_pages_fork(const clsample_page_pool_t* pool, const clsample_page_ba
   if (n == 0) return CLSAMPLE_SUCCESS;
   if (!src || !dst) return CLSAMPLE_ERR_NULL;
   if ((rc = check_device()) != CLSAMPLE_SUCCESS) return rc;
-  const cudaError_t e = launch_after(fork_kernel, n, kThreads, 0, reinterpret_cast<cudaStream_t>(stream),
-                                     PoolParams{*pool, *batch}, src, dst, n, status);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
+  fork_kernel<<<n, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(PoolParams{*pool, *batch}, src, dst, n, status);
+  return cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
 }
 
 int clsample_pages_reserve(const clsample_page_pool_t* pool, const clsample_page_batch_t* batch,
@@ -365,9 +361,9 @@ int clsample_pages_reserve(const clsample_page_pool_t* pool, const clsample_page
   if (batch->B == 0) return CLSAMPLE_SUCCESS;
   if (!new_tokens || !copies) return CLSAMPLE_ERR_NULL;
   if ((rc = check_device()) != CLSAMPLE_SUCCESS) return rc;
-  const cudaError_t e = launch_after(reserve_kernel, 1, kReserveThreads, 0, reinterpret_cast<cudaStream_t>(stream),
-                                     PoolParams{*pool, *batch}, new_tokens, copies, row_status, free_pages);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
+  reserve_kernel<<<1, kReserveThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      PoolParams{*pool, *batch}, new_tokens, copies, row_status, free_pages);
+  return cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
 }
 
 int clsample_pages_trim(const clsample_page_pool_t* pool, const clsample_page_batch_t* batch, int32_t* row_status,
@@ -377,9 +373,8 @@ int clsample_pages_trim(const clsample_page_pool_t* pool, const clsample_page_ba
   if (rc != CLSAMPLE_SUCCESS) return rc;
   if (batch->B == 0) return CLSAMPLE_SUCCESS;
   if ((rc = check_device()) != CLSAMPLE_SUCCESS) return rc;
-  const cudaError_t e = launch_after(trim_kernel, batch->B, kThreads, 0, reinterpret_cast<cudaStream_t>(stream),
-                                     PoolParams{*pool, *batch}, row_status);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
+  trim_kernel<<<batch->B, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(PoolParams{*pool, *batch}, row_status);
+  return cudaGetLastError() == cudaSuccess ? CLSAMPLE_SUCCESS : CLSAMPLE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -53,29 +53,6 @@ cudaError_t allow_smem_once(Kernel* fn, int bytes, std::atomic<uint64_t>* done) 
   return allow_once(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
 }
 
-// A launch that may start while the one before it ends.
-template <class Kernel, class... Args>
-cudaError_t launch_after(Kernel fn, int grid, int threads, int smem, cudaStream_t st, const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, args...);
-}
-
-// Launches that follow one another without a gap: the next grid may start as this one's blocks
-// leave, and takes no result before wait_for_earlier_grids().  A grid that may be launched behind anybody's
-// (launch_after as a call's first launch) waits before all else; its loads that need no other value
-// are plain ones, as one through the read-only path is not bound to stay behind the wait.
-__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_earlier_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // The 16-bit types: widening is exact, narrowing rounds to nearest even.

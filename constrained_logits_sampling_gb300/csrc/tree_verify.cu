@@ -90,9 +90,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   // a CTA's shared memory may be written from afar only once it has started
   cluster.barrier_arrive();
 
-  wait_for_earlier_grids();
-  const int lo = a.cu_draft[b], hi = a.cu_draft[b + 1];  // (all other places follow from them)
-  const float u_last = a.u_sample[b];
+  const int lo = __ldg(a.cu_draft + b), hi = __ldg(a.cu_draft + b + 1);
+  const float u_last = __ldg(a.u_sample + b);
   bool bad = lo < 0 || hi < lo || hi > a.N || hi - lo > a.max_draft || !(u_last >= 0.f && u_last < 1.f);
   const int n = bad ? 0 : hi - lo;  // at most kMaxNodes
   if (tid == 0) {
@@ -366,14 +365,12 @@ cudaError_t launch_tree(const clsample_verify_tree_args_t& a, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)smem_bytes<P, C>(a.V);
   cfg.stream = st;
-  cudaLaunchAttribute at[2];
+  cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = C;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   static std::atomic<uint64_t> allowed;
   cudaError_t e = allow_smem_once(verify_tree_kernel<P, C>, smem_bytes<P, C>(kMaxVocab), &allowed);
   if (C > 8 && e == cudaSuccess) {
