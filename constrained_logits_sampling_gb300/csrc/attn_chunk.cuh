@@ -120,7 +120,10 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int k) {
 }
 
 struct SoftmaxSync {  // the 256 softmax threads
-  static __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+  static __device__ __forceinline__ void sync() {
+    __syncwarp();  // the barrier counts whole warps
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+  }
   static __device__ __forceinline__ bool all(bool yes) {  // and whether all of them say yes
     uint32_t r;
     __syncwarp();
@@ -134,13 +137,16 @@ struct SoftmaxSync {  // the 256 softmax threads
 };
 
 // How a CTA ends when a wait has run out, so that nothing is left waiting or in flight and every
-// address stays one of the call's.  The wait's thread marks the CTA dead before it goes on, on
-// whatever is there.  Who waits for that one's arrivals goes on too, so the load warps look at the
-// mark after each wait: they announce and make no more copies, hand over no more units, and leave
-// after the unit that they have.  The warp of products issues none after a wait of its own that
-// failed.  The softmax threads finish the unit that they have, as its barriers take all 256 of
-// them, and go on to no other.  Then all pause while copies land.  The call's statuses tell that
-// its outputs are void.
+// address stays one of the call's.  The wait's warp marks the CTA dead, makes no copy, no product and
+// no arrival after it, and leaves: so no phase of a barrier ever completes by an arrival that is not its own,
+// and nobody passes a wait that it should not have passed.  Whoever waits for that warp sees the mark and
+// leaves as well.  (Load warps of the form without TMA once went on after a wait in vain: their next
+// tile's arrivals completed the barrier that had been waited for, and the products were issued over
+// scores, weights and keys that others were using.)  All waits of a warp are taken and answered by all its
+// lanes at once, as instructions follow that need the whole warp.  The softmax warps meet at
+// barriers of all 256 threads within a unit: one whose wait ran out does what is left of the unit without
+// tensor memory and without stores of rows, and none of them goes on to another unit.  Then all pause
+// while copies land.  The call's statuses tell that its outputs are void.
 
 template <class T, int D, bool kTma, bool kTree = false, bool kPairs = false>
 __global__ void __launch_bounds__(kChunkThreads, 1)
@@ -245,6 +251,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int r = pair ? at_row & 127 : at_row;                         // this thread's row
       const bool live = r < u.rows;
       float m = neg_inf, l = 0.f;  // reference maximum (log2 units) and weights' sum
+      bool alive = true;           // of the warp: no wait has run out
       if (cnt > jw) {
         const int first_pos = u.len - u.n, kb0 = (u.tile0 + j0) * kChunkKeys;
         const int pos = live ? first_pos + token_of(P, u.row0 + r) : -1;
@@ -265,7 +272,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             seen = make_uint4(seen.x | column_bits(lo, hi), seen.y | column_bits(lo - 32, hi - 32),
                               seen.z | column_bits(lo - 64, hi - 64), seen.w | column_bits(lo - 96, hi - 96));
           }
-          bounded_wait(&sh.s_full[w], s_phase, &sh.limit);
+          alive = warp_wait(&sh.s_full[w], s_phase, &sh.limit);
+          if (!alive) break;
           if (lane == 0) {
             if ((warp & 3) == 0 && (split || pair || w == 1)) mbar_arrive(&sh.tile_done[(tile + copy(j)) % (2 * NS)]);
           }
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float2 s0 = split_pair(add2(sums[0], sums[1]));
           l += s0.x + s0.y;
         }
-        bounded_wait(&sh.o_full[w], o_phase, &sh.limit);
+        if (alive) alive = warp_wait(&sh.o_full[w], o_phase, &sh.limit);
         o_phase ^= 1;
         tc_fence_after();
       }
@@ -426,25 +434,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int c = 0; c < D / 2; c += kCols) {
           uint32_t x[kCols];
           __syncwarp();
-          tmem_ld(x, o_tmem + (1 - w) * (D / 2) + c);
+          if (alive) {
+            tmem_ld(x, o_tmem + (1 - w) * (D / 2) + c);
 #pragma unroll
-          for (int e = 0; e < kCols; e += 4)  // a half without a key tile has no sums
-            *reinterpret_cast<uint4*>(x_smem + w * kRoom + e * 128 + r * 4) =
-                cnt > w ? make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]) : make_uint4(0, 0, 0, 0);
-          SoftmaxSync::sync();
-          tmem_ld(x, o_tmem + w * (D / 2) + c);
-#pragma unroll
-          for (int e = 0; e < kCols; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(x_smem + (1 - w) * kRoom + e * 128 + r * 4);
-            const float ov[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              x[e + i] = __float_as_uint((cnt > w ? __uint_as_float(x[e + i]) * mine : 0.f) + ov[i] * others);
+            for (int e = 0; e < kCols; e += 4)  // a half without a key tile has no sums
+              *reinterpret_cast<uint4*>(x_smem + w * kRoom + e * 128 + r * 4) =
+                  cnt > w ? make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]) : make_uint4(0, 0, 0, 0);
           }
-          put(x, w * (D / 2) + c);
+          SoftmaxSync::sync();
+          if (alive) {
+            tmem_ld(x, o_tmem + w * (D / 2) + c);
+#pragma unroll
+            for (int e = 0; e < kCols; e += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(x_smem + (1 - w) * kRoom + e * 128 + r * 4);
+              const float ov[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[e + i] = __float_as_uint((cnt > w ? __uint_as_float(x[e + i]) * mine : 0.f) + ov[i] * others);
+            }
+            put(x, w * (D / 2) + c);
+          }
           SoftmaxSync::sync();
         }
-      } else {
+      } else if (alive) {
 #pragma unroll 1
         for (int c = 0; c < D; c += kCols) {
           uint32_t x[kCols];
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       if (split) fence_async_proxy();  // the room may next be written by a box copy
       // (the next unit is published without this one's end)
-      go = SoftmaxSync::all(!last && bounded_wait(&sh.unit_full[(seg + 1) & 1], ((seg + 1) >> 1) & 1, &sh.limit) &&
+      go = SoftmaxSync::all(alive && !last && bounded_wait(&sh.unit_full[(seg + 1) & 1], ((seg + 1) >> 1) & 1, &sh.limit) &&
                             !sh.limit.dead);
       if (go && tid == 0) mbar_arrive(&sh.unit_done[seg & 1]);
     }
@@ -480,9 +492,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int lw = kTma ? 0 : warp - 8;  // of the warps that copy rows
     bool met = false;                    // the last unit's halves met in the second row tile's room
     // 32 rows to rows r0.. of a tile; lane i has the place of row i, bit i of `live` tells
-    // whether it is read or zero
+    // whether it is read or zero.  (Unrolled as far as registers go: 64 sequences of 12 tokens over 200 to
+    // 4000 keys, 48 rows each, in pages of 24 slots take 206 us, and 275 all at once.)
     auto copy_rows = [&](const T* src, int64_t off, unsigned live, uint32_t dst, int r0) {
-#pragma unroll kTree ? 2 : KC
+#pragma unroll kTree ? 2 : kTma ? KC : KC / 2
       for (int x = 0; x < KC; ++x) {
         const int i = x * 32 + lane, row = i / KC, ch = i % KC, r = r0 + row;
         const int64_t o = __shfl_sync(~0u, off, row) + ch * 8;
@@ -505,25 +518,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       // the unit's place is free when the softmax warps are done with the one before the last
-      const bool free = seg < 2 || bounded_wait(&sh.unit_done[seg & 1], ((seg - 2) >> 1) & 1, &sh.limit);
-      if (lw == 0 && lane == 0 && free && !sh.limit.dead) {
+      if (seg >= 2 && !warp_wait(&sh.unit_done[seg & 1], ((seg - 2) >> 1) & 1, &sh.limit)) return false;
+      if (lw == 0 && lane == 0) {
         sh.unit[seg & 1] = u;
         sh.unit_begin[seg & 1] = unit_begin;
         mbar_arrive(&sh.unit_full[seg & 1]);
       }
-      bounded_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.limit);
-      if (__any_sync(~0u, sh.limit.dead)) return false;
+      if (!warp_wait(&sh.q_empty, (seg & 1) ^ 1, &sh.limit)) return false;
       const int tiles_of_rows = split ? 1 : 2;
-      auto second_tile = [&]() {
-        if (met) bounded_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.limit);
-        __syncwarp();
+      auto second_tile = [&]() {  // is free
+        return !met || warp_wait(&sh.unit_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, &sh.limit);
       };
       if (box) {
         // (rows past the sequence's are other sequences' or zero, and are not stored)
         if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, tiles_of_rows * kTile);
         for (int w = 0; w < tiles_of_rows; ++w) {
-          if (w == 1) second_tile();
-          if (lane < D / 64 && !sh.limit.dead)
+          if (w == 1 && !second_tile()) return false;
+          if (lane < D / 64)
             tma_load3(q_smem + w * kTile + lane * kHalf, &q_map, lane * 64, (u.h + (pair ? w : 0)) * P.g,
                       u.q0 + token_of(P, u.row0 + (pair ? 0 : w * 128)), &sh.q_full);
         }
@@ -532,7 +543,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int i = 0; i < kBlocks; ++i) {
           const int first = (i * kRowWarps + lw) * 32;
           if (first >= 128 && tiles_of_rows == 1) break;
-          if (i == kBlocks / 2) second_tile();
+          if (i == kBlocks / 2 && !second_tile()) return false;
           if ((pair ? first & 127 : first) < u.rows) copy_rows((const T*)a.q, off[i], live[i], q_smem + (first >> 7) * kTile, first & 127);
         }
         cp_async_arrive(smem_addr(&sh.q_full));
@@ -546,11 +557,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // across units, where either may have been the case).  Of twice as many completions as there are key
     // slots the one waited for is still the last on its barrier.
     auto tile_done = [&](int64_t gate) {
-      if (gate >= 0) bounded_wait(&sh.tile_done[gate % (2 * NS)], (gate / (2 * NS)) & 1, &sh.limit);
-      __syncwarp();
+      return gate < 0 || warp_wait(&sh.tile_done[gate % (2 * NS)], (gate / (2 * NS)) & 1, &sh.limit);
     };
-    auto key_slot = [&](uint32_t it) { tile_done((int64_t)it - NS); };
-    auto value_slot = [&](uint32_t it, int j) { tile_done((int64_t)it - NV + (u.rows <= 128 || j < NV ? 2 : 1)); };
+    auto slot_free = [&](bool values, uint32_t it, int j) {
+      return tile_done((int64_t)it - (values ? NV - (u.rows <= 128 || j < NV ? 2 : 1) : NS));
+    };
     // a tile with values outside the unit's keys (kTree: or with values that perhaps no row sees)
     auto edge = [&](int tile) {
       return tile * kChunkKeys < u.key_lo || tile * kChunkKeys + kChunkKeys > (kTree ? u.len - u.n : u.key_hi);
@@ -562,6 +573,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const CUtensorMap* map = keys ? &k_map : &v_map;
       const int box = min(a.page_size, kChunkKeys), boxes = kChunkKeys / box;
       uint32_t it = 0;
+      bool alive = true;
       while (true) {
         const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, ours, u, unit_begin, t);
         const int32_t* table = a.page_table + (int64_t)u.b * a.table_stride;
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         };
         const int copies = Map::is_pair(P, u) ? 2 : 1;  // of a tile: of one head after the other
         int page = page_of(0);
-        for (int j = 0; j < cnt; ++j) {
+        for (int j = 0; alive && j < cnt; ++j) {
           const int tile = u.tile0 + j0 + j;
           const int key = tile * kChunkKeys + lane * box;
           const int slot = a.page_size > kChunkKeys ? key % a.page_size : 0;
@@ -584,8 +596,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int head = 0; head < copies; ++head, ++it) {
             unsigned long long* full;
             uint32_t dst;
+            alive = slot_free(!keys, it, j);
+            if (!alive) break;
             if (keys) {
-              key_slot(it);
               if (lane < 4) {
                 uint32_t word = ~0u;
                 if (bad)
@@ -596,28 +609,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               full = &sh.k_full[it % NS];
               dst = k_smem + it % NS * kTile;
             } else {
-              value_slot(it, j);
               full = edge(tile) ? &sh.v_landed[it % NV] : &sh.v_full[it % NV];
               dst = v_smem + it % NV * kTile;
             }
-            const bool dead = sh.limit.dead;
             __syncwarp();
-            if (lane == 0 && !dead) mbar_arrive_expect_tx(full, kTile);
+            if (lane == 0) mbar_arrive_expect_tx(full, kTile);
             __syncwarp();
-            if (lane < boxes && !dead)
+            if (lane < boxes)
               for (int x = 0; x < D / 64; ++x)
                 tma_load4(dst + x * kHalf + lane * box * 128, map, x * 64, slot, u.h + head, from, full);
           }
         }
-        if (!advance<Map>(P, ours, &u, &unit_begin, &t) || __any_sync(~0u, sh.limit.dead)) break;
+        if (!alive || !advance<Map>(P, ours, &u, &unit_begin, &t)) break;
       }
     } else if (kTma) {
       uint32_t it = 0, seg = 0, edges[NV] = {};  // phases of v_landed
+      bool alive = true;
       while (true) {
         const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, ours, u, unit_begin, t);
         if (!copy_queries(seg)) break;
         const int copies = Map::is_pair(P, u) ? 2 : 1;
-        for (int j = 0; j < cnt; ++j) {
+        for (int j = 0; alive && j < cnt; ++j) {
           const int tile = u.tile0 + j0 + j;
           if (!edge(tile)) continue;
           const int lo = u.key_lo - tile * kChunkKeys, hi = u.key_hi - tile * kChunkKeys;
@@ -630,9 +642,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
               if (i == st) parity = edges[i]++ & 1;
-            bounded_wait(&sh.v_landed[st], parity, &sh.limit);
-            const bool dead = sh.limit.dead;
-            __syncwarp();
+            alive = warp_wait(&sh.v_landed[st], parity, &sh.limit);
+            if (!alive) break;
             // a row's pieces may lie anywhere in it: all are cleared
             if constexpr (!kTree) {
               for (int i = lane; i < 128 * KC; i += 32) {
@@ -657,16 +668,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             fence_async_proxy();
             __syncwarp();
-            if (lane == 0 && !dead) mbar_arrive(&sh.v_full[st]);
+            if (lane == 0) mbar_arrive(&sh.v_full[st]);
           }
         }
         it += cnt * copies;
         ++seg;
-        if (!advance<Map>(P, ours, &u, &unit_begin, &t)) break;
+        if (!alive || !advance<Map>(P, ours, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (warp < 10) {
       uint32_t it = 0, seg = 0;
+      bool alive = true;
       while (true) {
         const int j0 = tile_in_unit<Map>(P, t, u, unit_begin), cnt = tiles_here<Map>(P, ours, u, unit_begin, t);
         if (!copy_queries(seg)) break;
@@ -684,7 +696,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           return id < a.num_pages ? id : -1;
         };
         int page[2] = {page_of(0, 0), page_of(0, 1)};
-        for (int j = 0; j < cnt; ++j) {
+        for (int j = 0; alive && j < cnt; ++j) {
           int64_t off[2];
           unsigned live[2], shown[2];
 #pragma unroll
@@ -699,15 +711,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             page[half] = page_of(j + 1, half);
           }
 #pragma unroll 1
-          for (int head = 0; head < copies; ++head, ++it) {
+          for (int head = 0; alive && head < copies; ++head, ++it) {
             const T* const kc = (const T*)a.k_cache + (int64_t)(u.h + head) * a.head_stride;
             const T* const vc = (const T*)a.v_cache + (int64_t)(u.h + head) * a.head_stride;
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
-              if (kv)
-                value_slot(it, j);
-              else
-                key_slot(it);
+              alive = slot_free(kv, it, j);
+              if (!alive) break;
               unsigned long long* landed = kv ? &sh.v_landed[it % NV] : &sh.k_landed[it % NS];
               if (kv == 0 && lane == 0) {
                 sh.key_ok[it % (2 * NS)][lw * 2] = shown[0];
@@ -723,7 +733,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         ++seg;
-        if (!advance<Map>(P, ours, &u, &unit_begin, &t)) break;
+        if (!alive || !advance<Map>(P, ours, &u, &unit_begin, &t)) break;
       }
       cp_async_wait_all();
     } else if (lane == 0) {
@@ -756,9 +766,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t base = uni(tmem), q_desc = uni(smem_desc_lo(q_smem, 16)), k_desc = uni(smem_desc_lo(k_smem, 16)),
                      v_desc = uni(smem_desc_lo(v_smem, kHalf));
       uint32_t it = 0, seg = 0, p_phase = 0;  // bit w of p_phase: half w
-      bool alive = true;
+      bool alive = true;  // false for good once a wait has run out
       auto wait = [&](unsigned long long* bar, uint32_t parity) {
-        alive = __all_sync(~0u, bounded_wait(bar, parity, &sh.limit)) && alive;
+        alive = warp_wait(bar, parity, &sh.limit) && alive;
+      };
+      auto commit = [&](unsigned long long* bar) {
+        if (alive) mma_commit(bar);
       };
       auto keys_ready = [&](uint32_t tile) { wait(&sh.k_full[tile % NS], (tile / NS) & 1); };
       auto values_ready = [&](uint32_t tile) { wait(&sh.v_full[tile % NV], (tile / NV) & 1); };
@@ -771,8 +784,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
             mma_ss(base + w * 128, q0 + off, k0 + off, kQk, ks > 0);
           }
+          mma_commit(&sh.s_full[w]);
         }
-        mma_commit(&sh.s_full[w]);
       };
       // O of half w (+)= P V, in two parts as P comes
       auto pv = [&](uint32_t w, uint32_t tile, bool add) {
@@ -804,8 +817,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!turns) {
           qk(0, 0, it);
           qk(1, 1, it);
-          if (cnt == 1) mma_commit(&sh.q_empty);
-          for (int j = 0; j + 1 < cnt; ++j, ++it) {
+          if (cnt == 1) commit(&sh.q_empty);
+          for (int j = 0; alive && j + 1 < cnt; ++j, ++it) {
             if (kTma) values_ready(it);
             keys_ready(it + 1);  // without TMA handed over after the values of tile it
             pv(0, it, j > 0);
@@ -813,12 +826,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             pv(1, it, j > 0);
             qk(1, 1, it + 1);
           }
-          if (cnt > 1) mma_commit(&sh.q_empty);
+          if (cnt > 1) commit(&sh.q_empty);
           values_ready(it);
           pv(0, it, cnt > 1);
-          mma_commit(&sh.o_full[0]);
+          commit(&sh.o_full[0]);
           pv(1, it, cnt > 1);
-          mma_commit(&sh.o_full[1]);
+          commit(&sh.o_full[1]);
           ++it;
         } else {
           const int n = pair ? 2 * cnt : cnt;
@@ -827,22 +840,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             keys_ready(it + 1);
             qk(1, pair, it + 1);
           }
-          if (n <= 2) mma_commit(&sh.q_empty);
-          for (int j = 0; j < n; ++j, ++it) {
+          if (n <= 2) commit(&sh.q_empty);
+          for (int j = 0; alive && j < n; ++j, ++it) {
             const uint32_t w = j & 1;
             values_ready(it);
             pv(w, it, j > 1);
             if (j + 2 < n) {
               keys_ready(it + 2);
               qk(w, pair ? w : 0, it + 2);
-              if (j + 3 == n) mma_commit(&sh.q_empty);
+              if (j + 3 == n) commit(&sh.q_empty);
             } else {
-              mma_commit(&sh.o_full[w]);
+              commit(&sh.o_full[w]);
             }
           }
         }
         ++seg;
-        if (!uni(advance<Map>(P, ours, &u, &unit_begin, &t))) break;
+        if (!alive || !uni(advance<Map>(P, ours, &u, &unit_begin, &t))) break;
       }
       // products still running when a wait gave up end before their memory is freed
       if (!alive) {

@@ -57,16 +57,20 @@ struct WaitLimit {
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 
 // Bounded wait for a phase: false if it ran out.  (A later wait of the same thread for the next
-// phase of that barrier would seem to succeed at once.)
+// phase of that barrier would seem to succeed at once, so there must be none.)
 __device__ __forceinline__ bool bounded_wait(unsigned long long* bar, uint32_t parity, WaitLimit* limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long start = clock64();
   for (uint32_t i = 1; i < kSpinLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0 && (limit->dead || clock64() - start > limit->cycles)) break;
+    if (limit->dead || clock64() - start > limit->cycles) break;
   }
   limit->dead = 1;
   return false;
+}
+// The same by a whole warp, whose lanes go on together and agree.
+__device__ __forceinline__ bool warp_wait(unsigned long long* bar, uint32_t parity, WaitLimit* limit) {
+  return __all_sync(~0u, bounded_wait(bar, parity, limit));
 }
 
 }  // namespace clsample
