@@ -100,24 +100,25 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(const __grid_constant__ 
 }
 
 // Sum over the block and each thread's exclusive prefix.
-__device__ __forceinline__ int block_prefix(int v, int* buf, int* total) {
+template <class T>
+__device__ __forceinline__ T block_prefix(T v, T* buf, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int run = v;
+  T run = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(~0u, run, o);
+    const T up = __shfl_up_sync(~0u, run, o);
     if (lane >= o) run += up;
   }
   __syncthreads();
   if (lane == 31) buf[warp] = run;
   __syncthreads();
-  int w = buf[lane];  // 32 warps
+  T w = buf[lane];  // 32 warps
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(~0u, w, o);
+    const T up = __shfl_up_sync(~0u, w, o);
     if (lane >= o) w += up;
   }
-  const int base = __shfl_sync(~0u, w, warp) - buf[warp];
+  const T base = __shfl_sync(~0u, w, warp) - buf[warp];
   *total = __shfl_sync(~0u, w, 31);
   return base + run - v;
 }
@@ -141,7 +142,8 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
   const clsample_page_batch_t& q = P.batch;
   constexpr int kAlone = 8;  // pages that a thread hands out by itself
   struct Long { int b, from, count, at; };
-  __shared__ int buf[32], near[kReserveThreads];  // near: the first pages of the list
+  __shared__ int64_t buf[32];
+  __shared__ int near[kReserveThreads];  // near: the first pages of the list
   __shared__ Long longs[kReserveThreads];
   __shared__ int long_count;
   const int tid = threadIdx.x, page = pool.page_size, cap = capacity_of(q.max_pages, page);
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
   const int words = (pool.num_pages + 31) / 32, each = (words + kReserveThreads - 1) / kReserveThreads;
   const int w0 = min(words, tid * each), w1 = min(words, w0 + each);
   uint32_t first_word = 0;
-  int mine = 0, available;
+  int64_t mine = 0, available;
 #pragma unroll 4
   for (int i = w0; i < w1; ++i) {
     const uint32_t bits = pool.free_bits[i];
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
     mine_w = w;
     mine_bad = bad;
   }
-  int rank = block_prefix(mine, buf, &available);
+  int64_t rank = block_prefix(mine, buf, &available);
   shares = __syncthreads_or(shares);
   if (shares) {
     for (int b = tid; b < q.B; b += kReserveThreads) {
@@ -218,14 +220,16 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
   int mine_at = 0, mine_need = 0;
   for (int base = 0; base < q.B; base += kReserveThreads) {  // uniform
     const int b = base + tid;
-    int need = 0, sum;
+    int need = 0;
+    int64_t sum;
     if (b < q.B && !is_bad(b)) {
       const Writes w = writes_of(b);
       if (shares)
         for (int k = w.first; k <= own_last(w); ++k) need += !keeps(b, page_at(b, w, k));
       need += max(0, w.last + 1 - max(w.held, w.first));
     }
-    const int before = block_prefix(need, buf, &sum);
+    // (in 64 bits: sequences may lack 2^30 pages each)
+    const int64_t before = block_prefix((int64_t)need, buf, &sum);
     mine_at = (int)min(total + before, (int64_t)0x7fffffff);
     mine_need = need;
     if (b < q.B && !one) {
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
   }
   if (tid == 0) {
     *pool.epoch = (uint32_t)(call >> 32);
-    if (free_pages) *free_pages = available - (enough ? (int)total : 0);
+    if (free_pages) *free_pages = (int)(available - (enough ? total : 0));
   }
 }
 
