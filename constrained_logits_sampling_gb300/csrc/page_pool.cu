@@ -148,7 +148,13 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
   __shared__ int long_count;
   const int tid = threadIdx.x, page = pool.page_size, cap = capacity_of(q.max_pages, page);
   const bool one = q.B <= kReserveThreads;
-  const uint64_t call = (uint64_t)(*pool.epoch + 1) << 32;
+  // the call's number; where 32 bits end, stamps start anew, as those of earlier calls would be larger
+  const uint32_t number = *pool.epoch + 1;
+  const uint64_t call = (uint64_t)max(number, 1u) << 32;
+  if (number == 0) {
+    for (int i = tid; i < pool.num_pages; i += kReserveThreads) pool.stamps[i] = 0;
+    __syncthreads();
+  }
   // free pages: each thread counts a run of the words
   const int words = (pool.num_pages + 31) / 32, each = (words + kReserveThreads - 1) / kReserveThreads;
   const int w0 = min(words, tid * each), w1 = min(words, w0 + each);

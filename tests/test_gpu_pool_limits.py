@@ -41,3 +41,31 @@ def test_sequences_that_lack_more_pages_than_32_bits_count(G, B, width, taken):
     got = pool.reserve(table, held, lens, new)
     assert not got["status"].any() and got["free"].tolist() == [0] and held[B - 1] == pages - taken
     assert table[B - 1, :pages - taken].tolist() == list(range(taken, pages))
+
+
+def test_the_call_number_wraps(G):
+    """Around the 2^32nd reservation of a pool, where its call number starts anew: of sequences that write to a
+    page that they share the last one keeps it, and no page is lost."""
+    for start in (-3, -2, -1, 0):
+        pool = G.PagePool(12, 4)
+        table = torch.full((3, 4), -1, dtype=I32, device="cuda")
+        held, lens = (torch.zeros(3, dtype=I32, device="cuda") for _ in range(2))
+        i32 = lambda x: torch.tensor(x, dtype=I32, device="cuda")
+        # stamps of the calls before, as large as they get
+        pool._stamps.fill_(start * (1 << 32) + 3 if start else 0)
+        pool._epoch.fill_(start)
+        assert not pool.reserve(table, held, lens, i32([6, 0, 0]))["status"].any()
+        lens[0] = 6
+        for _ in range(3):
+            assert not pool.fork(table, held, lens, i32([0, 0]), i32([1, 2])).any()
+            shared = int(table[0, 1])
+            assert pool.refs[shared] == 3
+            got = pool.reserve(table, held, lens, i32([1, 1, 1]))
+            assert not got["status"].any()
+            assert int(table[2, 1]) == shared and len({int(table[b, 1]) for b in range(3)}) == 3
+            assert got["copies"][:2, 0].tolist() == [shared] * 2 and got["copies"][2].tolist() == [-1, -1, 0]
+            assert [int(pool.refs[table[b, 1]]) for b in range(3)] == [1, 1, 1]
+            assert got["free"].tolist() == [8] and int((pool.refs == 0).sum()) == 8
+            lens[1:] = 0
+            assert not pool.trim(table, held, lens).any()
+            assert int((pool.refs == 0).sum()) == 10
