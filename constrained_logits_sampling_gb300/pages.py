@@ -166,7 +166,9 @@ class _PoolCall:
 
 class PagePool:
     """``num_pages`` pages of ``page_size`` slots on the current device, all of them free.  ``refs`` int32
-    [num_pages] tells how many sequences hold a page.  Calls on one pool have to be ordered."""
+    [num_pages] tells how many sequences hold a page.  Calls on one pool, ``load`` among them, have to be ordered;
+    a new pool is ready for any stream (making one waits for the current stream, except while a graph is captured:
+    such a pool starts anew with each replay, on the capture's streams)."""
 
     def __init__(self, num_pages: int, page_size: int):
         self._L = load_library()
@@ -185,6 +187,8 @@ class PagePool:
         p.refs, p.free_bits, p.stamps = self.refs.data_ptr(), self.free_bits.data_ptr(), self._stamps.data_ptr()
         p.epoch, p.list = self._epoch.data_ptr(), self._list.data_ptr()
         self._set_free()
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()
 
     def _set_free(self):
         free = torch.zeros(32 * self.free_bits.numel(), dtype=torch.int64, device=self.device)
@@ -192,12 +196,14 @@ class PagePool:
         bits = (free.view(-1, 32) << torch.arange(32, device=self.device)).sum(1)
         self.free_bits.copy_(torch.where(bits >= 1 << 31, bits - (1 << 32), bits))
 
-    def load(self, refs: torch.Tensor):
-        """Start from other counts of holders (int32 [num_pages]), those of tables made elsewhere."""
+    def load(self, refs: torch.Tensor, stream: Optional[torch.cuda.Stream] = None):
+        """Start from other counts of holders (int32 [num_pages]), those of tables made elsewhere.  Enqueued on
+        ``stream`` (default: current)."""
         if refs.dtype != torch.int32 or tuple(refs.shape) != (self.num_pages,):
             raise ValueError(f"refs must be int32 [{self.num_pages}]")
-        self.refs.copy_(refs)
-        self._set_free()
+        with _on_stream(stream):
+            self.refs.copy_(refs)
+            self._set_free()
 
     def _batch(self, page_table, held, kv_lens):
         b, dev = BatchArgs(), self.device

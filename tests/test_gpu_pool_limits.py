@@ -69,3 +69,48 @@ def test_the_call_number_wraps(G):
             lens[1:] = 0
             assert not pool.trim(table, held, lens).any()
             assert int((pool.refs == 0).sum()) == 10
+
+
+def busy(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+
+
+def test_a_new_pool_is_ready_for_any_stream(G):
+    """Made while the current stream is busy, in memory that held other things, and used on another stream at
+    once."""
+    n = 1000
+    table = torch.full((1, n), -1, dtype=I32, device="cuda")
+    held, lens = (torch.zeros(1, dtype=I32, device="cuda") for _ in range(2))
+    new = torch.full((1,), n, dtype=I32, device="cuda")
+    side = torch.cuda.Stream()
+    for _ in range(3):  # what the pool's arrays are made of
+        old = [torch.full((m,), -1, dtype=t, device="cuda") for m, t in ((n, I32), ((n + 31) // 32, I32), (n, torch.int64),
+                                                                         (1, I32), (n, I32), (1024, torch.int64))]
+    torch.cuda.synchronize()
+    del old
+    busy(torch.cuda.current_stream())
+    pool = G.PagePool(n, 1)
+    got = pool.reserve(table, held, lens, new, stream=side)
+    torch.cuda.synchronize()
+    assert got["status"].tolist() == [0] and got["free"].tolist() == [0]
+    assert table[0].tolist() == list(range(n)) and (pool.refs == 1).all()
+
+
+def test_loaded_counts_on_a_stream(G):
+    """load on a stream of its own comes before later calls there, whatever the current stream does."""
+    n = 200
+    table = torch.full((1, n), -1, dtype=I32, device="cuda")
+    held, lens = (torch.zeros(1, dtype=I32, device="cuda") for _ in range(2))
+    new = torch.full((1,), n // 2, dtype=I32, device="cuda")
+    refs = (torch.arange(n, device="cuda") % 2).to(I32)
+    side, pool = torch.cuda.Stream(), G.PagePool(n, 1)
+    torch.cuda.synchronize()
+    busy(torch.cuda.current_stream())
+    pool.load(refs, stream=side)
+    got = pool.reserve(table, held, lens, new, stream=side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()  # still asleep
+    with torch.cuda.stream(side):
+        assert got["status"].tolist() == [0] and got["free"].tolist() == [0]
+        assert table[0, :n // 2].tolist() == list(range(0, n, 2))
