@@ -108,16 +108,18 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
     T* at = reinterpret_cast<T*>(plane < a.layers ? a.k_cache : a.v_cache) + layer * c.layer;
     const T* src = at + from * c.page;
     T* dst = at + to * c.page;
-    // this thread's place (a slot, and a piece of it), which moves by the same step each time
+    // this thread's place (a slot, and a piece of it), which moves by the same step each time.  (Slots are
+    // below 2^31, and a thread's last places, past them, need the 32nd bit.)
     const int first = part * kThreads + threadIdx.x;
-    int slot = first / heads, piece = first % heads;
-    while (slot < slots) {
+    unsigned slot = first / heads;
+    int piece = first % heads;
+    while (slot < (unsigned)slots) {
       T x[kAhead];
       int64_t off[kAhead];
       bool live[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        live[k] = slot < slots;
+        live[k] = slot < (unsigned)slots;
         off[k] = slot * c.slot + (flat ? piece : piece / c.per_head * c.head + piece % c.per_head);
         if (live[k]) x[k] = src[off[k]];
         slot += step_slots;

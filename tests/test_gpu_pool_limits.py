@@ -114,3 +114,19 @@ def test_loaded_counts_on_a_stream(G):
     with torch.cuda.stream(side):
         assert got["status"].tolist() == [0] and got["free"].tolist() == [0]
         assert table[0, :n // 2].tolist() == list(range(0, n, 2))
+
+
+@pytest.mark.parametrize("slots", [(1 << 31) - 1, (1 << 31) - 20000])
+def test_copy_of_a_page_of_the_most_slots(G, slots):
+    """A page of 2^31 - 1 slots of one element: places past its end are none, though they pass 2^31."""
+    page = (1 << 31) - 1
+    room = torch.empty(2 * page + 4096, dtype=torch.bfloat16, device="cuda")
+    room[2 * page:] = 3.0
+    cache = room[:2 * page].view(2, page, 1, 1)
+    cache[0].view(torch.int16).random_(-30000, 30000)
+    cache[1] = 5.0
+    status = G.CopyPages()(cache, cache, torch.tensor([[0, 1, slots]], dtype=I32, device="cuda"))
+    assert status.tolist() == [0]
+    a, b = (c.view(torch.int16).view(-1) for c in cache)
+    assert torch.equal(a[:slots], b[:slots])
+    assert (cache[1].view(-1)[slots:] == 5).all() and (room[2 * page:] == 3).all()
