@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (!work) {
-    if (tid == 0) P.cut[blockIdx.x].rows = 0;
+    if (tid == 0) P.cut[blockIdx.x] = CutUnit{};
     if (warp == 10) tmem_free512(sh.tmem);
     return;
   }
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             !sh.limit.dead);
       if (go && tid == 0) mbar_arrive(&sh.unit_done[seg & 1]);
     }
-    if (tid == 0 && !noted) P.cut[blockIdx.x].rows = 0;  // what an earlier call left there is not joined
+    if (tid == 0 && !noted) P.cut[blockIdx.x] = CutUnit{};  // what an earlier call left there is not joined
   } else if (warp != 10) {
     // ------------------------------------------------------------------ loads
     const int lw = kTma ? 0 : warp - 8;  // of the warps that copy rows

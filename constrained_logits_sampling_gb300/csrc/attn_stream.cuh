@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kStreamThreads, StreamRing<D, RB, kTree>::kCta
   Unit u;
   int64_t unit_begin;
   if (!find_span<Map, kStreamThreads>(P, &span, &u, &unit_begin)) {
-    if (tid == 0) P.cut[blockIdx.x].rows = 0;
+    if (tid == 0) P.cut[blockIdx.x] = CutUnit{};
     wait_for_earlier_grids();  // this grid's end stands for theirs
     return;
   }

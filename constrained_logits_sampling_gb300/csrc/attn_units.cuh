@@ -51,7 +51,7 @@ __device__ __forceinline__ int head_of(const AttnParams& P, int row) { return ro
 constexpr int kChunkPad = 18, kStreamPad = 3;
 
 struct CutUnit {
-  int rows;          // 0: none
+  int rows;          // 0: none, and all else is 0 too: the join counts work by `pair` as well
   int row0, q0, h;   // as in Unit
   int c0, c1;        // the CTAs that have its parts: c0 in its second slot, the others in the first
   int pair;          // of two key heads
@@ -340,7 +340,7 @@ __device__ __forceinline__ int cta_of_tile(const Span& sp, int64_t t) {
 // it is another's.
 template <class M>
 __device__ __forceinline__ void note_cut(const AttnParams& P, const Span& span, const Unit& u, int64_t unit_begin) {
-  CutUnit c{0, 0, 0, 0, 0, 0, 0};
+  CutUnit c{};
   const int64_t last = unit_begin + (int64_t)(u.tiles - 1) * M::weight(P, u);  // where the last tile is
   if (unit_begin >= span.t0 && last >= span.t1)
     c = CutUnit{u.rows, u.row0, u.q0, u.h, (int)blockIdx.x, cta_of_tile(span, last), M::is_pair(P, u)};
