@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_join_kernel(const __grid
   __shared__ float part_m[8][32], part_l[8][32];
   __shared__ float part_o[8][32][17];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the first status of each CTA rests on the call's inputs alone, and is found while the grids before end
+  // The first status of each CTA rests on the call's inputs alone, and is found while the grids before end.  (Sound
+  // as long as the call's first launch has waited for all work before it, which an ordinary launch has.)
   bool bad = false;
   if (P.a.row_status && (int)blockIdx.x < P.a.B) bad = attention_bad<kJoinThreads, kTree>(P, blockIdx.x);
   wait_for_earlier_grids();

@@ -380,8 +380,11 @@ cudaError_t launch_tree(const clsample_verify_tree_args_t& a, cudaStream_t st) {
   return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, verify_tree_kernel<P, C>, a) : e;
 }
 
-// As for clsample_verify: the largest cluster with which all requests are resident at once.  One
-// request of 6 refusals over 151936 tokens: 29 us on 16 CTAs, 40 on 8.  (On an earlier version 64 requests
+// As for clsample_verify: the largest cluster with which all requests would be resident at once with four CTAs
+// a multiprocessor, which is what registers allow.  (Shared memory does not in all cases: with arrays for 1023
+// tokens and bits for refused ids, float32 and clusters of two, a CTA has 60 KB over 151936 tokens and 81 over
+// 262144, so three or two fit, and of 229 requests and more some begin when others have ended; with clusters of four
+// over 262144 three fit.)  One request of 6 refusals over 151936 tokens: 29 us on 16 CTAs, 40 on 8.  (On an earlier version 64 requests
 // on 16 CTAs each, not all resident: 47 us instead of 51 where one of them has far more refusals than the
 // others, but 110 instead of 82 where all have 6; now 48 and 77 on 8.  Three CTAs a multiprocessor of 80
 // registers, not all resident either: 41 and 98.)
