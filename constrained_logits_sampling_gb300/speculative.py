@@ -11,7 +11,8 @@ the drafted ones, or a chunk of a prompt) through
 
 As in ``sampler``, this is argument marshalling only: every step runs in libclsample.so, on
 CUDA tensors, without a CPU fallback.  ``make_args`` checks a call once and keeps its
-tensors alive; ``apply`` enqueues it, as often as wanted (the buffers' contents may change
+tensors alive, and the object whose scratch it takes (a captured graph needs them for as long as it is
+replayed); ``apply`` enqueues it, as often as wanted (the buffers' contents may change
 in between).  Calling an object does both and allocates the outputs.  An object belongs to the
 device that was current when it was made, and refuses calls while another one is.  The
 formulas and limits are stated in include/clsample.h.
@@ -268,7 +269,7 @@ class ChunkAttention:
         a.scale = 1.0 / math.sqrt(max(a.D, 1)) if scale is None else float(scale)
         a.lse = _dptr(lse, torch.float32, a.T * a.Hq, "lse", dev)
         a.row_status = _dptr(row_status, torch.int32, a.B, "row_status", dev)
-        a.keep = (q, k_cache, v_cache, page_table, cu_new, kv_lens, out, lse, row_status)
+        a.keep = (q, k_cache, v_cache, page_table, cu_new, kv_lens, out, lse, row_status, self)  # self: the scratch
         return a
 
     def apply(self, args: AttentionArgs, stream: Optional[torch.cuda.Stream] = None):

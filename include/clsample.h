@@ -546,9 +546,10 @@ typedef struct {
  * those in its mask.  A row that sees nothing gets out 0 and lse -inf.  kv_lens[b] < n_b, or a
  * position outside [kv_lens[b] - n_b, kv_lens[b]), makes the sequence INVALID.
  * Slots of new tokens that no row sees may hold anything, as may those below kv_lens[b] - n_b -
- * window + 1 with a window; the page ids of all others, and of the new tokens, have to be valid.  (A value that is not finite in a
- * slot that some row sees may reach other rows of the sequence.)  max_new, max_pages and window bound a call's
- * work, and kernels are chosen by them: tight ones are faster, results differ by roundings alone. */
+ * window + 1 with a window; the page ids of all others, and of the new tokens, have to be valid.  (A
+ * value that is not finite in a slot that some row sees may reach other rows of the sequence.)  max_new,
+ * max_pages and window bound a call's work, and kernels are chosen by them: tight ones are faster, results
+ * differ by roundings alone. */
 int clsample_tree_attention(clsample_attention_t* handle, const clsample_attention_args_t* args,
                             const clsample_tree_mask_t* tree, clsample_stream_t stream);
 
