@@ -142,24 +142,19 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
   const clsample_page_batch_t& q = P.batch;
   constexpr int kAlone = 8;  // pages that a thread hands out by itself
   struct Long { int b, from, count, at; };
-  __shared__ int64_t buf[32];
-  __shared__ int near[kReserveThreads];  // near: the first pages of the list
+  __shared__ int64_t wide_buf[32];
+  __shared__ int buf[32], near[kReserveThreads];  // near: the first pages of the list
   __shared__ Long longs[kReserveThreads];
   __shared__ int long_count;
   const int tid = threadIdx.x, page = pool.page_size, cap = capacity_of(q.max_pages, page);
   const bool one = q.B <= kReserveThreads;
-  // the call's number; where 32 bits end, stamps start anew, as those of earlier calls would be larger
-  const uint32_t number = *pool.epoch + 1;
+  const uint32_t number = *pool.epoch + 1;  // the call's
   const uint64_t call = (uint64_t)max(number, 1u) << 32;
-  if (number == 0) {
-    for (int i = tid; i < pool.num_pages; i += kReserveThreads) pool.stamps[i] = 0;
-    __syncthreads();
-  }
   // free pages: each thread counts a run of the words
   const int words = (pool.num_pages + 31) / 32, each = (words + kReserveThreads - 1) / kReserveThreads;
   const int w0 = min(words, tid * each), w1 = min(words, w0 + each);
   uint32_t first_word = 0;
-  int64_t mine = 0, available;
+  int mine = 0, available;
 #pragma unroll 4
   for (int i = w0; i < w1; ++i) {
     const uint32_t bits = pool.free_bits[i];
@@ -206,8 +201,12 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
     mine_w = w;
     mine_bad = bad;
   }
-  int64_t rank = block_prefix(mine, buf, &available);
+  int rank = block_prefix(mine, buf, &available);
   shares = __syncthreads_or(shares);
+  if (number == 0) {  // where 32 bits end stamps start anew, as those of earlier calls would be larger
+    for (int i = tid; i < pool.num_pages; i += kReserveThreads) pool.stamps[i] = 0;
+    __syncthreads();
+  }
   if (shares) {
     for (int b = tid; b < q.B; b += kReserveThreads) {
       if (is_bad(b)) continue;
@@ -234,8 +233,16 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
         for (int k = w.first; k <= own_last(w); ++k) need += !keeps(b, page_at(b, w, k));
       need += max(0, w.last + 1 - max(w.held, w.first));
     }
-    // (in 64 bits: sequences may lack 2^30 pages each)
-    const int64_t before = block_prefix((int64_t)need, buf, &sum);
+    // sequences may lack 2^30 pages each; where the table has no room for that 32 bits do (a reservation for one
+    // prompt's sequences 4.3 us, 4.5 in 64 bits)
+    int64_t before;
+    if (q.max_pages > kMaxLen / kReserveThreads) {
+      before = block_prefix((int64_t)need, wide_buf, &sum);
+    } else {
+      int narrow_sum;
+      before = block_prefix(need, buf, &narrow_sum);
+      sum = narrow_sum;
+    }
     mine_at = (int)min(total + before, (int64_t)0x7fffffff);
     mine_need = need;
     if (b < q.B && !one) {
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const __grid_c
   }
   if (tid == 0) {
     *pool.epoch = (uint32_t)(call >> 32);
-    if (free_pages) *free_pages = (int)(available - (enough ? total : 0));
+    if (free_pages) *free_pages = available - (enough ? (int)total : 0);
   }
 }
 

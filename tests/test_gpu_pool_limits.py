@@ -15,7 +15,8 @@ def G():
     return pages
 
 
-@pytest.mark.parametrize("B,width,taken", [(4, 1 << 29, 0), (4, 1 << 30, 0), (1030, 1 << 22, 0), (5, 1 << 30, 3)])
+@pytest.mark.parametrize("B,width,taken", [(4, 1 << 29, 0), (4, 1 << 30, 0), (1030, 1 << 22, 0), (5, 1 << 30, 3),
+                                           (1024, 1 << 20, 0), (1024, (1 << 20) + 1, 0), (2100, 1 << 20, 7)])
 def test_sequences_that_lack_more_pages_than_32_bits_count(G, B, width, taken):
     """With pages of one slot sequences may lack up to 2^30 pages each; their sum, 2^31, 2^32 or more, is
     more than the pool has: nothing is done."""
