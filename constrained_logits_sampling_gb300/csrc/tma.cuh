@@ -57,7 +57,7 @@ struct WaitLimit {
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 
 // Bounded wait for a phase: false if it ran out.  (A later wait of the same thread for the next
-// phase of that barrier would seem to succeed at once, so there must be none.)
+// phase of that barrier would seem to succeed at once, so nothing may rest on one.)
 __device__ __forceinline__ bool bounded_wait(unsigned long long* bar, uint32_t parity, WaitLimit* limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long start = clock64();

@@ -157,11 +157,12 @@ class CopyPages:
 
 
 class _PoolCall:
-    """A checked call of a pool, which it keeps alive: the name of the library's function and its arguments."""
+    """A checked call of a pool: the name of the library's function, its arguments, and what it keeps alive (the
+    pool among it)."""
 
     def __init__(self, name, pool, batch, args, keep):
         self.name, self.keep = name, (pool, batch, keep)
-        self.args = (ctypes.byref(pool._args), ctypes.byref(batch)) + args
+        self.args = (ctypes.byref(pool), ctypes.byref(batch)) + args
 
 
 class PagePool:
@@ -225,7 +226,8 @@ class PagePool:
         b = self._batch(page_table, held, kv_lens)
         args = (_dptr(src, torch.int32, n, "src", dev), _dptr(dst, torch.int32, n, "dst", dev), n,
                 _dptr(row_status, torch.int32, n, "row_status", dev))
-        return _PoolCall("clsample_pages_fork", self, b, args, (page_table, held, kv_lens, src, dst, row_status))
+        return _PoolCall("clsample_pages_fork", self._args, b, args,
+                         (self, page_table, held, kv_lens, src, dst, row_status))
 
     def reserve_args(self, page_table: torch.Tensor, held: torch.Tensor, kv_lens: torch.Tensor,
                      new_tokens: torch.Tensor, *, copies: torch.Tensor, row_status: Optional[torch.Tensor] = None,
@@ -237,15 +239,15 @@ class PagePool:
         args = (_dptr(new_tokens, torch.int32, b.B, "new_tokens", dev), _dptr(copies, torch.int32, 3 * b.B, "copies", dev),
                 _dptr(row_status, torch.int32, b.B, "row_status", dev),
                 _dptr(free_pages, torch.int32, 1, "free_pages", dev))
-        return _PoolCall("clsample_pages_reserve", self, b, args,
-                         (page_table, held, kv_lens, new_tokens, copies, row_status, free_pages))
+        return _PoolCall("clsample_pages_reserve", self._args, b, args,
+                         (self, page_table, held, kv_lens, new_tokens, copies, row_status, free_pages))
 
     def trim_args(self, page_table: torch.Tensor, held: torch.Tensor, kv_lens: torch.Tensor, *,
                   row_status: Optional[torch.Tensor] = None) -> _PoolCall:
         """Each sequence keeps the pages that kv_lens needs."""
         b = self._batch(page_table, held, kv_lens)
         args = (_dptr(row_status, torch.int32, b.B, "row_status", self.device),)
-        return _PoolCall("clsample_pages_trim", self, b, args, (page_table, held, kv_lens, row_status))
+        return _PoolCall("clsample_pages_trim", self._args, b, args, (self, page_table, held, kv_lens, row_status))
 
     def apply(self, call: _PoolCall, stream: Optional[torch.cuda.Stream] = None):
         """Enqueue one call on ``stream`` (default: current)."""
